@@ -141,9 +141,10 @@ def rows_to_c8(x):
     v = x.float()
     top = v.abs().amax(1)
     live = top > 0
-    inv = torch.where(live, 127.0 / top, torch.zeros_like(top))
+    full = torch.full_like(top, 127.0)      # (a Python number would be divided through its reciprocal)
+    inv = torch.where(live, full / top, torch.zeros_like(top))
     codes = torch.round(v * inv[:, None]).clamp_(-127, 127).to(torch.int8)
-    return codes, torch.where(live, top / 127.0, torch.zeros_like(top))
+    return codes, torch.where(live, top / full, torch.zeros_like(top))
 
 
 def groups_to_c8(x):
@@ -353,8 +354,8 @@ def exact(case, seed):
         if case["cfmt"] == "c8row":
             # the code is defined by float32 operations, the value is exact
             top = st["x"].float().abs().max(1, keepdim=True).values
-            q = (st["x"].float() * (127.0 / top)).round()
-            return q.to(d) * (top / 127.0).to(d)
+            q = (st["x"].float() * (127.0 / top.to(d)).float()).round()
+            return q.to(d) * (top.to(d) / 127.0).float().to(d)
         M, C = v.shape
         pad = -C % GROUP
         v = torch.cat((v, v.new_zeros(M, pad)), 1).reshape(M, -1, GROUP)
@@ -406,11 +407,12 @@ def exact(case, seed):
         x = st["x"].to(d)
         t = x @ A
         top = st["x"].float().abs().max(1, keepdim=True).values
-        codes = (st["x"].float() * (127.0 / top)).round()
+        codes = (st["x"].float() * (127.0 / top.to(d)).float()).round()
+        unit = (top.to(d) / 127.0).float().to(d)
         if case["save_x"]:
-            out.update(x_codes=None, x_scales=(top / 127.0)[:, 0].to(d))
+            out.update(x_codes=None, x_scales=unit[:, 0])
         if case["fmt"] == "w8":
-            x = codes.to(d) * (top / 127.0).to(d)
+            x = codes.to(d) * unit
         out.update(t=t)
     else:
         x, t = st["x_codes"].to(d) * st["x_scales"].to(d)[:, None], st["t"].to(d)
