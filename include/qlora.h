@@ -344,6 +344,133 @@ int qlora_bwd_timed(const qlora_linear* L, int M, int dtype, const void* x,
  * arithmetic; usable without a GPU. */
 const char* qlora_bwd_main_kernel(const qlora_linear* L, int M, int dtype);
 
+/* ---- the layer with its epilogue, and 8-bit activation checkpoints ---------
+ *
+ * A dense layer adds a bias and applies an activation, and a block adds its
+ * input back ("Introduce QLoRA-like technique", benchmark.py: Dense(1024)
+ * layers with ReLU; "Parameter-efficient fine-tuning of GPT-2 with LoRA": the
+ * transformer's feed-forward layers):
+ *
+ *   z = x deq(W) + s (x A) B + bias,     y = act(z) + residual
+ *
+ * with the base product of qlora_fwd for the layer's format. The backward
+ * needs x (for dA), t and z (for act'), and keeping them takes most of a
+ * training step's memory (keras-llm-light README, "Block-wise gradient
+ * checkpointing": block inputs are cached and blocks recomputed from them).
+ * They can be kept in 8 bits, in one of two forms of an activation [M, C]:
+ *
+ *   QLORA_C8ROW  codes int8 [M, C], scales float32 [M]: the forward's own row
+ *                quantizer (qlora_quantize_rows), so that the int8 forward
+ *                leaves x's checkpoint at no cost and repeats its base
+ *                product from it exactly;
+ *   QLORA_C8G32  codes int8 [M, C], scales uint8 [M, ceil(C / 32)]: 32
+ *                consecutive columns of a row share the scale 2^e, e the
+ *                smallest integer (at least -126) with absmax <= 127 2^e,
+ *                kept as the byte e + 127; code = round-half-even(v 2^-e),
+ *                but at least 1 in size where v is not 0, so the sign (and
+ *                relu') survives. An all-zero group has byte 1 and zero
+ *                codes; a group with an infinity or a NaN has byte 255 and
+ *                zero codes, and reads back as NaN.
+ *
+ * Activations: relu (relu'(0) = 0); gelu = z Phi(z); gelu_tanh = z (1 +
+ * tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2; silu = z / (1 + e^-z). They are
+ * evaluated in float32 on the unrounded z; -inf gives their limit (0, and
+ * slope 0), NaN stays NaN.
+ *
+ * Constraints as above, with M >= 1 and every pointer 16-byte aligned; of a
+ * pair (codes, scales) both or neither is given. Every tensor is dense
+ * row-major. Outputs must not overlap inputs or each other (EINVAL), except
+ * that y may be residual, dx may be add, and dz may be dy, exactly. */
+typedef enum {
+  QLORA_ACT_NONE = 0, QLORA_ACT_RELU = 1, QLORA_ACT_GELU = 2, QLORA_ACT_GELU_TANH = 3,
+  QLORA_ACT_SILU = 4
+} qlora_act;
+typedef enum { QLORA_C8ROW = 0, QLORA_C8G32 = 1 } qlora_cfmt;
+
+/* Bytes of the codes and scales of an activation [M, C] in form cfmt (C a
+ * multiple of 16, at least 16; ERANGE from M C = 2^31, and for QLORA_C8ROW
+ * past C = 2^30). Host-only arithmetic. */
+int qlora_ckpt_bytes(int M, int C, int cfmt, size_t* codes_bytes, size_t* scale_bytes);
+
+/* Write x [M, C] (compute dtype) in form cfmt, and read it back: value =
+ * code * scale, rounded once to the compute dtype (exact in either dtype for
+ * QLORA_C8G32). */
+int qlora_ckpt_write(const void* x, int M, int C, int dtype, int cfmt, int8_t* codes,
+                     void* scales, void* stream);
+int qlora_ckpt_read(const int8_t* codes, const void* scales, int M, int C, int cfmt,
+                    int dtype, void* x, void* stream);
+
+/* What qlora_fwd_epi and qlora_fwd_ckpt do beyond the product. Members may be
+ * NULL / 0. */
+typedef struct {
+  int32_t act;            /* qlora_act */
+  const float* bias;      /* float32 [N] */
+  const void* residual;   /* [M, N] in the compute dtype; may be y */
+  void* z;                /* out: z [M, N], rounded once to the compute dtype */
+  int8_t* z_codes;        /* out: z in form QLORA_C8G32 (from the unrounded z) */
+  uint8_t* z_scales;
+  int8_t* x_codes;        /* out: x in form QLORA_C8ROW (qlora_fwd_epi only) */
+  float* x_scales;
+} qlora_epilogue;
+
+/* qlora_fwd with the epilogue: y [M, N] = act(z) + residual, rounded once to
+ * the compute dtype. Workspace: qlora_fwd_workspace. For int8 formats x_codes
+ * costs nothing (the product reads the codes there). */
+int qlora_fwd_epi(const qlora_linear* L, int M, int dtype, const void* x,
+                  const qlora_epilogue* e, void* y, float* t_save, void* ws,
+                  size_t ws_bytes, void* stream);
+
+/* The same y (and z) again from x's row checkpoint and the t saved with it,
+ * for blocks recomputed in the backward pass. Int8 formats: the base product
+ * is exactly that of the call that wrote the checkpoint. QLORA_W4G128: the
+ * integer product of qlora_fwd_a8w4. Workspace: qlora_fwd_workspace. */
+int qlora_fwd_ckpt(const qlora_linear* L, int M, int dtype, const int8_t* x_codes,
+                   const float* x_scales, const float* t, const qlora_epilogue* e,
+                   void* y, void* ws, size_t ws_bytes, void* stream);
+
+/* What qlora_bwd_epi does to the input gradient: with x = act(z) made by the
+ * layer before and also (before or beside the activation) a skip connection
+ * carrying the gradient add,
+ *   dx = (dy deq(W)^T + s u A^T) act'(z) + add.
+ * z [M, K] comes in the compute dtype or in form QLORA_C8G32 (exactly one of
+ * them where act is not QLORA_ACT_NONE, none where it is). */
+typedef struct {
+  int32_t act;
+  const void* z;
+  const int8_t* z_codes;
+  const uint8_t* z_scales;
+  const void* add;        /* [M, K] in the compute dtype, or NULL; may be dx */
+} qlora_grad_epilogue;
+
+/* qlora_bwd with x either in the compute dtype or as its row checkpoint
+ * (exactly one of x and the pair x_codes, x_scales), and the gradient
+ * epilogue g (NULL: none) on dx. From a checkpoint
+ *   dA = s sum_m x_scales[m] x_codes[m, :]^T u[m, :],
+ * and t_saved is required. dx may be NULL where g is NULL. Workspace:
+ * qlora_bwd_workspace. */
+int qlora_bwd_epi(const qlora_linear* L, int M, int dtype, const void* x,
+                  const int8_t* x_codes, const float* x_scales, const void* dy,
+                  const float* t_saved, const qlora_grad_epilogue* g, void* dx,
+                  float* dA, float* dB, void* ws, size_t ws_bytes, void* stream);
+
+/* Its first half, for qlora_bwd_finish or qlora_bwd_finish_batch to complete
+ * (as qlora_bwd_partial). */
+int qlora_bwd_epi_partial(const qlora_linear* L, int M, int dtype, const void* x,
+                          const int8_t* x_codes, const float* x_scales, const void* dy,
+                          const float* t_saved, const qlora_grad_epilogue* g, void* dx,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/* The gradient through bias and activation alone, for a layer whose output
+ * gradient dy [M, N] is that of act(z):
+ *   dz = dy act'(z)   [M, N] in the compute dtype; may be dy, or NULL
+ *   dbias = sum_m dz  float32 [N], of the unrounded products; or NULL
+ * (at least one of them). z as in qlora_grad_epilogue; with QLORA_ACT_NONE
+ * dbias is the column sum of dy. N a multiple of 16. */
+int qlora_act_bwd_workspace(int M, int N, size_t* bytes);
+int qlora_act_bwd(int act, int M, int N, int dtype, const void* dy, const void* z,
+                  const int8_t* z_codes, const uint8_t* z_scales, void* dz, float* dbias,
+                  void* ws, size_t ws_bytes, void* stream);
+
 /* Merge the trained adapter into the frozen int8 weight ("Parameter-efficient
  * fine-tuning of GPT-2 with LoRA", "Merge weights and generate text!": the
  * merged kernel is the frozen kernel plus the adapter product; "Introduce

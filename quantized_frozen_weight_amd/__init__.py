@@ -7,7 +7,9 @@ library call does, and raises if the library has not been built.
 """
 
 from .binding import (  # noqa: F401
-    QLinear, QloraError, qlora_bwd, qlora_bwd_workspace, qlora_fwd,
-    qlora_fwd_acc, qlora_fwd_workspace, qlora_quantize, qlora_quantize_rows,
+    Checkpoint, QLinear, QloraError, qlora_act_bwd, qlora_bwd, qlora_bwd_epi,
+    qlora_bwd_epi_partial, qlora_bwd_workspace, qlora_ckpt_read,
+    qlora_ckpt_write, qlora_fwd, qlora_fwd_acc, qlora_fwd_ckpt, qlora_fwd_epi,
+    qlora_fwd_workspace, qlora_quantize, qlora_quantize_rows,
     qlora_status_str, qlora_weight_bytes,
 )

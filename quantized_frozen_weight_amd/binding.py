@@ -22,6 +22,10 @@ QLORA_OK, QLORA_EINVAL, QLORA_EUNSUPPORTED, QLORA_EWORKSPACE, QLORA_ERANGE, QLOR
 QLORA_F32, QLORA_BF16 = 0, 1
 QLORA_W8, QLORA_W4G128, QLORA_W8O = 0, 1, 2
 
+_ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}      # qlora_act
+_CFMT = {"c8row": 0, "c8g32": 1}                                         # qlora_cfmt
+CKPT_GROUP = 32          # columns per scale of a "c8g32" checkpoint
+
 _FMT = {"w8": QLORA_W8, "w4g128": QLORA_W4G128, "w8o": QLORA_W8O}
 
 
@@ -55,6 +59,9 @@ EXPORTS = (
     "qlora_merge", "qlora_bwd_partial", "qlora_bwd_finish", "qlora_fwd_a8w4",
     "qlora_quantize_heads", "qlora_outlier_layout", "qlora_bwd_finish_batch",
     "qlora_bwd_partials_bytes", "qlora_bwd_main_kernel", "qlora_bwd_noalloc",
+    "qlora_ckpt_bytes", "qlora_ckpt_write", "qlora_ckpt_read", "qlora_fwd_epi",
+    "qlora_fwd_ckpt", "qlora_bwd_epi", "qlora_bwd_epi_partial",
+    "qlora_act_bwd_workspace", "qlora_act_bwd",
 )
 QLORA_NOALLOC_SCRATCH_BYTES = 16 << 20
 # include/qlora_probe.h: measurement probes (not part of the layer)
@@ -71,6 +78,29 @@ class qlora_finish_item(ctypes.Structure):
         ("dB", ctypes.c_void_p),
         ("ws", ctypes.c_void_p),
         ("ws_bytes", ctypes.c_size_t),
+    ]
+
+
+class qlora_epilogue(ctypes.Structure):
+    _fields_ = [
+        ("act", ctypes.c_int32),
+        ("bias", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p),
+        ("z", ctypes.c_void_p),
+        ("z_codes", ctypes.c_void_p),
+        ("z_scales", ctypes.c_void_p),
+        ("x_codes", ctypes.c_void_p),
+        ("x_scales", ctypes.c_void_p),
+    ]
+
+
+class qlora_grad_epilogue(ctypes.Structure):
+    _fields_ = [
+        ("act", ctypes.c_int32),
+        ("z", ctypes.c_void_p),
+        ("z_codes", ctypes.c_void_p),
+        ("z_scales", ctypes.c_void_p),
+        ("add", ctypes.c_void_p),
     ]
 
 
@@ -109,6 +139,16 @@ def lib() -> ctypes.CDLL:
     L.qlora_outlier_layout.argtypes = [i, i, psz, psz, psz, ctypes.POINTER(ctypes.c_int32)]
     L.qlora_bwd_main_kernel.argtypes = [plin, i, i]
     L.qlora_bwd_noalloc.argtypes = [plin, i, i, vp, vp, vp, vp, vp, vp, vp]
+    L.qlora_ckpt_bytes.argtypes = [i, i, i, psz, psz]
+    L.qlora_ckpt_write.argtypes = [vp, i, i, i, i, vp, vp, vp]
+    L.qlora_ckpt_read.argtypes = [vp, vp, i, i, i, i, vp, vp]
+    pepi, pge = ctypes.POINTER(qlora_epilogue), ctypes.POINTER(qlora_grad_epilogue)
+    L.qlora_fwd_epi.argtypes = [plin, i, i, vp, pepi, vp, vp, vp, sz, vp]
+    L.qlora_fwd_ckpt.argtypes = [plin, i, i, vp, vp, vp, pepi, vp, vp, sz, vp]
+    L.qlora_bwd_epi.argtypes = [plin, i, i, vp, vp, vp, vp, vp, pge, vp, vp, vp, vp, sz, vp]
+    L.qlora_bwd_epi_partial.argtypes = [plin, i, i, vp, vp, vp, vp, vp, pge, vp, vp, sz, vp]
+    L.qlora_act_bwd_workspace.argtypes = [i, i, psz]
+    L.qlora_act_bwd.argtypes = [i, i, i, i, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     for name in EXPORTS[1:]:
         getattr(L, name).restype = ctypes.c_int
     L.qlora_bwd_main_kernel.restype = ctypes.c_char_p
@@ -446,3 +486,294 @@ def qlora_fwd_acc(layer: QLinear, x):
                                ws.numel() * ws.element_size(), _stream()),
            "qlora_fwd_acc")
     return acc
+
+
+# ---------------------------------------------------------------------------
+# The layer with its epilogue, and 8-bit activation checkpoints. These calls
+# run on the device their tensors are on (that device's current stream) and
+# raise ValueError / TypeError for tensors the C ABI could not check.
+# ---------------------------------------------------------------------------
+@dataclass
+class Checkpoint:
+    """An activation [M, C] in 8 bits: codes int8 [M, C] and its scales,
+    float32 [M] ("c8row") or uint8 [M, ceil(C / 32)] ("c8g32")."""
+    codes: object
+    scales: object
+    fmt: str
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+
+def _on(device):
+    """Context in which `device` is the current one."""
+    import contextlib
+
+    import torch
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _tensor(t, what: str, shape, dtype, device):
+    """t, checked to be a dense tensor of this shape, type and device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: not contiguous")
+    return t
+
+
+def _rows(x, what: str, columns=None):
+    """(M, C, dtype code) of a dense [M, C] activation on a GPU."""
+    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{what}: a contiguous 2-D GPU tensor is needed")
+    if columns is not None and x.shape[1] != columns:
+        raise ValueError(f"{what}: {x.shape[1]} columns, expected {columns}")
+    return x.shape[0], x.shape[1], _dtype_code(x)
+
+
+def _ckpt(c, what: str, fmt: str, shape, device) -> Checkpoint:
+    import torch
+    if c.fmt != fmt:
+        raise ValueError(f"{what}: form {c.fmt!r}, expected {fmt!r}")
+    _tensor(c.codes, f"{what}.codes", shape, torch.int8, device)
+    if fmt == "c8row":
+        _tensor(c.scales, f"{what}.scales", (shape[0],), torch.float32, device)
+    else:
+        _tensor(c.scales, f"{what}.scales", (shape[0], -(-shape[1] // CKPT_GROUP)), torch.uint8, device)
+    return c
+
+
+def _new_ckpt(M: int, C: int, fmt: str, device) -> Checkpoint:
+    import torch
+    if fmt not in _CFMT:
+        raise ValueError(f"unknown checkpoint form {fmt!r}")
+    codes = torch.empty((M, C), dtype=torch.int8, device=device)
+    if fmt == "c8row":
+        scales = torch.empty((M,), dtype=torch.float32, device=device)
+    else:
+        scales = torch.empty((M, -(-C // CKPT_GROUP)), dtype=torch.uint8, device=device)
+    return Checkpoint(codes, scales, fmt)
+
+
+def _layer_on(layer: QLinear, device) -> qlora_linear:
+    import torch
+    for t, what in ((layer.codes, "codes"), (layer.scales, "scales"), (layer.A, "A"), (layer.B, "B")):
+        if t.device != device:
+            raise ValueError(f"layer {what} on {t.device}, the activations on {device}")
+    _tensor(layer.A, "layer A", (layer.K, layer.r), torch.float32, device)
+    _tensor(layer.B, "layer B", _b_shape(layer), torch.float32, device)
+    return layer.cstruct()
+
+
+def _act(act: str) -> int:
+    if act not in _ACT:
+        raise ValueError(f"unknown activation {act!r}")
+    return _ACT[act]
+
+
+def qlora_ckpt_write(x, fmt: str = "c8row", out: Optional[Checkpoint] = None) -> Checkpoint:
+    """x [M, C] as an 8-bit checkpoint of form fmt."""
+    M, C, dt = _rows(x, "x")
+    c = _new_ckpt(M, C, fmt, x.device) if out is None else _ckpt(out, "out", fmt, (M, C), x.device)
+    with _on(x.device):
+        _check(lib().qlora_ckpt_write(_ptr(x), M, C, dt, _CFMT[fmt], _ptr(c.codes), _ptr(c.scales),
+                                      _stream()), "qlora_ckpt_write")
+    return c
+
+
+def qlora_ckpt_read(ckpt: Checkpoint, dtype, out=None):
+    """The values of a checkpoint in dtype (torch.float32 or torch.bfloat16)."""
+    import torch
+    M, C = ckpt.codes.shape
+    dev = ckpt.codes.device
+    _ckpt(ckpt, "ckpt", ckpt.fmt, (M, C), dev)
+    if not ckpt.codes.is_cuda:
+        raise ValueError("ckpt: GPU tensors are needed")
+    x = torch.empty((M, C), dtype=dtype, device=dev) if out is None else _tensor(out, "out", (M, C), dtype, dev)
+    with _on(dev):
+        _check(lib().qlora_ckpt_read(_ptr(ckpt.codes), _ptr(ckpt.scales), M, C, _CFMT[ckpt.fmt],
+                                     _dtype_code(x), _ptr(x), _stream()), "qlora_ckpt_read")
+    return x
+
+
+def _epilogue(layer, M, dtype, device, act, bias, residual, save_z, z, xc):
+    """(C struct, z) of a forward epilogue."""
+    import torch
+    e = qlora_epilogue(act=_act(act))
+    if bias is not None:
+        e.bias = _ptr(_tensor(bias, "bias", (layer.N,), torch.float32, device))
+    if residual is not None:
+        e.residual = _ptr(_tensor(residual, "residual", (M, layer.N), dtype, device))
+    if save_z == "full":
+        z = torch.empty((M, layer.N), dtype=dtype, device=device) if z is None else \
+            _tensor(z, "z", (M, layer.N), dtype, device)
+        e.z = _ptr(z)
+    elif save_z == "c8g32":
+        z = _new_ckpt(M, layer.N, "c8g32", device) if z is None else \
+            _ckpt(z, "z", "c8g32", (M, layer.N), device)
+        e.z_codes, e.z_scales = _ptr(z.codes), _ptr(z.scales)
+    elif save_z is not None:
+        raise ValueError(f"save_z: {save_z!r} is neither None, 'full' nor 'c8g32'")
+    else:
+        z = None
+    if xc is not None:
+        e.x_codes, e.x_scales = _ptr(xc.codes), _ptr(xc.scales)
+    return e, z
+
+
+def qlora_fwd_epi(layer: QLinear, x, act: str = "none", bias=None, residual=None, save_t: bool = True,
+                  save_z: Optional[str] = None, save_x: bool = False, y=None, t=None, z=None,
+                  xc: Optional[Checkpoint] = None, ws=None):
+    """y = act(x deq(W) + s (x A) B + bias) + residual. Returns (y, t, z, xc):
+    t = x A (None unless save_t), z the pre-activation (save_z "full": in x's
+    dtype, "c8g32": a Checkpoint, None: not saved) and xc x's row checkpoint
+    (None unless save_x). y may be the residual tensor itself."""
+    import torch
+    M, _, dt = _rows(x, "x", layer.K)
+    dev = x.device
+    cs = _layer_on(layer, dev)
+    y = torch.empty((M, layer.N), dtype=x.dtype, device=dev) if y is None else \
+        _tensor(y, "y", (M, layer.N), x.dtype, dev)
+    if save_t:
+        t = torch.empty((M, layer.r), dtype=torch.float32, device=dev) if t is None else \
+            _tensor(t, "t", (M, layer.r), torch.float32, dev)
+    if save_x:
+        xc = _new_ckpt(M, layer.K, "c8row", dev) if xc is None else _ckpt(xc, "xc", "c8row", (M, layer.K), dev)
+    else:
+        xc = None
+    e, z = _epilogue(layer, M, x.dtype, dev, act, bias, residual, save_z, z, xc)
+    ws = _workspace(qlora_fwd_workspace(layer, M, dt), dev, ws)
+    with _on(dev):
+        _check(lib().qlora_fwd_epi(ctypes.byref(cs), M, dt, _ptr(x), ctypes.byref(e), _ptr(y),
+                                   _ptr(t) if save_t else None, _ptr(ws),
+                                   ws.numel() * ws.element_size(), _stream()), "qlora_fwd_epi")
+    return y, (t if save_t else None), z, xc
+
+
+def qlora_fwd_ckpt(layer: QLinear, xc: Checkpoint, t, dtype, act: str = "none", bias=None, residual=None,
+                   save_z: Optional[str] = None, y=None, z=None, ws=None):
+    """qlora_fwd_epi's y (and z) again from x's row checkpoint and t; dtype is
+    the activations' torch dtype. Returns (y, z)."""
+    import torch
+    M, dev = xc.codes.shape[0], xc.codes.device
+    _ckpt(xc, "xc", "c8row", (M, layer.K), dev)
+    if not xc.codes.is_cuda:
+        raise ValueError("xc: GPU tensors are needed")
+    _tensor(t, "t", (M, layer.r), torch.float32, dev)
+    cs = _layer_on(layer, dev)
+    y = torch.empty((M, layer.N), dtype=dtype, device=dev) if y is None else \
+        _tensor(y, "y", (M, layer.N), dtype, dev)
+    dt = _dtype_code(y)
+    e, z = _epilogue(layer, M, dtype, dev, act, bias, residual, save_z, z, None)
+    ws = _workspace(qlora_fwd_workspace(layer, M, dt), dev, ws)
+    with _on(dev):
+        _check(lib().qlora_fwd_ckpt(ctypes.byref(cs), M, dt, _ptr(xc.codes), _ptr(xc.scales), _ptr(t),
+                                    ctypes.byref(e), _ptr(y), _ptr(ws), ws.numel() * ws.element_size(),
+                                    _stream()), "qlora_fwd_ckpt")
+    return y, z
+
+
+def _bwd_epi_args(layer, x, dy, t, act, z, add, need_dx, dx):
+    """The checked arguments that qlora_bwd_epi and its first half share."""
+    import torch
+    M, _, dt = _rows(dy, "dy", layer.N)
+    dev, shape = dy.device, (M, layer.K)
+    cs = _layer_on(layer, dev)
+    xp = xcodes = xscales = None
+    if isinstance(x, Checkpoint):
+        _ckpt(x, "x", "c8row", shape, dev)
+        if t is None:
+            raise ValueError("t: needed with a checkpoint")
+        xcodes, xscales = _ptr(x.codes), _ptr(x.scales)
+    else:
+        xp = _ptr(_tensor(x, "x", shape, dy.dtype, dev))
+    if t is not None:
+        _tensor(t, "t", (M, layer.r), torch.float32, dev)
+    g = qlora_grad_epilogue(act=_act(act))
+    if isinstance(z, Checkpoint):
+        _ckpt(z, "z", "c8g32", shape, dev)
+        g.z_codes, g.z_scales = _ptr(z.codes), _ptr(z.scales)
+    elif z is not None:
+        g.z = _ptr(_tensor(z, "z", shape, dy.dtype, dev))
+    if add is not None:
+        g.add = _ptr(_tensor(add, "add", shape, dy.dtype, dev))
+    if need_dx:
+        dx = torch.empty(shape, dtype=dy.dtype, device=dev) if dx is None else \
+            _tensor(dx, "dx", shape, dy.dtype, dev)
+    else:
+        if act != "none" or z is not None or add is not None:
+            raise ValueError("need_dx: act, z and add apply to dx")
+        dx = None
+    gp = ctypes.byref(g) if need_dx else None
+    return cs, M, dt, dev, (xp, xcodes, xscales, _ptr(dy), _ptr(t), gp, _ptr(dx)), dx, g
+
+
+def qlora_bwd_epi(layer: QLinear, x, dy, t=None, act: str = "none", z=None, add=None, need_dx: bool = True,
+                  dx=None, dA=None, dB=None, ws=None):
+    """qlora_bwd with x a tensor or its row Checkpoint (t then required), and
+    dx = (dy deq(W)^T + s u A^T) act'(z) + add, z a tensor or a "c8g32"
+    Checkpoint. dx may be the add tensor itself. Returns (dx or None, dA, dB)."""
+    import torch
+    cs, M, dt, dev, args, dx, _keep = _bwd_epi_args(layer, x, dy, t, act, z, add, need_dx, dx)
+    dA = torch.empty((layer.K, layer.r), dtype=torch.float32, device=dev) if dA is None else \
+        _tensor(dA, "dA", (layer.K, layer.r), torch.float32, dev)
+    dB = torch.empty(_b_shape(layer), dtype=torch.float32, device=dev) if dB is None else \
+        _tensor(dB, "dB", _b_shape(layer), torch.float32, dev)
+    ws = _workspace(qlora_bwd_workspace(layer, M, dt), dev, ws)
+    with _on(dev):
+        _check(lib().qlora_bwd_epi(ctypes.byref(cs), M, dt, *args, _ptr(dA), _ptr(dB), _ptr(ws),
+                                   ws.numel() * ws.element_size(), _stream()), "qlora_bwd_epi")
+    return dx, dA, dB
+
+
+def qlora_bwd_epi_partial(layer: QLinear, x, dy, t=None, act: str = "none", z=None, add=None,
+                          need_dx: bool = True, dx=None, ws=None):
+    """First half of qlora_bwd_epi: (dx or None, workspace), the adapter
+    gradients left to qlora_bwd_finish or qlora_bwd_finish_batch."""
+    cs, M, dt, dev, args, dx, _keep = _bwd_epi_args(layer, x, dy, t, act, z, add, need_dx, dx)
+    ws = _workspace(qlora_bwd_workspace(layer, M, dt), dev, ws)
+    with _on(dev):
+        _check(lib().qlora_bwd_epi_partial(ctypes.byref(cs), M, dt, *args, _ptr(ws),
+                                           ws.numel() * ws.element_size(), _stream()),
+               "qlora_bwd_epi_partial")
+    return dx, ws
+
+
+def qlora_act_bwd(act: str, dy, z=None, need_dz: bool = True, need_dbias: bool = True, dz=None, dbias=None,
+                  ws=None):
+    """dz = dy act'(z) and dbias = its float32 column sums, z a tensor or a
+    "c8g32" Checkpoint. dz may be dy itself. Returns (dz or None, dbias or
+    None); act "none" takes no z."""
+    import torch
+    M, N, dt = _rows(dy, "dy")
+    dev = dy.device
+    zp = zc = zs = None
+    if isinstance(z, Checkpoint):
+        _ckpt(z, "z", "c8g32", (M, N), dev)
+        zc, zs = _ptr(z.codes), _ptr(z.scales)
+    elif z is not None:
+        zp = _ptr(_tensor(z, "z", (M, N), dy.dtype, dev))
+    if need_dz:
+        dz = torch.empty_like(dy) if dz is None else _tensor(dz, "dz", (M, N), dy.dtype, dev)
+    else:
+        dz = None
+    if need_dbias:
+        dbias = torch.empty((N,), dtype=torch.float32, device=dev) if dbias is None else \
+            _tensor(dbias, "dbias", (N,), torch.float32, dev)
+        n = ctypes.c_size_t()
+        _check(lib().qlora_act_bwd_workspace(M, N, ctypes.byref(n)), "qlora_act_bwd_workspace")
+        ws = _workspace(n.value, dev, ws)
+    else:
+        dbias = None
+    with _on(dev):
+        _check(lib().qlora_act_bwd(_act(act), M, N, dt, _ptr(dy), zp, zc, zs, _ptr(dz), _ptr(dbias),
+                                   _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                                   _stream()), "qlora_act_bwd")
+    return dz, dbias

@@ -4,6 +4,7 @@
 
 #include <mutex>
 
+#include "epilogue.hpp"
 #include "launch.hpp"
 #include "outlier.hpp"
 #include "qlora.h"
@@ -189,6 +190,206 @@ int bwd_check_ws(const qlora_linear* L, int M, int dtype, void* ws, size_t ws_by
   return QLORA_OK;
 }
 
+// The launches of a backward's first half, arguments validated: dx (NULL:
+// none) and the partial sums of dA and dB in ws. x, or (xq not NULL) its row
+// checkpoint; ge (NULL: none) on dx.
+void enqueue_bwd_partial(const qlora_linear* L, int M, int dtype, const void* x, const int8_t* xq,
+                         const float* sx, const void* dy, const float* t_saved, const GradEpi* ge,
+                         void* dx, void* ws, hipStream_t s, int repeats, void* ev_start,
+                         void* ev_stop) {
+  const BwdLayout w = bwd_layout(L, M, dtype);
+  const float sc = lora_s(L);
+  float* u = reinterpret_cast<float*>(at(ws, w.u));
+  const float* t = t_saved;
+  if (t == nullptr) {
+    float* tw = reinterpret_cast<float*>(at(ws, w.t));
+    launch_lora_down(dtype, x, M, L->K, L->A, L->r, tw, s, reinterpret_cast<float*>(at(ws, w.rs)));
+    t = tw;
+  }
+  float* partB = reinterpret_cast<float*>(at(ws, w.pB));
+  float* partA = reinterpret_cast<float*>(at(ws, w.pA));
+  if (dtype == QLORA_BF16 && dx != nullptr) {
+    // one launch: dx, u, and the per-row-block partial sums of dA and dB
+    mark(ev_start, s);
+    for (int rep = 0; rep < repeats; ++rep)
+      launch_bwd_fused(L->fmt, M, L->K, L->N, static_cast<const uint16_t*>(dy),
+                       L->codes, L->scales, L->B, head_width(L), L->A, t,
+                       static_cast<const uint16_t*>(x), L->r, sc,
+                       static_cast<uint16_t*>(dx), partA, partB,
+                       reinterpret_cast<float*>(at(ws, w.pdx)),
+                       reinterpret_cast<float*>(at(ws, w.pu)), s, xq, sx, ge);
+    mark(ev_stop, s);
+    return;
+  }
+  launch_bwd_rows(dtype, dy, M, L->N, L->B, head_width(L), L->r, nullptr, nullptr, u, s);
+  SkinnyJobs sk = make_adapter_grad_jobs(M, L->r, sc, t, dy, L->N, nullptr, partB,
+                                         u, xq != nullptr ? static_cast<const void*>(xq) : x, L->K,
+                                         nullptr, partA);
+  sk.sx = sx;
+  sk.nsplit = bwd_splits(L, M);
+  sk.rows_per_split = (M + sk.nsplit - 1) / sk.nsplit;
+  sk.rows_per_split = (sk.rows_per_split + 3) / 4 * 4;
+  // float32 compute (int8 weights): the adapter-gradient stage 1, then the
+  // float32 input gradient; or no input gradient at all
+  launch_skinny_stage1(dtype, sk, s);
+  mark(ev_start, s);
+  if (dx != nullptr)
+    for (int rep = 0; rep < repeats; ++rep)
+      launch_gemm_dx_f32(M, L->K, L->N, static_cast<const float*>(dy),
+                         static_cast<const int8_t*>(L->codes),
+                         static_cast<const float*>(L->scales), u, L->A, L->r,
+                         sc, static_cast<float*>(dx), s, ge);
+  mark(ev_stop, s);
+}
+
+// ---- the epilogue and checkpoint calls -------------------------------------
+
+inline size_t dtype_bytes(int dtype) { return dtype == QLORA_F32 ? 4 : 2; }
+
+// A pointer that may be NULL and must be aligned where it is not.
+inline bool opt16(const void* p) { return p == nullptr || aligned16(p); }
+
+// Byte ranges of a call's arguments; NULL ranges are left out.
+struct Ranges {
+  struct { const char* p; size_t n; } r[24];
+  int count = 0;
+  void add(const void* p, size_t n) {
+    if (p != nullptr && n > 0) { r[count].p = static_cast<const char*>(p); r[count].n = n; ++count; }
+  }
+  bool hits(const void* p, size_t n) const {
+    const char* q = static_cast<const char*>(p);
+    for (int i = 0; i < count; ++i)
+      if (q < r[i].p + r[i].n && r[i].p < q + n) return true;
+    return false;
+  }
+};
+
+// Outputs against inputs and against each other.
+bool disjoint(const Ranges& outs, const Ranges& ins) {
+  Ranges seen = ins;
+  for (int i = 0; i < outs.count; ++i) {
+    if (seen.hits(outs.r[i].p, outs.r[i].n)) return false;
+    seen.add(outs.r[i].p, outs.r[i].n);
+  }
+  return true;
+}
+
+void add_layer(Ranges& in, const qlora_linear* L) {
+  size_t cb = 0, sb = 0;
+  qlora_weight_bytes(L->K, L->N, L->fmt, &cb, &sb);
+  in.add(L->codes, cb);
+  in.add(L->scales, sb);
+  in.add(L->A, (size_t)L->K * L->r * 4);
+  in.add(L->B, (size_t)L->N * L->r * 4);
+}
+
+inline bool pair_ok(const void* codes, const void* scales) {
+  return (codes == nullptr) == (scales == nullptr) && opt16(codes) && opt16(scales);
+}
+
+inline bool act_ok(int act) { return act >= QLORA_ACT_NONE && act <= QLORA_ACT_SILU; }
+
+// The forward epilogue: pointers checked, and its ranges added. in_y: y given
+// as the residual itself.
+int check_epilogue(const qlora_epilogue* e, int M, int K, int N, int dtype, const void* y,
+                   Ranges& in, Ranges& out) {
+  if (e == nullptr || !act_ok(e->act)) return QLORA_EINVAL;
+  if (!opt16(e->bias) || !opt16(e->residual) || !opt16(e->z)) return QLORA_EINVAL;
+  if (!pair_ok(e->z_codes, e->z_scales) || !pair_ok(e->x_codes, e->x_scales)) return QLORA_EINVAL;
+  const size_t mn = (size_t)M * N;
+  in.add(e->bias, (size_t)N * 4);
+  if (e->residual != y) in.add(e->residual, mn * dtype_bytes(dtype));
+  out.add(e->z, mn * dtype_bytes(dtype));
+  out.add(e->z_codes, mn);
+  out.add(e->z_scales, (size_t)M * group_count(N));
+  out.add(e->x_codes, (size_t)M * K);
+  out.add(e->x_scales, (size_t)M * 4);
+  return QLORA_OK;
+}
+
+FwdEpi fwd_epi(const qlora_epilogue* e, int N) {
+  FwdEpi f{};
+  f.act = act_params(e->act);
+  f.bias = e->bias; f.res = e->residual; f.z = e->z;
+  f.zc = e->z_codes; f.zs = e->z_scales; f.zg = group_count(N);
+  return f;
+}
+
+// The int8 and affine products of a call, from x's codes and scales.
+void enqueue_fwd_i8(const qlora_linear* L, int M, int dtype, const int8_t* xq, const float* sx,
+                    const float* asum, const float* t, const FwdEpi& epi, void* y, void* ws,
+                    const FwdLayout& w, hipStream_t s) {
+  const int8_t* codes = static_cast<const int8_t*>(L->codes);
+  int32_t* pacc = reinterpret_cast<int32_t*>(at(ws, w.pacc));
+  if (L->fmt == QLORA_W8)
+    launch_gemm_fwd_w8(dtype, M, L->N, L->K, xq, codes, sx, static_cast<const float*>(L->scales), t,
+                       L->B, head_width(L), L->r, lora_s(L), y, nullptr, pacc, &epi, s);
+  else
+    launch_gemm_fwd_w8o(M, L->N, L->K, xq, codes, sx, asum, L->scales, t, L->B, head_width(L), L->r,
+                        lora_s(L), static_cast<uint16_t*>(y), pacc,
+                        reinterpret_cast<float*>(at(ws, w.pcorr)), &epi, s);
+}
+
+// z of a gradient: given in exactly one form where act needs it, else not at
+// all.
+int check_z(int act, const void* z, const int8_t* zc, const uint8_t* zs) {
+  if (!act_ok(act) || !opt16(z) || !pair_ok(zc, zs)) return QLORA_EINVAL;
+  const int given = (z != nullptr) + (zc != nullptr);
+  return given == (act == QLORA_ACT_NONE ? 0 : 1) ? QLORA_OK : QLORA_EINVAL;
+}
+
+GradEpi grad_epi(int act, const void* z, const int8_t* zc, const uint8_t* zs, const void* add, int C) {
+  GradEpi g{};
+  g.act = act_params(act);
+  g.z = z; g.zc = zc; g.zs = zs; g.zg = group_count(C); g.add = add;
+  return g;
+}
+
+int bwd_epi_check(const qlora_linear* L, int M, int dtype, const void* x, const int8_t* x_codes,
+                  const float* x_scales, const void* dy, const float* t_saved,
+                  const qlora_grad_epilogue* g, void* dx, float* dA, float* dB, void* ws,
+                  size_t ws_bytes) {
+  int st = check_linear(L, M, dtype);
+  if (st) return st;
+  if (!dy || !aligned16(dy) || !opt16(x) || !opt16(t_saved) || !opt16(dx)) return QLORA_EINVAL;
+  if (!pair_ok(x_codes, x_scales) || (x != nullptr) == (x_codes != nullptr)) return QLORA_EINVAL;
+  if (x_codes != nullptr && t_saved == nullptr) return QLORA_EINVAL;
+  const size_t mk = (size_t)M * L->K, es = dtype_bytes(dtype);
+  Ranges in, out;
+  if (g != nullptr) {
+    if (dx == nullptr || !opt16(g->add)) return QLORA_EINVAL;
+    st = check_z(g->act, g->z, g->z_codes, g->z_scales);
+    if (st) return st;
+    in.add(g->z, mk * es);
+    in.add(g->z_codes, mk);
+    in.add(g->z_scales, (size_t)M * group_count(L->K));
+    if (g->add != dx) in.add(g->add, mk * es);
+  }
+  st = bwd_check_ws(L, M, dtype, ws, ws_bytes);
+  if (st) return st;
+  add_layer(in, L);
+  in.add(x, mk * es);
+  in.add(x_codes, mk);
+  in.add(x_scales, (size_t)M * 4);
+  in.add(dy, (size_t)M * L->N * es);
+  in.add(t_saved, (size_t)M * L->r * 4);
+  out.add(dx, mk * es);
+  out.add(dA, (size_t)L->K * L->r * 4);
+  out.add(dB, (size_t)L->N * L->r * 4);
+  out.add(ws, bwd_layout(L, M, dtype).total);
+  return disjoint(out, in) ? QLORA_OK : QLORA_EINVAL;
+}
+
+void enqueue_bwd_epi(const qlora_linear* L, int M, int dtype, const void* x, const int8_t* x_codes,
+                     const float* x_scales, const void* dy, const float* t_saved,
+                     const qlora_grad_epilogue* g, void* dx, void* ws, hipStream_t s) {
+  // (x dense and nothing done to dx: qlora_bwd's own kernels)
+  const bool plain = x != nullptr && (g == nullptr || (g->act == QLORA_ACT_NONE && g->add == nullptr));
+  const GradEpi ge = g != nullptr ? grad_epi(g->act, g->z, g->z_codes, g->z_scales, g->add, L->K) : GradEpi{};
+  enqueue_bwd_partial(L, M, dtype, x, x_codes, x_scales, dy, t_saved, plain ? nullptr : &ge, dx, ws, s,
+                      1, nullptr, nullptr);
+}
+
 
 }  // namespace
 
@@ -303,7 +504,7 @@ int qlora_fwd_timed(const qlora_linear* L, int M, int dtype, const void* x,
       launch_gemm_fwd_w8(dtype, M, L->N, L->K, xq,
                          static_cast<const int8_t*>(L->codes), sx,
                          static_cast<const float*>(L->scales), t, L->B, head_width(L), L->r,
-                         lora_s(L), y, nullptr, reinterpret_cast<int32_t*>(at(ws, w.pacc)), s);
+                         lora_s(L), y, nullptr, reinterpret_cast<int32_t*>(at(ws, w.pacc)), nullptr, s);
     mark(ev_stop, s);
   } else if (L->fmt == QLORA_W8O) {
     int8_t* xq = reinterpret_cast<int8_t*>(at(ws, w.xq));
@@ -316,7 +517,7 @@ int qlora_fwd_timed(const qlora_linear* L, int M, int dtype, const void* x,
       launch_gemm_fwd_w8o(M, L->N, L->K, xq, static_cast<const int8_t*>(L->codes), sx, asum,
                           L->scales, t, L->B, head_width(L), L->r, lora_s(L),
                           static_cast<uint16_t*>(y), reinterpret_cast<int32_t*>(at(ws, w.pacc)),
-                          reinterpret_cast<float*>(at(ws, w.pcorr)), s);
+                          reinterpret_cast<float*>(at(ws, w.pcorr)), nullptr, s);
     mark(ev_stop, s);
   } else {
     launch_lora_down(dtype, x, M, L->K, L->A, L->r, t, s, reinterpret_cast<float*>(at(ws, w.rs)));
@@ -326,7 +527,7 @@ int qlora_fwd_timed(const qlora_linear* L, int M, int dtype, const void* x,
                          static_cast<const uint8_t*>(L->codes),
                          static_cast<const _Float16*>(L->scales), t, L->B, head_width(L), L->r,
                          lora_s(L), static_cast<uint16_t*>(y),
-                         reinterpret_cast<float*>(at(ws, w.pacc)), s);
+                         reinterpret_cast<float*>(at(ws, w.pacc)), nullptr, s);
     mark(ev_stop, s);
   }
   return launch_status();
@@ -356,7 +557,7 @@ int qlora_fwd_a8w4(const qlora_linear* L, int M, int dtype, const void* x, void*
                   reinterpret_cast<float*>(at(ws, w.rs)));
   launch_gemm_fwd_a8w4(M, L->N, L->K, xq, sx, static_cast<const uint8_t*>(L->codes),
                        static_cast<const _Float16*>(L->scales), t, L->B, head_width(L), L->r, lora_s(L),
-                       static_cast<uint16_t*>(y), s);
+                       static_cast<uint16_t*>(y), nullptr, s);
   return launch_status();
 }
 
@@ -380,49 +581,9 @@ int qlora_bwd_partial_timed(const qlora_linear* L, int M, int dtype, const void*
   if ((t_saved && !aligned16(t_saved)) || (dx && !aligned16(dx))) return QLORA_EINVAL;
   st = bwd_check_ws(L, M, dtype, ws, ws_bytes);
   if (st) return st;
-  const BwdLayout w = bwd_layout(L, M, dtype);
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  const float sc = lora_s(L);
-  float* u = reinterpret_cast<float*>(at(ws, w.u));
   if (pending_error()) return QLORA_EHIP;
-  const float* t = t_saved;
-  if (t == nullptr) {
-    float* tw = reinterpret_cast<float*>(at(ws, w.t));
-    launch_lora_down(dtype, x, M, L->K, L->A, L->r, tw, s, reinterpret_cast<float*>(at(ws, w.rs)));
-    t = tw;
-  }
-  float* partB = reinterpret_cast<float*>(at(ws, w.pB));
-  float* partA = reinterpret_cast<float*>(at(ws, w.pA));
-  if (dtype == QLORA_BF16 && dx != nullptr) {
-    // one launch: dx, u, and the per-row-block partial sums of dA and dB
-    mark(ev_start, s);
-    for (int rep = 0; rep < repeats; ++rep)
-      launch_bwd_fused(L->fmt, M, L->K, L->N, static_cast<const uint16_t*>(dy),
-                       L->codes, L->scales, L->B, head_width(L), L->A, t,
-                       static_cast<const uint16_t*>(x), L->r, sc,
-                       static_cast<uint16_t*>(dx), partA, partB,
-                       reinterpret_cast<float*>(at(ws, w.pdx)),
-                       reinterpret_cast<float*>(at(ws, w.pu)), s);
-    mark(ev_stop, s);
-    return launch_status();
-  }
-  launch_bwd_rows(dtype, dy, M, L->N, L->B, head_width(L), L->r, nullptr, nullptr, u, s);
-  SkinnyJobs sk = make_adapter_grad_jobs(M, L->r, sc, t, dy, L->N, nullptr, partB,
-                                         u, x, L->K, nullptr, partA);
-  sk.nsplit = bwd_splits(L, M);
-  sk.rows_per_split = (M + sk.nsplit - 1) / sk.nsplit;
-  sk.rows_per_split = (sk.rows_per_split + 3) / 4 * 4;
-  // float32 compute (int8 weights): the adapter-gradient stage 1, then the
-  // float32 input gradient; or no input gradient at all
-  launch_skinny_stage1(dtype, sk, s);
-  mark(ev_start, s);
-  if (dx != nullptr)
-    for (int rep = 0; rep < repeats; ++rep)
-      launch_gemm_dx_f32(M, L->K, L->N, static_cast<const float*>(dy),
-                         static_cast<const int8_t*>(L->codes),
-                         static_cast<const float*>(L->scales), u, L->A, L->r,
-                         sc, static_cast<float*>(dx), s);
-  mark(ev_stop, s);
+  enqueue_bwd_partial(L, M, dtype, x, nullptr, nullptr, dy, t_saved, nullptr, dx, ws,
+                      static_cast<hipStream_t>(stream), repeats, ev_start, ev_stop);
   return launch_status();
 }
 
@@ -534,6 +695,208 @@ int qlora_bwd_noalloc(const qlora_linear* L, int M, int dtype, const void* x,
   return qlora_bwd(L, M, dtype, x, dy, t_saved, dx, dA, dB, ws, kNoAllocScratch, stream);
 }
 
+int qlora_ckpt_bytes(int M, int C, int cfmt, size_t* codes_bytes, size_t* scale_bytes) {
+  if (codes_bytes == nullptr || scale_bytes == nullptr) return QLORA_EINVAL;
+  if (M < 1 || C < 16 || C % 16) return QLORA_EINVAL;
+  if (!fits_int(M, C)) return QLORA_ERANGE;
+  if (cfmt != QLORA_C8ROW && cfmt != QLORA_C8G32) return QLORA_EINVAL;
+  // (the row quantizer counts a row's entries in slices with an int)
+  if (cfmt == QLORA_C8ROW && C > (1 << 30)) return QLORA_ERANGE;
+  *codes_bytes = (size_t)M * C;
+  *scale_bytes = cfmt == QLORA_C8ROW ? (size_t)M * 4 : (size_t)M * group_count(C);
+  return QLORA_OK;
+}
+
+int qlora_ckpt_write(const void* x, int M, int C, int dtype, int cfmt, int8_t* codes,
+                     void* scales, void* stream) {
+  size_t cb, sb;
+  int st = check_dtype(dtype);
+  if (st) return st;
+  st = qlora_ckpt_bytes(M, C, cfmt, &cb, &sb);
+  if (st) return st;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned16(scales))
+    return QLORA_EINVAL;
+  Ranges in, out;
+  in.add(x, cb * dtype_bytes(dtype));
+  out.add(codes, cb);
+  out.add(scales, sb);
+  if (!disjoint(out, in)) return QLORA_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (pending_error()) return QLORA_EHIP;
+  if (cfmt == QLORA_C8ROW)
+    launch_rowquant(dtype, x, M, C, nullptr, 1, codes, static_cast<float*>(scales), nullptr, s);
+  else
+    launch_ckpt_write_groups(dtype, x, M, C, codes, static_cast<uint8_t*>(scales), s);
+  return launch_status();
+}
+
+int qlora_ckpt_read(const int8_t* codes, const void* scales, int M, int C, int cfmt,
+                    int dtype, void* x, void* stream) {
+  size_t cb, sb;
+  int st = check_dtype(dtype);
+  if (st) return st;
+  st = qlora_ckpt_bytes(M, C, cfmt, &cb, &sb);
+  if (st) return st;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned16(scales))
+    return QLORA_EINVAL;
+  Ranges in, out;
+  in.add(codes, cb);
+  in.add(scales, sb);
+  out.add(x, cb * dtype_bytes(dtype));
+  if (!disjoint(out, in)) return QLORA_EINVAL;
+  if (pending_error()) return QLORA_EHIP;
+  launch_ckpt_read(dtype, cfmt, codes, scales, M, C, x, static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+int qlora_fwd_epi(const qlora_linear* L, int M, int dtype, const void* x,
+                  const qlora_epilogue* e, void* y, float* t_save, void* ws,
+                  size_t ws_bytes, void* stream) {
+  int st = check_linear(L, M, dtype);
+  if (st) return st;
+  if (!x || !y || !aligned16(x) || !aligned16(y) || !opt16(t_save)) return QLORA_EINVAL;
+  const int K = L->K, N = L->N;
+  Ranges in, out;
+  st = check_epilogue(e, M, K, N, dtype, y, in, out);
+  if (st) return st;
+  const FwdLayout w = fwd_layout(L, M);
+  if (ws_bytes < w.total || !ws || !aligned16(ws)) return QLORA_EWORKSPACE;
+  add_layer(in, L);
+  in.add(x, (size_t)M * K * dtype_bytes(dtype));
+  out.add(y, (size_t)M * N * dtype_bytes(dtype));
+  out.add(t_save, (size_t)M * L->r * 4);
+  out.add(ws, w.total);
+  if (!disjoint(out, in)) return QLORA_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const FwdEpi epi = fwd_epi(e, N);
+  float* t = t_save ? t_save : reinterpret_cast<float*>(at(ws, w.t));
+  int8_t* xq = e->x_codes ? e->x_codes : reinterpret_cast<int8_t*>(at(ws, w.xq));
+  float* sx = e->x_scales ? e->x_scales : reinterpret_cast<float*>(at(ws, w.sx));
+  float* rs = reinterpret_cast<float*>(at(ws, w.rs));
+  if (pending_error()) return QLORA_EHIP;
+  if (L->fmt == QLORA_W4G128) {
+    // the product takes x itself; its codes are made only where they are kept
+    if (e->x_codes)
+      launch_rowquant(dtype, x, M, K, L->A, L->r, xq, sx, t, s, nullptr, rs);
+    else
+      launch_lora_down(dtype, x, M, K, L->A, L->r, t, s, rs);
+    launch_gemm_fwd_w4(M, N, K, static_cast<const uint16_t*>(x), static_cast<const uint8_t*>(L->codes),
+                       static_cast<const _Float16*>(L->scales), t, L->B, head_width(L), L->r, lora_s(L),
+                       static_cast<uint16_t*>(y), reinterpret_cast<float*>(at(ws, w.pacc)), &epi, s);
+    return launch_status();
+  }
+  float* asum = L->fmt == QLORA_W8O ? reinterpret_cast<float*>(at(ws, w.asum)) : nullptr;
+  launch_rowquant(dtype, x, M, K, L->A, L->r, xq, sx, t, s, asum, rs);
+  enqueue_fwd_i8(L, M, dtype, xq, sx, asum, t, epi, y, ws, w, s);
+  return launch_status();
+}
+
+int qlora_fwd_ckpt(const qlora_linear* L, int M, int dtype, const int8_t* x_codes,
+                   const float* x_scales, const float* t, const qlora_epilogue* e,
+                   void* y, void* ws, size_t ws_bytes, void* stream) {
+  int st = check_linear(L, M, dtype);
+  if (st) return st;
+  if (!x_codes || !x_scales || !t || !y || !aligned16(x_codes) || !aligned16(x_scales) ||
+      !aligned16(t) || !aligned16(y))
+    return QLORA_EINVAL;
+  const int K = L->K, N = L->N;
+  Ranges in, out;
+  st = check_epilogue(e, M, K, N, dtype, y, in, out);
+  if (st) return st;
+  if (e->x_codes != nullptr) return QLORA_EINVAL;   // x is the checkpoint already
+  const FwdLayout w = fwd_layout(L, M);
+  if (ws_bytes < w.total || !ws || !aligned16(ws)) return QLORA_EWORKSPACE;
+  add_layer(in, L);
+  in.add(x_codes, (size_t)M * K);
+  in.add(x_scales, (size_t)M * 4);
+  in.add(t, (size_t)M * L->r * 4);
+  out.add(y, (size_t)M * N * dtype_bytes(dtype));
+  out.add(ws, w.total);
+  if (!disjoint(out, in)) return QLORA_EINVAL;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const FwdEpi epi = fwd_epi(e, N);
+  if (pending_error()) return QLORA_EHIP;
+  if (L->fmt == QLORA_W4G128) {
+    launch_gemm_fwd_a8w4(M, N, K, x_codes, x_scales, static_cast<const uint8_t*>(L->codes),
+                         static_cast<const _Float16*>(L->scales), t, L->B, head_width(L), L->r,
+                         lora_s(L), static_cast<uint16_t*>(y), &epi, s);
+    return launch_status();
+  }
+  float* asum = nullptr;
+  if (L->fmt == QLORA_W8O) {
+    asum = reinterpret_cast<float*>(at(ws, w.asum));
+    launch_code_sums(x_codes, M, K, asum, s);
+  }
+  enqueue_fwd_i8(L, M, dtype, x_codes, x_scales, asum, t, epi, y, ws, w, s);
+  return launch_status();
+}
+
+int qlora_bwd_epi_partial(const qlora_linear* L, int M, int dtype, const void* x,
+                          const int8_t* x_codes, const float* x_scales, const void* dy,
+                          const float* t_saved, const qlora_grad_epilogue* g, void* dx,
+                          void* ws, size_t ws_bytes, void* stream) {
+  const int st = bwd_epi_check(L, M, dtype, x, x_codes, x_scales, dy, t_saved, g, dx, nullptr, nullptr,
+                               ws, ws_bytes);
+  if (st) return st;
+  if (pending_error()) return QLORA_EHIP;
+  enqueue_bwd_epi(L, M, dtype, x, x_codes, x_scales, dy, t_saved, g, dx, ws,
+                  static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+int qlora_bwd_epi(const qlora_linear* L, int M, int dtype, const void* x,
+                  const int8_t* x_codes, const float* x_scales, const void* dy,
+                  const float* t_saved, const qlora_grad_epilogue* g, void* dx,
+                  float* dA, float* dB, void* ws, size_t ws_bytes, void* stream) {
+  int st = bwd_epi_check(L, M, dtype, x, x_codes, x_scales, dy, t_saved, g, dx, dA, dB, ws, ws_bytes);
+  if (st) return st;
+  st = finish_check(L, M, dtype, dA, dB, ws, ws_bytes);
+  if (st) return st;
+  if (pending_error()) return QLORA_EHIP;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  enqueue_bwd_epi(L, M, dtype, x, x_codes, x_scales, dy, t_saved, g, dx, ws, s);
+  st = launch_status();
+  if (st) return st;
+  launch_skinny_stage2(finish_jobs(L, M, dtype, dA, dB, ws), s);
+  return launch_status();
+}
+
+int qlora_act_bwd_workspace(int M, int N, size_t* bytes) {
+  if (bytes == nullptr || M < 1 || N < 16 || N % 16) return QLORA_EINVAL;
+  if (!fits_int(M, N)) return QLORA_ERANGE;
+  *bytes = act_bwd_floats(M, N) * 4;
+  return QLORA_OK;
+}
+
+int qlora_act_bwd(int act, int M, int N, int dtype, const void* dy, const void* z,
+                  const int8_t* z_codes, const uint8_t* z_scales, void* dz, float* dbias,
+                  void* ws, size_t ws_bytes, void* stream) {
+  size_t need = 0;
+  int st = check_dtype(dtype);
+  if (st) return st;
+  st = qlora_act_bwd_workspace(M, N, &need);
+  if (st) return st;
+  st = check_z(act, z, z_codes, z_scales);
+  if (st) return st;
+  if (!dy || !aligned16(dy) || !opt16(dz) || !opt16(dbias) || (!dz && !dbias)) return QLORA_EINVAL;
+  if (dbias == nullptr) need = 0;
+  if (ws_bytes < need || (need && (!ws || !aligned16(ws)))) return QLORA_EWORKSPACE;
+  const size_t mn = (size_t)M * N, es = dtype_bytes(dtype);
+  Ranges in, out;
+  if (dz != dy) in.add(dy, mn * es);
+  in.add(z, mn * es);
+  in.add(z_codes, mn);
+  in.add(z_scales, (size_t)M * group_count(N));
+  out.add(dz, mn * es);
+  out.add(dbias, (size_t)N * 4);
+  out.add(ws, need);
+  if (!disjoint(out, in)) return QLORA_EINVAL;
+  if (pending_error()) return QLORA_EHIP;
+  launch_act_bwd(dtype, M, N, dy, grad_epi(act, z, z_codes, z_scales, nullptr, N), dz, dbias,
+                 static_cast<float*>(ws), static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
 int qlora_merge(const qlora_linear* L, void* codes_out, void* scales_out,
                 void* stream) {
   int st = check_linear(L, 1, QLORA_BF16);
@@ -589,7 +952,7 @@ int qlora_fwd_acc(const qlora_linear* L, int M, int dtype, const void* x,
   // the integer product alone: no scale is read
   launch_gemm_fwd_w8(dtype, M, L->N, L->K, xq,
                      static_cast<const int8_t*>(L->codes), sx, nullptr, nullptr, L->B,
-                     head_width(L), L->r, 0.f, nullptr, acc, nullptr, s);
+                     head_width(L), L->r, 0.f, nullptr, acc, nullptr, nullptr, s);
   return launch_status();
 }
 

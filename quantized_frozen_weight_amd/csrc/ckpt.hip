@@ -1,0 +1,257 @@
+// 8-bit activation checkpoints (written and read back) and the gradient of an
+// activation on its own. All of it is memory-bound: a thread owns 8
+// consecutive columns of a row per unit (16 bytes of bf16, 8 of codes), four
+// units' loads in flight at a time.
+//
+// The group form is described in epilogue.hpp; the row form is the forward's
+// own activation quantizer (rows.hip), so only its reading is here.
+//
+// ("Introduce QLoRA-like technique": activations quantized per row under the
+// int8 kernel; keras-llm-light README, "Block-wise gradient checkpointing":
+// block inputs are kept and blocks recomputed or differentiated from them.)
+#include "epilogue.hpp"
+#include "launch.hpp"
+
+namespace qlora {
+
+namespace {
+
+constexpr int kUnits = 4;                    // 8-column units per thread
+
+// Units of a row padded to whole groups, so that the four lanes of a quad
+// always hold one group: unit u is columns [8 (u % upr), + 8) of row u / upr.
+template <typename T>
+__global__ __launch_bounds__(256) void ckpt_write_groups_kernel(
+    const typename Elem<T>::type* __restrict__ x, int M, int C, int8_t* __restrict__ codes,
+    uint8_t* __restrict__ scales) {
+  const int zg = group_count(C);
+  const uint32_t upr = 4u * zg, n = (uint32_t)M * upr;
+  const uint32_t u0 = blockIdx.x * (256u * kUnits) + threadIdx.x;
+  float v[kUnits][8];
+  uint32_t row[kUnits], col[kUnits];
+  bool ok[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const uint32_t u = u0 + 256u * i;
+    row[i] = u / upr;
+    col[i] = 8u * (u - row[i] * upr);
+    ok[i] = u < n && col[i] < (uint32_t)C;
+    load8(x + (ok[i] ? (long)row[i] * C + col[i] : 0), v[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) { const uint32_t b = abs_bits(v[i][e]); m = b > m ? b : m; }
+    const int b = group_byte(quad_max_u32(ok[i] ? m : 0u));
+    if (ok[i]) {
+      *reinterpret_cast<u32x2*>(codes + (long)row[i] * C + col[i]) = group_codes(v[i], b);
+      if (col[i] % kGroup == 0) scales[(long)row[i] * zg + col[i] / kGroup] = (uint8_t)b;
+    }
+  }
+}
+
+template <typename T, bool GROUPS>
+__global__ __launch_bounds__(256) void ckpt_read_kernel(
+    const int8_t* __restrict__ codes, const void* __restrict__ scales, int M, int C,
+    typename Elem<T>::type* __restrict__ x) {
+  const int zg = group_count(C);
+  const uint32_t upr = (uint32_t)C / 8u, n = (uint32_t)M * upr;
+  const uint32_t u0 = blockIdx.x * (256u * kUnits) + threadIdx.x;
+  u32x2 c[kUnits];
+  float s[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const uint32_t u = u0 + 256u * i, uc = u < n ? u : 0u;
+    const uint32_t row = uc / upr, col = 8u * (uc - row * upr);
+    c[i] = *reinterpret_cast<const u32x2*>(codes + 8L * uc);
+    if constexpr (GROUPS)
+      s[i] = group_scale(static_cast<const uint8_t*>(scales)[(long)row * zg + col / kGroup]);
+    else
+      s[i] = static_cast<const float*>(scales)[row];
+  }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const uint32_t u = u0 + 256u * i;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)(c[i][e >> 2] >> (8 * (e & 3))) * s[i];
+    if (u < n) store8(x + 8L * u, v);
+  }
+}
+
+// Row sums of codes, one wave per row (exact: |sum| <= 127 K < 2^31, and
+// below 2^24 for every K the layer takes).
+__global__ __launch_bounds__(256) void code_sums_kernel(const int8_t* __restrict__ codes, int M,
+                                                        int K, float* __restrict__ asum) {
+  const int lane = threadIdx.x & 63;
+  const int row = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= M) return;
+  int sum = 0;
+  for (int k = 16 * lane; k < K; k += 1024) {
+    const i32x4 c = *reinterpret_cast<const i32x4*>(codes + (long)row * K + k);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = __builtin_amdgcn_sdot4(c[i], 0x01010101, sum, false);
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+  if (lane == 0) asum[row] = (float)sum;
+}
+
+// ---- dz = dy act'(z), dbias = column sums -----------------------------------
+// A block owns 256 columns (32 lanes of 8) and a span of rows, 8 rows at a
+// time; a thread keeps the float32 sums of its 8 columns over its rows. The 8
+// row lanes are added in order through LDS, and (more than one span) a second
+// launch adds the spans in order. No atomics.
+constexpr int kActCols = 256, kActLanes = 8;
+
+inline int col_blocks(int C) { return C / kActCols + (C % kActCols != 0); }
+
+// Row spans, and rows per span: enough blocks to fill the chip, but one span
+// (one launch, no partial sums) while a thread has at most 16 rows.
+void act_bwd_plan(int M, int C, int* spans, int* rows) {
+  const int cb = col_blocks(C);
+  if (M <= 16 * kActLanes) {
+    *spans = 1;
+    *rows = M;
+    return;
+  }
+  int want = 2048 / cb;
+  if (want < 1) want = 1;
+  int r = (M + want - 1) / want;
+  if (r < 4 * kActLanes) r = 4 * kActLanes;
+  r = (r + kActLanes - 1) / kActLanes * kActLanes;
+  *rows = r;
+  *spans = (M + r - 1) / r;
+}
+
+template <typename T, bool SUMS>
+__global__ __launch_bounds__(256) void act_bwd_kernel(const typename Elem<T>::type* dy, int M, int C,
+                                                      GradEpi ge, typename Elem<T>::type* dz,
+                                                      float* __restrict__ out, int rows) {
+  __shared__ float red[SUMS ? kActLanes : 1][kActCols + 8];
+  const int tid = threadIdx.x, cl = tid & 31, rl = tid >> 5;
+  const uint32_t col = blockIdx.x * (uint32_t)kActCols + 8u * cl;   // (may pass 2^31 - 1 in the last block)
+  const bool okc = col < (uint32_t)C;
+  const uint32_t colc = okc ? col : 0u;
+  const int m0 = blockIdx.y * rows, m1 = M - m0 < rows ? M : m0 + rows;
+  float sum[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] = 0.f;
+  for (int mb = m0 + rl; mb < m1; mb += kActLanes * kUnits) {
+    float v[kUnits][8], z[kUnits][8];
+    // every load of the group from clamped addresses before the first use
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int m = mb + kActLanes * i < m1 ? mb + kActLanes * i : mb;
+      const long at = (long)m * C + colc;
+      load8(dy + at, v[i]);
+      if (ge.act.kind != 0) {
+        if (ge.zc != nullptr)
+          group_values(*reinterpret_cast<const u32x2*>(ge.zc + at), ge.zs[(long)m * ge.zg + colc / kGroup], z[i]);
+        else
+          load8(static_cast<const typename Elem<T>::type*>(ge.z) + at, z[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int m = mb + kActLanes * i;
+      if (m < m1) {
+        act_slope_mul(ge.act, z[i], v[i]);
+        if (dz != nullptr && okc) store8(dz + (long)m * C + col, v[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] += v[i][e];
+      }
+    }
+  }
+  if constexpr (SUMS) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) red[rl][8 * cl + e] = sum[e];
+    __syncthreads();
+    const uint32_t c = blockIdx.x * (uint32_t)kActCols + tid;
+    float s = red[0][tid];
+#pragma unroll
+    for (int l = 1; l < kActLanes; ++l) s += red[l][tid];
+    if (c < (uint32_t)C) out[(long)blockIdx.y * C + c] = s;
+  }
+}
+
+// dbias[c] = the spans' sums: 64 columns per block, wave w the spans w, w + 4,
+// ... in order, then the four waves in order.
+__global__ __launch_bounds__(256) void act_bwd_sum_kernel(const float* __restrict__ part, int spans,
+                                                          int C, float* __restrict__ dbias) {
+  __shared__ float red[4][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane, cc = c < C ? c : 0;
+  float s = 0.f;
+#pragma unroll 8
+  for (int k = w; k < spans; k += 4) s += part[(long)k * C + cc];
+  red[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < C) dbias[c] = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
+}
+
+inline unsigned unit_blocks(long units) {
+  return (unsigned)((units + 256 * kUnits - 1) / (256 * kUnits));
+}
+
+template <typename T>
+void act_bwd_launch(int M, int C, const void* dy, const GradEpi& ge, void* dz, float* dbias,
+                    float* partial, hipStream_t st) {
+  typedef typename Elem<T>::type E;
+  int spans, rows;
+  act_bwd_plan(M, C, &spans, &rows);
+  const dim3 grid((unsigned)col_blocks(C), (unsigned)spans);
+  if (dbias == nullptr) {
+    act_bwd_kernel<T, false><<<grid, 256, 0, st>>>(static_cast<const E*>(dy), M, C, ge,
+                                                   static_cast<E*>(dz), nullptr, rows);
+    return;
+  }
+  act_bwd_kernel<T, true><<<grid, 256, 0, st>>>(static_cast<const E*>(dy), M, C, ge, static_cast<E*>(dz),
+                                                spans == 1 ? dbias : partial, rows);
+  if (spans > 1)
+    act_bwd_sum_kernel<<<(unsigned)((C + 63) / 64), 256, 0, st>>>(partial, spans, C, dbias);
+}
+
+}  // namespace
+
+void launch_ckpt_write_groups(int dtype, const void* x, int M, int C, int8_t* codes,
+                              uint8_t* scales, hipStream_t st) {
+  const unsigned nb = unit_blocks(4L * M * group_count(C));
+  if (dtype == 0)
+    ckpt_write_groups_kernel<F32><<<nb, 256, 0, st>>>(static_cast<const float*>(x), M, C, codes, scales);
+  else
+    ckpt_write_groups_kernel<BF16><<<nb, 256, 0, st>>>(static_cast<const uint16_t*>(x), M, C, codes, scales);
+}
+
+void launch_ckpt_read(int dtype, int cfmt, const int8_t* codes, const void* scales, int M, int C,
+                      void* x, hipStream_t st) {
+  const unsigned nb = unit_blocks((long)M * (C / 8));
+  float* xf = static_cast<float*>(x);
+  uint16_t* xb = static_cast<uint16_t*>(x);
+  if (cfmt == 0) {
+    if (dtype == 0) ckpt_read_kernel<F32, false><<<nb, 256, 0, st>>>(codes, scales, M, C, xf);
+    else ckpt_read_kernel<BF16, false><<<nb, 256, 0, st>>>(codes, scales, M, C, xb);
+  } else {
+    if (dtype == 0) ckpt_read_kernel<F32, true><<<nb, 256, 0, st>>>(codes, scales, M, C, xf);
+    else ckpt_read_kernel<BF16, true><<<nb, 256, 0, st>>>(codes, scales, M, C, xb);
+  }
+}
+
+void launch_code_sums(const int8_t* codes, int M, int K, float* asum, hipStream_t st) {
+  code_sums_kernel<<<(unsigned)((M + 3) / 4), 256, 0, st>>>(codes, M, K, asum);
+}
+
+size_t act_bwd_floats(int M, int C) {
+  int spans, rows;
+  act_bwd_plan(M, C, &spans, &rows);
+  return spans > 1 ? (size_t)spans * (size_t)C : 0;
+}
+
+void launch_act_bwd(int dtype, int M, int C, const void* dy, const GradEpi& ge, void* dz,
+                    float* dbias, float* partial, hipStream_t st) {
+  if (dtype == 0) act_bwd_launch<F32>(M, C, dy, ge, dz, dbias, partial, st);
+  else act_bwd_launch<BF16>(M, C, dy, ge, dz, dbias, partial, st);
+}
+
+}  // namespace qlora

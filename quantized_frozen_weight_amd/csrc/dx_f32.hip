@@ -5,6 +5,7 @@
 // Plain LDS-tiled FMA kernel, no reduced-precision rounding anywhere; used
 // for the float32 compute dtype (small layers).
 #include "common.hpp"
+#include "epilogue.hpp"
 #include "launch.hpp"
 
 namespace qlora {
@@ -23,11 +24,14 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr int kT = 32, kS = 128;
 
+// EXT: dx goes through the gradient epilogue (epilogue.hpp), one value at a
+// time.
+template <bool EXT>
 __global__ __launch_bounds__(256) void gemm_dx_f32_kernel(
     int M, int K, int N, const float* __restrict__ dy,
     const int8_t* __restrict__ codes, const float* __restrict__ sw,
     const float* __restrict__ u, const float* __restrict__ A, int r, float s,
-    float* __restrict__ dx) {
+    float* __restrict__ dx, GradEpi ge) {
   __shared__ float Ds[kS][kT + 1];   // [n][m]
   __shared__ float Ws[kS][kT + 1];   // [n][k]
   const int tid = threadIdx.x;
@@ -97,7 +101,22 @@ __global__ __launch_bounds__(256) void gemm_dx_f32_kernel(
       float low = 0.f;
       for (int jj = 0; jj < r; ++jj)
         low = __builtin_fmaf(u[(long)m * r + jj], A[(long)k * r + jj], low);
-      dx[(long)m * K + k] = __builtin_fmaf(s, low, acc[i][j]);
+      float v[1] = {__builtin_fmaf(s, low, acc[i][j])};
+      if constexpr (EXT) {
+        const long at = (long)m * K + k;
+        if (ge.act.kind != 0) {
+          float z[1];
+          if (ge.zc != nullptr) {
+            const int b = ge.zs[(long)m * ge.zg + k / kGroup];
+            z[0] = (float)ge.zc[at] * group_scale(b);
+          } else {
+            z[0] = static_cast<const float*>(ge.z)[at];
+          }
+          act_slope_mul(ge.act, z, v);
+        }
+        if (ge.add != nullptr) v[0] += static_cast<const float*>(ge.add)[at];
+      }
+      dx[(long)m * K + k] = v[0];
     }
   }
 }
@@ -107,10 +126,12 @@ __global__ __launch_bounds__(256) void gemm_dx_f32_kernel(
 void launch_gemm_dx_f32(int M, int K, int N, const float* dy,
                         const int8_t* codes, const float* sw, const float* u,
                         const float* A, int r, float s, float* dx,
-                        hipStream_t st) {
+                        hipStream_t st, const GradEpi* ge) {
   dim3 grid((K + kT - 1) / kT, (M + kT - 1) / kT);
-  gemm_dx_f32_kernel<<<grid, 256, 0, st>>>(M, K, N, dy, codes, sw, u, A, r, s,
-                                           dx);
+  if (ge != nullptr)
+    gemm_dx_f32_kernel<true><<<grid, 256, 0, st>>>(M, K, N, dy, codes, sw, u, A, r, s, dx, *ge);
+  else
+    gemm_dx_f32_kernel<false><<<grid, 256, 0, st>>>(M, K, N, dy, codes, sw, u, A, r, s, dx, GradEpi{});
 }
 
 }  // namespace qlora

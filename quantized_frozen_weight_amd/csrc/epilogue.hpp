@@ -1,0 +1,351 @@
+// The layer's epilogue beyond the adapter, both ways:
+//
+//   forward:   z = base + s (t B) + bias,  y = act(z) + residual
+//   backward:  dx = (base + s (u A^T)) act'(z) + add
+//
+// (act: QLORA_ACT_*; base as in epilogue_lowrank, ring.hpp), and the 8-bit
+// group form of an activation that both sides share.
+//
+// Activations. relu; gelu = z Phi(z); and two of one family,
+// z sigma(z (p + q z^2)): silu has p = 1, q = 0, and the tanh form of gelu
+// p = 2 sqrt(2 / pi), q = 0.044715 p, since (1 + tanh(v)) / 2 = sigma(2 v).
+// The family shares one code path with two wave-uniform constants, so a
+// kernel carries three short branches instead of a variant per activation.
+//
+// Group form (QLORA_C8G32): 32 consecutive columns of a row share a scale
+// 2^e, e the smallest integer with absmax <= 127 2^e, kept as the byte
+// e + 127 (1 for an all-zero group, 255 for one with an infinity or a NaN:
+// every value of it reads back as NaN). code = round-half-even(v 2^-e), at
+// least 1 in size where v is not 0: the sign survives, so relu' taken from
+// the code is relu' of the value. A value reads back exactly in bfloat16
+// (7 bits times a power of two). The scale being a power of two costs up to
+// one of the 8 bits against absmax / 127, and buys a one-byte scale that the
+// product's epilogue can form without a division.
+#pragma once
+
+#include <type_traits>
+
+#include "ring.hpp"
+
+namespace qlora {
+
+constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4;
+constexpr int kGroup = 32;       // columns per scale of the group form
+
+inline __host__ __device__ int group_count(int C) { return C / kGroup + (C % kGroup != 0); }
+
+struct ActParams {
+  int kind;      // 0 none, 1 relu, 2 gelu, 3 the sigma family
+  float p, q;    // the sigma family's constants
+};
+
+inline ActParams act_params(int act) {
+  ActParams a{act, 1.f, 0.f};
+  if (act == kActGeluTanh) {
+    a.kind = 3;
+    a.p = 1.5957691216057308f;               // 2 sqrt(2 / pi)
+    a.q = 1.5957691216057308f * 0.044715f;
+  } else if (act == kActSilu) {
+    a.kind = 3;
+  }
+  return a;
+}
+
+// min / max that keep a NaN (v_min / v_max drop it)
+__device__ __forceinline__ float at_least(float v, float lo) { return v < lo ? lo : v; }
+__device__ __forceinline__ float at_most(float v, float hi) { return v > hi ? hi : v; }
+
+// e^w for |w| <= 150 as 2^(w log2 e), the product kept in two parts (its
+// rounding error, times |w|, would otherwise reach the result): within 3 ulp;
+// overflows to infinity and underflows to 0.
+__device__ __forceinline__ float exp_pos(float w) {
+  constexpr float kL = 1.44269504088896341f, kLlo = 1.925963033500e-8f, kLn2 = 0.693147180559945f;
+  const float hi = w * kL;
+  const float lo = __builtin_fmaf(w, kLlo, __builtin_fmaf(w, kL, -hi));
+  return __builtin_amdgcn_exp2f(hi) * __builtin_fmaf(lo, kLn2, 1.f);
+}
+
+// 1 / (1 + e^-w); 0 and 1 past |w| = 150, where float32 is there anyway
+__device__ __forceinline__ float sigma(float w) {
+  w = at_most(at_least(w, -150.f), 150.f);
+  return __builtin_amdgcn_rcpf(1.f + exp_pos(-w));
+}
+
+// Phi(z) = erfc(-z / sqrt 2) / 2, relative error below 1e-6 on either side of
+// 0 (from 1 + erf the left tail would cancel). For x = |z| / sqrt 2 and
+// t = 1 / (1 + 0.44 x), e^(x^2) erfc(x) is t times a polynomial of degree 7 in
+// t, fitted here to the smallest largest relative error (1.9e-7) on
+// 0 <= x <= 15. ex is e^(-x^2) (shared with the density).
+__device__ __forceinline__ float normal_cdf(float z, float ex) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_fabsf(z), 0.44f * 0.70710678118654752f, 1.f));
+  float c = 0.07150039076805115f;
+  c = __builtin_fmaf(c, t, -0.27915504574775696f);
+  c = __builtin_fmaf(c, t, 0.29887089133262634f);
+  c = __builtin_fmaf(c, t, -0.022297518327832222f);
+  c = __builtin_fmaf(c, t, 0.2169952094554901f);
+  c = __builtin_fmaf(c, t, 0.2169342190027237f);
+  c = __builtin_fmaf(c, t, 0.2489354908466339f);
+  c = __builtin_fmaf(c, t, 0.24821652472019196f);
+  const float h = 0.5f * t * c * ex;
+  return z < 0.f ? h : 1.f - h;
+}
+
+// e^(-z^2 / 2)
+__device__ __forceinline__ float normal_exp(float z) {
+  return exp_pos(at_least(-0.5f * z * z, -150.f));
+}
+
+// act of every v; -inf goes to the limit 0 (not -inf * 0), NaN stays NaN
+template <int NV>
+__device__ __forceinline__ void act_apply(const ActParams& a, float (&v)[NV]) {
+  if (a.kind == 0) return;
+  if (a.kind == 1) {
+#pragma unroll
+    for (int e = 0; e < NV; ++e) v[e] = at_least(v[e], 0.f);
+  } else if (a.kind == 2) {
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+      const float z = at_least(v[e], -1e9f);
+      v[e] = z * normal_cdf(z, normal_exp(z));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+      const float z = at_least(v[e], -1e9f), c = at_most(z, 1e9f);
+      v[e] = z * sigma(c * __builtin_fmaf(a.q, c * c, a.p));
+    }
+  }
+}
+
+// v[e] *= act'(z[e]); relu'(0) = 0, relu'(NaN) = NaN
+template <int NV>
+__device__ __forceinline__ void act_slope_mul(const ActParams& a, const float (&z)[NV], float (&v)[NV]) {
+  if (a.kind == 0) return;
+  if (a.kind == 1) {
+#pragma unroll
+    for (int e = 0; e < NV; ++e) v[e] *= z[e] > 0.f ? 1.f : z[e] <= 0.f ? 0.f : z[e];
+  } else if (a.kind == 2) {
+    // Phi + z phi; past |z| = 20 phi is 0 in float32
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+      const float c = at_most(at_least(z[e], -20.f), 20.f);
+      const float ex = normal_exp(c);
+      v[e] *= __builtin_fmaf(c * 0.3989422804014327f, ex, normal_cdf(c, ex));
+    }
+  } else {
+    // sigma + z sigma (1 - sigma) (p + 3 q z^2); past |z| = 200 it is 0 or 1
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+      const float c = at_most(at_least(z[e], -200.f), 200.f), c2 = c * c;
+      const float w = c * __builtin_fmaf(a.q, c2, a.p);
+      const float s = sigma(w), n = sigma(-w);       // 1 - s without cancellation
+      v[e] *= __builtin_fmaf(c * __builtin_fmaf(3.f * a.q, c2, a.p), s * n, s);
+    }
+  }
+}
+
+// ---- the group form ---------------------------------------------------------
+// max over the four lanes 4 i .. 4 i + 3, every lane ending with it
+__device__ __forceinline__ uint32_t quad_max_u32(uint32_t v) {
+#pragma unroll
+  for (int lvl = 2; lvl < 4; ++lvl) {
+    const uint32_t w = __float_as_uint(dpp_pair(__uint_as_float(v), lvl));
+    v = w > v ? w : v;
+  }
+  return v;
+}
+
+// The scale byte of a group from its abs-max bits: e = p - 6 where the
+// abs-max m 2^p (1 <= m < 2) has m <= 127 / 64, else p - 5.
+__device__ __forceinline__ int group_byte(uint32_t amax_bits) {
+  if (amax_bits >= 0x7f800000u) return 255;
+  int b = (int)(amax_bits >> 23) - 6 + ((amax_bits & 0x7fffffu) > 0x7e0000u ? 1 : 0);
+  return b < 1 ? 1 : b;
+}
+
+// Eight values as codes of scale byte b, packed four to a word.
+__device__ __forceinline__ u32x2 group_codes(const float (&v)[8], int b) {
+  // 2^-e = 2^(127 - b); b in [1, 249]
+  const float inv = __uint_as_float((uint32_t)(254 - b) << 23);
+  uint32_t w[2] = {0u, 0u};
+  if (b != 255) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      int q = (int)__builtin_rintf(v[e] * inv);
+      if (q == 0) q = v[e] > 0.f ? 1 : v[e] < 0.f ? -1 : 0;
+      w[e >> 2] |= (uint32_t)(q & 0xff) << (8 * (e & 3));
+    }
+  }
+  return u32x2{w[0], w[1]};
+}
+
+// The scale that byte b stands for; 255: NaN.
+__device__ __forceinline__ float group_scale(int b) {
+  return __uint_as_float(b == 255 ? 0x7fc00000u : (uint32_t)b << 23);
+}
+
+__device__ __forceinline__ void group_values(u32x2 c, int b, float (&v)[8]) {
+  const float s = group_scale(b);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)(c[e >> 2] >> (8 * (e & 3))) * s;
+}
+
+// ---- eight values of a row in either dtype ------------------------------------
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+  *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
+  *reinterpret_cast<u32x4*>(p) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+}
+
+// The forward epilogue of a call (pointers NULL where unused).
+struct FwdEpi {
+  ActParams act;
+  const float* bias;      // [N]
+  const void* res;        // [M, N], may be y
+  void* z;                // [M, N]
+  int8_t* zc;             // [M, N] codes and [M, zg] scale bytes of z
+  uint8_t* zs;
+  int zg;
+};
+
+// The backward one: z (dense, or group form) and add, [M, K].
+struct GradEpi {
+  ActParams act;
+  const void* z;
+  const int8_t* zc;
+  const uint8_t* zs;
+  int zg;
+  const void* add;
+};
+
+// LDS bytes of one wave's strip in epilogue_fused: 16 rows of FN * 16 floats,
+// each padded by 16 bytes.
+template <int FN> constexpr int fused_strip_bytes() { return 16 * (FN * 64 + 16); }
+
+// epilogue_lowrank (ring.hpp) with the rest of the layer behind it. One
+// 16-row strip of the wave's outputs at a time goes through LDS in float32,
+// so that a lane then holds 8 consecutive columns of a row: every operand
+// (residual, saved z, codes) moves in 16- or 8-byte pieces, the activation
+// sees the unrounded z, four neighbouring lanes hold one 32-column group,
+// and y is rounded once. The operands of a strip are fetched before its
+// low-rank product, which hides part of their latency.
+template <int BM, int BN, int R, bool SCALED, bool AFF = false, typename OutT, typename Epi,
+          typename AccT, int FM, int FN>
+__device__ __forceinline__ void epilogue_fused(const AccT (&acc)[FM][FN], const float* E, int M,
+                                               int N, int m0, int n0, int wr0, int wc0, float s,
+                                               OutT* out, const Epi& ep, int8_t* strip) {
+  constexpr bool GRAD = std::is_same<Epi, GradEpi>::value;
+  static_assert(!AFF || SCALED, "the affine form uses the row scales");
+  const int lane = threadIdx.x & 63;
+  const float* ts = E;
+  const float* qs = E + BM * R;
+  const float* rsv = E + (BM + BN) * R;
+  const float* csv = rsv + BM;
+  const float* rav = csv + BN;
+  constexpr int PITCH = FN * 64 + 16;
+  constexpr int CPR = 2 * FN;                 // 8-column pieces per strip row
+  constexpr int PN = CPR * 16 / 64;           // pieces per lane and strip
+  static_assert(CPR % 4 == 0, "four neighbouring lanes hold one 32-column group");
+
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    // the strip's side operands
+    float side[PN][8], aux[PN][8];             // residual or add; z (backward)
+    bool live[PN];
+    int pm[PN], pn[PN];
+#pragma unroll
+    for (int p = 0; p < PN; ++p) {
+      const int q = lane + 64 * p;
+      pm[p] = m0 + wr0 + i * 16 + q / CPR;
+      pn[p] = n0 + wc0 + (q % CPR) * 8;
+      live[p] = pm[p] < M && pn[p] < N;        // N % 16 == 0: 8 columns in or out
+      const long at = live[p] ? (long)pm[p] * N + pn[p] : 0;
+      if constexpr (GRAD) {
+        if (ep.add != nullptr) load8(static_cast<const OutT*>(ep.add) + at, side[p]);
+        if (ep.act.kind != 0) {
+          if (ep.zc != nullptr) {
+            const u32x2 c = *reinterpret_cast<const u32x2*>(ep.zc + at);
+            const int b = ep.zs[live[p] ? (long)pm[p] * ep.zg + pn[p] / kGroup : 0];
+            group_values(c, b, aux[p]);
+          } else {
+            load8(static_cast<const OutT*>(ep.z) + at, aux[p]);
+          }
+        }
+      } else {
+        if (ep.res != nullptr) load8(static_cast<const OutT*>(ep.res) + at, side[p]);
+        if (ep.bias != nullptr) load8(ep.bias + (live[p] ? pn[p] : 0), aux[p]);
+      }
+    }
+    f32x4 low[FN];
+#pragma unroll
+    for (int jn = 0; jn < FN; ++jn) low[jn] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kc = 0; kc < R / 4; ++kc) {
+      const int j = kc * 4 + (lane >> 4);
+      const float ta = ts[(wr0 + i * 16 + (lane & 15)) * R + j];
+#pragma unroll
+      for (int jn = 0; jn < FN; ++jn)
+        low[jn] = __builtin_amdgcn_mfma_f32_16x16x4f32(ta, qs[j * BN + wc0 + jn * 16 + (lane & 15)],
+                                                       low[jn], 0, 0, 0);
+    }
+#pragma unroll
+    for (int jn = 0; jn < FN; ++jn) {
+      const int nl = wc0 + jn * 16 + (lane & 15);
+      const float csn = SCALED ? csv[nl] : 1.f;
+#pragma unroll
+      for (int ii = 0; ii < 4; ++ii) {
+        const int rl = (lane >> 4) * 4 + ii, ml = wr0 + i * 16 + rl;
+        float base;
+        if constexpr (AFF)
+          base = rsv[ml] * ((float)acc[i][jn][ii] + rav[ml]);
+        else
+          base = SCALED ? (float)acc[i][jn][ii] * (rsv[ml] * csn) : (float)acc[i][jn][ii];
+        *reinterpret_cast<float*>(strip + rl * PITCH + (jn * 16 + (lane & 15)) * 4) =
+            __builtin_fmaf(s, low[jn][ii], base);
+      }
+    }
+    // (the LDS runs one wave's instructions in order: no wait before the
+    // read-back, nor before the next strip's writes)
+#pragma unroll
+    for (int p = 0; p < PN; ++p) {
+      const int q = lane + 64 * p;
+      float v[8];
+      load8(reinterpret_cast<const float*>(strip + (q / CPR) * PITCH + (q % CPR) * 32), v);
+      const long at = (long)pm[p] * N + pn[p];
+      if constexpr (GRAD) {
+        act_slope_mul(ep.act, aux[p], v);
+        if (ep.add != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += side[p][e];
+        }
+      } else {
+        if (ep.bias != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += aux[p][e];
+        }
+        if (ep.z != nullptr && live[p]) store8(static_cast<OutT*>(ep.z) + at, v);
+        if (ep.zc != nullptr) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) { const uint32_t b = abs_bits(v[e]); m = b > m ? b : m; }
+          const int b = group_byte(quad_max_u32(live[p] ? m : 0u));
+          if (live[p]) {
+            *reinterpret_cast<u32x2*>(ep.zc + at) = group_codes(v, b);
+            if (pn[p] % kGroup == 0) ep.zs[(long)pm[p] * ep.zg + pn[p] / kGroup] = (uint8_t)b;
+          }
+        }
+        act_apply(ep.act, v);
+        if (ep.res != nullptr) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += side[p][e];
+        }
+      }
+      if (live[p]) store8(out + at, v);
+    }
+  }
+}
+
+}  // namespace qlora

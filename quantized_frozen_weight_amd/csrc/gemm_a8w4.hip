@@ -23,6 +23,7 @@
 // the group's two 64-wide steps the int32 sums are weighted by the group's
 // scale and added into float32 accumulators; the epilogue multiplies by
 // sx[m] and adds the adapter term (ring.hpp).
+#include "epilogue.hpp"
 #include "launch.hpp"
 #include "ring.hpp"
 
@@ -45,6 +46,7 @@ struct A8W4Args {
   float s;
   uint16_t* y;              // [M, N] bf16
   int tiles_x;
+  FwdEpi epi;               // EPI kernels: bias, activation, residual, saved z
 };
 
 // Sixteen consecutive 4-bit codes (8 bytes, the even k in each low nibble)
@@ -64,7 +66,7 @@ __device__ __forceinline__ i32x4 widen_nibbles(u32x2 w) {
 }
 
 // G: the largest number of 128-wide k groups the block's scale slab holds.
-template <int BM, int BN, int S, int R, int G>
+template <int BM, int BN, int S, int R, int G, bool EPI>
 __global__ __launch_bounds__(256) void fwd_a8w4_kernel(A8W4Args a) {
   constexpr int BK = 128;                          // k per stage = one scale group
   constexpr int ASZ = BM * 128, BSZ = BN * 64, STG = ASZ + BSZ;
@@ -75,7 +77,9 @@ __global__ __launch_bounds__(256) void fwd_a8w4_kernel(A8W4Args a) {
   // after the loop the ring holds the epilogue operands, then one output
   // staging strip per wave
   constexpr int EPB = (EpiOps<BM, BN, R, true>::kFloats * 4 + 15) / 16 * 16;
-  static_assert(EPB + 4 * epi_strip_bytes<uint16_t, FN>() <= S * STG, "epilogue fits in the ring");
+  constexpr int STRIP = EPI ? fused_strip_bytes<FN>() : epi_strip_bytes<uint16_t, FN>();
+  // (the scale slab behind the ring is free too once the loop is done)
+  static_assert(EPB + 4 * STRIP <= S * STG + BN * G * 2, "epilogue fits");
   __shared__ __attribute__((aligned(1024))) int8_t lds[S * STG + BN * G * 2];
   int8_t* ring = lds;
   const _Float16* SC = reinterpret_cast<const _Float16*>(lds + S * STG);   // [BN][ngrp]
@@ -195,27 +199,31 @@ __global__ __launch_bounds__(256) void fwd_a8w4_kernel(A8W4Args a) {
   __syncthreads();                                    // every wave is done with the ring
   ep.store(E, M, N, m0, n0, a.r);
   __syncthreads();
-  epilogue_lowrank<BM, BN, R, true>(acc, E, M, N, m0, n0, wm * (BM / 2), wn * (BN / 2), a.s, a.y,
-                                    ring + EPB + wid * epi_strip_bytes<uint16_t, FN>());
+  if constexpr (EPI)
+    epilogue_fused<BM, BN, R, true>(acc, E, M, N, m0, n0, wm * (BM / 2), wn * (BN / 2), a.s, a.y,
+                                    a.epi, ring + EPB + wid * STRIP);
+  else
+    epilogue_lowrank<BM, BN, R, true>(acc, E, M, N, m0, n0, wm * (BM / 2), wn * (BN / 2), a.s, a.y,
+                                      ring + EPB + wid * STRIP);
 }
 
-template <int BM, int S, int G>
+template <int BM, int S, int G, bool EPI>
 void launch_tiles(A8W4Args a, hipStream_t st) {
   constexpr int BN = 128;
   a.tiles_x = (a.N + BN - 1) / BN;
   const dim3 grid((unsigned)(a.tiles_x * ((a.M + BM - 1) / BM)));
-  if (a.r <= 4) fwd_a8w4_kernel<BM, BN, S, 4, G><<<grid, 256, 0, st>>>(a);
-  else if (a.r <= 8) fwd_a8w4_kernel<BM, BN, S, 8, G><<<grid, 256, 0, st>>>(a);
-  else if (a.r <= 16) fwd_a8w4_kernel<BM, BN, S, 16, G><<<grid, 256, 0, st>>>(a);
-  else fwd_a8w4_kernel<BM, BN, S, 32, G><<<grid, 256, 0, st>>>(a);
+  if (a.r <= 4) fwd_a8w4_kernel<BM, BN, S, 4, G, EPI><<<grid, 256, 0, st>>>(a);
+  else if (a.r <= 8) fwd_a8w4_kernel<BM, BN, S, 8, G, EPI><<<grid, 256, 0, st>>>(a);
+  else if (a.r <= 16) fwd_a8w4_kernel<BM, BN, S, 16, G, EPI><<<grid, 256, 0, st>>>(a);
+  else fwd_a8w4_kernel<BM, BN, S, 32, G, EPI><<<grid, 256, 0, st>>>(a);
 }
 
-template <int BM, int S>
+template <int BM, int S, bool EPI>
 void launch_groups(const A8W4Args& a, hipStream_t st) {
   const int ngrp = a.K / 128;                      // validated: <= kW4MaxGroups
-  if (ngrp <= 8) launch_tiles<BM, S, 8>(a, st);
-  else if (ngrp <= 32) launch_tiles<BM, S, 32>(a, st);
-  else launch_tiles<BM, S, kW4MaxGroups>(a, st);
+  if (ngrp <= 8) launch_tiles<BM, S, 8, EPI>(a, st);
+  else if (ngrp <= 32) launch_tiles<BM, S, 32, EPI>(a, st);
+  else launch_tiles<BM, S, kW4MaxGroups, EPI>(a, st);
 }
 
 }  // namespace
@@ -223,13 +231,20 @@ void launch_groups(const A8W4Args& a, hipStream_t st) {
 void launch_gemm_fwd_a8w4(int M, int N, int K, const int8_t* xq, const float* sx,
                           const uint8_t* packed, const _Float16* scales,
                           const float* t, const float* B, int hd, int r, float s,
-                          uint16_t* y, hipStream_t st) {
+                          uint16_t* y, const FwdEpi* epi, hipStream_t st) {
   A8W4Args a{};
   a.M = M; a.N = N; a.K = K; a.xq = xq; a.sx = sx; a.packed = packed; a.scales = scales;
   a.t = t; a.B = B; a.hd = hd; a.r = r; a.s = s; a.y = y;
   const long t128 = (long)((M + 127) / 128) * ((N + 127) / 128);
-  if (t128 >= kCUs) launch_groups<128, 2>(a, st);
-  else launch_groups<64, 3>(a, st);
+  if (epi != nullptr) {
+    a.epi = *epi;
+    if (t128 >= kCUs) launch_groups<128, 2, true>(a, st);
+    else launch_groups<64, 3, true>(a, st);
+  } else if (t128 >= kCUs) {
+    launch_groups<128, 2, false>(a, st);
+  } else {
+    launch_groups<64, 3, false>(a, st);
+  }
 }
 
 }  // namespace qlora

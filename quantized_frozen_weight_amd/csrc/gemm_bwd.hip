@@ -68,6 +68,7 @@
 // partial u in the workspace, and a second launch adds them in split order
 // and does what the one-pass kernel does after its loop (u, the dA partial,
 // the epilogue).
+#include "epilogue.hpp"
 #include "launch.hpp"
 #include "outlier.hpp"
 #include "ring.hpp"
@@ -108,6 +109,11 @@ struct BwdArgs {
   float* pdx;              // [splits, tiles, 4 waves, 16 fragments, 64 lanes] float4
   float* pu;               // [splits, M, r]
   int splits, nks;
+  // EXT kernels: x as its 8-bit row checkpoint where xq is not NULL (x is
+  // then unused), and the gradient epilogue
+  const int8_t* xq;        // [M, K]
+  const float* sx;         // [M]
+  GradEpi ge;
 };
 
 __device__ __forceinline__ uint32_t pk_bf16(float lo, float hi) {
@@ -237,9 +243,11 @@ __device__ __forceinline__ int code_swz(int row) {
 // four rows at a time through transposing reads: in each 16-lane group,
 // lane 4 i + p fetches the 4 columns at 16 g + 4 p of row i, and lane q
 // receives column 16 g + q of the four rows.
-template <int BM, int BN, int R, int TPK, int JPT>
-__device__ __forceinline__ void da_partial(const int8_t* Xs, const float* E, int kl, int jb,
-                                           int rows, float (&da)[JPT]) {
+// rs (EXT kernels with x in 8 bits, else NULL): the tile then holds the codes
+// and row m's scale rs[m] multiplies them here, in float32.
+template <int BM, int BN, int R, int TPK, int JPT, bool EXT>
+__device__ __forceinline__ void da_partial(const int8_t* Xs, const float* E, const float* rs, int kl,
+                                           int jb, int rows, float (&da)[JPT]) {
   constexpr int RH = BN / 64;
   const int lane = threadIdx.x & 63, g = lane >> 4, q = lane & 15, h = kl / 64;
   auto batch = [&](int b0, bool check) {            // rows [b0, b0 + 16)
@@ -257,7 +265,8 @@ __device__ __forceinline__ void da_partial(const int8_t* Xs, const float* E, int
       for (int i = 0; i < 4; ++i) {
         const int m = b0 + 4 * u + i;
         if (check && m >= rows) continue;            // uniform
-        const float xv = __uint_as_float((uint32_t)(v[u] >> (16 * i)) << 16);
+        float xv = __uint_as_float((uint32_t)(v[u] >> (16 * i)) << 16);
+        if (EXT && rs != nullptr) xv *= rs[m];
 #pragma unroll
         for (int jj = 0; jj < JPT; ++jj) da[jj] = __builtin_fmaf(xv, E[m * R + jb + TPK * jj], da[jj]);
       }
@@ -267,7 +276,49 @@ __device__ __forceinline__ void da_partial(const int8_t* Xs, const float* E, int
   if (b0 < rows) batch(b0, true);
 }
 
+// An x tile from the 8-bit row checkpoint: sixteen codes of one row per
+// thread and unit, loaded to registers (fetch) and written (put) as exact
+// bfloat16 integers in the layout of the bf16 tile (swizzled 128-byte row
+// halves), so that the dA products read either tile alike. Half the bytes of
+// bf16 rows; the rows' scales stay out of the rounding (they multiply u or
+// the float32 products). thr: the thread among the 256 that share the tile.
+// Rows past M are zero, as are columns past K.
+template <int BM, int BN>
+struct X8Tile {
+  static constexpr int NU = BM * BN / 4096, UPR = BN / 16, RH = BN / 64;
+  u32x4 v[NU];
+  __device__ __forceinline__ void fetch(const int8_t* xq, int M, int K, int m0, int k0, int thr) {
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int u = thr + 256 * i, gm = m0 + u / UPR, gk = k0 + 16 * (u % UPR);
+      const bool ok = gm < M && gk < K;
+      const u32x4 w = *reinterpret_cast<const u32x4*>(xq + (ok ? (long)gm * K + gk : 0));
+      v[i] = ok ? w : u32x4{0u, 0u, 0u, 0u};
+    }
+  }
+  __device__ __forceinline__ void put(int8_t* Xs, int thr) const {
+#pragma unroll
+    for (int i = 0; i < NU; ++i) {
+      const int u = thr + 256 * i, row = u / UPR, col = 16 * (u % UPR);
+      const int hrow = row * RH + col / 64, c = (col % 64) / 8;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        u32x4 o;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t w = v[i][2 * h + e];
+          o[2 * e] = pack_int_bf16x2((int8_t)w, (int8_t)(w >> 8));
+          o[2 * e + 1] = pack_int_bf16x2((int8_t)(w >> 16), (int8_t)(w >> 24));
+        }
+        *reinterpret_cast<u32x4*>(Xs + swz128(hrow, c + h)) = o;
+      }
+    }
+  }
+};
+
 // W4: 4-bit weights (two codes per byte, fp16 scale per 128 k); else int8.
+// EXT: x may be its 8-bit row checkpoint, and dx goes through the gradient
+// epilogue (epilogue.hpp).
 // S: ring slots (at least 3: stage kt is multiplied while stage kt + 1 is
 // converted and the later stages are in flight).
 //
@@ -283,7 +334,8 @@ __device__ __forceinline__ void da_partial(const int8_t* Xs, const float* E, int
 // loop, so that a stage's loads are only its dy and code rows.
 constexpr int kBresN = 1024;
 
-template <bool W4, int BM, int BN, int S, int R, bool AFF = false, bool BRES = false>
+template <bool W4, int BM, int BN, int S, int R, bool AFF = false, bool BRES = false,
+          bool EXT = false>
 __global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgs a) {
   constexpr int KC = 64;                              // n per stage
   constexpr int RB = W4 ? BN / 2 : BN;                // code bytes per row of n
@@ -315,7 +367,8 @@ __global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgs a) {
   constexpr int XTSZ = BM * BN * 2;
   constexpr int AQSZ = BN * R * 4;                    // the block's rows of A [BN][r]
   constexpr int EFL = (BM + BN) * R;                  // epilogue floats: U [BM][R], A^T [R][BN]
-  static_assert(EFL * 4 + (XPRE ? 0 : XTSZ) <= S * STG, "epilogue and x tile fit in the ring");
+  static_assert(EFL * 4 + (XPRE ? 0 : XTSZ) + (EXT ? BM * 4 : 0) <= S * STG,
+                "epilogue, x tile and row scales fit in the ring");
   // One LDS array for everything: with a second __shared__ object the
   // compiler can no longer tell that the ring's reads do not wait on the
   // direct-to-LDS loads still in flight, and waits for all of them.
@@ -637,7 +690,11 @@ __global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgs a) {
         lds_dma16(e < bytes ? src0 + e : zero_chunk(lane), const_cast<float*>(Aq) + o / 4);
       }
     }
-    if constexpr (XPRE) issue_x();
+    X8Tile<BM, BN> x8;
+    if constexpr (XPRE) {
+      if (EXT && a.xq != nullptr) x8.fetch(a.xq, M, K, m0, k0, ptid);
+      else issue_x();
+    }
     if constexpr (BRES) {
       // sw [N] and B [r][N] (rows up to R, columns up to kBresN; zeros past
       // them), 16 bytes per lane, ahead of the stage loads (loads complete in
@@ -658,6 +715,9 @@ __global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgs a) {
       const int off = swz128(e / 32, (e % 32) >> 2) + (e & 3) * 4;
       *reinterpret_cast<uint32_t*>(BU0 + off) = 0u;
       *reinterpret_cast<uint32_t*>(BU0 + BUSZ + off) = 0u;
+    }
+    if constexpr (EXT && XPRE) {
+      if (a.xq != nullptr) x8.put(Xs, ptid);
     }
     // stage 0 landed (later prologue stages may still be in flight)
     wait_stages<LPS, 0, S - 2>(nk - 1);
@@ -840,8 +900,20 @@ __global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgs a) {
   // (producers) beside the dx epilogue (consumers) ----
   float* E = reinterpret_cast<float*>(ring);             // U [BM][R] | A^T [R][BN]
   __syncthreads();                                        // ring released
+  float* RSs = E + EFL + (XPRE ? 0 : XTSZ / 4);           // EXT: row scales of x [BM]
   if (producer) {
-    if constexpr (!XPRE) issue_x();
+    if constexpr (EXT) {
+      if (a.xq != nullptr && ptid < BM) RSs[ptid] = a.sx[m0 + ptid < M ? m0 + ptid : M - 1];
+    }
+    if constexpr (!XPRE) {
+      if (EXT && a.xq != nullptr) {
+        X8Tile<BM, BN> x8;
+        x8.fetch(a.xq, M, K, m0, k0, ptid);
+        x8.put(Xs, ptid);
+      } else {
+        issue_x();
+      }
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -873,7 +945,7 @@ __global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgs a) {
     float da[JPT];
 #pragma unroll
     for (int jj = 0; jj < JPT; ++jj) da[jj] = 0.f;
-    da_partial<BM, BN, R, TPK, JPT>(Xs, E, kl, jb, rows_here, da);
+    da_partial<BM, BN, R, TPK, JPT, EXT>(Xs, E, EXT && a.xq != nullptr ? RSs : nullptr, kl, jb, rows_here, da);
     if (k0 + kl < K) {
 #pragma unroll
       for (int jj = 0; jj < JPT; ++jj) {
@@ -883,9 +955,14 @@ __global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgs a) {
     }
   } else {
     // output staging strips in the converted-code buffers, free after the loop
-    static_assert(4 * epi_strip_bytes<uint16_t, FN>() <= 2 * CBSZ, "staging strips fit");
-    epilogue_lowrank<BM, BN, R, false>(acc, E, M, K, m0, k0, wm * (BM / 2), wn * (BN / 2), a.s, a.dx,
-                                       CB0 + wid * epi_strip_bytes<uint16_t, FN>());
+    constexpr int STRIP = EXT ? fused_strip_bytes<FN>() : epi_strip_bytes<uint16_t, FN>();
+    static_assert(4 * STRIP <= 2 * CBSZ, "staging strips fit");
+    if constexpr (EXT)
+      epilogue_fused<BM, BN, R, false>(acc, E, M, K, m0, k0, wm * (BM / 2), wn * (BN / 2), a.s, a.dx,
+                                       a.ge, CB0 + wid * STRIP);
+    else
+      epilogue_lowrank<BM, BN, R, false>(acc, E, M, K, m0, k0, wm * (BM / 2), wn * (BN / 2), a.s, a.dx,
+                                         CB0 + wid * STRIP);
   }
 }
 
@@ -898,8 +975,10 @@ __global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgs a) {
 // product, and the whole block's registers serve one role.
 // W4: 4-bit weights (two codes per byte, fp16 scale per 128 k, carried one
 // stage ahead in a register); else int8.
-template <bool W4, int BM, int BN, int S, int R, bool AFF = false, bool SPLIT = false>
+template <bool W4, int BM, int BN, int S, int R, bool AFF = false, bool SPLIT = false,
+          bool EXT = false>
 __global__ __launch_bounds__(256, 2) void bwd_wide_kernel(BwdArgs a) {
+  static_assert(!EXT || !SPLIT, "split: the second launch reads x and writes dx");
   constexpr int KC = 64;                              // n per stage
   constexpr int RB = W4 ? BN / 2 : BN;                // code bytes per row of n
   constexpr int AUXI = ((1 + R) * 256 + 4095) / 4096;  // aux DMA instructions per wave
@@ -1450,7 +1529,22 @@ __global__ __launch_bounds__(256, 2) void bwd_wide_kernel(BwdArgs a) {
   // ---- after the contraction: u to LDS, x tile, dA partial, dx epilogue ----
   float* E = reinterpret_cast<float*>(ring);             // U [BM][R] | A^T [R][BN]
   __syncthreads();                                        // ring released
-  if constexpr (!XPRE) issue_x();
+  // EXT with x in 8 bits: its codes, and the scales of the rows whose part of
+  // the u operand this wave builds below (rows 32 wid + 8 (lane / 16) + e)
+  const bool x8on = EXT && a.xq != nullptr;
+  X8Tile<BM, BN> x8;
+  float rsv[8];
+  if constexpr (EXT) static_assert(!XPRE && BM == 128, "wave w builds the rows 32 w .. 32 w + 31");
+  if (x8on) {
+    x8.fetch(a.xq, M, K, m0, k0, tid);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int gm = m0 + 32 * wid + 8 * (lane >> 4) + e;
+      rsv[e] = a.sx[gm < M ? gm : M - 1];
+    }
+  } else {
+    if constexpr (!XPRE) issue_x();
+  }
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     if ((i & 1) != wn) continue;
@@ -1470,6 +1564,7 @@ __global__ __launch_bounds__(256, 2) void bwd_wide_kernel(BwdArgs a) {
     const int e = tid + 256 * i, j = e / BN, col = e % BN;
     if (e < BN * R) E[BM * R + e] = (j < r && k0 + col < K) ? qv[i] : 0.f;
   }
+  if (x8on) x8.put(Xs, tid);
   __syncthreads();
 
   // dA partial on the matrix cores: dA^T[k][j] = sum_m x[m][k] u[m][j] over
@@ -1490,6 +1585,7 @@ __global__ __launch_bounds__(256, 2) void bwd_wide_kernel(BwdArgs a) {
     for (int e = 0; e < 8; ++e) {
       const int m = 32 * c + 8 * (lane >> 4) + e;
       v[e] = (jr < r && part < 3 && m < rows_here) ? E[m * R + (jr < r ? jr : 0)] : 0.f;
+      if (x8on) v[e] *= rsv[e];                        // (c = wid: BM / 32 = 4 fragments per column block)
     }
     u32x4 hi, mid, lo;
 #pragma unroll
@@ -1580,7 +1676,8 @@ __global__ __launch_bounds__(256, 2) void bwd_wide_kernel(BwdArgs a) {
       for (int m = 0; m < rows_here; ++m) {
         const int e = kl % 64;
         const uint16_t xb = *reinterpret_cast<const uint16_t*>(Xs + swz128(m * RH + kl / 64, e >> 3) + 2 * (e & 7));
-        const float xv = __uint_as_float((uint32_t)xb << 16);
+        float xv = __uint_as_float((uint32_t)xb << 16);
+        if (x8on) xv *= a.sx[m0 + m];
 #pragma unroll
         for (int jj = 0; jj < JPT; ++jj)
           if (jb + TPK * jj < R) da[jj] = __builtin_fmaf(xv, E[m * R + jb + TPK * jj], da[jj]);
@@ -1593,10 +1690,18 @@ __global__ __launch_bounds__(256, 2) void bwd_wide_kernel(BwdArgs a) {
     }
   }
 
-  // output staging strips in the converted-code buffer, free after the loop
-  static_assert(4 * epi_strip_bytes<uint16_t, FN>() <= CBSZ, "staging strips fit");
-  epilogue_lowrank<BM, BN, R, false>(acc, E, M, K, m0, k0, wm * (BM / 2), wn * (BN / 2), a.s, a.dx,
-                                     CB + wid * epi_strip_bytes<uint16_t, FN>());
+  if constexpr (EXT) {
+    // the float strips go over the x tile, once every wave has read it
+    static_assert(4 * fused_strip_bytes<FN>() <= XTSZ, "staging strips fit");
+    __syncthreads();
+    epilogue_fused<BM, BN, R, false>(acc, E, M, K, m0, k0, wm * (BM / 2), wn * (BN / 2), a.s, a.dx,
+                                     a.ge, Xs + wid * fused_strip_bytes<FN>());
+  } else {
+    // output staging strips in the converted-code buffer, free after the loop
+    static_assert(4 * epi_strip_bytes<uint16_t, FN>() <= CBSZ, "staging strips fit");
+    epilogue_lowrank<BM, BN, R, false>(acc, E, M, K, m0, k0, wm * (BM / 2), wn * (BN / 2), a.s, a.dx,
+                                       CB + wid * epi_strip_bytes<uint16_t, FN>());
+  }
 }
 
 
@@ -1610,16 +1715,17 @@ __global__ __launch_bounds__(256, 2) void bwd_wide_kernel(BwdArgs a) {
 // 2 (v / 4) + q / 2 for quarter q. Every split's loads are issued before
 // the first add (NSPL: the split count's bound; splits past the count read
 // split 0 and are dropped by a select).
-template <int R, int NSPL>
+template <int R, int NSPL, bool EXT>
 __global__ __launch_bounds__(512) void bwd_fixup_kernel(BwdArgs a) {
   constexpr int BM = 128, HN = 32, FN = 2;
   constexpr int EFL = (BM + HN) * R;                    // U [BM][R] | A^T [R][HN]
   constexpr int XSZ = BM * HN * 2;                      // x [BM][HN] bf16, 64-byte rows
-  constexpr int STRIP = epi_strip_bytes<uint16_t, FN>();
-  __shared__ __attribute__((aligned(1024))) int8_t lds[XSZ + EFL * 4 + 8 * STRIP];
+  constexpr int STRIP = EXT ? fused_strip_bytes<FN>() : epi_strip_bytes<uint16_t, FN>();
+  __shared__ __attribute__((aligned(1024))) int8_t lds[XSZ + EFL * 4 + 8 * STRIP + (EXT ? BM * 4 : 0)];
   int8_t* Xs = lds;
   float* E = reinterpret_cast<float*>(lds + XSZ);
   int8_t* strips = lds + XSZ + EFL * 4;
+  float* RSs = reinterpret_cast<float*>(strips + 8 * STRIP);   // EXT: row scales of x [BM]
 
   const int tid = threadIdx.x, lane = tid & 63, v = wave_id();
   const int M = a.M, K = a.K, r = a.r, nsp = a.splits;
@@ -1642,7 +1748,18 @@ __global__ __launch_bounds__(512) void bwd_fixup_kernel(BwdArgs a) {
   // x tile by DMA: [128 rows][32 columns] as 64-byte rows, 16 per
   // instruction; wave v moves rows 16 v .. + 16 (chunk c of row r lands at
   // 64 r + 16 (c ^ ((r >> 2) & 3)))
-  {
+  // (x in 8 bits: thread -> eight codes, widened to bf16 integers in the same
+  // layout, once the other loads are out)
+  const bool x8on = EXT && a.xq != nullptr;
+  u32x2 xc{};
+  const int xrow = tid >> 2, xc8 = tid & 3;
+  if (x8on) {
+    const int gm = m0 + xrow, gk = k0 + 8 * xc8;
+    const bool ok = gm < M && gk < K;
+    xc = *reinterpret_cast<const u32x2*>(a.xq + (ok ? (long)gm * K + gk : 0));
+    if (!ok) xc = u32x2{0u, 0u};
+    if (tid < BM) RSs[tid] = a.sx[m0 + tid < M ? m0 + tid : M - 1];
+  } else {
     const int row = 16 * v + (lane >> 2);
     const int c = (lane & 3) ^ ((row >> 2) & 3), gm = m0 + row, gk = k0 + c * 8;
     const void* src = gk < K ? (const void*)(a.x + (long)(gm < M ? gm : M - 1) * K + gk)
@@ -1676,6 +1793,15 @@ __global__ __launch_bounds__(512) void bwd_fixup_kernel(BwdArgs a) {
     for (int sp = 1; sp < NSPL; ++sp)
       if (sp < nsp) acc[0][j] += pv[sp][j];
   }
+  if (x8on) {
+    u32x4 o;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      o[2 * e] = pack_int_bf16x2((int8_t)xc[e], (int8_t)(xc[e] >> 8));
+      o[2 * e + 1] = pack_int_bf16x2((int8_t)(xc[e] >> 16), (int8_t)(xc[e] >> 24));
+    }
+    *reinterpret_cast<u32x4*>(Xs + xrow * 64 + ((xc8 ^ ((xrow >> 2) & 3)) << 4)) = o;
+  }
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
   __syncthreads();
 
@@ -1693,7 +1819,8 @@ __global__ __launch_bounds__(512) void bwd_fixup_kernel(BwdArgs a) {
       for (int m = 0; m < rows_here; ++m) {
         const uint16_t xb = *reinterpret_cast<const uint16_t*>(
             Xs + m * 64 + (((kl >> 3) ^ ((m >> 2) & 3)) << 4) + 2 * (kl & 7));
-        const float xv = __uint_as_float((uint32_t)xb << 16);
+        float xv = __uint_as_float((uint32_t)xb << 16);
+        if (x8on) xv *= RSs[m];
 #pragma unroll
         for (int jj = 0; jj < JPT; ++jj)
           if (jb + 16 * jj < R) da[jj] = __builtin_fmaf(xv, E[m * R + jb + 16 * jj], da[jj]);
@@ -1708,11 +1835,15 @@ __global__ __launch_bounds__(512) void bwd_fixup_kernel(BwdArgs a) {
     }
   }
 
-  epilogue_lowrank<BM, HN, R, false>(acc, E, M, K, m0, k0, 16 * v, 0, a.s, a.dx,
+  if constexpr (EXT)
+    epilogue_fused<BM, HN, R, false>(acc, E, M, K, m0, k0, 16 * v, 0, a.s, a.dx, a.ge,
                                      strips + v * STRIP);
+  else
+    epilogue_lowrank<BM, HN, R, false>(acc, E, M, K, m0, k0, 16 * v, 0, a.s, a.dx,
+                                       strips + v * STRIP);
 }
 
-template <bool W4, int BN, int S, bool AFF = false>
+template <bool W4, int BN, int S, bool EXT, bool AFF = false>
 void launch_pc(BwdArgs a, hipStream_t st) {
   constexpr int BM = 64;
   a.tiles_x = (a.K + BN - 1) / BN;
@@ -1724,39 +1855,39 @@ void launch_pc(BwdArgs a, hipStream_t st) {
     // than it saves). The block takes 112 KB, one per compute unit as
     // without them; at rank 4 they would cost the second block.
     if (a.N <= kBresN && a.hd == a.N && a.r > 4 && a.r <= 8 && a.M >= 512) {
-      bwd_pc_kernel<false, BM, BN, S, 8, false, true><<<grid, 512, 0, st>>>(a);
+      bwd_pc_kernel<false, BM, BN, S, 8, false, true, EXT><<<grid, 512, 0, st>>>(a);
       return;
     }
   }
-  if (a.r <= 4) bwd_pc_kernel<W4, BM, BN, S, 4, AFF><<<grid, 512, 0, st>>>(a);
-  else if (a.r <= 8) bwd_pc_kernel<W4, BM, BN, S, 8, AFF><<<grid, 512, 0, st>>>(a);
-  else if (a.r <= 16) bwd_pc_kernel<W4, BM, BN, S, 16, AFF><<<grid, 512, 0, st>>>(a);
-  else if constexpr (!W4) bwd_pc_kernel<W4, BM, BN, S, 32, AFF><<<grid, 512, 0, st>>>(a);
+  if (a.r <= 4) bwd_pc_kernel<W4, BM, BN, S, 4, AFF, false, EXT><<<grid, 512, 0, st>>>(a);
+  else if (a.r <= 8) bwd_pc_kernel<W4, BM, BN, S, 8, AFF, false, EXT><<<grid, 512, 0, st>>>(a);
+  else if (a.r <= 16) bwd_pc_kernel<W4, BM, BN, S, 16, AFF, false, EXT><<<grid, 512, 0, st>>>(a);
+  else if constexpr (!W4) bwd_pc_kernel<W4, BM, BN, S, 32, AFF, false, EXT><<<grid, 512, 0, st>>>(a);
   // (4-bit layers of rank above 16 take the 128 x 128 tiles: bwd_row_block)
 }
 
-template <bool W4, bool AFF = false, bool SPLIT = false, int BN = 128>
+template <bool W4, bool EXT, bool AFF = false, bool SPLIT = false, int BN = 128>
 void launch_wide(BwdArgs a, hipStream_t st) {
   static_assert(BN == 128 || (!W4 && !AFF && !SPLIT), "64-wide tiles: plain int8, one pass");
   constexpr int BM = 128, S = 2;
   a.tiles_x = (a.K + BN - 1) / BN;
   const dim3 grid((unsigned)(a.tiles_x * ((a.M + BM - 1) / BM) * (SPLIT ? a.splits : 1)));
-  if (a.r <= 4) bwd_wide_kernel<W4, BM, BN, S, 4, AFF, SPLIT><<<grid, 256, 0, st>>>(a);
-  else if (a.r <= 8) bwd_wide_kernel<W4, BM, BN, S, 8, AFF, SPLIT><<<grid, 256, 0, st>>>(a);
-  else if (a.r <= 16) bwd_wide_kernel<W4, BM, BN, S, 16, AFF, SPLIT><<<grid, 256, 0, st>>>(a);
-  else bwd_wide_kernel<W4, BM, BN, S, 32, AFF, SPLIT><<<grid, 256, 0, st>>>(a);
+  if (a.r <= 4) bwd_wide_kernel<W4, BM, BN, S, 4, AFF, SPLIT, EXT && !SPLIT><<<grid, 256, 0, st>>>(a);
+  else if (a.r <= 8) bwd_wide_kernel<W4, BM, BN, S, 8, AFF, SPLIT, EXT && !SPLIT><<<grid, 256, 0, st>>>(a);
+  else if (a.r <= 16) bwd_wide_kernel<W4, BM, BN, S, 16, AFF, SPLIT, EXT && !SPLIT><<<grid, 256, 0, st>>>(a);
+  else bwd_wide_kernel<W4, BM, BN, S, 32, AFF, SPLIT, EXT && !SPLIT><<<grid, 256, 0, st>>>(a);
   if constexpr (SPLIT) {
     const dim3 fgrid((unsigned)(4 * a.tiles_x * ((a.M + BM - 1) / BM)));
     if (a.splits <= 4) {
-      if (a.r <= 4) bwd_fixup_kernel<4, 4><<<fgrid, 512, 0, st>>>(a);
-      else if (a.r <= 8) bwd_fixup_kernel<8, 4><<<fgrid, 512, 0, st>>>(a);
-      else if (a.r <= 16) bwd_fixup_kernel<16, 4><<<fgrid, 512, 0, st>>>(a);
-      else bwd_fixup_kernel<32, 4><<<fgrid, 512, 0, st>>>(a);
+      if (a.r <= 4) bwd_fixup_kernel<4, 4, EXT><<<fgrid, 512, 0, st>>>(a);
+      else if (a.r <= 8) bwd_fixup_kernel<8, 4, EXT><<<fgrid, 512, 0, st>>>(a);
+      else if (a.r <= 16) bwd_fixup_kernel<16, 4, EXT><<<fgrid, 512, 0, st>>>(a);
+      else bwd_fixup_kernel<32, 4, EXT><<<fgrid, 512, 0, st>>>(a);
     } else {
-      if (a.r <= 4) bwd_fixup_kernel<4, kMaxWideSplits><<<fgrid, 512, 0, st>>>(a);
-      else if (a.r <= 8) bwd_fixup_kernel<8, kMaxWideSplits><<<fgrid, 512, 0, st>>>(a);
-      else if (a.r <= 16) bwd_fixup_kernel<16, kMaxWideSplits><<<fgrid, 512, 0, st>>>(a);
-      else bwd_fixup_kernel<32, kMaxWideSplits><<<fgrid, 512, 0, st>>>(a);
+      if (a.r <= 4) bwd_fixup_kernel<4, kMaxWideSplits, EXT><<<fgrid, 512, 0, st>>>(a);
+      else if (a.r <= 8) bwd_fixup_kernel<8, kMaxWideSplits, EXT><<<fgrid, 512, 0, st>>>(a);
+      else if (a.r <= 16) bwd_fixup_kernel<16, kMaxWideSplits, EXT><<<fgrid, 512, 0, st>>>(a);
+      else bwd_fixup_kernel<32, kMaxWideSplits, EXT><<<fgrid, 512, 0, st>>>(a);
     }
   }
 }
@@ -1830,11 +1961,41 @@ const char* bwd_fused_kernel_name(int fmt, int M, int K, int N, int r) {
   }
 }
 
+namespace {
+template <bool EXT>
+void launch_fmt(int fmt, BwdKind kind, const void* scales, BwdArgs a, hipStream_t st) {
+  if (fmt == 2) {
+    const W8OLayout L = w8o_layout(a.K, a.N);
+    const char* sb = static_cast<const char*>(scales);
+    a.w8o = reinterpret_cast<const W8OHeader*>(sb);
+    a.bptr = reinterpret_cast<const int*>(sb + L.bptr);
+    a.bent = reinterpret_cast<const u32x2*>(sb + L.bent);
+    a.kg = L.kg;
+    if (kind == BwdKind::kSplit) launch_wide<false, EXT, true, true>(a, st);
+    else if (kind == BwdKind::kPC) launch_pc<false, 64, 3, EXT, true>(a, st);
+    else launch_wide<false, EXT, true>(a, st);
+  } else if (fmt == 0) {
+    a.sw = static_cast<const float*>(scales);
+    if (kind == BwdKind::kSplit) launch_wide<false, EXT, false, true>(a, st);
+    else if (kind == BwdKind::kPC) launch_pc<false, 64, 3, EXT>(a, st);
+    else if (kind == BwdKind::kWide64) launch_wide<false, EXT, false, false, 64>(a, st);
+    else launch_wide<false, EXT>(a, st);
+  } else {
+    a.sc4 = static_cast<const uint16_t*>(scales);
+    if (kind == BwdKind::kSplit) launch_wide<true, EXT, false, true>(a, st);
+    else if (kind == BwdKind::kPC) launch_pc<true, 128, 3, EXT>(a, st);
+    else launch_wide<true, EXT>(a, st);
+  }
+}
+}  // namespace
+
 void launch_bwd_fused(int fmt, int M, int K, int N, const uint16_t* dy,
                       const void* codes, const void* scales, const float* B, int hd,
                       const float* A, const float* t, const uint16_t* x, int r,
                       float s, uint16_t* dx, float* partA, float* partB,
-                      float* pdx, float* pu, hipStream_t st) {
+                      float* pdx, float* pu, hipStream_t st, const int8_t* xq,
+                      const float* sx, const GradEpi* ge) {
+  const bool ext = ge != nullptr;
   BwdArgs a{};
   a.M = M; a.K = K; a.N = N; a.dy = dy; a.codes = static_cast<const int8_t*>(codes);
   a.B = B; a.hd = hd; a.A = A; a.t = t; a.x = x; a.r = r; a.s = s; a.dx = dx; a.partA = partA;
@@ -1842,27 +2003,11 @@ void launch_bwd_fused(int fmt, int M, int K, int N, const uint16_t* dy,
   a.pdx = pdx; a.pu = pu;
   wide_split_plan(M, K, N, &a.splits, &a.nks);
   const BwdKind kind = bwd_kind(fmt, M, K, N, r);
-  if (fmt == 2) {
-    const W8OLayout L = w8o_layout(K, N);
-    const char* sb = static_cast<const char*>(scales);
-    a.w8o = reinterpret_cast<const W8OHeader*>(sb);
-    a.bptr = reinterpret_cast<const int*>(sb + L.bptr);
-    a.bent = reinterpret_cast<const u32x2*>(sb + L.bent);
-    a.kg = L.kg;
-    if (kind == BwdKind::kSplit) launch_wide<false, true, true>(a, st);
-    else if (kind == BwdKind::kPC) launch_pc<false, 64, 3, true>(a, st);
-    else launch_wide<false, true>(a, st);
-  } else if (fmt == 0) {
-    a.sw = static_cast<const float*>(scales);
-    if (kind == BwdKind::kSplit) launch_wide<false, false, true>(a, st);
-    else if (kind == BwdKind::kPC) launch_pc<false, 64, 3>(a, st);
-    else if (kind == BwdKind::kWide64) launch_wide<false, false, false, 64>(a, st);
-    else launch_wide<false>(a, st);
+  if (ext) {
+    a.xq = xq; a.sx = sx; a.ge = *ge;
+    launch_fmt<true>(fmt, kind, scales, a, st);
   } else {
-    a.sc4 = static_cast<const uint16_t*>(scales);
-    if (kind == BwdKind::kSplit) launch_wide<true, false, true>(a, st);
-    else if (kind == BwdKind::kPC) launch_pc<true, 128, 3>(a, st);
-    else launch_wide<true>(a, st);
+    launch_fmt<false>(fmt, kind, scales, a, st);
   }
 }
 

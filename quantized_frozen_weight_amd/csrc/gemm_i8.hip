@@ -42,6 +42,7 @@
 // k axis split it (up to 8 ways, 4 for the affine form): each block leaves
 // its exact int32 sums (and the affine form its float corrections) in the
 // workspace, and a second launch adds them and applies the epilogue.
+#include "epilogue.hpp"
 #include "launch.hpp"
 #include "outlier.hpp"
 #include "ring.hpp"
@@ -77,11 +78,14 @@ struct I8Args {
   int32_t* pacc;         // [splits, tiles, 4 waves, FM FN fragments, 64 lanes] int4
   float* pcorr;          // affine: [splits, tiles, 4 waves, CR rows, 16 columns, 64 lanes]
   int splits, nks;
+  FwdEpi epi;            // EPI kernels: bias, activation, residual, saved z
 };
 
-template <int BM, int BN, int S, int R, typename OutT, bool ACC_OUT, bool AFF, bool SPLIT = false>
+template <int BM, int BN, int S, int R, typename OutT, bool ACC_OUT, bool AFF, bool SPLIT = false,
+          bool EPI = false>
 __global__ __launch_bounds__(256) void fwd_i8_kernel(I8Args a) {
   static_assert(!SPLIT || !ACC_OUT, "split: no integer test output");
+  static_assert(!EPI || (!SPLIT && !ACC_OUT), "the epilogue runs where y is formed");
   constexpr int BK = 128, ASZ = BM * BK, STG = (BM + BN) * BK;
   constexpr int AI = BM / 32, BI = BN / 32, LPS = AI + BI;   // loads per wave per stage
   constexpr int FM = BM / 32, FN = BN / 32;
@@ -90,7 +94,8 @@ __global__ __launch_bounds__(256) void fwd_i8_kernel(I8Args a) {
   // after the loop the ring holds the epilogue operands, then one output
   // staging strip per wave
   constexpr int EPB = (EpiOps<BM, BN, R, true, AFF>::kFloats * 4 + 15) / 16 * 16;
-  static_assert(EPB + 4 * epi_strip_bytes<OutT, FN>() <= S * STG, "epilogue fits in the ring");
+  constexpr int STRIP = EPI ? fused_strip_bytes<FN>() : epi_strip_bytes<OutT, FN>();
+  static_assert(EPB + 4 * STRIP <= S * STG, "epilogue fits in the ring");
   __shared__ __attribute__((aligned(1024))) int8_t ring[S * STG];
 
   const int tid = threadIdx.x, lane = tid & 63, wid = wave_id();
@@ -369,15 +374,25 @@ __global__ __launch_bounds__(256) void fwd_i8_kernel(I8Args a) {
       ep.store(E, M, N, m0, n0, a.r);
       ep.store_rows(E, M, m0, a.w8o->bias_q);
       __syncthreads();
-      epilogue_lowrank<BM, BN, R, true, true>(accf, E, M, N, m0, n0, wm * (BM / 2), wn * (BN / 2),
-                                              a.s, reinterpret_cast<OutT*>(a.y),
-                                              ring + EPB + wid * epi_strip_bytes<OutT, FN>());
+      if constexpr (EPI)
+        epilogue_fused<BM, BN, R, true, true>(accf, E, M, N, m0, n0, wm * (BM / 2), wn * (BN / 2),
+                                              a.s, reinterpret_cast<OutT*>(a.y), a.epi,
+                                              ring + EPB + wid * STRIP);
+      else
+        epilogue_lowrank<BM, BN, R, true, true>(accf, E, M, N, m0, n0, wm * (BM / 2), wn * (BN / 2),
+                                                a.s, reinterpret_cast<OutT*>(a.y),
+                                                ring + EPB + wid * STRIP);
     } else {
       ep.store(E, M, N, m0, n0, a.r);
       __syncthreads();
-      epilogue_lowrank<BM, BN, R, true>(acc, E, M, N, m0, n0, wm * (BM / 2), wn * (BN / 2),
-                                        a.s, reinterpret_cast<OutT*>(a.y),
-                                        ring + EPB + wid * epi_strip_bytes<OutT, FN>());
+      if constexpr (EPI)
+        epilogue_fused<BM, BN, R, true>(acc, E, M, N, m0, n0, wm * (BM / 2), wn * (BN / 2),
+                                        a.s, reinterpret_cast<OutT*>(a.y), a.epi,
+                                        ring + EPB + wid * STRIP);
+      else
+        epilogue_lowrank<BM, BN, R, true>(acc, E, M, N, m0, n0, wm * (BM / 2), wn * (BN / 2),
+                                          a.s, reinterpret_cast<OutT*>(a.y),
+                                          ring + EPB + wid * STRIP);
     }
   }
 }
@@ -389,12 +404,12 @@ __global__ __launch_bounds__(256) void fwd_i8_kernel(I8Args a) {
 // fragment columns 2 (q % 2) + {0, 1} of the product kernel's wave
 // 2 (v / 4) + q / 2 for quarter q; all of a lane's split loads are issued
 // before the first add.
-template <int R, int NSPL, typename OutT>
+template <int R, int NSPL, typename OutT, bool EPI>
 __global__ __launch_bounds__(512) void fwd_fixup_kernel(I8Args a) {
   constexpr int BM = 128, HN = 32, FN = 2;
   using Ep = EpiOps<BM, HN, R, true>;
   constexpr int EPB = (Ep::kFloats * 4 + 15) / 16 * 16;
-  constexpr int STRIP = epi_strip_bytes<OutT, FN>();
+  constexpr int STRIP = EPI ? fused_strip_bytes<FN>() : epi_strip_bytes<OutT, FN>();
   __shared__ __attribute__((aligned(1024))) int8_t lds[EPB + 8 * STRIP];
   float* E = reinterpret_cast<float*>(lds);
 
@@ -426,21 +441,25 @@ __global__ __launch_bounds__(512) void fwd_fixup_kernel(I8Args a) {
   }
   if (tid < 256) ep.store(E, M, N, m0, n0, a.r);
   __syncthreads();
-  epilogue_lowrank<BM, HN, R, true>(acc, E, M, N, m0, n0, 16 * v, 0, a.s,
-                                    reinterpret_cast<OutT*>(a.y), lds + EPB + v * STRIP);
+  if constexpr (EPI)
+    epilogue_fused<BM, HN, R, true>(acc, E, M, N, m0, n0, 16 * v, 0, a.s,
+                                    reinterpret_cast<OutT*>(a.y), a.epi, lds + EPB + v * STRIP);
+  else
+    epilogue_lowrank<BM, HN, R, true>(acc, E, M, N, m0, n0, 16 * v, 0, a.s,
+                                      reinterpret_cast<OutT*>(a.y), lds + EPB + v * STRIP);
 }
 
 // The same for outlier-compensated weights on 128 x 64 tiles, one 512-thread
 // block per tile: the int32 partial sums added (exact), the corrections added
 // in split order into LDS ([128][64 + 4] floats, from the product kernel's
 // cell layout), then acc' = c acc + corr and the affine epilogue.
-template <int R, int NSPL>
+template <int R, int NSPL, bool EPI>
 __global__ __launch_bounds__(512) void fwd_fixup_aff_kernel(I8Args a) {
   constexpr int BM = 128, BN = 64, FN = 4, CR = 2, CP = BN + 4;
   using Ep = EpiOps<BM, BN, R, true, true>;
   constexpr int EPB = (Ep::kFloats * 4 + 15) / 16 * 16;
   constexpr int CSZ = BM * CP * 4;
-  constexpr int STRIP = epi_strip_bytes<uint16_t, FN>();
+  constexpr int STRIP = EPI ? fused_strip_bytes<FN>() : epi_strip_bytes<uint16_t, FN>();
   __shared__ __attribute__((aligned(1024))) int8_t lds[CSZ + EPB + 8 * STRIP];
   float* C = reinterpret_cast<float*>(lds);
   float* E = reinterpret_cast<float*>(lds + CSZ);
@@ -515,8 +534,13 @@ __global__ __launch_bounds__(512) void fwd_fixup_aff_kernel(I8Args a) {
       const int ml = 16 * v + (lane >> 4) * 4 + ii, nl = j * 16 + (lane & 15);
       accf[0][j][ii] = __builtin_fmaf(cstep, (float)acc[j][ii], C[ml * CP + nl]);
     }
-  epilogue_lowrank<BM, BN, R, true, true>(accf, E, M, N, m0, n0, 16 * v, 0, a.s,
-                                          reinterpret_cast<uint16_t*>(a.y), lds + CSZ + EPB + v * STRIP);
+  if constexpr (EPI)
+    epilogue_fused<BM, BN, R, true, true>(accf, E, M, N, m0, n0, 16 * v, 0, a.s,
+                                          reinterpret_cast<uint16_t*>(a.y), a.epi,
+                                          lds + CSZ + EPB + v * STRIP);
+  else
+    epilogue_lowrank<BM, BN, R, true, true>(accf, E, M, N, m0, n0, 16 * v, 0, a.s,
+                                            reinterpret_cast<uint16_t*>(a.y), lds + CSZ + EPB + v * STRIP);
 }
 
 constexpr int kMaxFwdSplits = 8;
@@ -542,7 +566,7 @@ void fwd_split_plan(int M, int N, int K, int BN, int maxsp, int* splits, int* nk
   *splits = (nk + *nks - 1) / *nks;
 }
 
-template <typename OutT>
+template <typename OutT, bool EPI>
 void launch_split(I8Args a, hipStream_t st) {
   constexpr int BM = 128, BN = 128, S = 2;
   a.tiles_x = (a.N + BN - 1) / BN;
@@ -553,35 +577,35 @@ void launch_split(I8Args a, hipStream_t st) {
   else if (a.r <= 16) fwd_i8_kernel<BM, BN, S, 16, OutT, false, false, true><<<grid, 256, 0, st>>>(a);
   else fwd_i8_kernel<BM, BN, S, 32, OutT, false, false, true><<<grid, 256, 0, st>>>(a);
   if (a.splits <= 4) {
-    if (a.r <= 4) fwd_fixup_kernel<4, 4, OutT><<<fgrid, 512, 0, st>>>(a);
-    else if (a.r <= 8) fwd_fixup_kernel<8, 4, OutT><<<fgrid, 512, 0, st>>>(a);
-    else if (a.r <= 16) fwd_fixup_kernel<16, 4, OutT><<<fgrid, 512, 0, st>>>(a);
-    else fwd_fixup_kernel<32, 4, OutT><<<fgrid, 512, 0, st>>>(a);
+    if (a.r <= 4) fwd_fixup_kernel<4, 4, OutT, EPI><<<fgrid, 512, 0, st>>>(a);
+    else if (a.r <= 8) fwd_fixup_kernel<8, 4, OutT, EPI><<<fgrid, 512, 0, st>>>(a);
+    else if (a.r <= 16) fwd_fixup_kernel<16, 4, OutT, EPI><<<fgrid, 512, 0, st>>>(a);
+    else fwd_fixup_kernel<32, 4, OutT, EPI><<<fgrid, 512, 0, st>>>(a);
   } else {
-    if (a.r <= 4) fwd_fixup_kernel<4, kMaxFwdSplits, OutT><<<fgrid, 512, 0, st>>>(a);
-    else if (a.r <= 8) fwd_fixup_kernel<8, kMaxFwdSplits, OutT><<<fgrid, 512, 0, st>>>(a);
-    else if (a.r <= 16) fwd_fixup_kernel<16, kMaxFwdSplits, OutT><<<fgrid, 512, 0, st>>>(a);
-    else fwd_fixup_kernel<32, kMaxFwdSplits, OutT><<<fgrid, 512, 0, st>>>(a);
+    if (a.r <= 4) fwd_fixup_kernel<4, kMaxFwdSplits, OutT, EPI><<<fgrid, 512, 0, st>>>(a);
+    else if (a.r <= 8) fwd_fixup_kernel<8, kMaxFwdSplits, OutT, EPI><<<fgrid, 512, 0, st>>>(a);
+    else if (a.r <= 16) fwd_fixup_kernel<16, kMaxFwdSplits, OutT, EPI><<<fgrid, 512, 0, st>>>(a);
+    else fwd_fixup_kernel<32, kMaxFwdSplits, OutT, EPI><<<fgrid, 512, 0, st>>>(a);
   }
 }
 
-template <int BM, int BN, int S, typename OutT, bool ACC, bool AFF = false>
+template <int BM, int BN, int S, typename OutT, bool ACC, bool AFF, bool EPI>
 void launch_tiles(I8Args a, hipStream_t st) {
   a.tiles_x = (a.N + BN - 1) / BN;
   const dim3 grid((unsigned)(a.tiles_x * ((a.M + BM - 1) / BM)));
-  if (a.r <= 4) fwd_i8_kernel<BM, BN, S, 4, OutT, ACC, AFF><<<grid, 256, 0, st>>>(a);
-  else if (a.r <= 8) fwd_i8_kernel<BM, BN, S, 8, OutT, ACC, AFF><<<grid, 256, 0, st>>>(a);
-  else if (a.r <= 16) fwd_i8_kernel<BM, BN, S, 16, OutT, ACC, AFF><<<grid, 256, 0, st>>>(a);
-  else fwd_i8_kernel<BM, BN, S, 32, OutT, ACC, AFF><<<grid, 256, 0, st>>>(a);
+  if (a.r <= 4) fwd_i8_kernel<BM, BN, S, 4, OutT, ACC, AFF, false, EPI><<<grid, 256, 0, st>>>(a);
+  else if (a.r <= 8) fwd_i8_kernel<BM, BN, S, 8, OutT, ACC, AFF, false, EPI><<<grid, 256, 0, st>>>(a);
+  else if (a.r <= 16) fwd_i8_kernel<BM, BN, S, 16, OutT, ACC, AFF, false, EPI><<<grid, 256, 0, st>>>(a);
+  else fwd_i8_kernel<BM, BN, S, 32, OutT, ACC, AFF, false, EPI><<<grid, 256, 0, st>>>(a);
 }
 
-template <typename OutT, bool ACC>
+template <typename OutT, bool ACC, bool EPI>
 void launch_shape(I8Args a, hipStream_t st) {
   if constexpr (!ACC) {
     if (a.pacc != nullptr) {
       fwd_split_plan(a.M, a.N, a.K, 128, kMaxFwdSplits, &a.splits, &a.nks);
       if (a.splits > 1) {
-        launch_split<OutT>(a, st);
+        launch_split<OutT, EPI>(a, st);
         return;
       }
     }
@@ -595,11 +619,40 @@ void launch_shape(I8Args a, hipStream_t st) {
   // products: 576 and 768 blocks of 128 x 128 in two rounds, 384 and 512 of
   // 128 x 192 in one)
   const long rounds128 = (t128 + 2 * kCUs - 1) / (2 * kCUs), rounds192 = (t192 + 2 * kCUs - 1) / (2 * kCUs);
-  if (t64 <= 2 * kCUs) launch_tiles<64, 64, 3, OutT, ACC>(a, st);
+  if (t64 <= 2 * kCUs) launch_tiles<64, 64, 3, OutT, ACC, false, EPI>(a, st);
   else if (t128 >= 2 * kCUs && a.N % 192 == 0 && 3 * rounds192 < 2 * rounds128)
-    launch_tiles<128, 192, 2, OutT, ACC>(a, st);
-  else if (t128 >= 2 * kCUs) launch_tiles<128, 128, 2, OutT, ACC>(a, st);
-  else launch_tiles<128, 64, 2, OutT, ACC>(a, st);
+    launch_tiles<128, 192, 2, OutT, ACC, false, EPI>(a, st);
+  else if (t128 >= 2 * kCUs) launch_tiles<128, 128, 2, OutT, ACC, false, EPI>(a, st);
+  else launch_tiles<128, 64, 2, OutT, ACC, false, EPI>(a, st);
+}
+
+// The affine product: split with its fixup, or one of its two tile shapes.
+template <bool EPI>
+void launch_affine(I8Args a, hipStream_t st) {
+  if (a.pacc != nullptr && a.pcorr != nullptr) {
+    fwd_split_plan(a.M, a.N, a.K, 64, kMaxAffSplits, &a.splits, &a.nks);
+    if (a.splits > 1) {
+      // 128 x 64 tiles over the split contraction, then the fixup per tile
+      constexpr int BM = 128, BN = 64, S = 2;
+      a.tiles_x = (a.N + BN - 1) / BN;
+      const int tiles = a.tiles_x * ((a.M + BM - 1) / BM);
+      const dim3 grid((unsigned)(tiles * a.splits)), fgrid((unsigned)tiles);
+      if (a.r <= 4) fwd_i8_kernel<BM, BN, S, 4, uint16_t, false, true, true><<<grid, 256, 0, st>>>(a);
+      else if (a.r <= 8) fwd_i8_kernel<BM, BN, S, 8, uint16_t, false, true, true><<<grid, 256, 0, st>>>(a);
+      else if (a.r <= 16) fwd_i8_kernel<BM, BN, S, 16, uint16_t, false, true, true><<<grid, 256, 0, st>>>(a);
+      else fwd_i8_kernel<BM, BN, S, 32, uint16_t, false, true, true><<<grid, 256, 0, st>>>(a);
+      if (a.r <= 4) fwd_fixup_aff_kernel<4, kMaxAffSplits, EPI><<<fgrid, 512, 0, st>>>(a);
+      else if (a.r <= 8) fwd_fixup_aff_kernel<8, kMaxAffSplits, EPI><<<fgrid, 512, 0, st>>>(a);
+      else if (a.r <= 16) fwd_fixup_aff_kernel<16, kMaxAffSplits, EPI><<<fgrid, 512, 0, st>>>(a);
+      else fwd_fixup_aff_kernel<32, kMaxAffSplits, EPI><<<fgrid, 512, 0, st>>>(a);
+      return;
+    }
+  }
+  // the correction accumulators take registers: 64 x 64 (three stages) or
+  // 128 x 64 (two)
+  const long t64 = (long)((a.M + 63) / 64) * ((a.N + 63) / 64);
+  if (t64 <= 2 * kCUs) launch_tiles<64, 64, 3, uint16_t, false, true, EPI>(a, st);
+  else launch_tiles<128, 64, 2, uint16_t, false, true, EPI>(a, st);
 }
 
 }  // namespace
@@ -616,20 +669,30 @@ size_t fwd_split_ints(int M, int N, int K, bool affine) {
 void launch_gemm_fwd_w8(int dtype, int M, int N, int K, const int8_t* xq,
                         const int8_t* codes, const float* sx, const float* sw,
                         const float* t, const float* B, int hd, int r, float s,
-                        void* y, int32_t* acc_out, int32_t* pacc, hipStream_t st) {
+                        void* y, int32_t* acc_out, int32_t* pacc, const FwdEpi* epi,
+                        hipStream_t st) {
   I8Args a{};
   a.M = M; a.N = N; a.K = K; a.xq = xq; a.codes = codes; a.sx = sx; a.sw = sw;
   a.t = t; a.B = B; a.hd = hd; a.r = r; a.s = s; a.y = y; a.acc_out = acc_out;
   a.pacc = pacc;
-  if (acc_out != nullptr) launch_shape<float, true>(a, st);
-  else if (dtype == 0) launch_shape<float, false>(a, st);
-  else launch_shape<uint16_t, false>(a, st);
+  if (acc_out != nullptr) {
+    launch_shape<float, true, false>(a, st);
+  } else if (epi != nullptr) {
+    a.epi = *epi;
+    if (dtype == 0) launch_shape<float, false, true>(a, st);
+    else launch_shape<uint16_t, false, true>(a, st);
+  } else if (dtype == 0) {
+    launch_shape<float, false, false>(a, st);
+  } else {
+    launch_shape<uint16_t, false, false>(a, st);
+  }
 }
 
 void launch_gemm_fwd_w8o(int M, int N, int K, const int8_t* xq, const int8_t* codes,
                          const float* sx, const float* asum, const void* side,
                          const float* t, const float* B, int hd, int r, float s,
-                         uint16_t* y, int32_t* pacc, float* pcorr, hipStream_t st) {
+                         uint16_t* y, int32_t* pacc, float* pcorr, const FwdEpi* epi,
+                         hipStream_t st) {
   const W8OLayout L = w8o_layout(K, N);
   const char* sb = static_cast<const char*>(side);
   I8Args a{};
@@ -642,30 +705,12 @@ void launch_gemm_fwd_w8o(int M, int N, int K, const int8_t* xq, const int8_t* co
   a.ng = L.ng;
   a.pacc = pacc;
   a.pcorr = pcorr;
-  if (pacc != nullptr && pcorr != nullptr) {
-    fwd_split_plan(M, N, K, 64, kMaxAffSplits, &a.splits, &a.nks);
-    if (a.splits > 1) {
-      // 128 x 64 tiles over the split contraction, then the fixup per tile
-      constexpr int BM = 128, BN = 64, S = 2;
-      a.tiles_x = (N + BN - 1) / BN;
-      const int tiles = a.tiles_x * ((M + BM - 1) / BM);
-      const dim3 grid((unsigned)(tiles * a.splits)), fgrid((unsigned)tiles);
-      if (r <= 4) fwd_i8_kernel<BM, BN, S, 4, uint16_t, false, true, true><<<grid, 256, 0, st>>>(a);
-      else if (r <= 8) fwd_i8_kernel<BM, BN, S, 8, uint16_t, false, true, true><<<grid, 256, 0, st>>>(a);
-      else if (r <= 16) fwd_i8_kernel<BM, BN, S, 16, uint16_t, false, true, true><<<grid, 256, 0, st>>>(a);
-      else fwd_i8_kernel<BM, BN, S, 32, uint16_t, false, true, true><<<grid, 256, 0, st>>>(a);
-      if (r <= 4) fwd_fixup_aff_kernel<4, kMaxAffSplits><<<fgrid, 512, 0, st>>>(a);
-      else if (r <= 8) fwd_fixup_aff_kernel<8, kMaxAffSplits><<<fgrid, 512, 0, st>>>(a);
-      else if (r <= 16) fwd_fixup_aff_kernel<16, kMaxAffSplits><<<fgrid, 512, 0, st>>>(a);
-      else fwd_fixup_aff_kernel<32, kMaxAffSplits><<<fgrid, 512, 0, st>>>(a);
-      return;
-    }
+  if (epi != nullptr) {
+    a.epi = *epi;
+    launch_affine<true>(a, st);
+  } else {
+    launch_affine<false>(a, st);
   }
-  // the correction accumulators take registers: 64 x 64 (three stages) or
-  // 128 x 64 (two)
-  const long t64 = (long)((M + 63) / 64) * ((N + 63) / 64);
-  if (t64 <= 2 * kCUs) launch_tiles<64, 64, 3, uint16_t, false, true>(a, st);
-  else launch_tiles<128, 64, 2, uint16_t, false, true>(a, st);
 }
 
 }  // namespace qlora

@@ -22,6 +22,7 @@
 // multiplies one range of k and leaves its float32 accumulators in the
 // workspace, and a second launch adds them in split order and applies the
 // epilogue.
+#include "epilogue.hpp"
 #include "launch.hpp"
 #include "ring.hpp"
 
@@ -50,6 +51,7 @@ struct W4Args {
   // accumulator layout, the split count and stages of 64 k per split
   float* pacc;              // [splits, tiles, 4 waves, 16 fragments, 64 lanes] float4
   int splits, nks;
+  FwdEpi epi;               // EPI kernels: bias, activation, residual, saved z
 };
 
 constexpr int kMaxW4Splits = 8;
@@ -86,7 +88,7 @@ __device__ __forceinline__ u32x4 nibbles_bf16(uint32_t w, float sc) {
 // with no converted copy in LDS and no second barrier per stage. The
 // widening of one operand then overlaps the matrix work of the previous one
 // inside the wave.
-template <int BM, int S, int R, int G, bool SPLIT = false>
+template <int BM, int S, int R, int G, bool SPLIT = false, bool EPI = false>
 __global__ __launch_bounds__(256, 2) void fwd_w4_kernel(W4Args a) {
   static_assert(!SPLIT || BM == 128, "split contraction: 128-row tiles");
   constexpr int BN = 128, BK = 64;                 // k per stage: half a scale group
@@ -96,7 +98,9 @@ __global__ __launch_bounds__(256, 2) void fwd_w4_kernel(W4Args a) {
   // after the loop the ring holds the epilogue operands, then one output
   // staging strip per wave
   constexpr int EPB = (EpiOps<BM, BN, R, false>::kFloats * 4 + 15) / 16 * 16;
-  static_assert(EPB + 4 * epi_strip_bytes<uint16_t, FN>() <= S * STG, "epilogue fits");
+  constexpr int STRIP = EPI ? fused_strip_bytes<FN>() : epi_strip_bytes<uint16_t, FN>();
+  // (the scale slab behind the ring is free too once the loop is done)
+  static_assert(EPB + 4 * STRIP <= S * STG + BN * G * 2, "epilogue fits");
   const int K = a.K, M = a.M, N = a.N;
   const int ngrp = K / 128;
   static_assert(BN * G * 2 % 1024 == 0, "the scale slab takes whole 1 KB DMA instructions");
@@ -235,20 +239,24 @@ __global__ __launch_bounds__(256, 2) void fwd_w4_kernel(W4Args a) {
   __syncthreads();
   ep.store(E, M, N, m0, n0, a.r);
   __syncthreads();
-  epilogue_lowrank<BM, BN, R, false>(acc, E, M, N, m0, n0, 0, 32 * wid, a.s, a.y,
-                                     ring + EPB + wid * epi_strip_bytes<uint16_t, FN>());
+  if constexpr (EPI)
+    epilogue_fused<BM, BN, R, false>(acc, E, M, N, m0, n0, 0, 32 * wid, a.s, a.y, a.epi,
+                                     ring + EPB + wid * STRIP);
+  else
+    epilogue_lowrank<BM, BN, R, false>(acc, E, M, N, m0, n0, 0, 32 * wid, a.s, a.y,
+                                       ring + EPB + wid * STRIP);
 }
 
 // Second launch of the split contraction, one 512-thread block per 32-column
 // strip of a 128 x 128 tile (the strip one wave of the product kernel owns):
 // the partial sums added in split order, then the epilogue. Wave v takes the
 // strip's 16-row block v.
-template <int R, int NSPL>
+template <int R, int NSPL, bool EPI>
 __global__ __launch_bounds__(512) void fwd_w4_fixup_kernel(W4Args a) {
   constexpr int BM = 128, HN = 32, FM = 8, FN = 2;
   using Ep = EpiOps<BM, HN, R, false>;
   constexpr int EPB = (Ep::kFloats * 4 + 15) / 16 * 16;
-  constexpr int STRIP = epi_strip_bytes<uint16_t, FN>();
+  constexpr int STRIP = EPI ? fused_strip_bytes<FN>() : epi_strip_bytes<uint16_t, FN>();
   __shared__ __attribute__((aligned(1024))) int8_t lds[EPB + 8 * STRIP];
   float* E = reinterpret_cast<float*>(lds);
 
@@ -279,22 +287,26 @@ __global__ __launch_bounds__(512) void fwd_w4_fixup_kernel(W4Args a) {
   }
   if (tid < 256) ep.store(E, M, N, m0, n0, a.r);
   __syncthreads();
-  epilogue_lowrank<BM, HN, R, false>(acc, E, M, N, m0, n0, 16 * v, 0, a.s, a.y,
+  if constexpr (EPI)
+    epilogue_fused<BM, HN, R, false>(acc, E, M, N, m0, n0, 16 * v, 0, a.s, a.y, a.epi,
                                      lds + EPB + v * STRIP);
+  else
+    epilogue_lowrank<BM, HN, R, false>(acc, E, M, N, m0, n0, 16 * v, 0, a.s, a.y,
+                                       lds + EPB + v * STRIP);
 }
 
-template <int BM, int S, int G>
+template <int BM, int S, int G, bool EPI>
 void launch_tiles(W4Args a, hipStream_t st) {
   constexpr int BN = 128;
   a.tiles_x = (a.N + BN - 1) / BN;
   const dim3 grid((unsigned)(a.tiles_x * ((a.M + BM - 1) / BM)));
-  if (a.r <= 4) fwd_w4_kernel<BM, S, 4, G><<<grid, 256, 0, st>>>(a);
-  else if (a.r <= 8) fwd_w4_kernel<BM, S, 8, G><<<grid, 256, 0, st>>>(a);
-  else if (a.r <= 16) fwd_w4_kernel<BM, S, 16, G><<<grid, 256, 0, st>>>(a);
-  else fwd_w4_kernel<BM, S, 32, G><<<grid, 256, 0, st>>>(a);
+  if (a.r <= 4) fwd_w4_kernel<BM, S, 4, G, false, EPI><<<grid, 256, 0, st>>>(a);
+  else if (a.r <= 8) fwd_w4_kernel<BM, S, 8, G, false, EPI><<<grid, 256, 0, st>>>(a);
+  else if (a.r <= 16) fwd_w4_kernel<BM, S, 16, G, false, EPI><<<grid, 256, 0, st>>>(a);
+  else fwd_w4_kernel<BM, S, 32, G, false, EPI><<<grid, 256, 0, st>>>(a);
 }
 
-template <int S, int G>
+template <int S, int G, bool EPI>
 void launch_split_tiles(W4Args a, hipStream_t st) {
   constexpr int BM = 128, BN = 128;
   a.tiles_x = (a.N + BN - 1) / BN;
@@ -305,15 +317,15 @@ void launch_split_tiles(W4Args a, hipStream_t st) {
   else if (a.r <= 16) fwd_w4_kernel<BM, S, 16, G, true><<<grid, 256, 0, st>>>(a);
   else fwd_w4_kernel<BM, S, 32, G, true><<<grid, 256, 0, st>>>(a);
   if (a.splits <= 4) {
-    if (a.r <= 4) fwd_w4_fixup_kernel<4, 4><<<fgrid, 512, 0, st>>>(a);
-    else if (a.r <= 8) fwd_w4_fixup_kernel<8, 4><<<fgrid, 512, 0, st>>>(a);
-    else if (a.r <= 16) fwd_w4_fixup_kernel<16, 4><<<fgrid, 512, 0, st>>>(a);
-    else fwd_w4_fixup_kernel<32, 4><<<fgrid, 512, 0, st>>>(a);
+    if (a.r <= 4) fwd_w4_fixup_kernel<4, 4, EPI><<<fgrid, 512, 0, st>>>(a);
+    else if (a.r <= 8) fwd_w4_fixup_kernel<8, 4, EPI><<<fgrid, 512, 0, st>>>(a);
+    else if (a.r <= 16) fwd_w4_fixup_kernel<16, 4, EPI><<<fgrid, 512, 0, st>>>(a);
+    else fwd_w4_fixup_kernel<32, 4, EPI><<<fgrid, 512, 0, st>>>(a);
   } else {
-    if (a.r <= 4) fwd_w4_fixup_kernel<4, kMaxW4Splits><<<fgrid, 512, 0, st>>>(a);
-    else if (a.r <= 8) fwd_w4_fixup_kernel<8, kMaxW4Splits><<<fgrid, 512, 0, st>>>(a);
-    else if (a.r <= 16) fwd_w4_fixup_kernel<16, kMaxW4Splits><<<fgrid, 512, 0, st>>>(a);
-    else fwd_w4_fixup_kernel<32, kMaxW4Splits><<<fgrid, 512, 0, st>>>(a);
+    if (a.r <= 4) fwd_w4_fixup_kernel<4, kMaxW4Splits, EPI><<<fgrid, 512, 0, st>>>(a);
+    else if (a.r <= 8) fwd_w4_fixup_kernel<8, kMaxW4Splits, EPI><<<fgrid, 512, 0, st>>>(a);
+    else if (a.r <= 16) fwd_w4_fixup_kernel<16, kMaxW4Splits, EPI><<<fgrid, 512, 0, st>>>(a);
+    else fwd_w4_fixup_kernel<32, kMaxW4Splits, EPI><<<fgrid, 512, 0, st>>>(a);
   }
 }
 
@@ -332,18 +344,18 @@ void w4_split_plan(int M, int N, int K, int* splits, int* nks) {
 
 // Three ring slots where they fit beside the scale slab at two blocks per
 // compute unit (80 KB each), else two.
-template <int BM>
+template <int BM, bool EPI>
 void launch_groups(const W4Args& a, hipStream_t st) {
   const int ngrp = a.K / 128;                      // validated: <= kW4MaxGroups
   if (a.splits > 1) {
-    if (ngrp <= 8) launch_split_tiles<3, 8>(a, st);
-    else if (ngrp <= 32) launch_split_tiles<3, 32>(a, st);
-    else launch_split_tiles<2, kW4MaxGroups>(a, st);
+    if (ngrp <= 8) launch_split_tiles<3, 8, EPI>(a, st);
+    else if (ngrp <= 32) launch_split_tiles<3, 32, EPI>(a, st);
+    else launch_split_tiles<2, kW4MaxGroups, EPI>(a, st);
     return;
   }
-  if (ngrp <= 8) launch_tiles<BM, 3, 8>(a, st);
-  else if (ngrp <= 32) launch_tiles<BM, 3, 32>(a, st);
-  else launch_tiles<BM, BM == 128 ? 2 : 3, kW4MaxGroups>(a, st);
+  if (ngrp <= 8) launch_tiles<BM, 3, 8, EPI>(a, st);
+  else if (ngrp <= 32) launch_tiles<BM, 3, 32, EPI>(a, st);
+  else launch_tiles<BM, BM == 128 ? 2 : 3, kW4MaxGroups, EPI>(a, st);
 }
 
 }  // namespace
@@ -359,7 +371,7 @@ size_t fwd_w4_split_floats(int M, int N, int K) {
 void launch_gemm_fwd_w4(int M, int N, int K, const uint16_t* x,
                         const uint8_t* packed, const _Float16* scales,
                         const float* t, const float* B, int hd, int r, float s,
-                        uint16_t* y, float* pacc, hipStream_t st) {
+                        uint16_t* y, float* pacc, const FwdEpi* epi, hipStream_t st) {
   W4Args a{};
   a.M = M; a.N = N; a.K = K; a.x = x; a.packed = packed; a.scales = scales;
   a.t = t; a.B = B; a.hd = hd; a.r = r; a.s = s; a.y = y;
@@ -369,8 +381,16 @@ void launch_gemm_fwd_w4(int M, int N, int K, const uint16_t* x,
     a.pacc = pacc;
   }
   const long t128 = (long)((M + 127) / 128) * ((N + 127) / 128);
-  if (t128 >= kCUs || a.splits > 1) launch_groups<128>(a, st);
-  else launch_groups<64>(a, st);
+  const bool tall = t128 >= kCUs || a.splits > 1;
+  if (epi != nullptr) {
+    a.epi = *epi;
+    if (tall) launch_groups<128, true>(a, st);
+    else launch_groups<64, true>(a, st);
+  } else if (tall) {
+    launch_groups<128, false>(a, st);
+  } else {
+    launch_groups<64, false>(a, st);
+  }
 }
 
 }  // namespace qlora

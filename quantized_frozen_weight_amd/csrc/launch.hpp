@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "epilogue.hpp"
 #include "skinny.hpp"
 
 namespace qlora {
@@ -38,6 +39,8 @@ void launch_rowquant(int dtype, const void* x, int M, int K, const float* A,
 void launch_lora_down(int dtype, const void* x, int M, int K, const float* A,
                       int r, float* t, hipStream_t st, float* scratch = nullptr);
 
+// In the forward products below epi (NULL: none) adds the bias, activation,
+// residual and saved z of epilogue.hpp.
 // y = acc * sx[m] * sw[n] + s * t B   (acc_out != nullptr: write int32 acc).
 // Shapes with few output tiles and a long contraction split it when pacc is
 // given (fwd_split_ints(M, N, K, false) int32, 0 when the shape does not
@@ -46,7 +49,8 @@ size_t fwd_split_ints(int M, int N, int K, bool affine);
 void launch_gemm_fwd_w8(int dtype, int M, int N, int K, const int8_t* xq,
                         const int8_t* codes, const float* sx, const float* sw,
                         const float* t, const float* B, int hd, int r, float s,
-                        void* y, int32_t* acc_out, int32_t* pacc, hipStream_t st);
+                        void* y, int32_t* acc_out, int32_t* pacc, const FwdEpi* epi,
+                        hipStream_t st);
 // Outlier-compensated int8 weight (outlier.hpp) with int8 activations:
 // y = sx[m] (c acc + b' asum[m] + corr) + s t B (bf16 y). Split like the
 // int8 product when pacc and pcorr are given (fwd_split_ints(M, N, K, true)
@@ -54,7 +58,8 @@ void launch_gemm_fwd_w8(int dtype, int M, int N, int K, const int8_t* xq,
 void launch_gemm_fwd_w8o(int M, int N, int K, const int8_t* xq, const int8_t* codes,
                          const float* sx, const float* asum, const void* side,
                          const float* t, const float* B, int hd, int r, float s,
-                         uint16_t* y, int32_t* pacc, float* pcorr, hipStream_t st);
+                         uint16_t* y, int32_t* pacc, float* pcorr, const FwdEpi* epi,
+                         hipStream_t st);
 // 4-bit weights: the products hold the scales of up to this many 128-wide k
 // groups per block in LDS (K <= 16384).
 constexpr int kW4MaxGroups = 128;
@@ -69,11 +74,11 @@ size_t fwd_w4_split_floats(int M, int N, int K);
 void launch_gemm_fwd_a8w4(int M, int N, int K, const int8_t* xq, const float* sx,
                           const uint8_t* packed, const _Float16* scales,
                           const float* t, const float* B, int hd, int r, float s,
-                          uint16_t* y, hipStream_t st);
+                          uint16_t* y, const FwdEpi* epi, hipStream_t st);
 void launch_gemm_fwd_w4(int M, int N, int K, const uint16_t* x,
                         const uint8_t* packed, const _Float16* scales,
                         const float* t, const float* B, int hd, int r, float s,
-                        uint16_t* y, float* pacc, hipStream_t st);
+                        uint16_t* y, float* pacc, const FwdEpi* epi, hipStream_t st);
 
 // u = dy B^T (float32 [M, r]); if dys != nullptr also dys = bf16(dy * sw[n]).
 void launch_bwd_rows(int dtype, const void* dy, int M, int N, const float* B, int hd,
@@ -112,10 +117,27 @@ void launch_bwd_fused(int fmt, int M, int K, int N, const uint16_t* dy,
                       const void* codes, const void* scales, const float* B, int hd,
                       const float* A, const float* t, const uint16_t* x, int r,
                       float s, uint16_t* dx, float* partA, float* partB,
-                      float* pdx, float* pu, hipStream_t st);
-// dx = dy (codes * sw)^T + s u A^T in float32
+                      float* pdx, float* pu, hipStream_t st, const int8_t* xq = nullptr,
+                      const float* sx = nullptr, const GradEpi* ge = nullptr);
+// (ge not NULL: the kernels' extended form, in which x is the row checkpoint
+// xq, sx where xq is not NULL, and dx goes through ge)
+// dx = dy (codes * sw)^T + s u A^T in float32 (ge: as above)
 void launch_gemm_dx_f32(int M, int K, int N, const float* dy,
                         const int8_t* codes, const float* sw, const float* u,
                         const float* A, int r, float s, float* dx,
-                        hipStream_t st);
+                        hipStream_t st, const GradEpi* ge = nullptr);
+
+// The 8-bit forms of an activation [M, C] (cfmt 0: rows, 1: groups of 32
+// columns), and its gradient alone.
+void launch_ckpt_write_groups(int dtype, const void* x, int M, int C, int8_t* codes,
+                              uint8_t* scales, hipStream_t st);
+void launch_ckpt_read(int dtype, int cfmt, const int8_t* codes, const void* scales, int M, int C,
+                      void* x, hipStream_t st);
+// asum[m] = sum of row m of codes [M, K] (float32, exact)
+void launch_code_sums(const int8_t* codes, int M, int K, float* asum, hipStream_t st);
+// dz = dy act'(z) (dz may be NULL, or dy), dbias = its column sums in float32
+// (NULL: none; partial then unused). partial: act_bwd_floats(M, C) floats.
+size_t act_bwd_floats(int M, int C);
+void launch_act_bwd(int dtype, int M, int C, const void* dy, const GradEpi& ge, void* dz,
+                    float* dbias, float* partial, hipStream_t st);
 }  // namespace qlora

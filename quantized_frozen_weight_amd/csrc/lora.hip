@@ -8,10 +8,10 @@ namespace qlora {
 
 namespace {
 
-template <typename T, int R>
+template <typename T, int R, bool X8>
 __global__ __launch_bounds__(256) void skinny_stage1_kernel(SkinnyJobs p) {
   __shared__ float red[4 * (R < 4 ? R : 4) * kSkCols];
-  skinny_partial_block<T, R>(p, blockIdx.x, red);
+  skinny_partial_block<T, R, X8>(p, blockIdx.x, red);
 }
 
 // out = s * sum over splits (split order fixed); one thread per (job, j, c),
@@ -86,15 +86,15 @@ __global__ __launch_bounds__(256) void finish_batch_kernel(FinishBatch fb) {
   stage2_elem<NS, Stage2Job>(fb.job[i], (long)(b - fb.bstart[i]) * 256 + threadIdx.x);
 }
 
-template <typename T>
+template <typename T, bool X8>
 void stage1_dispatch(const SkinnyJobs& p, hipStream_t st) {
   const int r = p.r, blocks = p.blocks();
-  if (r <= 1) skinny_stage1_kernel<T, 1><<<blocks, 256, 0, st>>>(p);
-  else if (r <= 2) skinny_stage1_kernel<T, 2><<<blocks, 256, 0, st>>>(p);
-  else if (r <= 4) skinny_stage1_kernel<T, 4><<<blocks, 256, 0, st>>>(p);
-  else if (r <= 8) skinny_stage1_kernel<T, 8><<<blocks, 256, 0, st>>>(p);
-  else if (r <= 16) skinny_stage1_kernel<T, 16><<<blocks, 256, 0, st>>>(p);
-  else skinny_stage1_kernel<T, 32><<<blocks, 256, 0, st>>>(p);
+  if (r <= 1) skinny_stage1_kernel<T, 1, X8><<<blocks, 256, 0, st>>>(p);
+  else if (r <= 2) skinny_stage1_kernel<T, 2, X8><<<blocks, 256, 0, st>>>(p);
+  else if (r <= 4) skinny_stage1_kernel<T, 4, X8><<<blocks, 256, 0, st>>>(p);
+  else if (r <= 8) skinny_stage1_kernel<T, 8, X8><<<blocks, 256, 0, st>>>(p);
+  else if (r <= 16) skinny_stage1_kernel<T, 16, X8><<<blocks, 256, 0, st>>>(p);
+  else skinny_stage1_kernel<T, 32, X8><<<blocks, 256, 0, st>>>(p);
 }
 
 }  // namespace
@@ -117,8 +117,14 @@ SkinnyJobs make_adapter_grad_jobs(int M, int r, float s, const float* t,
 }
 
 void launch_skinny_stage1(int dtype, const SkinnyJobs& p, hipStream_t st) {
-  if (dtype == 0) stage1_dispatch<F32>(p, st);
-  else stage1_dispatch<BF16>(p, st);
+  if (p.sx != nullptr) {
+    if (dtype == 0) stage1_dispatch<F32, true>(p, st);
+    else stage1_dispatch<BF16, true>(p, st);
+  } else if (dtype == 0) {
+    stage1_dispatch<F32, false>(p, st);
+  } else {
+    stage1_dispatch<BF16, false>(p, st);
+  }
 }
 
 namespace {

@@ -33,6 +33,7 @@ struct SkinnyJobs {
   int transpose[2];
   int hd0;             // job 0's output (dB): head width ([heads, r, hd]; C[0]: [r, C])
   int njobs, M, r, nsplit, rows_per_split;
+  const float* sx;     // X8 stage 1: scales of the rows of job 1's int8 Q
   float s;
   int blocks() const { return (ncb[0] + (njobs > 1 ? ncb[1] : 0)) * nsplit; }
 };
@@ -52,9 +53,17 @@ __device__ __forceinline__ void sk_load4(const uint16_t* p, float q[4]) {
   q[2] = __uint_as_float(v.y << 16); q[3] = __uint_as_float(v.y & 0xffff0000u);
 }
 
+__device__ __forceinline__ void sk_load4(const int8_t* p, float q[4]) {
+  const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = (float)(int8_t)(v >> (8 * i));
+}
+
 // Stage 1 for block b of the skinny grid. Needs 4 * min(R, 4) * 256 floats of
 // LDS at red (and two barriers of the whole block).
-template <typename T, int R>
+// X8: job 1's Q is int8 codes with row scales (p.sx), read at a quarter or half
+// the bytes; the scale goes into the P row in float32.
+template <typename T, int R, bool X8 = false>
 __device__ __forceinline__ void skinny_partial_block(const SkinnyJobs& p, int b,
                                                      float* red) {
   constexpr int JC = R < 4 ? R : 4;
@@ -65,6 +74,7 @@ __device__ __forceinline__ void skinny_partial_block(const SkinnyJobs& p, int b,
   const int cb = b % ncb, sp = b / ncb;
   const float* __restrict__ P = p.P[job];
   const auto* __restrict__ Q = reinterpret_cast<const typename Elem<T>::type*>(p.Q[job]);
+  const bool q8 = X8 && job == 1;                // block-uniform
   const int c0 = cb * kSkCols + 4 * lane;
   const bool col_ok = c0 < C;                // C % 16 == 0: 4 columns all in or out
 
@@ -86,9 +96,15 @@ __device__ __forceinline__ void skinny_partial_block(const SkinnyJobs& p, int b,
     for (int g = 0; g < kSkGroup; ++g) {
       const int m = g0 + g;
       const int mc = m < m1 ? m : m0;
-      sk_load4(Q + (long)mc * C + cc0, q[g]);
+      if (q8) sk_load4(reinterpret_cast<const int8_t*>(Q) + (long)mc * C + cc0, q[g]);
+      else sk_load4(Q + (long)mc * C + cc0, q[g]);
 #pragma unroll
       for (int j = 0; j < R; ++j) pv[g][j] = P[(long)mc * r + (j < r ? j : 0)];
+      if (q8) {
+        const float rs = p.sx[mc];
+#pragma unroll
+        for (int j = 0; j < R; ++j) pv[g][j] *= rs;
+      }
     }
 #pragma unroll
     for (int g = 0; g < kSkGroup; ++g) {
