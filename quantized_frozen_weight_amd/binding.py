@@ -9,6 +9,7 @@ If libqlora.so is missing, every call raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional, Tuple
@@ -192,7 +193,11 @@ def _ptr(t) -> Optional[int]:
 
 
 def _stream() -> int:
+    """The current device's current stream."""
     import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None:            # the handle without a Stream object around it
+        return raw(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -506,36 +511,47 @@ class Checkpoint:
         return self.codes.shape
 
 
+class _here:
+    """Context that changes nothing: the device is the current one."""
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _here()
+
+
 def _on(device):
     """Context in which `device` is the current one."""
-    import contextlib
-
     import torch
     if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _HERE
     return torch.cuda.device(device)
 
 
 def _tensor(t, what: str, shape, dtype, device):
     """t, checked to be a dense tensor of this shape, type and device."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t
     if t.dtype != dtype:
         raise TypeError(f"{what}: {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{what}: on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: not contiguous")
-    return t
+    raise ValueError(f"{what}: not contiguous")
 
 
 def _rows(x, what: str, columns=None):
     """(M, C, dtype code) of a dense [M, C] activation on a GPU."""
-    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+    shape = x.shape
+    if len(shape) != 2 or not x.is_cuda or not x.is_contiguous():
         raise ValueError(f"{what}: a contiguous 2-D GPU tensor is needed")
-    if columns is not None and x.shape[1] != columns:
-        raise ValueError(f"{what}: {x.shape[1]} columns, expected {columns}")
-    return x.shape[0], x.shape[1], _dtype_code(x)
+    if columns is not None and shape[1] != columns:
+        raise ValueError(f"{what}: {shape[1]} columns, expected {columns}")
+    return shape[0], shape[1], _dtype_code(x)
 
 
 def _ckpt(c, what: str, fmt: str, shape, device) -> Checkpoint:
@@ -564,7 +580,7 @@ def _new_ckpt(M: int, C: int, fmt: str, device) -> Checkpoint:
 
 def _layer_on(layer: QLinear, device) -> qlora_linear:
     import torch
-    for t, what in ((layer.codes, "codes"), (layer.scales, "scales"), (layer.A, "A"), (layer.B, "B")):
+    for t, what in ((layer.codes, "codes"), (layer.scales, "scales")):
         if t.device != device:
             raise ValueError(f"layer {what} on {t.device}, the activations on {device}")
     _tensor(layer.A, "layer A", (layer.K, layer.r), torch.float32, device)
@@ -576,6 +592,34 @@ def _act(act: str) -> int:
     if act not in _ACT:
         raise ValueError(f"unknown activation {act!r}")
     return _ACT[act]
+
+
+@functools.lru_cache(maxsize=4096)
+def _sizes(query: str, K: int, N: int, r: int, fmt: int, heads: int, M: int, dtype: int) -> int:
+    """A workspace query's answer for these sizes (host arithmetic alone; the
+    pointers only have to pass its checks)."""
+    n = ctypes.c_size_t()
+    s = qlora_linear(K, N, r, 1.0, fmt, 256, 256, 256, 256, heads)
+    _check(getattr(lib(), query)(ctypes.byref(s), M, dtype, ctypes.byref(n)), query)
+    return n.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _act_bwd_bytes(M: int, N: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().qlora_act_bwd_workspace(M, N, ctypes.byref(n)), "qlora_act_bwd_workspace")
+    return n.value
+
+
+def _scratch(query: str, cs: qlora_linear, M: int, dtype: int, device, ws):
+    """The caller's workspace, or a new one of the queried size."""
+    import torch
+    if ws is not None:
+        if ws.device != device or not ws.is_contiguous():
+            raise ValueError(f"ws: a contiguous tensor on {device} is needed")
+        return ws
+    n = _sizes(query, cs.K, cs.N, cs.r, cs.fmt, cs.heads, M, dtype)
+    return torch.empty((max(n, 256),), dtype=torch.uint8, device=device)
 
 
 def qlora_ckpt_write(x, fmt: str = "c8row", out: Optional[Checkpoint] = None) -> Checkpoint:
@@ -649,7 +693,7 @@ def qlora_fwd_epi(layer: QLinear, x, act: str = "none", bias=None, residual=None
     else:
         xc = None
     e, z = _epilogue(layer, M, x.dtype, dev, act, bias, residual, save_z, z, xc)
-    ws = _workspace(qlora_fwd_workspace(layer, M, dt), dev, ws)
+    ws = _scratch("qlora_fwd_workspace", cs, M, dt, dev, ws)
     with _on(dev):
         _check(lib().qlora_fwd_epi(ctypes.byref(cs), M, dt, _ptr(x), ctypes.byref(e), _ptr(y),
                                    _ptr(t) if save_t else None, _ptr(ws),
@@ -672,7 +716,7 @@ def qlora_fwd_ckpt(layer: QLinear, xc: Checkpoint, t, dtype, act: str = "none", 
         _tensor(y, "y", (M, layer.N), dtype, dev)
     dt = _dtype_code(y)
     e, z = _epilogue(layer, M, dtype, dev, act, bias, residual, save_z, z, None)
-    ws = _workspace(qlora_fwd_workspace(layer, M, dt), dev, ws)
+    ws = _scratch("qlora_fwd_workspace", cs, M, dt, dev, ws)
     with _on(dev):
         _check(lib().qlora_fwd_ckpt(ctypes.byref(cs), M, dt, _ptr(xc.codes), _ptr(xc.scales), _ptr(t),
                                     ctypes.byref(e), _ptr(y), _ptr(ws), ws.numel() * ws.element_size(),
@@ -726,7 +770,7 @@ def qlora_bwd_epi(layer: QLinear, x, dy, t=None, act: str = "none", z=None, add=
         _tensor(dA, "dA", (layer.K, layer.r), torch.float32, dev)
     dB = torch.empty(_b_shape(layer), dtype=torch.float32, device=dev) if dB is None else \
         _tensor(dB, "dB", _b_shape(layer), torch.float32, dev)
-    ws = _workspace(qlora_bwd_workspace(layer, M, dt), dev, ws)
+    ws = _scratch("qlora_bwd_workspace", cs, M, dt, dev, ws)
     with _on(dev):
         _check(lib().qlora_bwd_epi(ctypes.byref(cs), M, dt, *args, _ptr(dA), _ptr(dB), _ptr(ws),
                                    ws.numel() * ws.element_size(), _stream()), "qlora_bwd_epi")
@@ -738,7 +782,7 @@ def qlora_bwd_epi_partial(layer: QLinear, x, dy, t=None, act: str = "none", z=No
     """First half of qlora_bwd_epi: (dx or None, workspace), the adapter
     gradients left to qlora_bwd_finish or qlora_bwd_finish_batch."""
     cs, M, dt, dev, args, dx, _keep = _bwd_epi_args(layer, x, dy, t, act, z, add, need_dx, dx)
-    ws = _workspace(qlora_bwd_workspace(layer, M, dt), dev, ws)
+    ws = _scratch("qlora_bwd_workspace", cs, M, dt, dev, ws)
     with _on(dev):
         _check(lib().qlora_bwd_epi_partial(ctypes.byref(cs), M, dt, *args, _ptr(ws),
                                            ws.numel() * ws.element_size(), _stream()),
@@ -767,11 +811,13 @@ def qlora_act_bwd(act: str, dy, z=None, need_dz: bool = True, need_dbias: bool =
     if need_dbias:
         dbias = torch.empty((N,), dtype=torch.float32, device=dev) if dbias is None else \
             _tensor(dbias, "dbias", (N,), torch.float32, dev)
-        n = ctypes.c_size_t()
-        _check(lib().qlora_act_bwd_workspace(M, N, ctypes.byref(n)), "qlora_act_bwd_workspace")
-        ws = _workspace(n.value, dev, ws)
+        if ws is None:
+            need = _act_bwd_bytes(M, N)
+            ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+        elif ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws: a contiguous tensor on {dev} is needed")
     else:
-        dbias = None
+        dbias = ws = None
     with _on(dev):
         _check(lib().qlora_act_bwd(_act(act), M, N, dt, _ptr(dy), zp, zc, zs, _ptr(dz), _ptr(dbias),
                                    _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),

@@ -71,7 +71,7 @@ inline float lora_s(const qlora_linear* L) {
 }
 
 struct FwdLayout {
-  size_t xq, sx, t, asum, pacc, pcorr, rs, total;
+  size_t xq, sx, t, asum, pacc, pcorr, rs, few, total;
 };
 FwdLayout fwd_layout(const qlora_linear* L, int M) {
   FwdLayout w{};
@@ -93,6 +93,8 @@ FwdLayout fwd_layout(const qlora_linear* L, int M) {
   w.pcorr = off; off = align_up(off + (w8o ? nsplit * 4 : 0));
   // the row pass of long rows split over k (0 bytes for other widths)
   w.rs = off; off = align_up(off + row_split_floats(M, L->K, L->r) * 4);
+  // the few-row forward's slices of t (0 bytes past four rows)
+  w.few = off; off = align_up(off + fwd_few_floats(M, L->K) * 4);
   w.total = off;
   return w;
 }
@@ -774,6 +776,12 @@ int qlora_fwd_epi(const qlora_linear* L, int M, int dtype, const void* x,
   float* sx = e->x_scales ? e->x_scales : reinterpret_cast<float*>(at(ws, w.sx));
   float* rs = reinterpret_cast<float*>(at(ws, w.rs));
   if (pending_error()) return QLORA_EHIP;
+  if (fwd_few_takes(L->fmt, M, K, N, L->r)) {
+    launch_fwd_few(dtype, L->fmt, M, N, K, x, L->codes, L->scales, L->A, L->B, head_width(L), L->r,
+                   lora_s(L), epi, y, t_save, e->x_codes, e->x_scales,
+                   reinterpret_cast<float*>(at(ws, w.few)), s);
+    return launch_status();
+  }
   if (L->fmt == QLORA_W4G128) {
     // the product takes x itself; its codes are made only where they are kept
     if (e->x_codes)

@@ -24,6 +24,8 @@ namespace {
 // ---------------------------------------------------------------------------
 constexpr int kT = 32, kS = 128;
 
+struct NoEpi {};
+
 // EXT: dx goes through the gradient epilogue (epilogue.hpp), one value at a
 // time.
 template <bool EXT>
@@ -31,7 +33,8 @@ __global__ __launch_bounds__(256) void gemm_dx_f32_kernel(
     int M, int K, int N, const float* __restrict__ dy,
     const int8_t* __restrict__ codes, const float* __restrict__ sw,
     const float* __restrict__ u, const float* __restrict__ A, int r, float s,
-    float* __restrict__ dx, GradEpi ge) {
+    float* __restrict__ dx,
+    typename std::conditional<EXT, GradEpi, NoEpi>::type ge) {
   __shared__ float Ds[kS][kT + 1];   // [n][m]
   __shared__ float Ws[kS][kT + 1];   // [n][k]
   const int tid = threadIdx.x;
@@ -131,7 +134,7 @@ void launch_gemm_dx_f32(int M, int K, int N, const float* dy,
   if (ge != nullptr)
     gemm_dx_f32_kernel<true><<<grid, 256, 0, st>>>(M, K, N, dy, codes, sw, u, A, r, s, dx, *ge);
   else
-    gemm_dx_f32_kernel<false><<<grid, 256, 0, st>>>(M, K, N, dy, codes, sw, u, A, r, s, dx, GradEpi{});
+    gemm_dx_f32_kernel<false><<<grid, 256, 0, st>>>(M, K, N, dy, codes, sw, u, A, r, s, dx, NoEpi{});
 }
 
 }  // namespace qlora

@@ -163,19 +163,19 @@ __device__ __forceinline__ int group_byte(uint32_t amax_bits) {
   return b < 1 ? 1 : b;
 }
 
+// The code of v under scale byte b (255: none).
+__device__ __forceinline__ int8_t group_code(float v, int b) {
+  if (b == 255) return 0;
+  // 2^-e = 2^(127 - b); b in [1, 249]
+  const int q = (int)__builtin_rintf(v * __uint_as_float((uint32_t)(254 - b) << 23));
+  return (int8_t)(q != 0 ? q : v > 0.f ? 1 : v < 0.f ? -1 : 0);
+}
+
 // Eight values as codes of scale byte b, packed four to a word.
 __device__ __forceinline__ u32x2 group_codes(const float (&v)[8], int b) {
-  // 2^-e = 2^(127 - b); b in [1, 249]
-  const float inv = __uint_as_float((uint32_t)(254 - b) << 23);
   uint32_t w[2] = {0u, 0u};
-  if (b != 255) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      int q = (int)__builtin_rintf(v[e] * inv);
-      if (q == 0) q = v[e] > 0.f ? 1 : v[e] < 0.f ? -1 : 0;
-      w[e >> 2] |= (uint32_t)(q & 0xff) << (8 * (e & 3));
-    }
-  }
+  for (int e = 0; e < 8; ++e) w[e >> 2] |= (uint32_t)(uint8_t)group_code(v[e], b) << (8 * (e & 3));
   return u32x2{w[0], w[1]};
 }
 
@@ -191,14 +191,49 @@ __device__ __forceinline__ void group_values(u32x2 c, int b, float (&v)[8]) {
 }
 
 // ---- eight values of a row in either dtype ------------------------------------
+typedef float f32x2v __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+
+// two floats to bfloat16, round to nearest even (v_cvt_pk_bf16_f32)
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2v{lo, hi}, bf16x2v));
+}
+
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
   *reinterpret_cast<f32x4*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
 }
 __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
-  *reinterpret_cast<u32x4*>(p) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+  *reinterpret_cast<u32x4*>(p) = u32x4{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
+                                       cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7])};
 }
+
+// eight values as loaded: 16 bytes of bf16, 32 of float32
+template <typename OutT> struct Raw8;
+template <> struct Raw8<uint16_t> {
+  u32x4 v;
+  __device__ __forceinline__ void load(const void* p, long at) {
+    v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at);
+  }
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      o[2 * i] = __uint_as_float(v[i] << 16);
+      o[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+    }
+  }
+};
+template <> struct Raw8<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const void* p, long at) {
+    a = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at);
+    b = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + at + 4);
+  }
+  __device__ __forceinline__ void get(float (&o)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { o[i] = a[i]; o[4 + i] = b[i]; }
+  }
+};
 
 // The forward epilogue of a call (pointers NULL where unused).
 struct FwdEpi {
@@ -225,13 +260,22 @@ struct GradEpi {
 // each padded by 16 bytes.
 template <int FN> constexpr int fused_strip_bytes() { return 16 * (FN * 64 + 16); }
 
+// What a piece of 8 outputs needs besides the product, as loaded.
+template <typename OutT> struct Side {
+  Raw8<OutT> r;      // residual, or add
+  Raw8<OutT> z;      // backward: dense z, or its codes in z's first 8 bytes
+  int b;             // scale byte of the codes
+};
+
 // epilogue_lowrank (ring.hpp) with the rest of the layer behind it. One
 // 16-row strip of the wave's outputs at a time goes through LDS in float32,
 // so that a lane then holds 8 consecutive columns of a row: every operand
 // (residual, saved z, codes) moves in 16- or 8-byte pieces, the activation
 // sees the unrounded z, four neighbouring lanes hold one 32-column group,
-// and y is rounded once. The operands of a strip are fetched before its
-// low-rank product, which hides part of their latency.
+// and y is rounded once. What bounds it is the latency of the side operands
+// (two or three waves per SIMD): in bfloat16 all strips' are fetched before
+// the first strip is formed, in float32 (twice the registers) one strip
+// ahead.
 template <int BM, int BN, int R, bool SCALED, bool AFF = false, typename OutT, typename Epi,
           typename AccT, int FM, int FN>
 __device__ __forceinline__ void epilogue_fused(const AccT (&acc)[FM][FN], const float* E, int M,
@@ -249,36 +293,56 @@ __device__ __forceinline__ void epilogue_fused(const AccT (&acc)[FM][FN], const 
   constexpr int CPR = 2 * FN;                 // 8-column pieces per strip row
   constexpr int PN = CPR * 16 / 64;           // pieces per lane and strip
   static_assert(CPR % 4 == 0, "four neighbouring lanes hold one 32-column group");
+  constexpr int AHEAD = sizeof(OutT) == 2 ? FM : 2;        // strips whose operands are held
+  constexpr int NB = 64 % CPR == 0 ? 1 : PN;               // distinct column pieces of a lane
 
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    // the strip's side operands
-    float side[PN][8], aux[PN][8];             // residual or add; z (backward)
-    bool live[PN];
-    int pm[PN], pn[PN];
+  Side<OutT> side[AHEAD][PN];
+  // output position of piece p of strip i (clamped to 0 where not live)
+  auto place = [&](int i, int p, int& m, int& n) {
+    const int q = lane + 64 * p;
+    m = m0 + wr0 + i * 16 + q / CPR;
+    n = n0 + wc0 + (q % CPR) * 8;
+    return m < M && n < N;                                 // N % 16 == 0: 8 columns in or out
+  };
+  auto fetch = [&](int i) {
 #pragma unroll
     for (int p = 0; p < PN; ++p) {
-      const int q = lane + 64 * p;
-      pm[p] = m0 + wr0 + i * 16 + q / CPR;
-      pn[p] = n0 + wc0 + (q % CPR) * 8;
-      live[p] = pm[p] < M && pn[p] < N;        // N % 16 == 0: 8 columns in or out
-      const long at = live[p] ? (long)pm[p] * N + pn[p] : 0;
+      int m, n;
+      const bool live = place(i, p, m, n);
+      const long at = live ? (long)m * N + n : 0;
+      Side<OutT>& sd = side[i % AHEAD][p];
       if constexpr (GRAD) {
-        if (ep.add != nullptr) load8(static_cast<const OutT*>(ep.add) + at, side[p]);
         if (ep.act.kind != 0) {
           if (ep.zc != nullptr) {
             const u32x2 c = *reinterpret_cast<const u32x2*>(ep.zc + at);
-            const int b = ep.zs[live[p] ? (long)pm[p] * ep.zg + pn[p] / kGroup : 0];
-            group_values(c, b, aux[p]);
+            sd.z.v[0] = c[0];
+            sd.z.v[1] = c[1];
+            sd.b = ep.zs[live ? (long)m * ep.zg + n / kGroup : 0];
           } else {
-            load8(static_cast<const OutT*>(ep.z) + at, aux[p]);
+            sd.z.load(ep.z, at);
           }
         }
+        if (ep.add != nullptr) sd.r.load(ep.add, at);
       } else {
-        if (ep.res != nullptr) load8(static_cast<const OutT*>(ep.res) + at, side[p]);
-        if (ep.bias != nullptr) load8(ep.bias + (live[p] ? pn[p] : 0), aux[p]);
+        if (ep.res != nullptr) sd.r.load(ep.res, at);
       }
     }
+  };
+  float bias[NB][8];
+  if constexpr (!GRAD) {
+    if (ep.bias != nullptr) {
+#pragma unroll
+      for (int p = 0; p < NB; ++p) {
+        const int n = n0 + wc0 + ((lane + 64 * p) % CPR) * 8;
+        load8(ep.bias + (n < N ? n : 0), bias[p]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < AHEAD && i < FM; ++i) fetch(i);
+
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
     f32x4 low[FN];
 #pragma unroll
     for (int jn = 0; jn < FN; ++jn) low[jn] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -312,39 +376,49 @@ __device__ __forceinline__ void epilogue_fused(const AccT (&acc)[FM][FN], const 
 #pragma unroll
     for (int p = 0; p < PN; ++p) {
       const int q = lane + 64 * p;
-      float v[8];
+      int m, n;
+      const bool live = place(i, p, m, n);
+      const long at = (long)m * N + n;
+      const Side<OutT>& sd = side[i % AHEAD][p];
+      float v[8], w[8];
       load8(reinterpret_cast<const float*>(strip + (q / CPR) * PITCH + (q % CPR) * 32), v);
-      const long at = (long)pm[p] * N + pn[p];
       if constexpr (GRAD) {
-        act_slope_mul(ep.act, aux[p], v);
+        if (ep.act.kind != 0) {
+          if (ep.zc != nullptr) group_values(u32x2{sd.z.v[0], sd.z.v[1]}, sd.b, w);
+          else sd.z.get(w);
+          act_slope_mul(ep.act, w, v);
+        }
         if (ep.add != nullptr) {
+          sd.r.get(w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += side[p][e];
+          for (int e = 0; e < 8; ++e) v[e] += w[e];
         }
       } else {
         if (ep.bias != nullptr) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += aux[p][e];
+          for (int e = 0; e < 8; ++e) v[e] += bias[p % NB][e];
         }
-        if (ep.z != nullptr && live[p]) store8(static_cast<OutT*>(ep.z) + at, v);
+        if (ep.z != nullptr && live) store8(static_cast<OutT*>(ep.z) + at, v);
         if (ep.zc != nullptr) {
-          uint32_t m = 0;
+          uint32_t t = 0;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) { const uint32_t b = abs_bits(v[e]); m = b > m ? b : m; }
-          const int b = group_byte(quad_max_u32(live[p] ? m : 0u));
-          if (live[p]) {
+          for (int e = 0; e < 8; ++e) { const uint32_t b = abs_bits(v[e]); t = b > t ? b : t; }
+          const int b = group_byte(quad_max_u32(live ? t : 0u));
+          if (live) {
             *reinterpret_cast<u32x2*>(ep.zc + at) = group_codes(v, b);
-            if (pn[p] % kGroup == 0) ep.zs[(long)pm[p] * ep.zg + pn[p] / kGroup] = (uint8_t)b;
+            if (n % kGroup == 0) ep.zs[(long)m * ep.zg + n / kGroup] = (uint8_t)b;
           }
         }
         act_apply(ep.act, v);
         if (ep.res != nullptr) {
+          sd.r.get(w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += side[p][e];
+          for (int e = 0; e < 8; ++e) v[e] += w[e];
         }
       }
-      if (live[p]) store8(out + at, v);
+      if (live) store8(out + at, v);
     }
+    if (i + AHEAD < FM) fetch(i + AHEAD);
   }
 }
 

@@ -46,8 +46,13 @@ struct A8W4Args {
   float s;
   uint16_t* y;              // [M, N] bf16
   int tiles_x;
-  FwdEpi epi;               // EPI kernels: bias, activation, residual, saved z
 };
+
+// EPI kernels: bias, activation, residual, saved z besides.
+struct A8W4EpiArgs : A8W4Args {
+  FwdEpi epi;
+};
+template <bool EPI> using A8W4ArgsOf = typename std::conditional<EPI, A8W4EpiArgs, A8W4Args>::type;
 
 // Sixteen consecutive 4-bit codes (8 bytes, the even k in each low nibble)
 // as sixteen int8 values in k order.
@@ -67,7 +72,7 @@ __device__ __forceinline__ i32x4 widen_nibbles(u32x2 w) {
 
 // G: the largest number of 128-wide k groups the block's scale slab holds.
 template <int BM, int BN, int S, int R, int G, bool EPI>
-__global__ __launch_bounds__(256) void fwd_a8w4_kernel(A8W4Args a) {
+__global__ __launch_bounds__(256) void fwd_a8w4_kernel(A8W4ArgsOf<EPI> a) {
   constexpr int BK = 128;                          // k per stage = one scale group
   constexpr int ASZ = BM * 128, BSZ = BN * 64, STG = ASZ + BSZ;
   constexpr int AI = BM / 32, BI = BN / 64, LPS = AI + BI;   // DMA per wave per stage
@@ -208,7 +213,7 @@ __global__ __launch_bounds__(256) void fwd_a8w4_kernel(A8W4Args a) {
 }
 
 template <int BM, int S, int G, bool EPI>
-void launch_tiles(A8W4Args a, hipStream_t st) {
+void launch_tiles(A8W4ArgsOf<EPI> a, hipStream_t st) {
   constexpr int BN = 128;
   a.tiles_x = (a.N + BN - 1) / BN;
   const dim3 grid((unsigned)(a.tiles_x * ((a.M + BM - 1) / BM)));
@@ -219,7 +224,7 @@ void launch_tiles(A8W4Args a, hipStream_t st) {
 }
 
 template <int BM, int S, bool EPI>
-void launch_groups(const A8W4Args& a, hipStream_t st) {
+void launch_groups(const A8W4ArgsOf<EPI>& a, hipStream_t st) {
   const int ngrp = a.K / 128;                      // validated: <= kW4MaxGroups
   if (ngrp <= 8) launch_tiles<BM, S, 8, EPI>(a, st);
   else if (ngrp <= 32) launch_tiles<BM, S, 32, EPI>(a, st);
@@ -237,9 +242,9 @@ void launch_gemm_fwd_a8w4(int M, int N, int K, const int8_t* xq, const float* sx
   a.t = t; a.B = B; a.hd = hd; a.r = r; a.s = s; a.y = y;
   const long t128 = (long)((M + 127) / 128) * ((N + 127) / 128);
   if (epi != nullptr) {
-    a.epi = *epi;
-    if (t128 >= kCUs) launch_groups<128, 2, true>(a, st);
-    else launch_groups<64, 3, true>(a, st);
+    const A8W4EpiArgs ea{a, *epi};
+    if (t128 >= kCUs) launch_groups<128, 2, true>(ea, st);
+    else launch_groups<64, 3, true>(ea, st);
   } else if (t128 >= kCUs) {
     launch_groups<128, 2, false>(a, st);
   } else {

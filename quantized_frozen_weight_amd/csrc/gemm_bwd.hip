@@ -109,12 +109,21 @@ struct BwdArgs {
   float* pdx;              // [splits, tiles, 4 waves, 16 fragments, 64 lanes] float4
   float* pu;               // [splits, M, r]
   int splits, nks;
-  // EXT kernels: x as its 8-bit row checkpoint where xq is not NULL (x is
-  // then unused), and the gradient epilogue
+};
+
+// EXT kernels: x as its 8-bit row checkpoint where xq is not NULL (x is then
+// unused), and the gradient epilogue. (A type of its own, so that the other
+// launches do not carry these arguments.)
+struct BwdExtArgs : BwdArgs {
   const int8_t* xq;        // [M, K]
   const float* sx;         // [M]
   GradEpi ge;
 };
+template <bool EXT> using BwdArgsOf = typename std::conditional<EXT, BwdExtArgs, BwdArgs>::type;
+__device__ __forceinline__ const int8_t* x8_codes(const BwdArgs&) { return nullptr; }
+__device__ __forceinline__ const int8_t* x8_codes(const BwdExtArgs& a) { return a.xq; }
+__device__ __forceinline__ const float* x8_scales(const BwdArgs&) { return nullptr; }
+__device__ __forceinline__ const float* x8_scales(const BwdExtArgs& a) { return a.sx; }
 
 __device__ __forceinline__ uint32_t pk_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
@@ -336,7 +345,7 @@ constexpr int kBresN = 1024;
 
 template <bool W4, int BM, int BN, int S, int R, bool AFF = false, bool BRES = false,
           bool EXT = false>
-__global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgs a) {
+__global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgsOf<EXT> a) {
   constexpr int KC = 64;                              // n per stage
   constexpr int RB = W4 ? BN / 2 : BN;                // code bytes per row of n
   static_assert(!AFF || (!W4 && BN == 64 && KC == kW8OBwdCellN), "affine: int8, 64 x 64 cells");
@@ -692,7 +701,7 @@ __global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgs a) {
     }
     X8Tile<BM, BN> x8;
     if constexpr (XPRE) {
-      if (EXT && a.xq != nullptr) x8.fetch(a.xq, M, K, m0, k0, ptid);
+      if (x8_codes(a) != nullptr) x8.fetch(x8_codes(a), M, K, m0, k0, ptid);
       else issue_x();
     }
     if constexpr (BRES) {
@@ -717,7 +726,7 @@ __global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgs a) {
       *reinterpret_cast<uint32_t*>(BU0 + BUSZ + off) = 0u;
     }
     if constexpr (EXT && XPRE) {
-      if (a.xq != nullptr) x8.put(Xs, ptid);
+      if (x8_codes(a) != nullptr) x8.put(Xs, ptid);
     }
     // stage 0 landed (later prologue stages may still be in flight)
     wait_stages<LPS, 0, S - 2>(nk - 1);
@@ -903,12 +912,12 @@ __global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgs a) {
   float* RSs = E + EFL + (XPRE ? 0 : XTSZ / 4);           // EXT: row scales of x [BM]
   if (producer) {
     if constexpr (EXT) {
-      if (a.xq != nullptr && ptid < BM) RSs[ptid] = a.sx[m0 + ptid < M ? m0 + ptid : M - 1];
+      if (x8_codes(a) != nullptr && ptid < BM) RSs[ptid] = x8_scales(a)[m0 + ptid < M ? m0 + ptid : M - 1];
     }
     if constexpr (!XPRE) {
-      if (EXT && a.xq != nullptr) {
+      if (x8_codes(a) != nullptr) {
         X8Tile<BM, BN> x8;
-        x8.fetch(a.xq, M, K, m0, k0, ptid);
+        x8.fetch(x8_codes(a), M, K, m0, k0, ptid);
         x8.put(Xs, ptid);
       } else {
         issue_x();
@@ -945,7 +954,7 @@ __global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgs a) {
     float da[JPT];
 #pragma unroll
     for (int jj = 0; jj < JPT; ++jj) da[jj] = 0.f;
-    da_partial<BM, BN, R, TPK, JPT, EXT>(Xs, E, EXT && a.xq != nullptr ? RSs : nullptr, kl, jb, rows_here, da);
+    da_partial<BM, BN, R, TPK, JPT, EXT>(Xs, E, x8_codes(a) != nullptr ? RSs : nullptr, kl, jb, rows_here, da);
     if (k0 + kl < K) {
 #pragma unroll
       for (int jj = 0; jj < JPT; ++jj) {
@@ -977,7 +986,7 @@ __global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgs a) {
 // stage ahead in a register); else int8.
 template <bool W4, int BM, int BN, int S, int R, bool AFF = false, bool SPLIT = false,
           bool EXT = false>
-__global__ __launch_bounds__(256, 2) void bwd_wide_kernel(BwdArgs a) {
+__global__ __launch_bounds__(256, 2) void bwd_wide_kernel(BwdArgsOf<EXT> a) {
   static_assert(!EXT || !SPLIT, "split: the second launch reads x and writes dx");
   constexpr int KC = 64;                              // n per stage
   constexpr int RB = W4 ? BN / 2 : BN;                // code bytes per row of n
@@ -1531,16 +1540,16 @@ __global__ __launch_bounds__(256, 2) void bwd_wide_kernel(BwdArgs a) {
   __syncthreads();                                        // ring released
   // EXT with x in 8 bits: its codes, and the scales of the rows whose part of
   // the u operand this wave builds below (rows 32 wid + 8 (lane / 16) + e)
-  const bool x8on = EXT && a.xq != nullptr;
+  const bool x8on = x8_codes(a) != nullptr;
   X8Tile<BM, BN> x8;
   float rsv[8];
   if constexpr (EXT) static_assert(!XPRE && BM == 128, "wave w builds the rows 32 w .. 32 w + 31");
   if (x8on) {
-    x8.fetch(a.xq, M, K, m0, k0, tid);
+    x8.fetch(x8_codes(a), M, K, m0, k0, tid);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int gm = m0 + 32 * wid + 8 * (lane >> 4) + e;
-      rsv[e] = a.sx[gm < M ? gm : M - 1];
+      rsv[e] = x8_scales(a)[gm < M ? gm : M - 1];
     }
   } else {
     if constexpr (!XPRE) issue_x();
@@ -1677,7 +1686,7 @@ __global__ __launch_bounds__(256, 2) void bwd_wide_kernel(BwdArgs a) {
         const int e = kl % 64;
         const uint16_t xb = *reinterpret_cast<const uint16_t*>(Xs + swz128(m * RH + kl / 64, e >> 3) + 2 * (e & 7));
         float xv = __uint_as_float((uint32_t)xb << 16);
-        if (x8on) xv *= a.sx[m0 + m];
+        if (x8on) xv *= x8_scales(a)[m0 + m];
 #pragma unroll
         for (int jj = 0; jj < JPT; ++jj)
           if (jb + TPK * jj < R) da[jj] = __builtin_fmaf(xv, E[m * R + jb + TPK * jj], da[jj]);
@@ -1716,7 +1725,7 @@ __global__ __launch_bounds__(256, 2) void bwd_wide_kernel(BwdArgs a) {
 // the first add (NSPL: the split count's bound; splits past the count read
 // split 0 and are dropped by a select).
 template <int R, int NSPL, bool EXT>
-__global__ __launch_bounds__(512) void bwd_fixup_kernel(BwdArgs a) {
+__global__ __launch_bounds__(512) void bwd_fixup_kernel(BwdArgsOf<EXT> a) {
   constexpr int BM = 128, HN = 32, FN = 2;
   constexpr int EFL = (BM + HN) * R;                    // U [BM][R] | A^T [R][HN]
   constexpr int XSZ = BM * HN * 2;                      // x [BM][HN] bf16, 64-byte rows
@@ -1750,15 +1759,15 @@ __global__ __launch_bounds__(512) void bwd_fixup_kernel(BwdArgs a) {
   // 64 r + 16 (c ^ ((r >> 2) & 3)))
   // (x in 8 bits: thread -> eight codes, widened to bf16 integers in the same
   // layout, once the other loads are out)
-  const bool x8on = EXT && a.xq != nullptr;
+  const bool x8on = x8_codes(a) != nullptr;
   u32x2 xc{};
   const int xrow = tid >> 2, xc8 = tid & 3;
   if (x8on) {
     const int gm = m0 + xrow, gk = k0 + 8 * xc8;
     const bool ok = gm < M && gk < K;
-    xc = *reinterpret_cast<const u32x2*>(a.xq + (ok ? (long)gm * K + gk : 0));
+    xc = *reinterpret_cast<const u32x2*>(x8_codes(a) + (ok ? (long)gm * K + gk : 0));
     if (!ok) xc = u32x2{0u, 0u};
-    if (tid < BM) RSs[tid] = a.sx[m0 + tid < M ? m0 + tid : M - 1];
+    if (tid < BM) RSs[tid] = x8_scales(a)[m0 + tid < M ? m0 + tid : M - 1];
   } else {
     const int row = 16 * v + (lane >> 2);
     const int c = (lane & 3) ^ ((row >> 2) & 3), gm = m0 + row, gk = k0 + c * 8;
@@ -1844,7 +1853,7 @@ __global__ __launch_bounds__(512) void bwd_fixup_kernel(BwdArgs a) {
 }
 
 template <bool W4, int BN, int S, bool EXT, bool AFF = false>
-void launch_pc(BwdArgs a, hipStream_t st) {
+void launch_pc(BwdArgsOf<EXT> a, hipStream_t st) {
   constexpr int BM = 64;
   a.tiles_x = (a.K + BN - 1) / BN;
   const dim3 grid((unsigned)(a.tiles_x * ((a.M + BM - 1) / BM)));
@@ -1867,7 +1876,7 @@ void launch_pc(BwdArgs a, hipStream_t st) {
 }
 
 template <bool W4, bool EXT, bool AFF = false, bool SPLIT = false, int BN = 128>
-void launch_wide(BwdArgs a, hipStream_t st) {
+void launch_wide(BwdArgsOf<EXT> a, hipStream_t st) {
   static_assert(BN == 128 || (!W4 && !AFF && !SPLIT), "64-wide tiles: plain int8, one pass");
   constexpr int BM = 128, S = 2;
   a.tiles_x = (a.K + BN - 1) / BN;
@@ -1963,7 +1972,7 @@ const char* bwd_fused_kernel_name(int fmt, int M, int K, int N, int r) {
 
 namespace {
 template <bool EXT>
-void launch_fmt(int fmt, BwdKind kind, const void* scales, BwdArgs a, hipStream_t st) {
+void launch_fmt(int fmt, BwdKind kind, const void* scales, BwdArgsOf<EXT> a, hipStream_t st) {
   if (fmt == 2) {
     const W8OLayout L = w8o_layout(a.K, a.N);
     const char* sb = static_cast<const char*>(scales);
@@ -2004,8 +2013,7 @@ void launch_bwd_fused(int fmt, int M, int K, int N, const uint16_t* dy,
   wide_split_plan(M, K, N, &a.splits, &a.nks);
   const BwdKind kind = bwd_kind(fmt, M, K, N, r);
   if (ext) {
-    a.xq = xq; a.sx = sx; a.ge = *ge;
-    launch_fmt<true>(fmt, kind, scales, a, st);
+    launch_fmt<true>(fmt, kind, scales, BwdExtArgs{a, xq, sx, *ge}, st);
   } else {
     launch_fmt<false>(fmt, kind, scales, a, st);
   }

@@ -78,12 +78,18 @@ struct I8Args {
   int32_t* pacc;         // [splits, tiles, 4 waves, FM FN fragments, 64 lanes] int4
   float* pcorr;          // affine: [splits, tiles, 4 waves, CR rows, 16 columns, 64 lanes]
   int splits, nks;
-  FwdEpi epi;            // EPI kernels: bias, activation, residual, saved z
 };
+
+// EPI kernels: bias, activation, residual, saved z besides. (A type of its own,
+// so that the other launches do not carry these arguments.)
+struct I8EpiArgs : I8Args {
+  FwdEpi epi;
+};
+template <bool EPI> using I8ArgsOf = typename std::conditional<EPI, I8EpiArgs, I8Args>::type;
 
 template <int BM, int BN, int S, int R, typename OutT, bool ACC_OUT, bool AFF, bool SPLIT = false,
           bool EPI = false>
-__global__ __launch_bounds__(256) void fwd_i8_kernel(I8Args a) {
+__global__ __launch_bounds__(256) void fwd_i8_kernel(I8ArgsOf<EPI> a) {
   static_assert(!SPLIT || !ACC_OUT, "split: no integer test output");
   static_assert(!EPI || (!SPLIT && !ACC_OUT), "the epilogue runs where y is formed");
   constexpr int BK = 128, ASZ = BM * BK, STG = (BM + BN) * BK;
@@ -405,7 +411,7 @@ __global__ __launch_bounds__(256) void fwd_i8_kernel(I8Args a) {
 // 2 (v / 4) + q / 2 for quarter q; all of a lane's split loads are issued
 // before the first add.
 template <int R, int NSPL, typename OutT, bool EPI>
-__global__ __launch_bounds__(512) void fwd_fixup_kernel(I8Args a) {
+__global__ __launch_bounds__(512) void fwd_fixup_kernel(I8ArgsOf<EPI> a) {
   constexpr int BM = 128, HN = 32, FN = 2;
   using Ep = EpiOps<BM, HN, R, true>;
   constexpr int EPB = (Ep::kFloats * 4 + 15) / 16 * 16;
@@ -454,7 +460,7 @@ __global__ __launch_bounds__(512) void fwd_fixup_kernel(I8Args a) {
 // in split order into LDS ([128][64 + 4] floats, from the product kernel's
 // cell layout), then acc' = c acc + corr and the affine epilogue.
 template <int R, int NSPL, bool EPI>
-__global__ __launch_bounds__(512) void fwd_fixup_aff_kernel(I8Args a) {
+__global__ __launch_bounds__(512) void fwd_fixup_aff_kernel(I8ArgsOf<EPI> a) {
   constexpr int BM = 128, BN = 64, FN = 4, CR = 2, CP = BN + 4;
   using Ep = EpiOps<BM, BN, R, true, true>;
   constexpr int EPB = (Ep::kFloats * 4 + 15) / 16 * 16;
@@ -567,7 +573,7 @@ void fwd_split_plan(int M, int N, int K, int BN, int maxsp, int* splits, int* nk
 }
 
 template <typename OutT, bool EPI>
-void launch_split(I8Args a, hipStream_t st) {
+void launch_split(I8ArgsOf<EPI> a, hipStream_t st) {
   constexpr int BM = 128, BN = 128, S = 2;
   a.tiles_x = (a.N + BN - 1) / BN;
   const int tiles = a.tiles_x * ((a.M + BM - 1) / BM);
@@ -590,7 +596,7 @@ void launch_split(I8Args a, hipStream_t st) {
 }
 
 template <int BM, int BN, int S, typename OutT, bool ACC, bool AFF, bool EPI>
-void launch_tiles(I8Args a, hipStream_t st) {
+void launch_tiles(I8ArgsOf<EPI> a, hipStream_t st) {
   a.tiles_x = (a.N + BN - 1) / BN;
   const dim3 grid((unsigned)(a.tiles_x * ((a.M + BM - 1) / BM)));
   if (a.r <= 4) fwd_i8_kernel<BM, BN, S, 4, OutT, ACC, AFF, false, EPI><<<grid, 256, 0, st>>>(a);
@@ -600,7 +606,7 @@ void launch_tiles(I8Args a, hipStream_t st) {
 }
 
 template <typename OutT, bool ACC, bool EPI>
-void launch_shape(I8Args a, hipStream_t st) {
+void launch_shape(I8ArgsOf<EPI> a, hipStream_t st) {
   if constexpr (!ACC) {
     if (a.pacc != nullptr) {
       fwd_split_plan(a.M, a.N, a.K, 128, kMaxFwdSplits, &a.splits, &a.nks);
@@ -628,7 +634,7 @@ void launch_shape(I8Args a, hipStream_t st) {
 
 // The affine product: split with its fixup, or one of its two tile shapes.
 template <bool EPI>
-void launch_affine(I8Args a, hipStream_t st) {
+void launch_affine(I8ArgsOf<EPI> a, hipStream_t st) {
   if (a.pacc != nullptr && a.pcorr != nullptr) {
     fwd_split_plan(a.M, a.N, a.K, 64, kMaxAffSplits, &a.splits, &a.nks);
     if (a.splits > 1) {
@@ -678,9 +684,9 @@ void launch_gemm_fwd_w8(int dtype, int M, int N, int K, const int8_t* xq,
   if (acc_out != nullptr) {
     launch_shape<float, true, false>(a, st);
   } else if (epi != nullptr) {
-    a.epi = *epi;
-    if (dtype == 0) launch_shape<float, false, true>(a, st);
-    else launch_shape<uint16_t, false, true>(a, st);
+    const I8EpiArgs ea{a, *epi};
+    if (dtype == 0) launch_shape<float, false, true>(ea, st);
+    else launch_shape<uint16_t, false, true>(ea, st);
   } else if (dtype == 0) {
     launch_shape<float, false, false>(a, st);
   } else {
@@ -706,8 +712,7 @@ void launch_gemm_fwd_w8o(int M, int N, int K, const int8_t* xq, const int8_t* co
   a.pacc = pacc;
   a.pcorr = pcorr;
   if (epi != nullptr) {
-    a.epi = *epi;
-    launch_affine<true>(a, st);
+    launch_affine<true>(I8EpiArgs{a, *epi}, st);
   } else {
     launch_affine<false>(a, st);
   }

@@ -51,8 +51,13 @@ struct W4Args {
   // accumulator layout, the split count and stages of 64 k per split
   float* pacc;              // [splits, tiles, 4 waves, 16 fragments, 64 lanes] float4
   int splits, nks;
-  FwdEpi epi;               // EPI kernels: bias, activation, residual, saved z
 };
+
+// EPI kernels: bias, activation, residual, saved z besides.
+struct W4EpiArgs : W4Args {
+  FwdEpi epi;
+};
+template <bool EPI> using W4ArgsOf = typename std::conditional<EPI, W4EpiArgs, W4Args>::type;
 
 constexpr int kMaxW4Splits = 8;
 
@@ -89,7 +94,7 @@ __device__ __forceinline__ u32x4 nibbles_bf16(uint32_t w, float sc) {
 // widening of one operand then overlaps the matrix work of the previous one
 // inside the wave.
 template <int BM, int S, int R, int G, bool SPLIT = false, bool EPI = false>
-__global__ __launch_bounds__(256, 2) void fwd_w4_kernel(W4Args a) {
+__global__ __launch_bounds__(256, 2) void fwd_w4_kernel(W4ArgsOf<EPI> a) {
   static_assert(!SPLIT || BM == 128, "split contraction: 128-row tiles");
   constexpr int BN = 128, BK = 64;                 // k per stage: half a scale group
   constexpr int ASZ = BM * 128, BSZ = BN * 32, STG = ASZ + BSZ;
@@ -252,7 +257,7 @@ __global__ __launch_bounds__(256, 2) void fwd_w4_kernel(W4Args a) {
 // the partial sums added in split order, then the epilogue. Wave v takes the
 // strip's 16-row block v.
 template <int R, int NSPL, bool EPI>
-__global__ __launch_bounds__(512) void fwd_w4_fixup_kernel(W4Args a) {
+__global__ __launch_bounds__(512) void fwd_w4_fixup_kernel(W4ArgsOf<EPI> a) {
   constexpr int BM = 128, HN = 32, FM = 8, FN = 2;
   using Ep = EpiOps<BM, HN, R, false>;
   constexpr int EPB = (Ep::kFloats * 4 + 15) / 16 * 16;
@@ -296,7 +301,7 @@ __global__ __launch_bounds__(512) void fwd_w4_fixup_kernel(W4Args a) {
 }
 
 template <int BM, int S, int G, bool EPI>
-void launch_tiles(W4Args a, hipStream_t st) {
+void launch_tiles(W4ArgsOf<EPI> a, hipStream_t st) {
   constexpr int BN = 128;
   a.tiles_x = (a.N + BN - 1) / BN;
   const dim3 grid((unsigned)(a.tiles_x * ((a.M + BM - 1) / BM)));
@@ -307,7 +312,7 @@ void launch_tiles(W4Args a, hipStream_t st) {
 }
 
 template <int S, int G, bool EPI>
-void launch_split_tiles(W4Args a, hipStream_t st) {
+void launch_split_tiles(W4ArgsOf<EPI> a, hipStream_t st) {
   constexpr int BM = 128, BN = 128;
   a.tiles_x = (a.N + BN - 1) / BN;
   const int tiles = a.tiles_x * ((a.M + BM - 1) / BM);
@@ -345,7 +350,7 @@ void w4_split_plan(int M, int N, int K, int* splits, int* nks) {
 // Three ring slots where they fit beside the scale slab at two blocks per
 // compute unit (80 KB each), else two.
 template <int BM, bool EPI>
-void launch_groups(const W4Args& a, hipStream_t st) {
+void launch_groups(const W4ArgsOf<EPI>& a, hipStream_t st) {
   const int ngrp = a.K / 128;                      // validated: <= kW4MaxGroups
   if (a.splits > 1) {
     if (ngrp <= 8) launch_split_tiles<3, 8, EPI>(a, st);
@@ -383,9 +388,9 @@ void launch_gemm_fwd_w4(int M, int N, int K, const uint16_t* x,
   const long t128 = (long)((M + 127) / 128) * ((N + 127) / 128);
   const bool tall = t128 >= kCUs || a.splits > 1;
   if (epi != nullptr) {
-    a.epi = *epi;
-    if (tall) launch_groups<128, true>(a, st);
-    else launch_groups<64, true>(a, st);
+    const W4EpiArgs ea{a, *epi};
+    if (tall) launch_groups<128, true>(ea, st);
+    else launch_groups<64, true>(ea, st);
   } else if (tall) {
     launch_groups<128, false>(a, st);
   } else {

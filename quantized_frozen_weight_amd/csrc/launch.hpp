@@ -80,6 +80,16 @@ void launch_gemm_fwd_w4(int M, int N, int K, const uint16_t* x,
                         const float* t, const float* B, int hd, int r, float s,
                         uint16_t* y, float* pacc, const FwdEpi* epi, hipStream_t st);
 
+// The layer with its epilogue for at most four rows in one launch (fmt 0 or
+// 1, rank up to 16, K <= 16384: fwd_few_takes); t, xq and sx (x's row
+// checkpoint) may be NULL; scratch: fwd_few_floats(M, K) floats.
+size_t fwd_few_floats(int M, int K);
+bool fwd_few_takes(int fmt, int M, int K, int N, int r);
+void launch_fwd_few(int dtype, int fmt, int M, int N, int K, const void* x, const void* codes,
+                    const void* scales, const float* A, const float* B, int hd, int r, float s,
+                    const FwdEpi& epi, void* y, float* t, int8_t* xq, float* sx, float* scratch,
+                    hipStream_t st);
+
 // u = dy B^T (float32 [M, r]); if dys != nullptr also dys = bf16(dy * sw[n]).
 void launch_bwd_rows(int dtype, const void* dy, int M, int N, const float* B, int hd,
                      int r, const float* sw, uint16_t* dys, float* u,

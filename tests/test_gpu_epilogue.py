@@ -180,6 +180,13 @@ FWD = [
     (1, 16, 16, 1, "w8", "f32", 1),            # the smallest layer
     (130, 144, 272, 32, "w8", "f32", 1),
     (1, 2048, 1040, 8, "w8", "bf16", 1),       # one token
+    (2, 208, 80, 1, "w8", "f32", 1),           # few rows, ranks below the padded ones
+    (3, 784, 16400, 3, "w8", "bf16", 1),       # ... wide: 64 columns a block, a ragged one
+    (4, 16384, 272, 8, "w8", "bf16", 1),       # ... long rows: codes in two batches
+    (4, 4096, 8256, 16, "w8", "bf16", 3),      # ... heads, 32 columns a block
+    (4, 16384, 144, 16, "w4g128", "bf16", 1),
+    (3, 128, 16, 4, "w4g128", "bf16", 1),
+    (4, 256, 144, 32, "w8", "bf16", 1),        # rank 32: the tiled product
     (7, 784, 208, 3, "w8", "bf16", 1),
     (1001, 784, 1024, 8, "w8", "bf16", 1),     # 64 x 64 tiles, ragged rows and k
     (700, 256, 4112, 16, "w8", "bf16", 1),     # 128 x 64 tiles, last group of 16 columns
@@ -236,7 +243,7 @@ def test_forward(spec):
                 assert torch.equal(bits(y), bits(y2)), "y from the checkpoint differs"
 
 
-@pytest.mark.parametrize("spec", [FWD[0], FWD[5], FWD[9], FWD[13], FWD[17], FWD[20]],
+@pytest.mark.parametrize("spec", [f for f in FWD if f[0] in (64, 1001, 100, 77, 90)],
                          ids=lambda s: "-".join(map(str, s)))
 def test_empty_epilogue_is_the_plain_forward(spec):
     c = Case(*spec)
