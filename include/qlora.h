@@ -442,12 +442,20 @@ typedef struct {
   const void* add;        /* [M, K] in the compute dtype, or NULL; may be dx */
 } qlora_grad_epilogue;
 
+/* Workspace needed by qlora_bwd_epi and qlora_bwd_epi_partial for M rows: that
+ * of qlora_bwd and, in bf16 for int8 and 4-bit weights, the dequantized
+ * weight as bf16 [K, N] and B in three bf16 parts (scratch of one call, 2 K N
+ * bytes and at most 192 N; qlora_bwd_partials_bytes says what outlives
+ * qlora_bwd_epi_partial). */
+int qlora_bwd_epi_workspace(const qlora_linear* L, int M, int dtype, size_t* bytes);
+
 /* qlora_bwd with x either in the compute dtype or as its row checkpoint
  * (exactly one of x and the pair x_codes, x_scales), and the gradient
  * epilogue g (NULL: none) on dx. From a checkpoint
  *   dA = s sum_m x_scales[m] x_codes[m, :]^T u[m, :],
- * and t_saved is required. dx may be NULL where g is NULL. Workspace:
- * qlora_bwd_workspace. */
+ * and t_saved is required. dx may be NULL where g is NULL. With x in the
+ * compute dtype and nothing to do to dx the results are bitwise qlora_bwd's;
+ * else they may differ from it in the order of float32 sums. */
 int qlora_bwd_epi(const qlora_linear* L, int M, int dtype, const void* x,
                   const int8_t* x_codes, const float* x_scales, const void* dy,
                   const float* t_saved, const qlora_grad_epilogue* g, void* dx,

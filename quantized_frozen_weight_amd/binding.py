@@ -61,7 +61,7 @@ EXPORTS = (
     "qlora_quantize_heads", "qlora_outlier_layout", "qlora_bwd_finish_batch",
     "qlora_bwd_partials_bytes", "qlora_bwd_main_kernel", "qlora_bwd_noalloc",
     "qlora_ckpt_bytes", "qlora_ckpt_write", "qlora_ckpt_read", "qlora_fwd_epi",
-    "qlora_fwd_ckpt", "qlora_bwd_epi", "qlora_bwd_epi_partial",
+    "qlora_fwd_ckpt", "qlora_bwd_epi", "qlora_bwd_epi_partial", "qlora_bwd_epi_workspace",
     "qlora_act_bwd_workspace", "qlora_act_bwd",
 )
 QLORA_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -148,6 +148,7 @@ def lib() -> ctypes.CDLL:
     L.qlora_fwd_ckpt.argtypes = [plin, i, i, vp, vp, vp, pepi, vp, vp, sz, vp]
     L.qlora_bwd_epi.argtypes = [plin, i, i, vp, vp, vp, vp, vp, pge, vp, vp, vp, vp, sz, vp]
     L.qlora_bwd_epi_partial.argtypes = [plin, i, i, vp, vp, vp, vp, vp, pge, vp, vp, sz, vp]
+    L.qlora_bwd_epi_workspace.argtypes = [plin, i, i, psz]
     L.qlora_act_bwd_workspace.argtypes = [i, i, psz]
     L.qlora_act_bwd.argtypes = [i, i, i, i, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     for name in EXPORTS[1:]:
@@ -770,7 +771,7 @@ def qlora_bwd_epi(layer: QLinear, x, dy, t=None, act: str = "none", z=None, add=
         _tensor(dA, "dA", (layer.K, layer.r), torch.float32, dev)
     dB = torch.empty(_b_shape(layer), dtype=torch.float32, device=dev) if dB is None else \
         _tensor(dB, "dB", _b_shape(layer), torch.float32, dev)
-    ws = _scratch("qlora_bwd_workspace", cs, M, dt, dev, ws)
+    ws = _scratch("qlora_bwd_epi_workspace", cs, M, dt, dev, ws)
     with _on(dev):
         _check(lib().qlora_bwd_epi(ctypes.byref(cs), M, dt, *args, _ptr(dA), _ptr(dB), _ptr(ws),
                                    ws.numel() * ws.element_size(), _stream()), "qlora_bwd_epi")
@@ -782,7 +783,7 @@ def qlora_bwd_epi_partial(layer: QLinear, x, dy, t=None, act: str = "none", z=No
     """First half of qlora_bwd_epi: (dx or None, workspace), the adapter
     gradients left to qlora_bwd_finish or qlora_bwd_finish_batch."""
     cs, M, dt, dev, args, dx, _keep = _bwd_epi_args(layer, x, dy, t, act, z, add, need_dx, dx)
-    ws = _scratch("qlora_bwd_workspace", cs, M, dt, dev, ws)
+    ws = _scratch("qlora_bwd_epi_workspace", cs, M, dt, dev, ws)
     with _on(dev):
         _check(lib().qlora_bwd_epi_partial(ctypes.byref(cs), M, dt, *args, _ptr(ws),
                                            ws.numel() * ws.element_size(), _stream()),

@@ -128,6 +128,15 @@ BwdLayout bwd_layout(const qlora_linear* L, int M, int dtype) {
   return w;
 }
 
+// Whether qlora_bwd_epi lays the weight out first, and the workspace it then
+// needs after a backward's own.
+bool lays_out(const qlora_linear* L, int M, int dtype) {
+  return dtype == QLORA_BF16 && bwd_tn_takes(L->fmt, M, L->K, L->N, L->r);
+}
+size_t bwd_epi_bytes(const qlora_linear* L, int M, int dtype) {
+  return bwd_layout(L, M, dtype).total + (lays_out(L, M, dtype) ? bwd_tn_bytes(L->K, L->N, L->r) : 0);
+}
+
 inline char* at(void* ws, size_t off) { return static_cast<char*>(ws) + off; }
 
 // Scratch of qlora_bwd_noalloc: a static device array, one copy per GPU the
@@ -198,7 +207,7 @@ int bwd_check_ws(const qlora_linear* L, int M, int dtype, void* ws, size_t ws_by
 void enqueue_bwd_partial(const qlora_linear* L, int M, int dtype, const void* x, const int8_t* xq,
                          const float* sx, const void* dy, const float* t_saved, const GradEpi* ge,
                          void* dx, void* ws, hipStream_t s, int repeats, void* ev_start,
-                         void* ev_stop) {
+                         void* ev_stop, bool laid_out = false) {
   const BwdLayout w = bwd_layout(L, M, dtype);
   const float sc = lora_s(L);
   float* u = reinterpret_cast<float*>(at(ws, w.u));
@@ -210,6 +219,13 @@ void enqueue_bwd_partial(const qlora_linear* L, int M, int dtype, const void* x,
   }
   float* partB = reinterpret_cast<float*>(at(ws, w.pB));
   float* partA = reinterpret_cast<float*>(at(ws, w.pA));
+  if (laid_out) {
+    launch_bwd_tn(L->fmt, M, L->K, L->N, static_cast<const uint16_t*>(dy), L->codes, L->scales, L->B,
+                  head_width(L), L->A, t, static_cast<const uint16_t*>(x), xq, sx, L->r, sc,
+                  static_cast<uint16_t*>(dx), partA, partB, reinterpret_cast<float*>(at(ws, w.pdx)),
+                  reinterpret_cast<float*>(at(ws, w.pu)), at(ws, w.total), *ge, s);
+    return;
+  }
   if (dtype == QLORA_BF16 && dx != nullptr) {
     // one launch: dx, u, and the per-row-block partial sums of dA and dB
     mark(ev_start, s);
@@ -367,8 +383,8 @@ int bwd_epi_check(const qlora_linear* L, int M, int dtype, const void* x, const 
     in.add(g->z_scales, (size_t)M * group_count(L->K));
     if (g->add != dx) in.add(g->add, mk * es);
   }
-  st = bwd_check_ws(L, M, dtype, ws, ws_bytes);
-  if (st) return st;
+  const size_t need = bwd_epi_bytes(L, M, dtype);
+  if (ws_bytes < need || !ws || !aligned16(ws)) return QLORA_EWORKSPACE;
   add_layer(in, L);
   in.add(x, mk * es);
   in.add(x_codes, mk);
@@ -378,7 +394,7 @@ int bwd_epi_check(const qlora_linear* L, int M, int dtype, const void* x, const 
   out.add(dx, mk * es);
   out.add(dA, (size_t)L->K * L->r * 4);
   out.add(dB, (size_t)L->N * L->r * 4);
-  out.add(ws, bwd_layout(L, M, dtype).total);
+  out.add(ws, need);
   return disjoint(out, in) ? QLORA_OK : QLORA_EINVAL;
 }
 
@@ -389,7 +405,7 @@ void enqueue_bwd_epi(const qlora_linear* L, int M, int dtype, const void* x, con
   const bool plain = x != nullptr && (g == nullptr || (g->act == QLORA_ACT_NONE && g->add == nullptr));
   const GradEpi ge = g != nullptr ? grad_epi(g->act, g->z, g->z_codes, g->z_scales, g->add, L->K) : GradEpi{};
   enqueue_bwd_partial(L, M, dtype, x, x_codes, x_scales, dy, t_saved, plain ? nullptr : &ge, dx, ws, s,
-                      1, nullptr, nullptr);
+                      1, nullptr, nullptr, !plain && dx != nullptr && lays_out(L, M, dtype));
 }
 
 
@@ -837,6 +853,14 @@ int qlora_fwd_ckpt(const qlora_linear* L, int M, int dtype, const int8_t* x_code
   }
   enqueue_fwd_i8(L, M, dtype, x_codes, x_scales, asum, t, epi, y, ws, w, s);
   return launch_status();
+}
+
+int qlora_bwd_epi_workspace(const qlora_linear* L, int M, int dtype, size_t* bytes) {
+  if (bytes == nullptr) return QLORA_EINVAL;
+  const int st = check_linear(L, M, dtype);
+  if (st) return st;
+  *bytes = bwd_epi_bytes(L, M, dtype);
+  return QLORA_OK;
 }
 
 int qlora_bwd_epi_partial(const qlora_linear* L, int M, int dtype, const void* x,

@@ -99,37 +99,44 @@ __global__ __launch_bounds__(256) void code_sums_kernel(const int8_t* __restrict
 }
 
 // ---- dz = dy act'(z), dbias = column sums -----------------------------------
-// A block owns 256 columns (32 lanes of 8) and a span of rows, 8 rows at a
-// time; a thread keeps the float32 sums of its 8 columns over its rows. The 8
-// row lanes are added in order through LDS, and (more than one span) a second
-// launch adds the spans in order. No atomics.
-constexpr int kActCols = 256, kActLanes = 8;
+// A block owns 256 columns (32 lanes of 8) and a span of rows, LANES rows at a
+// time; a thread keeps the float32 sums of its 8 columns over its rows, four
+// rows' loads in flight. The row lanes are added in order through LDS, and
+// (more than one span) a second launch adds the spans in order. No atomics.
+// Up to 128 rows one span of 32 row lanes does: every thread then has one
+// group of loads, and there is no second launch (77 rows of 1040 float32: one
+// span of 8 lanes took 12 us). Past that 8 lanes and enough spans to fill the
+// chip. The activation's slope is as much work as the traffic: 4096 x 2304
+// bf16 with gelu moves 47 MB (9.3 us at the 5.1 TB/s of a large copy) and
+// does about 25 vector instructions and two transcendental ones per value
+// (8 us).
+constexpr int kActCols = 256;
 
 inline int col_blocks(int C) { return C / kActCols + (C % kActCols != 0); }
 
-// Row spans, and rows per span: enough blocks to fill the chip, but one span
-// (one launch, no partial sums) while a thread has at most 16 rows.
-void act_bwd_plan(int M, int C, int* spans, int* rows) {
-  const int cb = col_blocks(C);
-  if (M <= 16 * kActLanes) {
+// Rows per span and row lanes.
+void act_bwd_plan(int M, int C, int* spans, int* rows, int* lanes) {
+  if (M <= 32 * kUnits) {
     *spans = 1;
     *rows = M;
+    *lanes = 32;
     return;
   }
-  int want = 2048 / cb;
+  *lanes = 8;
+  int want = 2048 / col_blocks(C);
   if (want < 1) want = 1;
   int r = (M + want - 1) / want;
-  if (r < 4 * kActLanes) r = 4 * kActLanes;
-  r = (r + kActLanes - 1) / kActLanes * kActLanes;
+  if (r < 8 * kUnits) r = 8 * kUnits;
+  r = (r + 7) / 8 * 8;
   *rows = r;
   *spans = (M + r - 1) / r;
 }
 
-template <typename T, bool SUMS>
-__global__ __launch_bounds__(256) void act_bwd_kernel(const typename Elem<T>::type* dy, int M, int C,
+template <typename T, bool SUMS, int LANES>
+__global__ __launch_bounds__(32 * LANES) void act_bwd_kernel(const typename Elem<T>::type* dy, int M, int C,
                                                       GradEpi ge, typename Elem<T>::type* dz,
                                                       float* __restrict__ out, int rows) {
-  __shared__ float red[SUMS ? kActLanes : 1][kActCols + 8];
+  __shared__ float red[SUMS ? LANES : 1][kActCols + 8];
   const int tid = threadIdx.x, cl = tid & 31, rl = tid >> 5;
   const uint32_t col = blockIdx.x * (uint32_t)kActCols + 8u * cl;   // (may pass 2^31 - 1 in the last block)
   const bool okc = col < (uint32_t)C;
@@ -138,12 +145,12 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(const typename Elem<T>::ty
   float sum[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.f;
-  for (int mb = m0 + rl; mb < m1; mb += kActLanes * kUnits) {
+  for (int mb = m0 + rl; mb < m1; mb += LANES * kUnits) {
     float v[kUnits][8], z[kUnits][8];
     // every load of the group from clamped addresses before the first use
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int m = mb + kActLanes * i < m1 ? mb + kActLanes * i : mb;
+      const int m = mb + LANES * i < m1 ? mb + LANES * i : mb;
       const long at = (long)m * C + colc;
       load8(dy + at, v[i]);
       if (ge.act.kind != 0) {
@@ -155,9 +162,9 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(const typename Elem<T>::ty
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const int m = mb + kActLanes * i;
+      const int m = mb + LANES * i;
       if (m < m1) {
-        act_slope_mul(ge.act, z[i], v[i]);
+        act_slope_mul<std::is_same<T, F32>::value>(ge.act, z[i], v[i]);
         if (dz != nullptr && okc) store8(dz + (long)m * C + col, v[i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] += v[i][e];
@@ -168,10 +175,11 @@ __global__ __launch_bounds__(256) void act_bwd_kernel(const typename Elem<T>::ty
 #pragma unroll
     for (int e = 0; e < 8; ++e) red[rl][8 * cl + e] = sum[e];
     __syncthreads();
+    if (tid >= kActCols) return;
     const uint32_t c = blockIdx.x * (uint32_t)kActCols + tid;
     float s = red[0][tid];
 #pragma unroll
-    for (int l = 1; l < kActLanes; ++l) s += red[l][tid];
+    for (int l = 1; l < LANES; ++l) s += red[l][tid];
     if (c < (uint32_t)C) out[(long)blockIdx.y * C + c] = s;
   }
 }
@@ -199,16 +207,19 @@ template <typename T>
 void act_bwd_launch(int M, int C, const void* dy, const GradEpi& ge, void* dz, float* dbias,
                     float* partial, hipStream_t st) {
   typedef typename Elem<T>::type E;
-  int spans, rows;
-  act_bwd_plan(M, C, &spans, &rows);
+  int spans, rows, lanes;
+  act_bwd_plan(M, C, &spans, &rows, &lanes);
   const dim3 grid((unsigned)col_blocks(C), (unsigned)spans);
+  const E* d = static_cast<const E*>(dy);
+  E* o = static_cast<E*>(dz);
   if (dbias == nullptr) {
-    act_bwd_kernel<T, false><<<grid, 256, 0, st>>>(static_cast<const E*>(dy), M, C, ge,
-                                                   static_cast<E*>(dz), nullptr, rows);
+    if (lanes == 32) act_bwd_kernel<T, false, 32><<<grid, 1024, 0, st>>>(d, M, C, ge, o, nullptr, rows);
+    else act_bwd_kernel<T, false, 8><<<grid, 256, 0, st>>>(d, M, C, ge, o, nullptr, rows);
     return;
   }
-  act_bwd_kernel<T, true><<<grid, 256, 0, st>>>(static_cast<const E*>(dy), M, C, ge, static_cast<E*>(dz),
-                                                spans == 1 ? dbias : partial, rows);
+  float* sums = spans == 1 ? dbias : partial;
+  if (lanes == 32) act_bwd_kernel<T, true, 32><<<grid, 1024, 0, st>>>(d, M, C, ge, o, sums, rows);
+  else act_bwd_kernel<T, true, 8><<<grid, 256, 0, st>>>(d, M, C, ge, o, sums, rows);
   if (spans > 1)
     act_bwd_sum_kernel<<<(unsigned)((C + 63) / 64), 256, 0, st>>>(partial, spans, C, dbias);
 }
@@ -243,8 +254,8 @@ void launch_code_sums(const int8_t* codes, int M, int K, float* asum, hipStream_
 }
 
 size_t act_bwd_floats(int M, int C) {
-  int spans, rows;
-  act_bwd_plan(M, C, &spans, &rows);
+  int spans, rows, lanes;
+  act_bwd_plan(M, C, &spans, &rows, &lanes);
   return spans > 1 ? (size_t)spans * (size_t)C : 0;
 }
 

@@ -115,7 +115,7 @@ __global__ __launch_bounds__(256) void gemm_dx_f32_kernel(
           } else {
             z[0] = static_cast<const float*>(ge.z)[at];
           }
-          act_slope_mul(ge.act, z, v);
+          act_slope_mul<true>(ge.act, z, v);
         }
         if (ge.add != nullptr) v[0] += static_cast<const float*>(ge.add)[at];
       }

@@ -37,10 +37,11 @@ inline __host__ __device__ int group_count(int C) { return C / kGroup + (C % kGr
 struct ActParams {
   int kind;      // 0 none, 1 relu, 2 gelu, 3 the sigma family
   float p, q;    // the sigma family's constants
+  float p2, q2;  // -log2 e times them
 };
 
 inline ActParams act_params(int act) {
-  ActParams a{act, 1.f, 0.f};
+  ActParams a{act, 1.f, 0.f, 0.f, 0.f};
   if (act == kActGeluTanh) {
     a.kind = 3;
     a.p = 1.5957691216057308f;               // 2 sqrt(2 / pi)
@@ -48,98 +49,110 @@ inline ActParams act_params(int act) {
   } else if (act == kActSilu) {
     a.kind = 3;
   }
+  a.p2 = -1.44269504088896341f * a.p;
+  a.q2 = -1.44269504088896341f * a.q;
   return a;
 }
 
-// min / max that keep a NaN (v_min / v_max drop it)
+// max that keeps a NaN (v_max drops it)
 __device__ __forceinline__ float at_least(float v, float lo) { return v < lo ? lo : v; }
-__device__ __forceinline__ float at_most(float v, float hi) { return v > hi ? hi : v; }
 
 // e^w for |w| <= 150 as 2^(w log2 e), the product kept in two parts (its
-// rounding error, times |w|, would otherwise reach the result): within 3 ulp;
-// overflows to infinity and underflows to 0.
-__device__ __forceinline__ float exp_pos(float w) {
+// rounding error, times |w|, would otherwise reach the result): within 3 ulp.
+// Overflows to infinity, underflows to 0. For float32 outputs; bfloat16 ones
+// take 2^w2 of the rounded exponent w2 = w log2 e (FINE false below), whose
+// error, |w| 2^-24 of e^w, they cannot show: e^w only matters where it is not
+// far from 1.
+__device__ __forceinline__ float exp_fine(float w) {
   constexpr float kL = 1.44269504088896341f, kLlo = 1.925963033500e-8f, kLn2 = 0.693147180559945f;
   const float hi = w * kL;
   const float lo = __builtin_fmaf(w, kLlo, __builtin_fmaf(w, kL, -hi));
   return __builtin_amdgcn_exp2f(hi) * __builtin_fmaf(lo, kLn2, 1.f);
 }
 
-// 1 / (1 + e^-w); 0 and 1 past |w| = 150, where float32 is there anyway
-__device__ __forceinline__ float sigma(float w) {
-  w = at_most(at_least(w, -150.f), 150.f);
-  return __builtin_amdgcn_rcpf(1.f + exp_pos(-w));
+// e^(-c^2 / 2), |c| <= 16
+template <bool FINE>
+__device__ __forceinline__ float normal_exp(float c) {
+  if constexpr (FINE) return exp_fine(-0.5f * c * c);
+  else return __builtin_amdgcn_exp2f(c * c * -0.72134752044448170f);
 }
 
-// Phi(z) = erfc(-z / sqrt 2) / 2, relative error below 1e-6 on either side of
-// 0 (from 1 + erf the left tail would cancel). For x = |z| / sqrt 2 and
+// The smaller tail Phi(-|z|) = erfc(|z| / sqrt 2) / 2 with a relative error
+// below 1e-6 (1 + erf would cancel there). For x = |z| / sqrt 2 and
 // t = 1 / (1 + 0.44 x), e^(x^2) erfc(x) is t times a polynomial of degree 7 in
 // t, fitted here to the smallest largest relative error (1.9e-7) on
-// 0 <= x <= 15. ex is e^(-x^2) (shared with the density).
-__device__ __forceinline__ float normal_cdf(float z, float ex) {
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_fabsf(z), 0.44f * 0.70710678118654752f, 1.f));
-  float c = 0.07150039076805115f;
-  c = __builtin_fmaf(c, t, -0.27915504574775696f);
-  c = __builtin_fmaf(c, t, 0.29887089133262634f);
-  c = __builtin_fmaf(c, t, -0.022297518327832222f);
-  c = __builtin_fmaf(c, t, 0.2169952094554901f);
-  c = __builtin_fmaf(c, t, 0.2169342190027237f);
-  c = __builtin_fmaf(c, t, 0.2489354908466339f);
-  c = __builtin_fmaf(c, t, 0.24821652472019196f);
-  const float h = 0.5f * t * c * ex;
-  return z < 0.f ? h : 1.f - h;
+// 0 <= x <= 15; its coefficients are halved below. a = |z|, ex = e^(-z^2 / 2).
+__device__ __forceinline__ float normal_tail(float a, float ex) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(a, 0.44f * 0.70710678118654752f, 1.f));
+  float c = 0.5f * 0.07150039076805115f;
+  c = __builtin_fmaf(c, t, 0.5f * -0.27915504574775696f);
+  c = __builtin_fmaf(c, t, 0.5f * 0.29887089133262634f);
+  c = __builtin_fmaf(c, t, 0.5f * -0.022297518327832222f);
+  c = __builtin_fmaf(c, t, 0.5f * 0.2169952094554901f);
+  c = __builtin_fmaf(c, t, 0.5f * 0.2169342190027237f);
+  c = __builtin_fmaf(c, t, 0.5f * 0.2489354908466339f);
+  c = __builtin_fmaf(c, t, 0.5f * 0.24821652472019196f);
+  return t * c * ex;
 }
 
-// e^(-z^2 / 2)
-__device__ __forceinline__ float normal_exp(float z) {
-  return exp_pos(at_least(-0.5f * z * z, -150.f));
-}
+// Arguments are bounded with fminf / fmaxf, which drop a NaN, where z itself
+// brings it back or nan_or does.
+__device__ __forceinline__ float nan_or(float z, float v) { return z != z ? z : v; }
 
 // act of every v; -inf goes to the limit 0 (not -inf * 0), NaN stays NaN
-template <int NV>
+template <bool FINE, int NV>
 __device__ __forceinline__ void act_apply(const ActParams& a, float (&v)[NV]) {
   if (a.kind == 0) return;
   if (a.kind == 1) {
 #pragma unroll
     for (int e = 0; e < NV; ++e) v[e] = at_least(v[e], 0.f);
   } else if (a.kind == 2) {
+    // z Phi(z) = max(z, 0) - |z| Phi(-|z|); past |z| = 16 the tail is 0
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
-      const float z = at_least(v[e], -1e9f);
-      v[e] = z * normal_cdf(z, normal_exp(z));
+      const float c = fminf(__builtin_fabsf(v[e]), 16.f);
+      v[e] = __builtin_fmaf(-c, normal_tail(c, normal_exp<FINE>(c)), at_least(v[e], 0.f));
     }
   } else {
+    // z / (1 + e^-w), w = z (p + q z^2)
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
-      const float z = at_least(v[e], -1e9f), c = at_most(z, 1e9f);
-      v[e] = z * sigma(c * __builtin_fmaf(a.q, c * c, a.p));
+      const float z = at_least(v[e], -1e9f), c = fminf(z, 1e9f), c2 = c * c;
+      float x;
+      if constexpr (FINE) x = exp_fine(fminf(fmaxf(-c * __builtin_fmaf(a.q, c2, a.p), -150.f), 150.f));
+      else x = __builtin_amdgcn_exp2f(c * __builtin_fmaf(a.q2, c2, a.p2));
+      v[e] = z * __builtin_amdgcn_rcpf(1.f + x);
     }
   }
 }
 
 // v[e] *= act'(z[e]); relu'(0) = 0, relu'(NaN) = NaN
-template <int NV>
+template <bool FINE, int NV>
 __device__ __forceinline__ void act_slope_mul(const ActParams& a, const float (&z)[NV], float (&v)[NV]) {
   if (a.kind == 0) return;
   if (a.kind == 1) {
 #pragma unroll
-    for (int e = 0; e < NV; ++e) v[e] *= z[e] > 0.f ? 1.f : z[e] <= 0.f ? 0.f : z[e];
+    for (int e = 0; e < NV; ++e) v[e] *= nan_or(z[e], z[e] > 0.f ? 1.f : 0.f);
   } else if (a.kind == 2) {
-    // Phi + z phi; past |z| = 20 phi is 0 in float32
+    // Phi + z phi; past |z| = 16 phi is 0 in float32
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
-      const float c = at_most(at_least(z[e], -20.f), 20.f);
-      const float ex = normal_exp(c);
-      v[e] *= __builtin_fmaf(c * 0.3989422804014327f, ex, normal_cdf(c, ex));
+      const float c = __builtin_amdgcn_fmed3f(z[e], -16.f, 16.f), ex = normal_exp<FINE>(c);
+      const float h = normal_tail(__builtin_fabsf(c), ex);
+      v[e] *= nan_or(z[e], __builtin_fmaf(c * 0.3989422804014327f, ex, c < 0.f ? h : 1.f - h));
     }
   } else {
-    // sigma + z sigma (1 - sigma) (p + 3 q z^2); past |z| = 200 it is 0 or 1
+    // sigma + z sigma (1 - sigma) (p + 3 q z^2) with sigma = 1 / (1 + x),
+    // 1 - sigma = x sigma, x = e^-w (bounded by 2^115: sigma (1 - sigma) is
+    // then below 2^-115 anyway); past |z| = 100 it is 0 or 1
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
-      const float c = at_most(at_least(z[e], -200.f), 200.f), c2 = c * c;
-      const float w = c * __builtin_fmaf(a.q, c2, a.p);
-      const float s = sigma(w), n = sigma(-w);       // 1 - s without cancellation
-      v[e] *= __builtin_fmaf(c * __builtin_fmaf(3.f * a.q, c2, a.p), s * n, s);
+      const float c = __builtin_amdgcn_fmed3f(z[e], -100.f, 100.f), c2 = c * c;
+      float x;
+      if constexpr (FINE) x = exp_fine(fminf(fmaxf(-c * __builtin_fmaf(a.q, c2, a.p), -80.f), 80.f));
+      else x = __builtin_amdgcn_exp2f(fminf(c * __builtin_fmaf(a.q2, c2, a.p2), 115.f));
+      const float s = __builtin_amdgcn_rcpf(1.f + x);
+      v[e] *= nan_or(z[e], __builtin_fmaf(c * __builtin_fmaf(3.f * a.q, c2, a.p), s * (x * s), s));
     }
   }
 }
@@ -163,20 +176,36 @@ __device__ __forceinline__ int group_byte(uint32_t amax_bits) {
   return b < 1 ? 1 : b;
 }
 
-// The code of v under scale byte b (255: none).
+// The code of v under scale byte b (not 255) in the low byte; the rest of the
+// word is not its sign. v 2^-e, moved out to +-0.75 where it is smaller but
+// not 0 (so that it rounds to +-1), is rounded to an integer, ties to even, by
+// adding 3 2^22: the sum's last 8 bits are the code.
+__device__ __forceinline__ uint32_t group_code_bits(float v, float inv) {
+  const float t = v * inv;
+  const float m = __builtin_copysignf(fmaxf(__builtin_fabsf(t), 0.75f), t);
+  return __float_as_uint((t == 0.f ? t : m) + 12582912.f);
+}
+// 2^-e = 2^(127 - b); b in [1, 249]
+__device__ __forceinline__ float group_inverse(int b) { return __uint_as_float((uint32_t)(254 - b) << 23); }
+
 __device__ __forceinline__ int8_t group_code(float v, int b) {
-  if (b == 255) return 0;
-  // 2^-e = 2^(127 - b); b in [1, 249]
-  const int q = (int)__builtin_rintf(v * __uint_as_float((uint32_t)(254 - b) << 23));
-  return (int8_t)(q != 0 ? q : v > 0.f ? 1 : v < 0.f ? -1 : 0);
+  return b == 255 ? 0 : (int8_t)group_code_bits(v, group_inverse(b));
 }
 
 // Eight values as codes of scale byte b, packed four to a word.
 __device__ __forceinline__ u32x2 group_codes(const float (&v)[8], int b) {
-  uint32_t w[2] = {0u, 0u};
+  const float inv = group_inverse(b);
+  u32x2 w;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w[e >> 2] |= (uint32_t)(uint8_t)group_code(v[e], b) << (8 * (e & 3));
-  return u32x2{w[0], w[1]};
+  for (int h = 0; h < 2; ++h) {
+    uint32_t c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = group_code_bits(v[4 * h + e], inv);
+    const uint32_t lo = __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400u);   // bytes c0, c1, 0, 0
+    const uint32_t hi = __builtin_amdgcn_perm(c[3], c[2], 0x04000c0cu);   // bytes 0, 0, c2, c3
+    w[h] = b == 255 ? 0u : lo | hi;
+  }
+  return w;
 }
 
 // The scale that byte b stands for; 255: NaN.
@@ -215,6 +244,9 @@ template <> struct Raw8<uint16_t> {
   __device__ __forceinline__ void load(const void* p, long at) {
     v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + at);
   }
+  // eight bytes of codes in their place
+  __device__ __forceinline__ void set2(u32x2 c) { v[0] = c[0]; v[1] = c[1]; }
+  __device__ __forceinline__ u32x2 get2() const { return u32x2{v[0], v[1]}; }
   __device__ __forceinline__ void get(float (&o)[8]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -267,56 +299,44 @@ template <typename OutT> struct Side {
   int b;             // scale byte of the codes
 };
 
-// epilogue_lowrank (ring.hpp) with the rest of the layer behind it. One
-// 16-row strip of the wave's outputs at a time goes through LDS in float32,
-// so that a lane then holds 8 consecutive columns of a row: every operand
-// (residual, saved z, codes) moves in 16- or 8-byte pieces, the activation
-// sees the unrounded z, four neighbouring lanes hold one 32-column group,
-// and y is rounded once. What bounds it is the latency of the side operands
-// (two or three waves per SIMD): in bfloat16 all strips' are fetched before
-// the first strip is formed, in float32 (twice the registers) one strip
-// ahead.
-template <int BM, int BN, int R, bool SCALED, bool AFF = false, typename OutT, typename Epi,
-          typename AccT, int FM, int FN>
-__device__ __forceinline__ void epilogue_fused(const AccT (&acc)[FM][FN], const float* E, int M,
-                                               int N, int m0, int n0, int wr0, int wc0, float s,
-                                               OutT* out, const Epi& ep, int8_t* strip) {
-  constexpr bool GRAD = std::is_same<Epi, GradEpi>::value;
-  static_assert(!AFF || SCALED, "the affine form uses the row scales");
-  const int lane = threadIdx.x & 63;
-  const float* ts = E;
-  const float* qs = E + BM * R;
-  const float* rsv = E + (BM + BN) * R;
-  const float* csv = rsv + BM;
-  const float* rav = csv + BN;
-  constexpr int PITCH = FN * 64 + 16;
-  constexpr int CPR = 2 * FN;                 // 8-column pieces per strip row
-  constexpr int PN = CPR * 16 / 64;           // pieces per lane and strip
+// Shape of a wave's FM x FN grid of 16 x 16 blocks in epilogue_fused.
+template <typename OutT, int FM, int FN> struct EpiShape {
+  static constexpr int PITCH = FN * 64 + 16;               // bytes of a strip row
+  static constexpr int CPR = 2 * FN;                       // 8-column pieces per strip row
+  static constexpr int PN = CPR * 16 / 64;                 // pieces per lane and strip
+  static constexpr int AHEAD = sizeof(OutT) == 2 ? FM : FM < 2 ? FM : 2;   // strips whose operands are held
+  static constexpr int NB = 64 % CPR == 0 ? 1 : PN;        // distinct column pieces of a lane
   static_assert(CPR % 4 == 0, "four neighbouring lanes hold one 32-column group");
-  constexpr int AHEAD = sizeof(OutT) == 2 ? FM : 2;        // strips whose operands are held
-  constexpr int NB = 64 % CPR == 0 ? 1 : PN;               // distinct column pieces of a lane
+};
 
-  Side<OutT> side[AHEAD][PN];
-  // output position of piece p of strip i (clamped to 0 where not live)
-  auto place = [&](int i, int p, int& m, int& n) {
-    const int q = lane + 64 * p;
-    m = m0 + wr0 + i * 16 + q / CPR;
-    n = n0 + wc0 + (q % CPR) * 8;
-    return m < M && n < N;                                 // N % 16 == 0: 8 columns in or out
-  };
-  auto fetch = [&](int i) {
+// The side operands of a wave's outputs: fetched (start) as early as the
+// caller has registers for them, before what is left of its own work.
+template <typename OutT, typename Epi, int FM, int FN> struct EpiSide {
+  typedef EpiShape<OutT, FM, FN> Sh;
+  static constexpr bool GRAD = std::is_same<Epi, GradEpi>::value;
+  Side<OutT> side[Sh::AHEAD][Sh::PN];
+  float bias[Sh::NB][8];
+
+  // output position of piece p of strip i; N % 16 == 0: 8 columns in or out
+  static __device__ __forceinline__ bool place(int i, int p, int M, int N, int row0, int col0, int& m, int& n) {
+    const int q = (threadIdx.x & 63) + 64 * p;
+    m = row0 + i * 16 + q / Sh::CPR;
+    n = col0 + (q % Sh::CPR) * 8;
+    return m < M && n < N;
+  }
+
+  __device__ __forceinline__ void fetch(const Epi& ep, int i, int M, int N, int row0, int col0) {
 #pragma unroll
-    for (int p = 0; p < PN; ++p) {
+    for (int p = 0; p < Sh::PN; ++p) {
       int m, n;
-      const bool live = place(i, p, m, n);
+      const bool live = place(i, p, M, N, row0, col0, m, n);
       const long at = live ? (long)m * N + n : 0;
-      Side<OutT>& sd = side[i % AHEAD][p];
+      Side<OutT>& sd = side[i % Sh::AHEAD][p];
       if constexpr (GRAD) {
         if (ep.act.kind != 0) {
           if (ep.zc != nullptr) {
             const u32x2 c = *reinterpret_cast<const u32x2*>(ep.zc + at);
-            sd.z.v[0] = c[0];
-            sd.z.v[1] = c[1];
+            sd.z.set2(c);
             sd.b = ep.zs[live ? (long)m * ep.zg + n / kGroup : 0];
           } else {
             sd.z.load(ep.z, at);
@@ -327,19 +347,48 @@ __device__ __forceinline__ void epilogue_fused(const AccT (&acc)[FM][FN], const 
         if (ep.res != nullptr) sd.r.load(ep.res, at);
       }
     }
-  };
-  float bias[NB][8];
-  if constexpr (!GRAD) {
-    if (ep.bias != nullptr) {
+  }
+
+  __device__ __forceinline__ void start(const Epi& ep, int M, int N, int row0, int col0) {
+    if constexpr (!GRAD) {
+      if (ep.bias != nullptr) {
 #pragma unroll
-      for (int p = 0; p < NB; ++p) {
-        const int n = n0 + wc0 + ((lane + 64 * p) % CPR) * 8;
-        load8(ep.bias + (n < N ? n : 0), bias[p]);
+        for (int p = 0; p < Sh::NB; ++p) {
+          const int n = col0 + (((threadIdx.x & 63) + 64 * p) % Sh::CPR) * 8;
+          load8(ep.bias + (n < N ? n : 0), bias[p]);
+        }
       }
     }
-  }
 #pragma unroll
-  for (int i = 0; i < AHEAD && i < FM; ++i) fetch(i);
+    for (int i = 0; i < Sh::AHEAD; ++i) fetch(ep, i, M, N, row0, col0);
+  }
+};
+
+// epilogue_lowrank (ring.hpp) with the rest of the layer behind it. One
+// 16-row strip of the wave's outputs at a time goes through LDS in float32,
+// so that a lane then holds 8 consecutive columns of a row: every operand
+// (residual, saved z, codes) moves in 16- or 8-byte pieces, the activation
+// sees the unrounded z, four neighbouring lanes hold one 32-column group,
+// and y is rounded once. What bounds it is the latency of the side operands
+// (two or three waves per SIMD), hence EpiSide: in bfloat16 all strips' are
+// fetched before the first strip is formed, in float32 (twice the registers)
+// two strips'.
+template <int BM, int BN, int R, bool SCALED, bool AFF = false, typename OutT, typename Epi,
+          typename AccT, int FM, int FN>
+__device__ __forceinline__ void epilogue_fused(const AccT (&acc)[FM][FN], const float* E, int M,
+                                               int N, int m0, int n0, int wr0, int wc0, float s,
+                                               OutT* out, const Epi& ep, EpiSide<OutT, Epi, FM, FN>& es,
+                                               int8_t* strip) {
+  typedef EpiShape<OutT, FM, FN> Sh;
+  constexpr bool GRAD = std::is_same<Epi, GradEpi>::value;
+  constexpr int PITCH = Sh::PITCH, CPR = Sh::CPR, PN = Sh::PN, AHEAD = Sh::AHEAD, NB = Sh::NB;
+  static_assert(!AFF || SCALED, "the affine form uses the row scales");
+  const int lane = threadIdx.x & 63;
+  const float* ts = E;
+  const float* qs = E + BM * R;
+  const float* rsv = E + (BM + BN) * R;
+  const float* csv = rsv + BM;
+  const float* rav = csv + BN;
 
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
@@ -377,16 +426,16 @@ __device__ __forceinline__ void epilogue_fused(const AccT (&acc)[FM][FN], const 
     for (int p = 0; p < PN; ++p) {
       const int q = lane + 64 * p;
       int m, n;
-      const bool live = place(i, p, m, n);
+      const bool live = es.place(i, p, M, N, m0 + wr0, n0 + wc0, m, n);
       const long at = (long)m * N + n;
-      const Side<OutT>& sd = side[i % AHEAD][p];
+      const Side<OutT>& sd = es.side[i % AHEAD][p];
       float v[8], w[8];
       load8(reinterpret_cast<const float*>(strip + (q / CPR) * PITCH + (q % CPR) * 32), v);
       if constexpr (GRAD) {
         if (ep.act.kind != 0) {
-          if (ep.zc != nullptr) group_values(u32x2{sd.z.v[0], sd.z.v[1]}, sd.b, w);
+          if (ep.zc != nullptr) group_values(sd.z.get2(), sd.b, w);
           else sd.z.get(w);
-          act_slope_mul(ep.act, w, v);
+          act_slope_mul<sizeof(OutT) == 4>(ep.act, w, v);
         }
         if (ep.add != nullptr) {
           sd.r.get(w);
@@ -396,7 +445,7 @@ __device__ __forceinline__ void epilogue_fused(const AccT (&acc)[FM][FN], const 
       } else {
         if (ep.bias != nullptr) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += bias[p % NB][e];
+          for (int e = 0; e < 8; ++e) v[e] += es.bias[p % NB][e];
         }
         if (ep.z != nullptr && live) store8(static_cast<OutT*>(ep.z) + at, v);
         if (ep.zc != nullptr) {
@@ -409,7 +458,7 @@ __device__ __forceinline__ void epilogue_fused(const AccT (&acc)[FM][FN], const 
             if (n % kGroup == 0) ep.zs[(long)m * ep.zg + n / kGroup] = (uint8_t)b;
           }
         }
-        act_apply(ep.act, v);
+        act_apply<sizeof(OutT) == 4>(ep.act, v);
         if (ep.res != nullptr) {
           sd.r.get(w);
 #pragma unroll
@@ -418,7 +467,7 @@ __device__ __forceinline__ void epilogue_fused(const AccT (&acc)[FM][FN], const 
       }
       if (live) store8(out + at, v);
     }
-    if (i + AHEAD < FM) fetch(i + AHEAD);
+    if (i + AHEAD < FM) es.fetch(ep, i + AHEAD, M, N, m0 + wr0, n0 + wc0);
   }
 }
 

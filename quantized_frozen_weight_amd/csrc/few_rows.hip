@@ -406,7 +406,7 @@ __global__ __launch_bounds__(kThreads) void fwd_few_kernel(FewArgs a) {
   }
   if (mine) {
     float v[1] = {z};
-    act_apply(a.epi.act, v);
+    act_apply<std::is_same<T, F32>::value>(a.epi.act, v);
     if (a.epi.res != nullptr) v[0] += eres;
     store_out(static_cast<E*>(a.y) + (long)em * N + en, v[0]);
   }

@@ -201,12 +201,14 @@ __global__ __launch_bounds__(256) void fwd_a8w4_kernel(A8W4ArgsOf<EPI> a) {
   }
 
   float* E = reinterpret_cast<float*>(ring);
+  EpiSide<uint16_t, FwdEpi, FM, FN> es;
+  if constexpr (EPI) es.start(a.epi, M, N, m0 + wm * (BM / 2), n0 + wn * (BN / 2));
   __syncthreads();                                    // every wave is done with the ring
   ep.store(E, M, N, m0, n0, a.r);
   __syncthreads();
   if constexpr (EPI)
     epilogue_fused<BM, BN, R, true>(acc, E, M, N, m0, n0, wm * (BM / 2), wn * (BN / 2), a.s, a.y,
-                                    a.epi, ring + EPB + wid * STRIP);
+                                    a.epi, es, ring + EPB + wid * STRIP);
   else
     epilogue_lowrank<BM, BN, R, true>(acc, E, M, N, m0, n0, wm * (BM / 2), wn * (BN / 2), a.s, a.y,
                                       ring + EPB + wid * STRIP);

@@ -68,6 +68,7 @@
 // partial u in the workspace, and a second launch adds them in split order
 // and does what the one-pass kernel does after its loop (u, the dA partial,
 // the epilogue).
+#include "bwd_common.hpp"
 #include "epilogue.hpp"
 #include "launch.hpp"
 #include "outlier.hpp"
@@ -76,9 +77,6 @@
 namespace qlora {
 
 namespace {
-
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kMaxWideSplits = 8;   // contraction splits of the 128 x 128 backward
 
@@ -124,119 +122,6 @@ __device__ __forceinline__ const int8_t* x8_codes(const BwdArgs&) { return nullp
 __device__ __forceinline__ const int8_t* x8_codes(const BwdExtArgs& a) { return a.xq; }
 __device__ __forceinline__ const float* x8_scales(const BwdArgs&) { return nullptr; }
 __device__ __forceinline__ const float* x8_scales(const BwdExtArgs& a) { return a.sx; }
-
-__device__ __forceinline__ uint32_t pk_bf16(float lo, float hi) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
-}
-
-// Two float32 values each as a sum of three bf16 values, v = hi + mid + lo:
-// hi is the bf16 nearest to v, mid the bf16 nearest to the remainder
-// v - hi, lo the bf16 nearest to v - hi - mid (both remainders exact in
-// float32). Products with a bf16 operand on the matrix cores then carry v to
-// float32 precision (relative error at most 2^-24) instead of 8 significant
-// bits, which keeps the float32 adapter's gradients float32-accurate: B (for
-// u = dy B^T) and t (for dB = s t^T dy) enter their products as hi, mid and
-// lo columns of one operand. A non-finite hi (v infinite or NaN, or past the
-// bf16 range) takes mid = lo = 0, so hi alone carries the infinity or NaN.
-// Returns the packed hi pair; the mid and lo pairs go to mid2 and lo2.
-__device__ __forceinline__ uint32_t pk_bf16_split3(float a, float b, uint32_t& mid2, uint32_t& lo2) {
-  const uint32_t h = pk_bf16(a, b);
-  const bool fa = (h & 0x7f80u) != 0x7f80u, fb = (h & 0x7f800000u) != 0x7f800000u;
-  const float ra = fa ? a - __uint_as_float(h << 16) : 0.f;
-  const float rb = fb ? b - __uint_as_float(h & 0xffff0000u) : 0.f;
-  mid2 = pk_bf16(ra, rb);
-  lo2 = pk_bf16(ra - __uint_as_float(mid2 << 16), rb - __uint_as_float(mid2 & 0xffff0000u));
-  return h;
-}
-
-// The rank-r products u = dy B^T and dB^T = dy^T t run with 3R operand
-// columns: j in [0, R) the hi parts, [R, 2R) the mid parts, [2R, 3R) the lo
-// parts. The sum for rank j (j = cb * 16 + lane % 16 < R) of its columns j,
-// j + R, j + 2R of the accumulators (column c at block c / 16, lane c % 16 of
-// the 16-lane group): R = 4 and 8 put some of them in other lanes of the
-// group, read through a lane permute that every lane executes; for R >= 16
-// all three are the same lane of blocks cb, cb + R / 16, cb + R / 8.
-template <int R, int UCB>
-__device__ __forceinline__ float split3_sum(const f32x4 (&v)[UCB], int cb, int ii, int lane) {
-  if constexpr (R == 4) {
-    static_assert(UCB == 1, "12 columns in one block");
-    const int g = lane & ~15;
-    return v[0][ii] + __shfl(v[0][ii], g | ((lane + 4) & 15)) + __shfl(v[0][ii], g | ((lane + 8) & 15));
-  } else if constexpr (R == 8) {
-    static_assert(UCB == 2, "24 columns in two blocks");
-    return v[0][ii] + __shfl(v[0][ii], (lane & ~15) | ((lane + 8) & 15)) + v[1][ii];
-  } else {
-    static_assert(R % 16 == 0 && UCB == 3 * R / 16, "whole blocks per part");
-    return v[cb][ii] + v[cb + R / 16][ii] + v[cb + R / 8][ii];
-  }
-}
-
-// NR transposing LDS reads (ds_read_b64_tr_b16) issued together and completed
-// in the same asm block. Written as asm because the builtin form makes the
-// compiler wait for every direct-to-LDS load in flight (the ring's later
-// stages included) before each read.
-template <int NR>
-__device__ __forceinline__ void tr16_reads(const uint32_t (&addr)[NR], uint64_t (&out)[NR]) {
-  static_assert(NR == 4 || NR == 8, "4 or 8 reads");
-  if constexpr (NR == 4) {
-    asm volatile(
-        "ds_read_b64_tr_b16 %0, %4\n\t"
-        "ds_read_b64_tr_b16 %1, %5\n\t"
-        "ds_read_b64_tr_b16 %2, %6\n\t"
-        "ds_read_b64_tr_b16 %3, %7\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(out[0]), "=&v"(out[1]), "=&v"(out[2]), "=&v"(out[3])
-        : "v"(addr[0]), "v"(addr[1]), "v"(addr[2]), "v"(addr[3])
-        : "memory");
-  } else {
-    asm volatile(
-        "ds_read_b64_tr_b16 %0, %8\n\t"
-        "ds_read_b64_tr_b16 %1, %9\n\t"
-        "ds_read_b64_tr_b16 %2, %10\n\t"
-        "ds_read_b64_tr_b16 %3, %11\n\t"
-        "ds_read_b64_tr_b16 %4, %12\n\t"
-        "ds_read_b64_tr_b16 %5, %13\n\t"
-        "ds_read_b64_tr_b16 %6, %14\n\t"
-        "ds_read_b64_tr_b16 %7, %15\n\t"
-        "s_waitcnt lgkmcnt(0)"
-        : "=&v"(out[0]), "=&v"(out[1]), "=&v"(out[2]), "=&v"(out[3]),
-          "=&v"(out[4]), "=&v"(out[5]), "=&v"(out[6]), "=&v"(out[7])
-        : "v"(addr[0]), "v"(addr[1]), "v"(addr[2]), "v"(addr[3]),
-          "v"(addr[4]), "v"(addr[5]), "v"(addr[6]), "v"(addr[7])
-        : "memory");
-  }
-}
-
-// The eight codes of a packed 4-bit word (nibble e = k offset e, two's
-// complement) times sc: w ^ 0x88888888 turns each code q into q + 8 in
-// [0, 15], two masks spread the nibbles over bytes (v_cvt_f32_ubyte takes a
-// byte in one instruction), and fma(q + 8, sc, -8 sc) rounds q sc exactly
-// once, as q * sc would.
-__device__ __forceinline__ void nibble_vals(uint32_t w, float sc, float (&v)[8]) {
-  const uint32_t u = w ^ 0x88888888u;
-  const uint32_t lo = u & 0x0f0f0f0fu, hi = (u >> 4) & 0x0f0f0f0fu;   // even, odd e
-  const float nsc = -8.f * sc;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    v[2 * b] = __builtin_fmaf((float)((lo >> (8 * b)) & 0xffu), sc, nsc);
-    v[2 * b + 1] = __builtin_fmaf((float)((hi >> (8 * b)) & 0xffu), sc, nsc);
-  }
-}
-
-// a0 or a1 by a wave-uniform flag, as selects rather than a branch (the u
-// products take the odd or even row blocks of A by the wave's column half)
-__device__ __forceinline__ bf16x8 pick_frag(const bf16x8& a0, const bf16x8& a1, bool second) {
-  const u32x4 x = __builtin_bit_cast(u32x4, a0), y = __builtin_bit_cast(u32x4, a1);
-  u32x4 r;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) r[e] = second ? y[e] : x[e];
-  return __builtin_bit_cast(bf16x8, r);
-}
-
-// 32-bit LDS address of a pointer into a __shared__ array.
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
-}
 
 // Chunk swizzle of a code tile with RB-byte rows (RB = 64 or 128).
 template <int RB>
@@ -284,46 +169,6 @@ __device__ __forceinline__ void da_partial(const int8_t* Xs, const float* E, con
   for (; b0 + 16 <= rows; b0 += 16) batch(b0, false);
   if (b0 < rows) batch(b0, true);
 }
-
-// An x tile from the 8-bit row checkpoint: sixteen codes of one row per
-// thread and unit, loaded to registers (fetch) and written (put) as exact
-// bfloat16 integers in the layout of the bf16 tile (swizzled 128-byte row
-// halves), so that the dA products read either tile alike. Half the bytes of
-// bf16 rows; the rows' scales stay out of the rounding (they multiply u or
-// the float32 products). thr: the thread among the 256 that share the tile.
-// Rows past M are zero, as are columns past K.
-template <int BM, int BN>
-struct X8Tile {
-  static constexpr int NU = BM * BN / 4096, UPR = BN / 16, RH = BN / 64;
-  u32x4 v[NU];
-  __device__ __forceinline__ void fetch(const int8_t* xq, int M, int K, int m0, int k0, int thr) {
-#pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      const int u = thr + 256 * i, gm = m0 + u / UPR, gk = k0 + 16 * (u % UPR);
-      const bool ok = gm < M && gk < K;
-      const u32x4 w = *reinterpret_cast<const u32x4*>(xq + (ok ? (long)gm * K + gk : 0));
-      v[i] = ok ? w : u32x4{0u, 0u, 0u, 0u};
-    }
-  }
-  __device__ __forceinline__ void put(int8_t* Xs, int thr) const {
-#pragma unroll
-    for (int i = 0; i < NU; ++i) {
-      const int u = thr + 256 * i, row = u / UPR, col = 16 * (u % UPR);
-      const int hrow = row * RH + col / 64, c = (col % 64) / 8;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        u32x4 o;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t w = v[i][2 * h + e];
-          o[2 * e] = pack_int_bf16x2((int8_t)w, (int8_t)(w >> 8));
-          o[2 * e + 1] = pack_int_bf16x2((int8_t)(w >> 16), (int8_t)(w >> 24));
-        }
-        *reinterpret_cast<u32x4*>(Xs + swz128(hrow, c + h)) = o;
-      }
-    }
-  }
-};
 
 // W4: 4-bit weights (two codes per byte, fp16 scale per 128 k); else int8.
 // EXT: x may be its 8-bit row checkpoint, and dx goes through the gradient
@@ -966,10 +811,12 @@ __global__ __launch_bounds__(512) void bwd_pc_kernel(BwdArgsOf<EXT> a) {
     // output staging strips in the converted-code buffers, free after the loop
     constexpr int STRIP = EXT ? fused_strip_bytes<FN>() : epi_strip_bytes<uint16_t, FN>();
     static_assert(4 * STRIP <= 2 * CBSZ, "staging strips fit");
-    if constexpr (EXT)
+    if constexpr (EXT) {
+      EpiSide<uint16_t, GradEpi, FM, FN> es;
+      es.start(a.ge, M, K, m0 + wm * (BM / 2), k0 + wn * (BN / 2));
       epilogue_fused<BM, BN, R, false>(acc, E, M, K, m0, k0, wm * (BM / 2), wn * (BN / 2), a.s, a.dx,
-                                       a.ge, CB0 + wid * STRIP);
-    else
+                                       a.ge, es, CB0 + wid * STRIP);
+    } else
       epilogue_lowrank<BM, BN, R, false>(acc, E, M, K, m0, k0, wm * (BM / 2), wn * (BN / 2), a.s, a.dx,
                                          CB0 + wid * STRIP);
   }
@@ -1702,9 +1549,11 @@ __global__ __launch_bounds__(256, 2) void bwd_wide_kernel(BwdArgsOf<EXT> a) {
   if constexpr (EXT) {
     // the float strips go over the x tile, once every wave has read it
     static_assert(4 * fused_strip_bytes<FN>() <= XTSZ, "staging strips fit");
+    EpiSide<uint16_t, GradEpi, FM, FN> es;
+    es.start(a.ge, M, K, m0 + wm * (BM / 2), k0 + wn * (BN / 2));
     __syncthreads();
     epilogue_fused<BM, BN, R, false>(acc, E, M, K, m0, k0, wm * (BM / 2), wn * (BN / 2), a.s, a.dx,
-                                     a.ge, Xs + wid * fused_strip_bytes<FN>());
+                                     a.ge, es, Xs + wid * fused_strip_bytes<FN>());
   } else {
     // output staging strips in the converted-code buffer, free after the loop
     static_assert(4 * epi_strip_bytes<uint16_t, FN>() <= CBSZ, "staging strips fit");
@@ -1730,11 +1579,12 @@ __global__ __launch_bounds__(512) void bwd_fixup_kernel(BwdArgsOf<EXT> a) {
   constexpr int EFL = (BM + HN) * R;                    // U [BM][R] | A^T [R][HN]
   constexpr int XSZ = BM * HN * 2;                      // x [BM][HN] bf16, 64-byte rows
   constexpr int STRIP = EXT ? fused_strip_bytes<FN>() : epi_strip_bytes<uint16_t, FN>();
-  __shared__ __attribute__((aligned(1024))) int8_t lds[XSZ + EFL * 4 + 8 * STRIP + (EXT ? BM * 4 : 0)];
+  __shared__ __attribute__((aligned(1024))) int8_t lds[XSZ + EFL * 4 + 8 * STRIP + (EXT ? BM * R * 4 : 0)];
   int8_t* Xs = lds;
   float* E = reinterpret_cast<float*>(lds + XSZ);
   int8_t* strips = lds + XSZ + EFL * 4;
-  float* RSs = reinterpret_cast<float*>(strips + 8 * STRIP);   // EXT: row scales of x [BM]
+  // the dA partial's operand: U, or (x in 8 bits) U times the row scales
+  float* V = EXT ? reinterpret_cast<float*>(strips + 8 * STRIP) : E;
 
   const int tid = threadIdx.x, lane = tid & 63, v = wave_id();
   const int M = a.M, K = a.K, r = a.r, nsp = a.splits;
@@ -1767,7 +1617,6 @@ __global__ __launch_bounds__(512) void bwd_fixup_kernel(BwdArgsOf<EXT> a) {
     const bool ok = gm < M && gk < K;
     xc = *reinterpret_cast<const u32x2*>(x8_codes(a) + (ok ? (long)gm * K + gk : 0));
     if (!ok) xc = u32x2{0u, 0u};
-    if (tid < BM) RSs[tid] = x8_scales(a)[m0 + tid < M ? m0 + tid : M - 1];
   } else {
     const int row = 16 * v + (lane >> 2);
     const int c = (lane & 3) ^ ((row >> 2) & 3), gm = m0 + row, gk = k0 + c * 8;
@@ -1775,6 +1624,9 @@ __global__ __launch_bounds__(512) void bwd_fixup_kernel(BwdArgsOf<EXT> a) {
                              : (const void*)zero_chunk(lane);
     lds_dma16(src, Xs + 16 * v * 64);
   }
+
+  EpiSide<uint16_t, GradEpi, 1, FN> es;
+  if constexpr (EXT) es.start(a.ge, M, K, m0 + 16 * v, k0);
 
   // U[m][j] = sum over splits of the partial u (rows past M and ranks past r: 0)
   for (int e = tid; e < BM * R; e += 512) {
@@ -1784,10 +1636,13 @@ __global__ __launch_bounds__(512) void bwd_fixup_kernel(BwdArgsOf<EXT> a) {
     float uv[NSPL];
 #pragma unroll
     for (int sp = 0; sp < NSPL; ++sp) uv[sp] = pu[(long)(sp < nsp ? sp : 0) * M * r];
+    float rs = 1.f;
+    if (x8on) rs = x8_scales(a)[gm < M ? gm : M - 1];
     float u = 0.f;
 #pragma unroll
     for (int sp = 0; sp < NSPL; ++sp) u += sp < nsp ? uv[sp] : 0.f;
     E[e] = ok ? u : 0.f;
+    if constexpr (EXT) V[e] = ok ? u * rs : 0.f;
   }
   for (int e = tid; e < R * HN; e += 512) {
     const int j = e / HN, col = e % HN, gk = k0 + col;
@@ -1828,11 +1683,10 @@ __global__ __launch_bounds__(512) void bwd_fixup_kernel(BwdArgsOf<EXT> a) {
       for (int m = 0; m < rows_here; ++m) {
         const uint16_t xb = *reinterpret_cast<const uint16_t*>(
             Xs + m * 64 + (((kl >> 3) ^ ((m >> 2) & 3)) << 4) + 2 * (kl & 7));
-        float xv = __uint_as_float((uint32_t)xb << 16);
-        if (x8on) xv *= RSs[m];
+        const float xv = __uint_as_float((uint32_t)xb << 16);
 #pragma unroll
         for (int jj = 0; jj < JPT; ++jj)
-          if (jb + 16 * jj < R) da[jj] = __builtin_fmaf(xv, E[m * R + jb + 16 * jj], da[jj]);
+          if (jb + 16 * jj < R) da[jj] = __builtin_fmaf(xv, V[m * R + jb + 16 * jj], da[jj]);
       }
     }
     if (k0 + kl < K) {
@@ -1845,7 +1699,7 @@ __global__ __launch_bounds__(512) void bwd_fixup_kernel(BwdArgsOf<EXT> a) {
   }
 
   if constexpr (EXT)
-    epilogue_fused<BM, HN, R, false>(acc, E, M, K, m0, k0, 16 * v, 0, a.s, a.dx, a.ge,
+    epilogue_fused<BM, HN, R, false>(acc, E, M, K, m0, k0, 16 * v, 0, a.s, a.dx, a.ge, es,
                                      strips + v * STRIP);
   else
     epilogue_lowrank<BM, HN, R, false>(acc, E, M, K, m0, k0, 16 * v, 0, a.s, a.dx,
@@ -1875,6 +1729,23 @@ void launch_pc(BwdArgsOf<EXT> a, hipStream_t st) {
   // (4-bit layers of rank above 16 take the 128 x 128 tiles: bwd_row_block)
 }
 
+// The split contraction's second launch (tiles_x set for 128-wide tiles).
+template <bool EXT>
+void fixup_launch(const BwdArgsOf<EXT>& a, hipStream_t st) {
+  const dim3 fgrid((unsigned)(4 * a.tiles_x * ((a.M + 127) / 128)));
+  if (a.splits <= 4) {
+    if (a.r <= 4) bwd_fixup_kernel<4, 4, EXT><<<fgrid, 512, 0, st>>>(a);
+    else if (a.r <= 8) bwd_fixup_kernel<8, 4, EXT><<<fgrid, 512, 0, st>>>(a);
+    else if (a.r <= 16) bwd_fixup_kernel<16, 4, EXT><<<fgrid, 512, 0, st>>>(a);
+    else bwd_fixup_kernel<32, 4, EXT><<<fgrid, 512, 0, st>>>(a);
+  } else {
+    if (a.r <= 4) bwd_fixup_kernel<4, kMaxWideSplits, EXT><<<fgrid, 512, 0, st>>>(a);
+    else if (a.r <= 8) bwd_fixup_kernel<8, kMaxWideSplits, EXT><<<fgrid, 512, 0, st>>>(a);
+    else if (a.r <= 16) bwd_fixup_kernel<16, kMaxWideSplits, EXT><<<fgrid, 512, 0, st>>>(a);
+    else bwd_fixup_kernel<32, kMaxWideSplits, EXT><<<fgrid, 512, 0, st>>>(a);
+  }
+}
+
 template <bool W4, bool EXT, bool AFF = false, bool SPLIT = false, int BN = 128>
 void launch_wide(BwdArgsOf<EXT> a, hipStream_t st) {
   static_assert(BN == 128 || (!W4 && !AFF && !SPLIT), "64-wide tiles: plain int8, one pass");
@@ -1885,20 +1756,7 @@ void launch_wide(BwdArgsOf<EXT> a, hipStream_t st) {
   else if (a.r <= 8) bwd_wide_kernel<W4, BM, BN, S, 8, AFF, SPLIT, EXT && !SPLIT><<<grid, 256, 0, st>>>(a);
   else if (a.r <= 16) bwd_wide_kernel<W4, BM, BN, S, 16, AFF, SPLIT, EXT && !SPLIT><<<grid, 256, 0, st>>>(a);
   else bwd_wide_kernel<W4, BM, BN, S, 32, AFF, SPLIT, EXT && !SPLIT><<<grid, 256, 0, st>>>(a);
-  if constexpr (SPLIT) {
-    const dim3 fgrid((unsigned)(4 * a.tiles_x * ((a.M + BM - 1) / BM)));
-    if (a.splits <= 4) {
-      if (a.r <= 4) bwd_fixup_kernel<4, 4, EXT><<<fgrid, 512, 0, st>>>(a);
-      else if (a.r <= 8) bwd_fixup_kernel<8, 4, EXT><<<fgrid, 512, 0, st>>>(a);
-      else if (a.r <= 16) bwd_fixup_kernel<16, 4, EXT><<<fgrid, 512, 0, st>>>(a);
-      else bwd_fixup_kernel<32, 4, EXT><<<fgrid, 512, 0, st>>>(a);
-    } else {
-      if (a.r <= 4) bwd_fixup_kernel<4, kMaxWideSplits, EXT><<<fgrid, 512, 0, st>>>(a);
-      else if (a.r <= 8) bwd_fixup_kernel<8, kMaxWideSplits, EXT><<<fgrid, 512, 0, st>>>(a);
-      else if (a.r <= 16) bwd_fixup_kernel<16, kMaxWideSplits, EXT><<<fgrid, 512, 0, st>>>(a);
-      else bwd_fixup_kernel<32, kMaxWideSplits, EXT><<<fgrid, 512, 0, st>>>(a);
-    }
-  }
+  if constexpr (SPLIT) fixup_launch<EXT>(a, st);
 }
 
 // Stages per split of the 128 x 128 contraction, and the split count: split
@@ -1931,6 +1789,18 @@ void bwd_split_sizes(int M, int K, int N, int r, size_t* pdx_floats, size_t* pu_
   const size_t tiles = (size_t)((M + 127) / 128) * (size_t)((K + 127) / 128);
   *pdx_floats = (size_t)sp * tiles * 128 * 128;
   *pu_floats = (size_t)sp * (size_t)M * (size_t)r;
+}
+
+void bwd_split_plan(int M, int K, int N, int* splits, int* nks) { wide_split_plan(M, K, N, splits, nks); }
+
+void launch_bwd_fixup(int M, int K, int r, float s, const float* A, const uint16_t* x, const int8_t* xq,
+                      const float* sx, float* pdx, float* pu, int splits, uint16_t* dx, float* partA,
+                      const GradEpi& ge, hipStream_t st) {
+  BwdExtArgs a{};
+  a.M = M; a.K = K; a.r = r; a.s = s; a.A = A; a.x = x; a.xq = xq; a.sx = sx; a.pdx = pdx; a.pu = pu;
+  a.splits = splits; a.dx = dx; a.partA = partA; a.ge = ge;
+  a.tiles_x = (K + 127) / 128;
+  fixup_launch<true>(a, st);
 }
 
 int bwd_row_block(int fmt, int M, int K, int N, int r) {

@@ -353,6 +353,8 @@ __global__ __launch_bounds__(256) void fwd_i8_kernel(I8ArgsOf<EPI> a) {
         }
   } else {
     float* E = reinterpret_cast<float*>(ring);
+    EpiSide<OutT, FwdEpi, FM, FN> es;
+    if constexpr (EPI) es.start(a.epi, M, N, m0 + wm * (BM / 2), n0 + wn * (BN / 2));
     __syncthreads();                 // every wave is done with the ring
     if constexpr (AFF) {
       // corrections to the accumulators' owners through LDS ([BM][BN + 4]
@@ -382,7 +384,7 @@ __global__ __launch_bounds__(256) void fwd_i8_kernel(I8ArgsOf<EPI> a) {
       __syncthreads();
       if constexpr (EPI)
         epilogue_fused<BM, BN, R, true, true>(accf, E, M, N, m0, n0, wm * (BM / 2), wn * (BN / 2),
-                                              a.s, reinterpret_cast<OutT*>(a.y), a.epi,
+                                              a.s, reinterpret_cast<OutT*>(a.y), a.epi, es,
                                               ring + EPB + wid * STRIP);
       else
         epilogue_lowrank<BM, BN, R, true, true>(accf, E, M, N, m0, n0, wm * (BM / 2), wn * (BN / 2),
@@ -393,7 +395,7 @@ __global__ __launch_bounds__(256) void fwd_i8_kernel(I8ArgsOf<EPI> a) {
       __syncthreads();
       if constexpr (EPI)
         epilogue_fused<BM, BN, R, true>(acc, E, M, N, m0, n0, wm * (BM / 2), wn * (BN / 2),
-                                        a.s, reinterpret_cast<OutT*>(a.y), a.epi,
+                                        a.s, reinterpret_cast<OutT*>(a.y), a.epi, es,
                                         ring + EPB + wid * STRIP);
       else
         epilogue_lowrank<BM, BN, R, true>(acc, E, M, N, m0, n0, wm * (BM / 2), wn * (BN / 2),
@@ -435,6 +437,8 @@ __global__ __launch_bounds__(512) void fwd_fixup_kernel(I8ArgsOf<EPI> a) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) pv[sp][j] = P[(sp < nsp ? sp : 0) * pstride + j * 64];
 
+  EpiSide<OutT, FwdEpi, 1, FN> es;
+  if constexpr (EPI) es.start(a.epi, M, N, m0 + 16 * v, n0);
   Ep ep;
   if (tid < 256) ep.load(M, N, m0, n0, a.r, a.t, a.B, a.hd, a.sx, a.sw);
   i32x4 acc[1][FN];
@@ -449,7 +453,7 @@ __global__ __launch_bounds__(512) void fwd_fixup_kernel(I8ArgsOf<EPI> a) {
   __syncthreads();
   if constexpr (EPI)
     epilogue_fused<BM, HN, R, true>(acc, E, M, N, m0, n0, 16 * v, 0, a.s,
-                                    reinterpret_cast<OutT*>(a.y), a.epi, lds + EPB + v * STRIP);
+                                    reinterpret_cast<OutT*>(a.y), a.epi, es, lds + EPB + v * STRIP);
   else
     epilogue_lowrank<BM, HN, R, true>(acc, E, M, N, m0, n0, 16 * v, 0, a.s,
                                       reinterpret_cast<OutT*>(a.y), lds + EPB + v * STRIP);
@@ -503,6 +507,8 @@ __global__ __launch_bounds__(512) void fwd_fixup_aff_kernel(I8ArgsOf<EPI> a) {
 #pragma unroll
     for (int sp = 0; sp < NSPL; ++sp) cv[q][sp] = Qp[(sp < nsp ? sp : 0) * qstride];
   }
+  EpiSide<uint16_t, FwdEpi, 1, FN> es;
+  if constexpr (EPI) es.start(a.epi, M, N, m0 + 16 * v, n0);
   Ep ep;
   if (tid < 256) {
     ep.load(M, N, m0, n0, a.r, a.t, a.B, a.hd, a.sx, nullptr);
@@ -542,7 +548,7 @@ __global__ __launch_bounds__(512) void fwd_fixup_aff_kernel(I8ArgsOf<EPI> a) {
     }
   if constexpr (EPI)
     epilogue_fused<BM, BN, R, true, true>(accf, E, M, N, m0, n0, 16 * v, 0, a.s,
-                                          reinterpret_cast<uint16_t*>(a.y), a.epi,
+                                          reinterpret_cast<uint16_t*>(a.y), a.epi, es,
                                           lds + CSZ + EPB + v * STRIP);
   else
     epilogue_lowrank<BM, BN, R, true, true>(accf, E, M, N, m0, n0, 16 * v, 0, a.s,
@@ -625,10 +631,23 @@ void launch_shape(I8ArgsOf<EPI> a, hipStream_t st) {
   // products: 576 and 768 blocks of 128 x 128 in two rounds, 384 and 512 of
   // 128 x 192 in one)
   const long rounds128 = (t128 + 2 * kCUs - 1) / (2 * kCUs), rounds192 = (t192 + 2 * kCUs - 1) / (2 * kCUs);
-  if (t64 <= 2 * kCUs) launch_tiles<64, 64, 3, OutT, ACC, false, EPI>(a, st);
-  else if (t128 >= 2 * kCUs && a.N % 192 == 0 && 3 * rounds192 < 2 * rounds128)
-    launch_tiles<128, 192, 2, OutT, ACC, false, EPI>(a, st);
-  else if (t128 >= 2 * kCUs) launch_tiles<128, 128, 2, OutT, ACC, false, EPI>(a, st);
+  // With the epilogue behind it a block ends in vector work as long as a short
+  // contraction's matrix work, and smaller tiles let one block's epilogue run
+  // beside another's products (measured, gelu and z in 8 bits: 4096 rows of
+  // 768 -> 2304 36.1 us at 128 x 64, 39.7 at 128 x 192, 48.7 at 128 x 128;
+  // 4096 rows of 768 -> 768 19.9 at 64 x 64, 21.4 at 128 x 64; but 512 rows of
+  // 2048 -> 16384 40.7 at 128 x 128, 44.4 at 128 x 64).
+  if (t64 <= (EPI ? 3 : 2) * kCUs) {
+    launch_tiles<64, 64, 3, OutT, ACC, false, EPI>(a, st);
+    return;
+  }
+  if constexpr (!EPI) {
+    if (t128 >= 2 * kCUs && a.N % 192 == 0 && 3 * rounds192 < 2 * rounds128) {
+      launch_tiles<128, 192, 2, OutT, ACC, false, EPI>(a, st);
+      return;
+    }
+  }
+  if (t128 >= 2 * kCUs && !(EPI && a.K <= 1024)) launch_tiles<128, 128, 2, OutT, ACC, false, EPI>(a, st);
   else launch_tiles<128, 64, 2, OutT, ACC, false, EPI>(a, st);
 }
 

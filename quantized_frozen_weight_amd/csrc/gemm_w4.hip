@@ -241,11 +241,13 @@ __global__ __launch_bounds__(256, 2) void fwd_w4_kernel(W4ArgsOf<EPI> a) {
   }
 
   float* E = reinterpret_cast<float*>(ring);
+  EpiSide<uint16_t, FwdEpi, FM, FN> es;
+  if constexpr (EPI) es.start(a.epi, M, N, m0, n0 + 32 * wid);
   __syncthreads();
   ep.store(E, M, N, m0, n0, a.r);
   __syncthreads();
   if constexpr (EPI)
-    epilogue_fused<BM, BN, R, false>(acc, E, M, N, m0, n0, 0, 32 * wid, a.s, a.y, a.epi,
+    epilogue_fused<BM, BN, R, false>(acc, E, M, N, m0, n0, 0, 32 * wid, a.s, a.y, a.epi, es,
                                      ring + EPB + wid * STRIP);
   else
     epilogue_lowrank<BM, BN, R, false>(acc, E, M, N, m0, n0, 0, 32 * wid, a.s, a.y,
@@ -280,6 +282,8 @@ __global__ __launch_bounds__(512) void fwd_w4_fixup_kernel(W4ArgsOf<EPI> a) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) pv[sp][j] = P[(sp < nsp ? sp : 0) * pstride + j * 64];
 
+  EpiSide<uint16_t, FwdEpi, 1, FN> es;
+  if constexpr (EPI) es.start(a.epi, M, N, m0 + 16 * v, n0);
   Ep ep;
   if (tid < 256) ep.load(M, N, m0, n0, a.r, a.t, a.B, a.hd, nullptr, nullptr);
   f32x4 acc[1][FN];
@@ -293,7 +297,7 @@ __global__ __launch_bounds__(512) void fwd_w4_fixup_kernel(W4ArgsOf<EPI> a) {
   if (tid < 256) ep.store(E, M, N, m0, n0, a.r);
   __syncthreads();
   if constexpr (EPI)
-    epilogue_fused<BM, HN, R, false>(acc, E, M, N, m0, n0, 16 * v, 0, a.s, a.y, a.epi,
+    epilogue_fused<BM, HN, R, false>(acc, E, M, N, m0, n0, 16 * v, 0, a.s, a.y, a.epi, es,
                                      lds + EPB + v * STRIP);
   else
     epilogue_lowrank<BM, HN, R, false>(acc, E, M, N, m0, n0, 16 * v, 0, a.s, a.y,

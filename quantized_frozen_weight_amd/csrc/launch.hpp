@@ -131,6 +131,22 @@ void launch_bwd_fused(int fmt, int M, int K, int N, const uint16_t* dy,
                       const float* sx = nullptr, const GradEpi* ge = nullptr);
 // (ge not NULL: the kernels' extended form, in which x is the row checkpoint
 // xq, sx where xq is not NULL, and dx goes through ge)
+// Split count and stages per split of the 128 x 128 bf16 input gradient, and
+// its second launch (the partial sums added, u, the dA partial, dx).
+void bwd_split_plan(int M, int K, int N, int* splits, int* nks);
+void launch_bwd_fixup(int M, int K, int r, float s, const float* A, const uint16_t* x, const int8_t* xq,
+                      const float* sx, float* pdx, float* pu, int splits, uint16_t* dx, float* partA,
+                      const GradEpi& ge, hipStream_t st);
+// The same backward over a weight laid out for it first (bwd_tn.hip), for
+// int8 and 4-bit weights; wt: bwd_tn_bytes of scratch. The same partial sums
+// (bwd_row_block) and split buffers.
+bool bwd_tn_takes(int fmt, int M, int K, int N, int r);
+size_t bwd_tn_bytes(int K, int N, int r);
+void launch_bwd_tn(int fmt, int M, int K, int N, const uint16_t* dy, const void* codes,
+                   const void* scales, const float* B, int hd, const float* A, const float* t,
+                   const uint16_t* x, const int8_t* xq, const float* sx, int r, float s, uint16_t* dx,
+                   float* partA, float* partB, float* pdx, float* pu, void* wt, const GradEpi& ge,
+                   hipStream_t st);
 // dx = dy (codes * sw)^T + s u A^T in float32 (ge: as above)
 void launch_gemm_dx_f32(int M, int K, int N, const float* dy,
                         const int8_t* codes, const float* sw, const float* u,

@@ -82,7 +82,9 @@ int main(void) {
     e.act = INT_MIN;
     expect(qlora_fwd_epi(&L, M, QLORA_BF16, P(1024), &e, P(2048), NULL, P(4096), need, NULL), QLORA_EINVAL,
            "activation");
-    expect(qlora_bwd_workspace(&L, M, QLORA_BF16, &need), QLORA_OK, "bwd_workspace");
+    expect(qlora_bwd_epi_workspace(&L, M, QLORA_BF16, &need), QLORA_OK, "bwd_epi_workspace");
+    expect(qlora_bwd_epi_workspace(&L, 0, QLORA_BF16, &need), QLORA_EINVAL, "bwd_epi_workspace rows");
+    expect(qlora_bwd_epi_workspace(&L, M, QLORA_BF16, NULL), QLORA_EINVAL, "bwd_epi_workspace null");
     expect(qlora_bwd_epi(&L, M, QLORA_BF16, NULL, P(1024), P(1280), P(1536), NULL, NULL, P(2048), P(2304),
                          P(2560), P(4096), need, NULL), QLORA_EINVAL, "bwd_epi without t");
     expect(qlora_bwd_epi(&L, M, QLORA_BF16, NULL, P(1024), P(1280), P(1536), P(1792), NULL, P(2048), P(2304),
