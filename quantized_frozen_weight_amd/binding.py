@@ -581,12 +581,17 @@ def _new_ckpt(M: int, C: int, fmt: str, device) -> Checkpoint:
 
 def _layer_on(layer: QLinear, device) -> qlora_linear:
     import torch
+    A, B = layer.A, layer.B
+    if (A.dtype is torch.float32 and A.shape == (layer.K, layer.r) and A.device == device and A.is_contiguous()
+            and B.dtype is torch.float32 and B.shape == _b_shape(layer) and B.device == device
+            and B.is_contiguous() and layer.codes.device == device and layer.scales.device == device):
+        return layer.cstruct()
     for t, what in ((layer.codes, "codes"), (layer.scales, "scales")):
         if t.device != device:
             raise ValueError(f"layer {what} on {t.device}, the activations on {device}")
     _tensor(layer.A, "layer A", (layer.K, layer.r), torch.float32, device)
     _tensor(layer.B, "layer B", _b_shape(layer), torch.float32, device)
-    return layer.cstruct()
+    raise AssertionError("unreachable: one of the checks above fails")
 
 
 def _act(act: str) -> int:

@@ -131,7 +131,7 @@ BwdLayout bwd_layout(const qlora_linear* L, int M, int dtype) {
 // Whether qlora_bwd_epi lays the weight out first, and the workspace it then
 // needs after a backward's own.
 bool lays_out(const qlora_linear* L, int M, int dtype) {
-  return dtype == QLORA_BF16 && bwd_tn_takes(L->fmt, M, L->K, L->N, L->r);
+  return dtype == QLORA_BF16 && bwd_tn_takes(L->fmt, M, L->K, L->N);
 }
 size_t bwd_epi_bytes(const qlora_linear* L, int M, int dtype) {
   return bwd_layout(L, M, dtype).total + (lays_out(L, M, dtype) ? bwd_tn_bytes(L->K, L->N, L->r) : 0);
@@ -792,7 +792,7 @@ int qlora_fwd_epi(const qlora_linear* L, int M, int dtype, const void* x,
   float* sx = e->x_scales ? e->x_scales : reinterpret_cast<float*>(at(ws, w.sx));
   float* rs = reinterpret_cast<float*>(at(ws, w.rs));
   if (pending_error()) return QLORA_EHIP;
-  if (fwd_few_takes(L->fmt, M, K, N, L->r)) {
+  if (fwd_few_takes(L->fmt, M, K, L->r)) {
     launch_fwd_few(dtype, L->fmt, M, N, K, x, L->codes, L->scales, L->A, L->B, head_width(L), L->r,
                    lora_s(L), epi, y, t_save, e->x_codes, e->x_scales,
                    reinterpret_cast<float*>(at(ws, w.few)), s);

@@ -11,9 +11,13 @@
 // of a stage once per block and stage instead: it reads a quarter of the
 // weight bytes, but at 128 x 128 tiles its vector work and its second barrier
 // cost more than the matrix instructions (the measurements are at
-// bwd_tn_takes). What bounds this kernel is the LDS: a stage of a 128 x 128
-// block moves 36 KB in and 72 KB out at 128 bytes a cycle, against 576 cycles
-// of matrix work per SIMD.
+// bwd_tn_takes). Counters of the second launch: at 128 x 64 tiles (4096 x 768
+// x 2304) the matrix cores are busy 26 % of the time, 40 % of a wave's time
+// goes to waiting for its stage's loads and the barrier, 24 % to waiting for
+// an issue slot; at 128 x 128 (4096 x 2048 x 16384) 36 % busy and the LDS 23 %:
+// a stage's 36 KB in and 72 KB out and its 576 cycles of matrix work a SIMD
+// follow one another in each block, and two blocks a compute unit overlap
+// them in part.
 //
 // Around the product it does what gemm_bwd.hip does, with the same operands
 // and the same partial-sum layout (so the same combine and, where the
@@ -580,8 +584,13 @@ inline int rank_width(int r) { return r <= 4 ? 4 : r <= 8 ? 8 : r <= 16 ? 16 : 3
 
 }  // namespace
 
-bool bwd_tn_takes(int fmt, int M, int K, int N, int r) {
-  (void)r;
+bool bwd_tn_takes(int fmt, int M, int K, int N) {
+  // From 1024 rows the second launch's gain pays for the first launch and its
+  // 3 bytes a weight (with tanh gelu and z in 8 bits: 1024 x 16384 x 2048 128
+  // against 142 us, 4096 x 768 x 2304 46 against 56, 4096 x 2048 x 16384 369
+  // against 470); below it does not (512 x 16384 x 2048 80 against 76), nor do
+  // layers of so few weights that a launch is what it costs (4096 x 256 x 256
+  // 17.8 against 17.5).
   return (fmt == 0 || fmt == 1) && M >= 1024 && (long)K * N >= 1L << 19;
 }
 
@@ -620,7 +629,9 @@ void launch_bwd_tn(int fmt, int M, int K, int N, const uint16_t* dy, const void*
     launch_bwd_fixup(M, K, r, s, A, x, xq, sx, pdx, pu, a.splits, dx, partA, ge, st);
   } else if (bm == 64) {
     tn_launch<64, 64, 3, false>(a, st);
-  } else if ((long)((M + 127) / 128) * ((K + 127) / 128) < 256) {
+  } else if ((long)((M + 127) / 128) * ((K + 127) / 128) <= 256) {
+    // one 128 x 128 block per compute unit or fewer (4-bit 1024 x 4096 x 4096,
+    // 256 of them: 75 against 90 us; 512 of them: 165 against 160)
     tn_launch<128, 64, 2, false>(a, st);
   } else {
     tn_launch<128, 128, 2, false>(a, st);

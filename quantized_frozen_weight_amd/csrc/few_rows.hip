@@ -453,8 +453,7 @@ void few_ranks(const FewArgs& a, hipStream_t st) {
 // above; the four rows' sums of x A are vector work that grows with them),
 // int8 and 4-bit weights, ranks up to 16, and rows whose bf16 form fits in
 // LDS four times.
-bool fwd_few_takes(int fmt, int M, int K, int N, int r) {
-  (void)N;
+bool fwd_few_takes(int fmt, int M, int K, int r) {
   return (fmt == 0 || fmt == 1) && M <= 4 && r <= 16 && K <= kFewMaxK;
 }
 

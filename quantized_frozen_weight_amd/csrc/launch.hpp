@@ -84,7 +84,7 @@ void launch_gemm_fwd_w4(int M, int N, int K, const uint16_t* x,
 // 1, rank up to 16, K <= 16384: fwd_few_takes); t, xq and sx (x's row
 // checkpoint) may be NULL; scratch: fwd_few_floats(M, K) floats.
 size_t fwd_few_floats(int M, int K);
-bool fwd_few_takes(int fmt, int M, int K, int N, int r);
+bool fwd_few_takes(int fmt, int M, int K, int r);
 void launch_fwd_few(int dtype, int fmt, int M, int N, int K, const void* x, const void* codes,
                     const void* scales, const float* A, const float* B, int hd, int r, float s,
                     const FwdEpi& epi, void* y, float* t, int8_t* xq, float* sx, float* scratch,
@@ -140,7 +140,7 @@ void launch_bwd_fixup(int M, int K, int r, float s, const float* A, const uint16
 // The same backward over a weight laid out for it first (bwd_tn.hip), for
 // int8 and 4-bit weights; wt: bwd_tn_bytes of scratch. The same partial sums
 // (bwd_row_block) and split buffers.
-bool bwd_tn_takes(int fmt, int M, int K, int N, int r);
+bool bwd_tn_takes(int fmt, int M, int K, int N);
 size_t bwd_tn_bytes(int K, int N, int r);
 void launch_bwd_tn(int fmt, int M, int K, int N, const uint16_t* dy, const void* codes,
                    const void* scales, const float* B, int hd, const float* A, const float* t,

@@ -189,9 +189,11 @@ FWD = [
     (4, 256, 144, 32, "w8", "bf16", 1),        # rank 32: the tiled product
     (7, 784, 208, 3, "w8", "bf16", 1),
     (1001, 784, 1024, 8, "w8", "bf16", 1),     # 64 x 64 tiles, ragged rows and k
-    (700, 256, 4112, 16, "w8", "bf16", 1),     # 128 x 64 tiles, last group of 16 columns
-    (2100, 128, 2304, 4, "w8", "bf16", 1),     # 128 x 192 tiles
-    (2100, 128, 4096, 32, "w8", "bf16", 1),    # 128 x 128 tiles, rank 32
+    (700, 256, 4112, 16, "w8", "bf16", 1),     # ... last group of 16 columns
+    (2100, 128, 2304, 4, "w8", "bf16", 1),     # 128 x 64 tiles (128 x 192 without an epilogue)
+    (2100, 128, 4096, 32, "w8", "bf16", 1),    # ... at rank 32 (128 x 128 without)
+    (2100, 1040, 4112, 32, "w8", "bf16", 1),   # 128 x 128 tiles, rank 32, ragged k and columns
+    (4100, 1168, 2064, 3, "w8", "bf16", 1),    # ... at rank 3
     (100, 4096, 272, 8, "w8", "bf16", 1),      # split contraction and its second launch
     (130, 16384, 144, 4, "w8", "bf16", 1),     # split 8 ways, long rows
     (40, 4096, 144, 8, "w8", "f32", 1),        # split, float32 outputs
@@ -277,6 +279,18 @@ BWD = [
     (77, 384, 144, 32, "w4g128", "bf16", 1),   # 4-bit, rank 32: 128-row tiles
     (4200, 2176, 80, 16, "w4g128", "bf16", 1),
     (77, 256, 4160, 8, "w4g128", "bf16", 1),   # 4-bit, split
+    # with the weight laid out first (from 1024 rows and 2^19 weights)
+    (1030, 1040, 528, 8, "w8", "bf16", 1),     # 64 x 64 tiles
+    (1024, 1056, 576, 3, "w8", "bf16", 3),     # ... heads, whole row tiles
+    (4200, 528, 1040, 1, "w8", "bf16", 1),     # 128 x 64 tiles
+    (4200, 1040, 528, 32, "w8", "bf16", 1),    # 128 x 128 tiles, rank 32
+    (4200, 1056, 576, 16, "w8", "bf16", 3),    # ... heads
+    (1030, 528, 2080, 4, "w8", "bf16", 1),     # split 4 ways
+    (1100, 144, 8208, 16, "w8", "bf16", 1),    # split 8 ways, ragged last stage
+    (1100, 1152, 528, 4, "w4g128", "bf16", 1),
+    (1100, 1152, 528, 32, "w4g128", "bf16", 1),  # 4-bit, rank 32: 128 x 64 tiles
+    (4200, 1152, 464, 16, "w4g128", "bf16", 1),  # 4-bit, 128 x 128 tiles
+    (1030, 256, 2064, 8, "w4g128", "bf16", 1),   # 4-bit, split
 ]
 GRADS = [("gelu", "c8", False), ("relu", "full", True), ("silu", "c8", True), ("gelu_tanh", "c8", False),
          ("none", None, True), ("none", None, False)]
@@ -475,7 +489,9 @@ def test_activations_at_the_ends_of_the_range():
 
 @pytest.mark.parametrize("what", ["nan", "inf", "zero"])
 @pytest.mark.parametrize("spec", [(70, 256, 272, 8, "w8", "bf16", 1), (2100, 2064, 144, 8, "w8", "bf16", 1),
-                                  (130, 528, 2080, 4, "w8", "bf16", 1), (70, 64, 80, 4, "w8", "f32", 1)],
+                                  (130, 528, 2080, 4, "w8", "bf16", 1), (70, 64, 80, 4, "w8", "f32", 1),
+                                  (1030, 1040, 528, 8, "w8", "bf16", 1), (4200, 528, 1040, 4, "w8", "bf16", 1),
+                                  (1030, 528, 2080, 4, "w8", "bf16", 1)],
                          ids=lambda s: "-".join(map(str, s)) if isinstance(s, tuple) else s)
 def test_non_finite_and_empty_rows(spec, what):
     """A row of x that is NaN, infinite or all zero: its checkpoint carries it,
@@ -505,7 +521,9 @@ def test_in_place_operands():
     layer, split and not."""
     for spec in ((333, 784, 272, 8, "w8", "bf16", 1), (100, 4096, 272, 8, "w8", "bf16", 1),
                  (130, 528, 2080, 4, "w8", "bf16", 1), (64, 256, 256, 4, "w8", "f32", 1),
-                 (77, 256, 272, 8, "w4g128", "bf16", 1)):
+                 (77, 256, 272, 8, "w4g128", "bf16", 1), (1030, 1040, 528, 8, "w8", "bf16", 1),
+                 (4200, 528, 1040, 4, "w8", "bf16", 1), (1030, 528, 2080, 4, "w8", "bf16", 1),
+                 (4, 784, 272, 8, "w8", "bf16", 1), (3, 256, 272, 8, "w4g128", "bf16", 1)):
         c = Case(*spec)
         say("in place", spec)
         y, t, _, xc = Q.qlora_fwd_epi(c.lin, c.x_t, act="silu", residual=c.res_t, save_x=True)
@@ -608,7 +626,9 @@ def test_a_block_as_it_is_trained(fmt, dtype, M, D, H):
 
 @pytest.mark.parametrize("fmt,dtype,M,D,H", [("w8", "bf16", 333, 256, 1040), ("w8", "f32", 65, 64, 144),
                                              ("w4g128", "bf16", 130, 256, 1024), ("w8o", "bf16", 130, 256, 1040),
-                                             ("w8", "bf16", 1, 2048, 4096), ("w8", "bf16", 130, 2048, 4096)])
+                                             ("w8", "bf16", 1, 2048, 4096), ("w8", "bf16", 130, 2048, 4096),
+                                             ("w8", "bf16", 1030, 528, 1040), ("w4g128", "bf16", 4, 256, 1024),
+                                             ("w4g128", "bf16", 1030, 512, 1152)])
 def test_block_captured_and_replayed(fmt, dtype, M, D, H):
     """The block in a HIP graph: replays between eager calls, on new inputs,
     give the eager bytes; so does a call on another stream."""
@@ -640,6 +660,29 @@ def test_block_captured_and_replayed(fmt, dtype, M, D, H):
         if it == 0:
             for n in want:
                 assert torch.equal(bits(other[n]), bits(want[n])), f"other stream: {n}"
+
+
+def test_two_streams_at_once():
+    """The same layers used on two streams at a time, each with its own
+    workspaces: the bytes of one call after the other."""
+    for fmt, M, D, H in (("w8", 1030, 528, 1040), ("w8", 130, 2048, 4096), ("w4g128", 3, 512, 1152)):
+        say("two streams", fmt, M, D, H)
+        c1, c2 = Case(M, D, H, 8, fmt, seed=1), Case(M, H, D, 8, fmt, seed=2)
+        b1, b2 = dev(c1.bias), dev(c2.bias)
+        ins = [(c1.x_t, c2.dy_t), (c1.x_t.flip(0).contiguous(), c2.dy_t.flip(1).contiguous())]
+        want = [_block(c1, c2, "silu", *i, b1, b2) for i in ins]
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+        got = [[], []]
+        for _ in range(8):
+            for st, i, g in zip(streams, ins, got):
+                with torch.cuda.stream(st):
+                    g.append(_block(c1, c2, "silu", *i, b1, b2))
+        torch.cuda.synchronize()
+        for w, gs in zip(want, got):
+            for g in gs:
+                for n in w:
+                    assert torch.equal(bits(w[n]), bits(g[n])), n
 
 
 def test_refusals():
