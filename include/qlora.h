@@ -375,7 +375,9 @@ const char* qlora_bwd_main_kernel(const qlora_linear* L, int M, int dtype);
  * Activations: relu (relu'(0) = 0); gelu = z Phi(z); gelu_tanh = z (1 +
  * tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2; silu = z / (1 + e^-z). They are
  * evaluated in float32 on the unrounded z; -inf gives their limit (0, and
- * slope 0), NaN stays NaN.
+ * slope 0), NaN stays NaN. A row of x with an infinity or a NaN in it gives a
+ * row of NaN in y under the int8 formats and their checkpoints, and touches no
+ * other row.
  *
  * Constraints as above, with M >= 1 and every pointer 16-byte aligned; of a
  * pair (codes, scales) both or neither is given. Every tensor is dense
@@ -415,7 +417,12 @@ typedef struct {
 
 /* qlora_fwd with the epilogue: y [M, N] = act(z) + residual, rounded once to
  * the compute dtype. Workspace: qlora_fwd_workspace. For int8 formats x_codes
- * costs nothing (the product reads the codes there). */
+ * costs nothing (the product reads the codes there). With an empty epilogue
+ * the results are bitwise qlora_fwd's, except that up to four rows of int8 and
+ * 4-bit layers (rank <= 16, K <= 16384) take a kernel of their own, whose int8
+ * base product is the same and whose float32 sums (t; 4-bit: the base too) run
+ * in another order; a 4-bit row may come out non-finite there where |x| passes
+ * 2^113. */
 int qlora_fwd_epi(const qlora_linear* L, int M, int dtype, const void* x,
                   const qlora_epilogue* e, void* y, float* t_save, void* ws,
                   size_t ws_bytes, void* stream);

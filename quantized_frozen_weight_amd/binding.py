@@ -617,15 +617,15 @@ def _act_bwd_bytes(M: int, N: int) -> int:
     return n.value
 
 
-def _scratch(query: str, cs: qlora_linear, M: int, dtype: int, device, ws):
-    """The caller's workspace, or a new one of the queried size."""
-    import torch
+def _scratch(query: str, layer: QLinear, cs: qlora_linear, M: int, dtype: int, device, ws):
+    """The caller's workspace, or a new one of the queried size (bytes, as the
+    codes are)."""
     if ws is not None:
         if ws.device != device or not ws.is_contiguous():
             raise ValueError(f"ws: a contiguous tensor on {device} is needed")
         return ws
     n = _sizes(query, cs.K, cs.N, cs.r, cs.fmt, cs.heads, M, dtype)
-    return torch.empty((max(n, 256),), dtype=torch.uint8, device=device)
+    return layer.codes.new_empty((max(n, 256),))
 
 
 def qlora_ckpt_write(x, fmt: str = "c8row", out: Optional[Checkpoint] = None) -> Checkpoint:
@@ -689,21 +689,21 @@ def qlora_fwd_epi(layer: QLinear, x, act: str = "none", bias=None, residual=None
     M, _, dt = _rows(x, "x", layer.K)
     dev = x.device
     cs = _layer_on(layer, dev)
-    y = torch.empty((M, layer.N), dtype=x.dtype, device=dev) if y is None else \
+    y = x.new_empty((M, layer.N)) if y is None else \
         _tensor(y, "y", (M, layer.N), x.dtype, dev)
     if save_t:
-        t = torch.empty((M, layer.r), dtype=torch.float32, device=dev) if t is None else \
+        t = layer.A.new_empty((M, layer.r)) if t is None else \
             _tensor(t, "t", (M, layer.r), torch.float32, dev)
     if save_x:
         xc = _new_ckpt(M, layer.K, "c8row", dev) if xc is None else _ckpt(xc, "xc", "c8row", (M, layer.K), dev)
     else:
         xc = None
     e, z = _epilogue(layer, M, x.dtype, dev, act, bias, residual, save_z, z, xc)
-    ws = _scratch("qlora_fwd_workspace", cs, M, dt, dev, ws)
+    ws = _scratch("qlora_fwd_workspace", layer, cs, M, dt, dev, ws)
     with _on(dev):
         _check(lib().qlora_fwd_epi(ctypes.byref(cs), M, dt, _ptr(x), ctypes.byref(e), _ptr(y),
                                    _ptr(t) if save_t else None, _ptr(ws),
-                                   ws.numel() * ws.element_size(), _stream()), "qlora_fwd_epi")
+                                   ws.nbytes, _stream()), "qlora_fwd_epi")
     return y, (t if save_t else None), z, xc
 
 
@@ -722,10 +722,10 @@ def qlora_fwd_ckpt(layer: QLinear, xc: Checkpoint, t, dtype, act: str = "none", 
         _tensor(y, "y", (M, layer.N), dtype, dev)
     dt = _dtype_code(y)
     e, z = _epilogue(layer, M, dtype, dev, act, bias, residual, save_z, z, None)
-    ws = _scratch("qlora_fwd_workspace", cs, M, dt, dev, ws)
+    ws = _scratch("qlora_fwd_workspace", layer, cs, M, dt, dev, ws)
     with _on(dev):
         _check(lib().qlora_fwd_ckpt(ctypes.byref(cs), M, dt, _ptr(xc.codes), _ptr(xc.scales), _ptr(t),
-                                    ctypes.byref(e), _ptr(y), _ptr(ws), ws.numel() * ws.element_size(),
+                                    ctypes.byref(e), _ptr(y), _ptr(ws), ws.nbytes,
                                     _stream()), "qlora_fwd_ckpt")
     return y, z
 
@@ -755,7 +755,7 @@ def _bwd_epi_args(layer, x, dy, t, act, z, add, need_dx, dx):
     if add is not None:
         g.add = _ptr(_tensor(add, "add", shape, dy.dtype, dev))
     if need_dx:
-        dx = torch.empty(shape, dtype=dy.dtype, device=dev) if dx is None else \
+        dx = dy.new_empty(shape) if dx is None else \
             _tensor(dx, "dx", shape, dy.dtype, dev)
     else:
         if act != "none" or z is not None or add is not None:
@@ -772,14 +772,14 @@ def qlora_bwd_epi(layer: QLinear, x, dy, t=None, act: str = "none", z=None, add=
     Checkpoint. dx may be the add tensor itself. Returns (dx or None, dA, dB)."""
     import torch
     cs, M, dt, dev, args, dx, _keep = _bwd_epi_args(layer, x, dy, t, act, z, add, need_dx, dx)
-    dA = torch.empty((layer.K, layer.r), dtype=torch.float32, device=dev) if dA is None else \
+    dA = layer.A.new_empty((layer.K, layer.r)) if dA is None else \
         _tensor(dA, "dA", (layer.K, layer.r), torch.float32, dev)
-    dB = torch.empty(_b_shape(layer), dtype=torch.float32, device=dev) if dB is None else \
+    dB = layer.B.new_empty(_b_shape(layer)) if dB is None else \
         _tensor(dB, "dB", _b_shape(layer), torch.float32, dev)
-    ws = _scratch("qlora_bwd_epi_workspace", cs, M, dt, dev, ws)
+    ws = _scratch("qlora_bwd_epi_workspace", layer, cs, M, dt, dev, ws)
     with _on(dev):
         _check(lib().qlora_bwd_epi(ctypes.byref(cs), M, dt, *args, _ptr(dA), _ptr(dB), _ptr(ws),
-                                   ws.numel() * ws.element_size(), _stream()), "qlora_bwd_epi")
+                                   ws.nbytes, _stream()), "qlora_bwd_epi")
     return dx, dA, dB
 
 
@@ -788,10 +788,10 @@ def qlora_bwd_epi_partial(layer: QLinear, x, dy, t=None, act: str = "none", z=No
     """First half of qlora_bwd_epi: (dx or None, workspace), the adapter
     gradients left to qlora_bwd_finish or qlora_bwd_finish_batch."""
     cs, M, dt, dev, args, dx, _keep = _bwd_epi_args(layer, x, dy, t, act, z, add, need_dx, dx)
-    ws = _scratch("qlora_bwd_epi_workspace", cs, M, dt, dev, ws)
+    ws = _scratch("qlora_bwd_epi_workspace", layer, cs, M, dt, dev, ws)
     with _on(dev):
         _check(lib().qlora_bwd_epi_partial(ctypes.byref(cs), M, dt, *args, _ptr(ws),
-                                           ws.numel() * ws.element_size(), _stream()),
+                                           ws.nbytes, _stream()),
                "qlora_bwd_epi_partial")
     return dx, ws
 
@@ -826,6 +826,6 @@ def qlora_act_bwd(act: str, dy, z=None, need_dz: bool = True, need_dbias: bool =
         dbias = ws = None
     with _on(dev):
         _check(lib().qlora_act_bwd(_act(act), M, N, dt, _ptr(dy), zp, zc, zs, _ptr(dz), _ptr(dbias),
-                                   _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                                   _ptr(ws), 0 if ws is None else ws.nbytes,
                                    _stream()), "qlora_act_bwd")
     return dz, dbias

@@ -245,7 +245,7 @@ def test_forward(spec):
                 assert torch.equal(bits(y), bits(y2)), "y from the checkpoint differs"
 
 
-@pytest.mark.parametrize("spec", [f for f in FWD if f[0] in (64, 1001, 100, 77, 90)],
+@pytest.mark.parametrize("spec", [f for f in FWD if f[0] in (64, 1001, 100, 77, 90, 300, 700, 2100)],
                          ids=lambda s: "-".join(map(str, s)))
 def test_empty_epilogue_is_the_plain_forward(spec):
     c = Case(*spec)
