@@ -567,15 +567,16 @@ def _ckpt(c, what: str, fmt: str, shape, device) -> Checkpoint:
     return c
 
 
-def _new_ckpt(M: int, C: int, fmt: str, device) -> Checkpoint:
+def _new_ckpt(M: int, C: int, fmt: str, like) -> Checkpoint:
+    """A checkpoint's tensors on the device of `like`."""
     import torch
     if fmt not in _CFMT:
         raise ValueError(f"unknown checkpoint form {fmt!r}")
-    codes = torch.empty((M, C), dtype=torch.int8, device=device)
+    codes = like.new_empty((M, C), dtype=torch.int8)
     if fmt == "c8row":
-        scales = torch.empty((M,), dtype=torch.float32, device=device)
+        scales = like.new_empty((M,), dtype=torch.float32)
     else:
-        scales = torch.empty((M, -(-C // CKPT_GROUP)), dtype=torch.uint8, device=device)
+        scales = like.new_empty((M, -(-C // CKPT_GROUP)), dtype=torch.uint8)
     return Checkpoint(codes, scales, fmt)
 
 
@@ -631,7 +632,7 @@ def _scratch(query: str, layer: QLinear, cs: qlora_linear, M: int, dtype: int, d
 def qlora_ckpt_write(x, fmt: str = "c8row", out: Optional[Checkpoint] = None) -> Checkpoint:
     """x [M, C] as an 8-bit checkpoint of form fmt."""
     M, C, dt = _rows(x, "x")
-    c = _new_ckpt(M, C, fmt, x.device) if out is None else _ckpt(out, "out", fmt, (M, C), x.device)
+    c = _new_ckpt(M, C, fmt, x) if out is None else _ckpt(out, "out", fmt, (M, C), x.device)
     with _on(x.device):
         _check(lib().qlora_ckpt_write(_ptr(x), M, C, dt, _CFMT[fmt], _ptr(c.codes), _ptr(c.scales),
                                       _stream()), "qlora_ckpt_write")
@@ -666,7 +667,7 @@ def _epilogue(layer, M, dtype, device, act, bias, residual, save_z, z, xc):
             _tensor(z, "z", (M, layer.N), dtype, device)
         e.z = _ptr(z)
     elif save_z == "c8g32":
-        z = _new_ckpt(M, layer.N, "c8g32", device) if z is None else \
+        z = _new_ckpt(M, layer.N, "c8g32", layer.A) if z is None else \
             _ckpt(z, "z", "c8g32", (M, layer.N), device)
         e.z_codes, e.z_scales = _ptr(z.codes), _ptr(z.scales)
     elif save_z is not None:
@@ -695,7 +696,7 @@ def qlora_fwd_epi(layer: QLinear, x, act: str = "none", bias=None, residual=None
         t = layer.A.new_empty((M, layer.r)) if t is None else \
             _tensor(t, "t", (M, layer.r), torch.float32, dev)
     if save_x:
-        xc = _new_ckpt(M, layer.K, "c8row", dev) if xc is None else _ckpt(xc, "xc", "c8row", (M, layer.K), dev)
+        xc = _new_ckpt(M, layer.K, "c8row", x) if xc is None else _ckpt(xc, "xc", "c8row", (M, layer.K), dev)
     else:
         xc = None
     e, z = _epilogue(layer, M, x.dtype, dev, act, bias, residual, save_z, z, xc)

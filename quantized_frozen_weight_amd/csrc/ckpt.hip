@@ -1,7 +1,9 @@
 // 8-bit activation checkpoints (written and read back) and the gradient of an
-// activation on its own. All of it is memory-bound: a thread owns 8
-// consecutive columns of a row per unit (16 bytes of bf16, 8 of codes), four
-// units' loads in flight at a time.
+// activation on its own. All of it is memory-bound: a thread owns one unit of
+// 8 consecutive columns of a row (16 bytes of bf16, 8 of codes), and eight
+// waves per SIMD cover the latency (two and four units a thread, their loads
+// together in flight, are no faster: 512 x 16384 bf16 written in 5.6, 5.8 and
+// 6.2 us, read back in 4.9, 5.3 and 5.4).
 //
 // The group form is described in epilogue.hpp; the row form is the forward's
 // own activation quantizer (rows.hip), so only its reading is here.
@@ -16,8 +18,6 @@ namespace qlora {
 
 namespace {
 
-constexpr int kUnits = 4;                    // 8-column units per thread
-
 // Units of a row padded to whole groups, so that the four lanes of a quad
 // always hold one group: unit u is columns [8 (u % upr), + 8) of row u / upr.
 template <typename T>
@@ -25,29 +25,19 @@ __global__ __launch_bounds__(256) void ckpt_write_groups_kernel(
     const typename Elem<T>::type* __restrict__ x, int M, int C, int8_t* __restrict__ codes,
     uint8_t* __restrict__ scales) {
   const int zg = group_count(C);
-  const uint32_t upr = 4u * zg, n = (uint32_t)M * upr;
-  const uint32_t u0 = blockIdx.x * (256u * kUnits) + threadIdx.x;
-  float v[kUnits][8];
-  uint32_t row[kUnits], col[kUnits];
-  bool ok[kUnits];
+  const uint32_t upr = 4u * zg, n = (uint32_t)M * upr, u = blockIdx.x * 256u + threadIdx.x;
+  const uint32_t row = u / upr, col = 8u * (u - row * upr);
+  const bool ok = u < n && col < (uint32_t)C;
+  const long at = ok ? (long)row * C + col : 0;
+  float v[8];
+  load8(x + at, v);
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const uint32_t u = u0 + 256u * i;
-    row[i] = u / upr;
-    col[i] = 8u * (u - row[i] * upr);
-    ok[i] = u < n && col[i] < (uint32_t)C;
-    load8(x + (ok[i] ? (long)row[i] * C + col[i] : 0), v[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) { const uint32_t b = abs_bits(v[i][e]); m = b > m ? b : m; }
-    const int b = group_byte(quad_max_u32(ok[i] ? m : 0u));
-    if (ok[i]) {
-      *reinterpret_cast<u32x2*>(codes + (long)row[i] * C + col[i]) = group_codes(v[i], b);
-      if (col[i] % kGroup == 0) scales[(long)row[i] * zg + col[i] / kGroup] = (uint8_t)b;
-    }
+  for (int e = 0; e < 8; ++e) { const uint32_t b = abs_bits(v[e]); m = b > m ? b : m; }
+  const int b = group_byte(quad_max_u32(ok ? m : 0u));
+  if (ok) {
+    *reinterpret_cast<u32x2*>(codes + at) = group_codes(v, b);
+    if (col % kGroup == 0) scales[(long)row * zg + col / kGroup] = (uint8_t)b;
   }
 }
 
@@ -55,29 +45,19 @@ template <typename T, bool GROUPS>
 __global__ __launch_bounds__(256) void ckpt_read_kernel(
     const int8_t* __restrict__ codes, const void* __restrict__ scales, int M, int C,
     typename Elem<T>::type* __restrict__ x) {
-  const int zg = group_count(C);
-  const uint32_t upr = (uint32_t)C / 8u, n = (uint32_t)M * upr;
-  const uint32_t u0 = blockIdx.x * (256u * kUnits) + threadIdx.x;
-  u32x2 c[kUnits];
-  float s[kUnits];
+  const uint32_t upr = (uint32_t)C / 8u, n = (uint32_t)M * upr, u = blockIdx.x * 256u + threadIdx.x;
+  if (u >= n) return;
+  const uint32_t row = u / upr, col = 8u * (u - row * upr);
+  const u32x2 c = *reinterpret_cast<const u32x2*>(codes + 8L * u);
+  float v[8];
+  if constexpr (GROUPS) {
+    group_values(c, static_cast<const uint8_t*>(scales)[(long)row * group_count(C) + col / kGroup], v);
+  } else {
+    const float s = static_cast<const float*>(scales)[row];
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const uint32_t u = u0 + 256u * i, uc = u < n ? u : 0u;
-    const uint32_t row = uc / upr, col = 8u * (uc - row * upr);
-    c[i] = *reinterpret_cast<const u32x2*>(codes + 8L * uc);
-    if constexpr (GROUPS)
-      s[i] = group_scale(static_cast<const uint8_t*>(scales)[(long)row * zg + col / kGroup]);
-    else
-      s[i] = static_cast<const float*>(scales)[row];
+    for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)(c[e >> 2] >> (8 * (e & 3))) * s;
   }
-#pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const uint32_t u = u0 + 256u * i;
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)(c[i][e >> 2] >> (8 * (e & 3))) * s[i];
-    if (u < n) store8(x + 8L * u, v);
-  }
+  store8(x + 8L * u, v);
 }
 
 // Row sums of codes, one wave per row (exact: |sum| <= 127 K < 2^31, and
@@ -100,33 +80,41 @@ __global__ __launch_bounds__(256) void code_sums_kernel(const int8_t* __restrict
 
 // ---- dz = dy act'(z), dbias = column sums -----------------------------------
 // A block owns 256 columns (32 lanes of 8) and a span of rows, LANES rows at a
-// time; a thread keeps the float32 sums of its 8 columns over its rows, four
-// rows' loads in flight. The row lanes are added in order through LDS, and
-// (more than one span) a second launch adds the spans in order. No atomics.
+// time; a thread keeps the float32 sums of its 8 columns over its rows. The
+// row lanes are added in order through LDS, and (more than one span) a second
+// launch adds the spans in order. No atomics.
 // Up to 128 rows one span of 32 row lanes does: every thread then has one
-// group of loads, and there is no second launch (77 rows of 1040 float32: one
-// span of 8 lanes took 12 us). Past that 8 lanes and enough spans to fill the
-// chip. The activation's slope is as much work as the traffic: 4096 x 2304
-// bf16 with gelu moves 47 MB (9.3 us at the 5.1 TB/s of a large copy) and
-// does about 25 vector instructions and two transcendental ones per value
-// (8 us).
+// group of four rows' loads in flight, and there is no second launch (77 rows
+// of 1040 float32: one span of 8 lanes took 12 us). Past that 8 lanes, and a
+// thread takes a row at a time: the loads of other waves cover one wave's
+// arithmetic better than its own loads of more rows do, which cost registers
+// and so waves (gelu, 4096 x 2304: 16.7 us at one row, 18.1 at two, 18.8 at
+// four; 8192 x 4096: 35.5, 38.4, 43). The activation's slope is as much work
+// as the traffic: 4096 x 2304 bf16 with gelu moves 47 MB (9.3 us at the 5.1
+// TB/s of a large copy) and does about 25 vector instructions and two
+// transcendental ones per value (8 us).
 constexpr int kActCols = 256;
+constexpr int act_units(int lanes) { return lanes == 32 ? 4 : 1; }   // rows a thread loads at once
 
 inline int col_blocks(int C) { return C / kActCols + (C % kActCols != 0); }
 
 // Rows per span and row lanes.
 void act_bwd_plan(int M, int C, int* spans, int* rows, int* lanes) {
-  if (M <= 32 * kUnits) {
+  if (M <= 32 * act_units(32)) {
     *spans = 1;
     *rows = M;
     *lanes = 32;
     return;
   }
+  // 4096 blocks where there are that many rows, but 16 rows a span at least,
+  // and 32 rather than more than 128 spans: the second launch reads them all
+  // (1024 x 1024 6.9 us at 16 rows, 8.4 at 32; 4096 x 768 10.8 and 10.2)
   *lanes = 8;
-  int want = 2048 / col_blocks(C);
+  int want = 4096 / col_blocks(C);
   if (want < 1) want = 1;
   int r = (M + want - 1) / want;
-  if (r < 8 * kUnits) r = 8 * kUnits;
+  const int least = M > 4096 ? 32 : M > 2048 ? (M + 127) / 128 : 16;
+  if (r < least) r = least;
   r = (r + 7) / 8 * 8;
   *rows = r;
   *spans = (M + r - 1) / r;
@@ -136,6 +124,7 @@ template <typename T, bool SUMS, int LANES>
 __global__ __launch_bounds__(32 * LANES) void act_bwd_kernel(const typename Elem<T>::type* dy, int M, int C,
                                                       GradEpi ge, typename Elem<T>::type* dz,
                                                       float* __restrict__ out, int rows) {
+  constexpr int UNITS = act_units(LANES);
   __shared__ float red[SUMS ? LANES : 1][kActCols + 8];
   const int tid = threadIdx.x, cl = tid & 31, rl = tid >> 5;
   const uint32_t col = blockIdx.x * (uint32_t)kActCols + 8u * cl;   // (may pass 2^31 - 1 in the last block)
@@ -145,11 +134,11 @@ __global__ __launch_bounds__(32 * LANES) void act_bwd_kernel(const typename Elem
   float sum[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) sum[e] = 0.f;
-  for (int mb = m0 + rl; mb < m1; mb += LANES * kUnits) {
-    float v[kUnits][8], z[kUnits][8];
+  for (int mb = m0 + rl; mb < m1; mb += LANES * UNITS) {
+    float v[UNITS][8], z[UNITS][8];
     // every load of the group from clamped addresses before the first use
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
+    for (int i = 0; i < UNITS; ++i) {
       const int m = mb + LANES * i < m1 ? mb + LANES * i : mb;
       const long at = (long)m * C + colc;
       load8(dy + at, v[i]);
@@ -161,7 +150,7 @@ __global__ __launch_bounds__(32 * LANES) void act_bwd_kernel(const typename Elem
       }
     }
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
+    for (int i = 0; i < UNITS; ++i) {
       const int m = mb + LANES * i;
       if (m < m1) {
         act_slope_mul<std::is_same<T, F32>::value>(ge.act, z[i], v[i]);
@@ -199,9 +188,7 @@ __global__ __launch_bounds__(256) void act_bwd_sum_kernel(const float* __restric
   if (w == 0 && c < C) dbias[c] = ((red[0][lane] + red[1][lane]) + red[2][lane]) + red[3][lane];
 }
 
-inline unsigned unit_blocks(long units) {
-  return (unsigned)((units + 256 * kUnits - 1) / (256 * kUnits));
-}
+inline unsigned unit_blocks(long units) { return (unsigned)((units + 255) / 256); }
 
 template <typename T>
 void act_bwd_launch(int M, int C, const void* dy, const GradEpi& ge, void* dz, float* dbias,

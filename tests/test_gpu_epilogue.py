@@ -427,7 +427,7 @@ def test_checkpoints_bit_exact(M, C, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("M,N", [(1, 16), (77, 1040), (128, 48), (129, 272), (1000, 4112), (5000, 144)])
+@pytest.mark.parametrize("M,N", [(1, 16), (77, 1040), (128, 48), (129, 272), (1000, 4112), (2500, 272), (5000, 144)])
 def test_activation_backward(M, N, dtype):
     rng = np.random.default_rng(M + N)
     dy_t, dy = WL.as_compute_dtype(rng.standard_normal((M, N)).astype(np.float32), dtype)
