@@ -390,8 +390,7 @@ typedef enum {
 typedef enum { QLORA_C8ROW = 0, QLORA_C8G32 = 1 } qlora_cfmt;
 
 /* Bytes of the codes and scales of an activation [M, C] in form cfmt (C a
- * multiple of 16, at least 16; ERANGE from M C = 2^31, and for QLORA_C8ROW
- * past C = 2^30). Host-only arithmetic. */
+ * multiple of 16, at least 16; ERANGE from M C = 2^31). Host-only arithmetic. */
 int qlora_ckpt_bytes(int M, int C, int cfmt, size_t* codes_bytes, size_t* scale_bytes);
 
 /* Write x [M, C] (compute dtype) in form cfmt, and read it back: value =

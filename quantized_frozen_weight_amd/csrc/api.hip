@@ -718,8 +718,6 @@ int qlora_ckpt_bytes(int M, int C, int cfmt, size_t* codes_bytes, size_t* scale_
   if (M < 1 || C < 16 || C % 16) return QLORA_EINVAL;
   if (!fits_int(M, C)) return QLORA_ERANGE;
   if (cfmt != QLORA_C8ROW && cfmt != QLORA_C8G32) return QLORA_EINVAL;
-  // (the row quantizer counts a row's entries in slices with an int)
-  if (cfmt == QLORA_C8ROW && C > (1 << 30)) return QLORA_ERANGE;
   *codes_bytes = (size_t)M * C;
   *scale_bytes = cfmt == QLORA_C8ROW ? (size_t)M * 4 : (size_t)M * group_count(C);
   return QLORA_OK;
@@ -742,7 +740,7 @@ int qlora_ckpt_write(const void* x, int M, int C, int dtype, int cfmt, int8_t* c
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (pending_error()) return QLORA_EHIP;
   if (cfmt == QLORA_C8ROW)
-    launch_rowquant(dtype, x, M, C, nullptr, 1, codes, static_cast<float*>(scales), nullptr, s);
+    launch_ckpt_write_rows(dtype, x, M, C, codes, static_cast<float*>(scales), s);
   else
     launch_ckpt_write_groups(dtype, x, M, C, codes, static_cast<uint8_t*>(scales), s);
   return launch_status();

@@ -6,7 +6,7 @@
 // 6.2 us, read back in 4.9, 5.3 and 5.4).
 //
 // The group form is described in epilogue.hpp; the row form is the forward's
-// own activation quantizer (rows.hip), so only its reading is here.
+// own activation quantizer, and its launches (rows.hip) write most of it here.
 //
 // ("Introduce QLoRA-like technique": activations quantized per row under the
 // int8 kernel; keras-llm-light README, "Block-wise gradient checkpointing":
@@ -58,6 +58,56 @@ __global__ __launch_bounds__(256) void ckpt_read_kernel(
     for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)(c[e >> 2] >> (8 * (e & 3))) * s;
   }
   store8(x + 8L * u, v);
+}
+
+// The row form, a block per row, which reads the row twice, the second time
+// from the caches. rows.hip has a wave or half a block per row and holds the
+// row in registers up to 16384 entries: better for many rows (bf16, 2048 x
+// 16384 18.9 against 19.6 us here, 8192 x 4112 20 against 33), while up to two
+// rows per compute unit of more than 4096 entries are quicker here (512 x
+// 16384 5.9 against 7.5, 512 x 4112 3.8 against 4.5, one of 16384 3.3 against
+// 5.6), and longer ones in any case (64 x 65536 7.4 against 61). The same codes
+// and scale: abs-max over the row's bits, then the shared rounding.
+bool ckpt_block_per_row(int M, int C) { return C > 16384 || (C > 4096 && M <= 512); }
+
+template <typename T>
+__global__ __launch_bounds__(1024) void ckpt_write_rows_kernel(
+    const typename Elem<T>::type* __restrict__ x, int C, int8_t* __restrict__ codes,
+    float* __restrict__ scales) {
+  __shared__ uint32_t red[16];
+  const int tid = threadIdx.x;
+  const long row = blockIdx.x;
+  x += row * C;
+  codes += row * C;
+  uint32_t m = 0;
+#pragma unroll 4
+  for (int c = tid; c < C / 8; c += 1024) {
+    float v[8];
+    load8(x + 8L * c, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) { const uint32_t b = abs_bits(v[e]); m = b > m ? b : m; }
+  }
+  m = wave_max_u32(m);
+  if ((tid & 63) == 0) red[tid >> 6] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 16; ++w) m = red[w] > m ? red[w] : m;
+  const QuantParams q = absmax_params(m, 127.f);
+  if (tid == 0) scales[row] = q.scale;
+#pragma unroll 4
+  for (int c = tid; c < C / 8; c += 1024) {
+    float v[8];
+    load8(x + 8L * c, v);
+    uint32_t lo = 0, hi = 0;
+    if (q.live) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        lo |= (uint32_t)(quant_code(v[e], q.inv, 127.f) & 0xff) << (8 * e);
+        hi |= (uint32_t)(quant_code(v[e + 4], q.inv, 127.f) & 0xff) << (8 * e);
+      }
+    }
+    *reinterpret_cast<u32x2*>(codes + 8L * c) = u32x2{lo, hi};
+  }
 }
 
 // Row sums of codes, one wave per row (exact: |sum| <= 127 K < 2^31, and
@@ -212,6 +262,16 @@ void act_bwd_launch(int M, int C, const void* dy, const GradEpi& ge, void* dz, f
 }
 
 }  // namespace
+
+void launch_ckpt_write_rows(int dtype, const void* x, int M, int C, int8_t* codes, float* scales,
+                            hipStream_t st) {
+  if (!ckpt_block_per_row(M, C))
+    launch_rowquant(dtype, x, M, C, nullptr, 1, codes, scales, nullptr, st);
+  else if (dtype == 0)
+    ckpt_write_rows_kernel<F32><<<(unsigned)M, 1024, 0, st>>>(static_cast<const float*>(x), C, codes, scales);
+  else
+    ckpt_write_rows_kernel<BF16><<<(unsigned)M, 1024, 0, st>>>(static_cast<const uint16_t*>(x), C, codes, scales);
+}
 
 void launch_ckpt_write_groups(int dtype, const void* x, int M, int C, int8_t* codes,
                               uint8_t* scales, hipStream_t st) {

@@ -155,6 +155,8 @@ void launch_gemm_dx_f32(int M, int K, int N, const float* dy,
 
 // The 8-bit forms of an activation [M, C] (cfmt 0: rows, 1: groups of 32
 // columns), and its gradient alone.
+void launch_ckpt_write_rows(int dtype, const void* x, int M, int C, int8_t* codes, float* scales,
+                            hipStream_t st);
 void launch_ckpt_write_groups(int dtype, const void* x, int M, int C, int8_t* codes,
                               uint8_t* scales, hipStream_t st);
 void launch_ckpt_read(int dtype, int cfmt, const int8_t* codes, const void* scales, int M, int C,

@@ -39,7 +39,7 @@ int main(void) {
   static const int sizes[][4] = {
       /* M, C, form, status */
       {1, 16, 0, 0}, {1, 16, 1, 0}, {0, 16, 0, 1}, {-1, 16, 1, 1}, {INT_MIN, 16, 0, 1}, {1, 0, 0, 1},
-      {1, -16, 0, 1}, {1, 17, 1, 1}, {INT_MAX, 16, 0, 4}, {1, INT_MAX - 15, 0, 4}, {1, INT_MAX - 15, 1, 0}, {1, 1 << 30, 0, 0}, {2, 1 << 30, 1, 4},
+      {1, -16, 0, 1}, {1, 17, 1, 1}, {INT_MAX, 16, 0, 4}, {1, INT_MAX - 15, 0, 0}, {1, INT_MAX - 15, 1, 0}, {1, 1 << 30, 0, 0}, {2, 1 << 30, 1, 4},
       {134217727, 16, 1, 0}, {134217728, 16, 1, 4}, {5, 80, 2, 1}, {5, 80, -1, 1}, {5, 80, INT_MAX, 1},
   };
   for (size_t i = 0; i < sizeof sizes / sizeof sizes[0]; ++i)

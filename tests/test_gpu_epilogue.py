@@ -397,7 +397,8 @@ def test_gradients_are_differences_of_the_forward():
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("M,C", [(1, 16), (3, 48), (5, 80), (130, 1040), (1000, 16384), (4096, 2304)])
+@pytest.mark.parametrize("M,C", [(1, 16), (3, 48), (5, 80), (130, 1040), (1000, 16384), (4096, 2304), (1, 65536), (6, 16400),
+                                 (7, 40016)])
 def test_checkpoints_bit_exact(M, C, dtype):
     rng = np.random.default_rng(M * C)
     x = rng.standard_normal((M, C)).astype(np.float32) * (10.0 ** rng.integers(-6, 6, (M, 1))).astype(np.float32)
