@@ -595,6 +595,11 @@ def _layer_on(layer: QLinear, device) -> qlora_linear:
     raise AssertionError("unreachable: one of the checks above fails")
 
 
+def _unused(t, what: str, flag: str) -> None:
+    if t is not None:
+        raise ValueError(f"{what}: given, but {flag} does not ask for it")
+
+
 def _act(act: str) -> int:
     if act not in _ACT:
         raise ValueError(f"unknown activation {act!r}")
@@ -673,7 +678,7 @@ def _epilogue(layer, M, dtype, device, act, bias, residual, save_z, z, xc):
     elif save_z is not None:
         raise ValueError(f"save_z: {save_z!r} is neither None, 'full' nor 'c8g32'")
     else:
-        z = None
+        _unused(z, "z", "save_z")
     if xc is not None:
         e.x_codes, e.x_scales = _ptr(xc.codes), _ptr(xc.scales)
     return e, z
@@ -695,17 +700,18 @@ def qlora_fwd_epi(layer: QLinear, x, act: str = "none", bias=None, residual=None
     if save_t:
         t = layer.A.new_empty((M, layer.r)) if t is None else \
             _tensor(t, "t", (M, layer.r), torch.float32, dev)
+    else:
+        _unused(t, "t", "save_t")
     if save_x:
         xc = _new_ckpt(M, layer.K, "c8row", x) if xc is None else _ckpt(xc, "xc", "c8row", (M, layer.K), dev)
     else:
-        xc = None
+        _unused(xc, "xc", "save_x")
     e, z = _epilogue(layer, M, x.dtype, dev, act, bias, residual, save_z, z, xc)
     ws = _scratch("qlora_fwd_workspace", layer, cs, M, dt, dev, ws)
     with _on(dev):
         _check(lib().qlora_fwd_epi(ctypes.byref(cs), M, dt, _ptr(x), ctypes.byref(e), _ptr(y),
-                                   _ptr(t) if save_t else None, _ptr(ws),
-                                   ws.nbytes, _stream()), "qlora_fwd_epi")
-    return y, (t if save_t else None), z, xc
+                                   _ptr(t), _ptr(ws), ws.nbytes, _stream()), "qlora_fwd_epi")
+    return y, t, z, xc
 
 
 def qlora_fwd_ckpt(layer: QLinear, xc: Checkpoint, t, dtype, act: str = "none", bias=None, residual=None,
@@ -761,7 +767,7 @@ def _bwd_epi_args(layer, x, dy, t, act, z, add, need_dx, dx):
     else:
         if act != "none" or z is not None or add is not None:
             raise ValueError("need_dx: act, z and add apply to dx")
-        dx = None
+        _unused(dx, "dx", "need_dx")
     gp = ctypes.byref(g) if need_dx else None
     return cs, M, dt, dev, (xp, xcodes, xscales, _ptr(dy), _ptr(t), gp, _ptr(dx)), dx, g
 
@@ -814,7 +820,7 @@ def qlora_act_bwd(act: str, dy, z=None, need_dz: bool = True, need_dbias: bool =
     if need_dz:
         dz = torch.empty_like(dy) if dz is None else _tensor(dz, "dz", (M, N), dy.dtype, dev)
     else:
-        dz = None
+        _unused(dz, "dz", "need_dz")
     if need_dbias:
         dbias = torch.empty((N,), dtype=torch.float32, device=dev) if dbias is None else \
             _tensor(dbias, "dbias", (N,), torch.float32, dev)
@@ -824,7 +830,8 @@ def qlora_act_bwd(act: str, dy, z=None, need_dz: bool = True, need_dbias: bool =
         elif ws.device != dev or not ws.is_contiguous():
             raise ValueError(f"ws: a contiguous tensor on {dev} is needed")
     else:
-        dbias = ws = None
+        _unused(dbias, "dbias", "need_dbias")
+        ws = None
     with _on(dev):
         _check(lib().qlora_act_bwd(_act(act), M, N, dt, _ptr(dy), zp, zc, zs, _ptr(dz), _ptr(dbias),
                                    _ptr(ws), 0 if ws is None else ws.nbytes,

@@ -698,6 +698,15 @@ def test_refusals():
     for bad in (c.x_t[:, :48], c.x_t.t(), c.x_t[0], c.x_t.cpu(), torch.cat([c.x_t, c.x_t], 1)[:, ::2]):
         with val:
             Q.qlora_fwd_epi(c.lin, bad)
+    # buffers for what is not asked for
+    for kw in (dict(t=t, save_t=False), dict(xc=xc), dict(z=c.dy_t)):
+        with val:
+            Q.qlora_fwd_epi(c.lin, c.x_t, **kw)
+    with val:
+        Q.qlora_bwd_epi(c.lin, xc, c.dy_t, t, need_dx=False, dx=c.add_t.clone())
+    for kw in (dict(need_dz=False, dz=c.dy_t.clone()), dict(need_dbias=False, dbias=bias.clone())):
+        with val:
+            Q.qlora_act_bwd("none", c.dy_t, **kw)
     with typ:
         Q.qlora_fwd_epi(c.lin, c.x_t.half())
     for kw in (dict(bias=bias[:64]), dict(bias=bias.cpu()), dict(residual=c.res_t[:4]), dict(act="tanh"),
