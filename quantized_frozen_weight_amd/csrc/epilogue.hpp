@@ -177,13 +177,14 @@ __device__ __forceinline__ int group_byte(uint32_t amax_bits) {
 }
 
 // The code of v under scale byte b (not 255) in the low byte; the rest of the
-// word is not its sign. v 2^-e, moved out to +-0.75 where it is smaller but
-// not 0 (so that it rounds to +-1), is rounded to an integer, ties to even, by
-// adding 3 2^22: the sum's last 8 bits are the code.
+// word is not its sign. v 2^-e, moved out to +-0.75 where it is smaller but v
+// is not 0 (so that it rounds to +-1), is rounded to an integer, ties to even,
+// by adding 3 2^22: the sum's last 8 bits are the code. (v itself decides, not
+// v 2^-e, which underflows to 0 where v is below 2^-149 of the scale.)
 __device__ __forceinline__ uint32_t group_code_bits(float v, float inv) {
   const float t = v * inv;
-  const float m = __builtin_copysignf(fmaxf(__builtin_fabsf(t), 0.75f), t);
-  return __float_as_uint((t == 0.f ? t : m) + 12582912.f);
+  const float m = __builtin_copysignf(fmaxf(__builtin_fabsf(t), 0.75f), v);
+  return __float_as_uint((v == 0.f ? v : m) + 12582912.f);
 }
 // 2^-e = 2^(127 - b); b in [1, 249]
 __device__ __forceinline__ float group_inverse(int b) { return __uint_as_float((uint32_t)(254 - b) << 23); }

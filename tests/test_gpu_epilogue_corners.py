@@ -1,0 +1,85 @@
+"""Corners of the epilogue and checkpoint calls on the GPU: values far apart in
+one group, the ends of the float range, odd rows among few, the largest sizes."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from oracle import epilogue_oracle as E
+from oracle import qlora_oracle as O
+from quantized_frozen_weight_amd import binding as Q
+from quantized_frozen_weight_amd import workloads as WL
+from tests.helpers import to_numpy
+from tests.test_gpu_epilogue import bits, dev, say
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+F64 = np.float64
+TD = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU visible")
+    Q.lib()
+
+
+def zero_layer(K, N, fmt):
+    """A layer whose product and adapter are zero, so that z is the bias."""
+    z = lambda *s, dtype=torch.float32: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
+    if fmt == "w4g128":
+        codes, scales = z(N, K // 2, dtype=torch.uint8), z(N, K // 128, dtype=torch.float16)
+    elif fmt == "w8o":
+        codes, scales = Q.qlora_quantize(z(K, N), "w8o")
+    else:
+        codes, scales = z(N, K, dtype=torch.int8), z(N)
+    return Q.QLinear(K, N, 4, 8.0, fmt, codes, scales, z(K, 4), z(4, N))
+
+
+# pairs (abs-max of a group, a value in it) whose ratio takes the value under
+# the smallest float once the group's scale is divided out
+FAR = [(1e30, 1e-20), (1e30, -1e-20), (1e20, -1e-30), (1e10, 1e-38), (3e38, -1e-9), (1e3, 1e-45), (-1e3, -1e-45),
+       (2.0, 1e-39)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_group_codes_keep_the_sign_of_values_far_below_their_group(dtype):
+    x = np.zeros((len(FAR), 80), np.float32)
+    for i, (top, v) in enumerate(FAR):
+        x[i, 5], x[i, 6:30], x[i, 40], x[i, 79] = top, v, v, v
+    x_t, x = WL.as_compute_dtype(x, dtype)
+    say("far below the group", dtype)
+    c = Q.qlora_ckpt_write(x_t.cuda(), "c8g32")
+    dz, _ = Q.qlora_act_bwd("relu", torch.ones_like(x_t).cuda(), c, need_dbias=False)
+    torch.cuda.synchronize()
+    q, b = E.write_groups(x)
+    assert np.array_equal(c.scales.cpu().numpy(), b)
+    assert np.array_equal(c.codes.cpu().numpy(), q)
+    assert np.array_equal(np.sign(q), np.sign(x))
+    assert np.array_equal(to_numpy(dz), (x > 0).astype(np.float32))
+
+
+@pytest.mark.parametrize("M,K,N,fmt,dtype", [
+    (1, 64, 272, "w8", "f32"), (3, 64, 272, "w8", "bf16"), (2, 16384, 144, "w8", "bf16"),   # few rows
+    (4, 256, 272, "w4g128", "bf16"), (70, 64, 272, "w8", "f32"), (70, 64, 272, "w8", "bf16"),
+    (100, 4096, 272, "w8", "bf16"), (70, 256, 272, "w4g128", "bf16"), (90, 8192, 144, "w4g128", "bf16"),
+    (70, 256, 272, "w8o", "bf16"), (130, 4096, 80, "w8o", "bf16")])
+def test_saved_z_keeps_the_sign_of_values_far_below_their_group(M, K, N, fmt, dtype):
+    z = np.zeros(N, np.float32)
+    for i in range(N // 16):
+        top, v = FAR[i % len(FAR)]
+        z[16 * i + 3], z[16 * i + 4: 16 * i + 9] = top, v
+    lin = zero_layer(K, N, fmt)
+    x = torch.ones((M, K), device="cuda", dtype=TD[dtype])
+    say("saved z far below the group", M, K, N, fmt, dtype)
+    _, t, c, xc = Q.qlora_fwd_epi(lin, x, bias=dev(z), save_z="c8g32", save_x=True)
+    c2 = Q.qlora_fwd_ckpt(lin, xc, t, x.dtype, bias=dev(z), save_z="c8g32")[1]
+    torch.cuda.synchronize()
+    q, b = E.write_groups(np.tile(z, (M, 1)))
+    for got in (c, c2):
+        assert np.array_equal(got.scales.cpu().numpy(), b)
+        assert np.array_equal(got.codes.cpu().numpy(), q)
