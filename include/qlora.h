@@ -394,8 +394,9 @@ typedef enum { QLORA_C8ROW = 0, QLORA_C8G32 = 1 } qlora_cfmt;
 int qlora_ckpt_bytes(int M, int C, int cfmt, size_t* codes_bytes, size_t* scale_bytes);
 
 /* Write x [M, C] (compute dtype) in form cfmt, and read it back: value =
- * code * scale, rounded once to the compute dtype (exact in either dtype for
- * QLORA_C8G32). */
+ * code * scale in float32, rounded to the compute dtype (both steps exact for
+ * QLORA_C8G32). A product past the dtype's largest finite value, which the
+ * top of a group or row near it may give, reads back as that value. */
 int qlora_ckpt_write(const void* x, int M, int C, int dtype, int cfmt, int8_t* codes,
                      void* scales, void* stream);
 int qlora_ckpt_read(const int8_t* codes, const void* scales, int M, int C, int cfmt,

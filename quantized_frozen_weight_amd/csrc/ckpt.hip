@@ -41,6 +41,10 @@ __global__ __launch_bounds__(256) void ckpt_write_groups_kernel(
   }
 }
 
+// The abs-max of a row or group may round up to a product past the largest
+// finite value (127 (FLT_MAX / 127); groups from 127 / 64 2^127 on, whose code
+// 64 stands for 2^128): such a product reads back as that value, so that
+// finite activations stay finite. (The comparisons keep a NaN.)
 template <typename T, bool GROUPS>
 __global__ __launch_bounds__(256) void ckpt_read_kernel(
     const int8_t* __restrict__ codes, const void* __restrict__ scales, int M, int C,
@@ -57,6 +61,9 @@ __global__ __launch_bounds__(256) void ckpt_read_kernel(
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = (float)(int8_t)(c[e >> 2] >> (8 * (e & 3))) * s;
   }
+  const float top = __uint_as_float(std::is_same<T, F32>::value ? 0x7f7fffffu : 0x7f7f0000u);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = v[e] > top ? top : v[e] < -top ? -top : v[e];
   store8(x + 8L * u, v);
 }
 

@@ -214,6 +214,8 @@ __device__ __forceinline__ float group_scale(int b) {
   return __uint_as_float(b == 255 ? 0x7fc00000u : (uint32_t)b << 23);
 }
 
+// (Code 64 of byte 249 is an infinity here; every slope has its limit from
+// 100 on, so z may stay that.)
 __device__ __forceinline__ void group_values(u32x2 c, int b, float (&v)[8]) {
   const float s = group_scale(b);
 #pragma unroll

@@ -83,3 +83,27 @@ def test_saved_z_keeps_the_sign_of_values_far_below_their_group(M, K, N, fmt, dt
     for got in (c, c2):
         assert np.array_equal(got.scales.cpu().numpy(), b)
         assert np.array_equal(got.codes.cpu().numpy(), q)
+
+
+@pytest.mark.parametrize("fmt", ["c8row", "c8g32"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_checkpoints_of_the_largest_finite_values_read_back_finite(dtype, fmt):
+    top = np.float32(np.finfo(np.float32).max) if dtype == "f32" else np.float32(2.0 ** 128 - 2.0 ** 120)
+    x = np.zeros((7, 48), np.float32)
+    x[0, 3], x[1, 40], x[2, :] = top, -top, top
+    x[3, 0], x[4, 1] = np.float32(3.4e38) if dtype == "f32" else top, 127 / 64 * 2.0 ** 127
+    x[5, 7], x[6, 9] = np.inf, np.nan
+    x_t, x = WL.as_compute_dtype(x, dtype)
+    say("largest values", dtype, fmt)
+    c = Q.qlora_ckpt_write(x_t.cuda(), fmt)
+    got = {d: to_numpy(Q.qlora_ckpt_read(c, TD[d])) for d in TD}      # in its own dtype and the other
+    if fmt == "c8row":
+        want = E.read_rows(*O.quantize_rows(x))
+    else:
+        want = E.read_groups(*E.write_groups(x))
+    for d, g in got.items():
+        lim = np.finfo(np.float32).max if d == "f32" else 2.0 ** 128 - 2.0 ** 120
+        with np.errstate(over="ignore"):
+            w = np.clip(O.round_to(want, d).astype(F64), -lim, lim)
+        assert np.array_equal(g.astype(F64), w, equal_nan=True), d
+        assert np.isfinite(g[:5]).all() and np.array_equal(np.sign(g[:5]), np.sign(x[:5]))
