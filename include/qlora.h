@@ -201,8 +201,9 @@ int qlora_fwd_workspace(const qlora_linear* L, int M, int dtype,
 
 /* Forward ("LoRA equation"): y [M, N] = x . deq(W) + s (x A) B, rounded once
  * to the compute dtype. For QLORA_W8, x is quantized per row and the base
- * product is an int8 x int8 -> int32 sum rescaled by sx[m] * sw[n]. If t_save
- * is not NULL, t = x A (float32 [M, r]) is written there for the backward. */
+ * product is an int8 x int8 -> int32 sum rescaled by sx[m] * sw[n] (exact up
+ * to K = 132096; past it rows and channels of nearly all the largest codes
+ * could pass int32, which is not checked). If t_save is not NULL, t = x A (float32 [M, r]) is written there for the backward. */
 int qlora_fwd(const qlora_linear* L, int M, int dtype, const void* x, void* y,
               float* t_save, void* ws, size_t ws_bytes, void* stream);
 
@@ -379,8 +380,9 @@ const char* qlora_bwd_main_kernel(const qlora_linear* L, int M, int dtype);
  * row of NaN in y under the int8 formats and their checkpoints, and touches no
  * other row.
  *
- * Constraints as above, with M >= 1 and every pointer 16-byte aligned; of a
- * pair (codes, scales) both or neither is given. Every tensor is dense
+ * Constraints as above, with M >= 1 and every pointer 16-byte aligned; the two
+ * forwards take int8 formats up to K = 132096, where the int32 and float32
+ * sums of codes are exact for any codes (EUNSUPPORTED above); of a pair (codes, scales) both or neither is given. Every tensor is dense
  * row-major. Outputs must not overlap inputs or each other (EINVAL), except
  * that y may be residual, dx may be add, and dz may be dy, exactly. */
 typedef enum {

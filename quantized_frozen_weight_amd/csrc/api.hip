@@ -305,6 +305,12 @@ inline bool pair_ok(const void* codes, const void* scales) {
   return (codes == nullptr) == (scales == nullptr) && opt16(codes) && opt16(scales);
 }
 
+// The longest contraction whose int8 sums cannot pass their registers: int32
+// products of codes up to 127 and 128 (127 * 128 K < 2^31) and, for the affine
+// weights, float32 sums of the row's codes (127 K < 2^24).
+constexpr int kI8ExactK = 132096;
+inline bool exact_sums(const qlora_linear* L) { return L->fmt == QLORA_W4G128 || L->K <= kI8ExactK; }
+
 inline bool act_ok(int act) { return act >= QLORA_ACT_NONE && act <= QLORA_ACT_SILU; }
 
 // The forward epilogue: pointers checked, and its ranges added. in_y: y given
@@ -770,6 +776,7 @@ int qlora_fwd_epi(const qlora_linear* L, int M, int dtype, const void* x,
                   size_t ws_bytes, void* stream) {
   int st = check_linear(L, M, dtype);
   if (st) return st;
+  if (!exact_sums(L)) return QLORA_EUNSUPPORTED;
   if (!x || !y || !aligned16(x) || !aligned16(y) || !opt16(t_save)) return QLORA_EINVAL;
   const int K = L->K, N = L->N;
   Ranges in, out;
@@ -818,6 +825,7 @@ int qlora_fwd_ckpt(const qlora_linear* L, int M, int dtype, const int8_t* x_code
                    void* y, void* ws, size_t ws_bytes, void* stream) {
   int st = check_linear(L, M, dtype);
   if (st) return st;
+  if (!exact_sums(L)) return QLORA_EUNSUPPORTED;
   if (!x_codes || !x_scales || !t || !y || !aligned16(x_codes) || !aligned16(x_scales) ||
       !aligned16(t) || !aligned16(y))
     return QLORA_EINVAL;
