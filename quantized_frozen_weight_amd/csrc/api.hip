@@ -71,13 +71,14 @@ inline float lora_s(const qlora_linear* L) {
 }
 
 struct FwdLayout {
-  size_t xq, sx, t, asum, pacc, pcorr, rs, few, total;
+  size_t xq, sx, t, asum, pacc, pcorr, rs, total;
 };
 FwdLayout fwd_layout(const qlora_linear* L, int M) {
   FwdLayout w{};
   size_t off = 0;
   // activation codes and scales: the int8 product, and the integer forward
-  // of 4-bit layers
+  // of 4-bit layers (the few-row forward, which keeps its codes in LDS, has
+  // its slices of t there)
   w.xq = off; off = align_up(off + (size_t)M * L->K);
   w.sx = off; off = align_up(off + (size_t)M * 4);
   w.t = off; off = align_up(off + (size_t)M * L->r * 4);
@@ -93,8 +94,6 @@ FwdLayout fwd_layout(const qlora_linear* L, int M) {
   w.pcorr = off; off = align_up(off + (w8o ? nsplit * 4 : 0));
   // the row pass of long rows split over k (0 bytes for other widths)
   w.rs = off; off = align_up(off + row_split_floats(M, L->K, L->r) * 4);
-  // the few-row forward's slices of t (0 bytes past four rows)
-  w.few = off; off = align_up(off + fwd_few_floats(M, L->K) * 4);
   w.total = off;
   return w;
 }
@@ -800,7 +799,7 @@ int qlora_fwd_epi(const qlora_linear* L, int M, int dtype, const void* x,
   if (fwd_few_takes(L->fmt, M, K, L->r)) {
     launch_fwd_few(dtype, L->fmt, M, N, K, x, L->codes, L->scales, L->A, L->B, head_width(L), L->r,
                    lora_s(L), epi, y, t_save, e->x_codes, e->x_scales,
-                   reinterpret_cast<float*>(at(ws, w.few)), s);
+                   reinterpret_cast<float*>(at(ws, w.xq)), s);
     return launch_status();
   }
   if (L->fmt == QLORA_W4G128) {

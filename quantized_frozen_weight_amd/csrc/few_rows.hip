@@ -418,6 +418,9 @@ void few_rows(FewArgs a, hipStream_t st) {
   const size_t lds = (size_t)a.M * ((a.K + step - 1) / step * step) * (W4 ? 2 : 1);
   const unsigned grid = (unsigned)((a.N + 16 * NG - 1) / (16 * NG));
   if ((long)a.K * R > kPreWords) {
+    // the slices' maxima and sums, 4 MB (R + 1) bytes each, in the M K bytes of
+    // scratch: K is past 2048 here, so a slice stands for 409 k at least, and
+    // 68 (one row) or 272 (MB = 4, two rows or more) is below 409 M
     a.slices = (a.K + kSlice - 1) / kSlice;
     a.pre_max = reinterpret_cast<uint32_t*>(a.pre_t + (size_t)a.slices * MB * R);
     fwd_few_pre_kernel<T, R, MB><<<(unsigned)a.slices, 512, 0, st>>>(a);
@@ -455,11 +458,6 @@ void few_ranks(const FewArgs& a, hipStream_t st) {
 // LDS four times.
 bool fwd_few_takes(int fmt, int M, int K, int r) {
   return (fmt == 0 || fmt == 1) && M <= 4 && r <= 16 && K <= kFewMaxK;
-}
-
-size_t fwd_few_floats(int M, int K) {
-  if (M > 4) return 0;
-  return (size_t)((K + kSlice - 1) / kSlice) * 4 * (16 + 1);
 }
 
 void launch_fwd_few(int dtype, int fmt, int M, int N, int K, const void* x, const void* codes,

@@ -29,3 +29,15 @@ def test_contractions_whose_code_sums_could_overflow_are_refused(lib, fmt, dt):
     n = ctypes.c_size_t()
     # the plain forward takes what it took
     assert lib.qlora_fwd_workspace(ctypes.byref(layer(fmt, K=last + 16, N=16)), 1, dt, ctypes.byref(n)) == OK
+
+
+@pytest.mark.parametrize("fmt", [Q.QLORA_W8, Q.QLORA_W8O, Q.QLORA_W4G128])
+@pytest.mark.parametrize("m", [1, 4, 5])
+def test_forward_workspace_of_few_rows_is_that_of_the_plain_forward(lib, m, fmt):
+    """Codes, scales, t and (affine) the rows' code sums, each to 256 bytes; no
+    split of so wide an output, and nothing for the few-row kernel."""
+    k, n_out, r = 4096, 25600, 8
+    up = lambda v: -(-v // 256) * 256  # noqa: E731
+    n = ctypes.c_size_t()
+    assert lib.qlora_fwd_workspace(ctypes.byref(layer(fmt, K=k, N=n_out, r=r)), m, BF, ctypes.byref(n)) == OK
+    assert n.value == up(m * k) + up(4 * m) + up(4 * m * r) + (up(4 * m) if fmt == Q.QLORA_W8O else 0)
