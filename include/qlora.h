@@ -423,8 +423,7 @@ typedef struct {
  * the results are bitwise qlora_fwd's, except that up to four rows of int8 and
  * 4-bit layers (rank <= 16, K <= 16384) take a kernel of their own, whose int8
  * base product is the same and whose float32 sums (t; 4-bit: the base too) run
- * in another order; a 4-bit row may come out non-finite there where |x| passes
- * 2^113. */
+ * in another order. */
 int qlora_fwd_epi(const qlora_linear* L, int M, int dtype, const void* x,
                   const qlora_epilogue* e, void* y, float* t_save, void* ws,
                   size_t ws_bytes, void* stream);

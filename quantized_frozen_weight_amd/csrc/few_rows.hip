@@ -88,6 +88,22 @@ __device__ __forceinline__ bf16x8 nibbles_136(uint32_t w) {
 }
 constexpr uint32_t kNib = 0xC308C308u;         // bf16 -136, twice
 
+// The same codes as the tiled product takes them, bf16(q sc), pair i again
+// nibbles i and i + 4. A wave whose sums come out non-finite takes its steps
+// again with these: 136 |x| and |x q| pass the float range (from |x| = 2^113
+// on) where x times the weight does not.
+__device__ __forceinline__ bf16x8 nibbles_scaled(uint32_t w, float sc) {
+  const uint32_t u = w ^ 0x88888888u;          // q + 8
+  const float nsc = -8.f * sc;
+  u32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = cvt_bf16x2(__builtin_fmaf((float)((u >> (4 * i)) & 15u), sc, nsc),
+                      __builtin_fmaf((float)((u >> (4 * i + 16)) & 15u), sc, nsc));
+  return __builtin_bit_cast(bf16x8, o);
+}
+__device__ __forceinline__ bool finite(float v) { return abs_bits(v) < 0x7f800000u; }
+
 // eight bf16 values in the order 0 4 1 5 2 6 3 7
 __device__ __forceinline__ u32x4 nibble_order(u32x4 v) {
   return u32x4{__builtin_amdgcn_perm(v[2], v[0], 0x05040100u), __builtin_amdgcn_perm(v[2], v[0], 0x07060302u),
@@ -357,6 +373,25 @@ __global__ __launch_bounds__(kThreads) void fwd_few_kernel(FewArgs a) {
           if constexpr (W4) hsc[i] = scb[s0 + ib + i + kHold];
         }
       }
+    }
+  }
+  if constexpr (W4) {
+    bool all = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) all &= finite(accf[i]);
+    if (__builtin_amdgcn_ballot_w64(!all) != 0) {
+      f32x4 again = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int s = s0; s < s0 + cnt; ++s) {
+        const u32x4 w = load(s);
+        const float sc = (float)scb[s];
+        const int8_t* xp = xs + ((long)xm * kpad + 128 * s + 32 * (lane >> 4)) * 2;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          again = __builtin_amdgcn_mfma_f32_16x16x32_bf16(*reinterpret_cast<const bf16x8*>(xp + 16 * q),
+                                                          nibbles_scaled(w[q], sc), again, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) accf[i] = finite(accf[i]) ? accf[i] : again[i];   // other rows as they were
     }
   }
   // rows 0..3 of the 16 x 16 block: lanes 0..15

@@ -11,7 +11,7 @@ from oracle import qlora_oracle as O
 from quantized_frozen_weight_amd import binding as Q
 from quantized_frozen_weight_amd import workloads as WL
 from tests.helpers import to_numpy
-from tests.test_gpu_epilogue import bits, dev, say
+from tests.test_gpu_epilogue import Case, bits, dev, say, within
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +107,57 @@ def test_checkpoints_of_the_largest_finite_values_read_back_finite(dtype, fmt):
             w = np.clip(O.round_to(want, d).astype(F64), -lim, lim)
         assert np.array_equal(g.astype(F64), w, equal_nan=True), d
         assert np.isfinite(g[:5]).all() and np.array_equal(np.sign(g[:5]), np.sign(x[:5]))
+
+
+@pytest.mark.parametrize("M,K,N,r", [(1, 256, 272, 4), (3, 4096, 144, 8), (4, 4096, 528, 16), (2, 16384, 80, 1)])
+def test_few_4bit_rows_with_huge_inputs(M, K, N, r):
+    """Inputs up to the largest finite one, whose products with the weight stay
+    finite, give finite outputs within the bounds of any other input; the other
+    rows are the bytes they are without them."""
+    c = Case(M, K, N, r, "w4g128")
+    y0 = Q.qlora_fwd_epi(c.lin, c.x_t)[0]
+    for big in (2.0 ** 114, -2.0 ** 126, 2.0 ** 127 * 1.98):
+        say("huge few rows", M, K, N, r, big)
+        x = c.x.copy()
+        x[M - 1, 5::131] = big
+        x[M - 1, 7::509] = -big
+        c2 = Case(M, K, N, r, "w4g128")
+        c2.x_t, c2.x = WL.as_compute_dtype(x, "bf16")
+        W = c2.W
+        # (finite: every output, and every sum of absolute products on the way)
+        low = c2.s * (np.abs(c2.x.astype(F64)) @ np.abs(c2.A64)) @ np.abs(c2.B64)
+        scale = (np.abs(c2.x.astype(F64)) @ np.abs(W) + low).max() / 2.0 ** 126
+        if scale > 1:
+            c2.x_t, c2.x = WL.as_compute_dtype(x * np.float32(2.0 ** -np.ceil(np.log2(scale))), "bf16")
+        y, t, _, _ = Q.qlora_fwd_epi(c2.lin, c2.x_t.cuda())
+        torch.cuda.synchronize()
+        (wy, _, wt), (ty, _, tt) = c2.forward("none", False, False)
+        assert np.isfinite(to_numpy(y)).all()
+        within(to_numpy(y), wy, ty, "y")
+        within(to_numpy(t), wt, tt, "t")
+        if scale <= 1 and M > 1:
+            assert torch.equal(bits(y[:M - 1]), bits(y0[:M - 1]))
+
+
+@pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("M,K,N,r", [(1, 256, 272, 4), (3, 4096, 144, 8), (4, 16384, 80, 16)])
+def test_few_4bit_rows_that_are_not_finite(M, K, N, r, what):
+    """NaN and infinities sit where the tiled product and the oracle have
+    them, and touch no other row."""
+    c = Case(M, K, N, r, "w4g128")
+    # one sign in the adapter: its term is an infinity then, and no NaN
+    c.A64, c.B64 = np.abs(c.A64), np.abs(c.B64)
+    c.lin.A, c.lin.B = c.lin.A.abs(), c.lin.B.abs()
+    x = c.x_t.clone()
+    x[M - 1, 9] = what
+    say("few rows not finite", M, K, N, r, what)
+    y0, y = (Q.qlora_fwd_epi(c.lin, v)[0] for v in (c.x_t, x))
+    tiled = Q.qlora_fwd(c.lin, x)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(bits(y[:M - 1]), bits(y0[:M - 1]))
+    x64 = to_numpy(x).astype(F64)
+    with np.errstate(invalid="ignore"):
+        want = x64 @ c.W + c.s * ((x64 @ c.A64) @ c.B64)
+    for name, g in (("few", to_numpy(y)), ("tiled", to_numpy(tiled))):
+        for f in (np.isnan, np.isposinf, np.isneginf):
+            assert (f(g) != f(want)).sum() == 0, (name, f.__name__)
