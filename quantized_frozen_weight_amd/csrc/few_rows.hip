@@ -322,7 +322,7 @@ __global__ __launch_bounds__(kThreads) void fwd_few_kernel(FewArgs a) {
       for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor(v, d);
       if ((tid & 31) == 0) {
         const int m = o / R, j = o % R;
-        ts[m][j] = v;
+        ts[m][j] = j < r ? v : 0.f;            // (an infinite x times the padded ranks' zeros is NaN)
         if (blockIdx.x == 0 && a.t != nullptr && m < M && j < r) a.t[(long)m * r + j] = v;
       }
     }
@@ -331,7 +331,7 @@ __global__ __launch_bounds__(kThreads) void fwd_few_kernel(FewArgs a) {
     float v = red_t[j / 4][4 * m + j % 4];
 #pragma unroll
     for (int w = 1; w < KW; ++w) v += red_t[w * JW + j / 4][4 * m + j % 4];
-    ts[m][j] = v;
+    ts[m][j] = j < r ? v : 0.f;
     if (blockIdx.x == 0 && a.t != nullptr && m < M && j < r) a.t[(long)m * r + j] = v;
   }
   if (blockIdx.x == 0 && a.sx != nullptr && tid < M) {

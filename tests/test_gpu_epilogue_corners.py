@@ -140,7 +140,8 @@ def test_few_4bit_rows_with_huge_inputs(M, K, N, r):
 
 
 @pytest.mark.parametrize("what", [np.inf, -np.inf, np.nan])
-@pytest.mark.parametrize("M,K,N,r", [(1, 256, 272, 4), (3, 4096, 144, 8), (4, 16384, 80, 16)])
+@pytest.mark.parametrize("M,K,N,r", [(1, 256, 272, 4), (3, 4096, 144, 8), (4, 16384, 80, 16),
+                                     (1, 256, 272, 1), (2, 16384, 80, 3), (4, 384, 80, 11)])
 def test_few_4bit_rows_that_are_not_finite(M, K, N, r, what):
     """NaN and infinities sit where the tiled product and the oracle have
     them, and touch no other row."""
