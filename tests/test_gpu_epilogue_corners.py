@@ -162,3 +162,31 @@ def test_few_4bit_rows_that_are_not_finite(M, K, N, r, what):
     for name, g in (("few", to_numpy(y)), ("tiled", to_numpy(tiled))):
         for f in (np.isnan, np.isposinf, np.isneginf):
             assert (f(g) != f(want)).sum() == 0, (name, f.__name__)
+
+
+@pytest.mark.parametrize("M", [1, 70])
+def test_float32_gelu_tail_to_a_millionth(M):
+    """Float32 GELU and its slope down to the smallest normal results. y for z
+    < 0 is -|z| Phi(-|z|): 1e-6 of the tail (the polynomial's 6e-7 with its own
+    roundings, and one step of 2^-23 each for the exponential and the
+    reciprocal) and the output's rounding. The slope is Phi + z phi: 1e-6 of
+    the first; the exponential's 4e-7 and three roundings of the second; and
+    the output's."""
+    N = 16384
+    z = np.concatenate([-np.linspace(0, 12.6, N - 4096), np.geomspace(1e-6, 12, 4096)]).astype(np.float32)
+    lin = zero_layer(16, N, "w8")
+    say("gelu tail", M)
+    y = Q.qlora_fwd_epi(lin, torch.ones((M, 16), device="cuda"), act="gelu", bias=dev(z))[0]
+    zt = dev(np.tile(z, (M, 1)))
+    dz, _ = Q.qlora_act_bwd("gelu", torch.ones_like(zt), zt)
+    torch.cuda.synchronize()
+    u = 2.0 ** -24
+    z64 = z.astype(F64)
+    w = E.act("gelu", z64)
+    tail = np.abs(z64) * E.act("gelu", -np.abs(z64)) / np.minimum(-np.abs(z64), -1e-300)   # |z| Phi(-|z|)
+    within(to_numpy(y), np.tile(w, (M, 1)), np.tile(1e-6 * tail + u * np.abs(w) + 2.0 ** -149, (M, 1)), "gelu")
+    phi = np.exp(-0.5 * z64 * z64) / np.sqrt(2 * np.pi)
+    sl = E.slope("gelu", z64)
+    cdf = tail / np.maximum(np.abs(z64), 1e-300)
+    tol = 1e-6 * cdf + (4e-7 + 3 * u) * np.abs(z64) * phi + 2 * u * np.abs(sl) + 2.0 ** -149
+    within(to_numpy(dz), np.tile(sl, (M, 1)), np.tile(tol, (M, 1)), "gelu slope")
