@@ -122,17 +122,17 @@ __global__ __launch_bounds__(1024) void ckpt_write_rows_kernel(
 __global__ __launch_bounds__(256) void code_sums_kernel(const int8_t* __restrict__ codes, int M,
                                                         int K, float* __restrict__ asum) {
   const int lane = threadIdx.x & 63;
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= M) return;
-  int sum = 0;
-  for (int k = 16 * lane; k < K; k += 1024) {
-    const i32x4 c = *reinterpret_cast<const i32x4*>(codes + (long)row * K + k);
+  for (int row = blockIdx.x * 4 + (threadIdx.x >> 6); row < M; row += 4 * (int)gridDim.x) {
+    int sum = 0;
+    for (int k = 16 * lane; k < K; k += 1024) {
+      const i32x4 c = *reinterpret_cast<const i32x4*>(codes + (long)row * K + k);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum = __builtin_amdgcn_sdot4(c[i], 0x01010101, sum, false);
+      for (int i = 0; i < 4; ++i) sum = __builtin_amdgcn_sdot4(c[i], 0x01010101, sum, false);
+    }
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+    if (lane == 0) asum[row] = (float)sum;
   }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
-  if (lane == 0) asum[row] = (float)sum;
 }
 
 // ---- dz = dy act'(z), dbias = column sums -----------------------------------
@@ -158,9 +158,11 @@ inline int col_blocks(int C) { return C / kActCols + (C % kActCols != 0); }
 // Rows per span and row lanes.
 void act_bwd_plan(int M, int C, int* spans, int* rows, int* lanes) {
   if (M <= 32 * act_units(32)) {
+    // (a launch takes fewer than 2^32 threads: rows past 2^29, at most three
+    // of them, get blocks of 8 lanes)
     *spans = 1;
     *rows = M;
-    *lanes = 32;
+    *lanes = col_blocks(C) < 1 << 21 ? 32 : 8;
     return;
   }
   // 4096 blocks where there are that many rows, but 16 rows a span at least,
@@ -304,7 +306,8 @@ void launch_ckpt_read(int dtype, int cfmt, const int8_t* codes, const void* scal
 }
 
 void launch_code_sums(const int8_t* codes, int M, int K, float* asum, hipStream_t st) {
-  code_sums_kernel<<<(unsigned)((M + 3) / 4), 256, 0, st>>>(codes, M, K, asum);
+  const int nb = M / 4 + (M % 4 != 0);
+  code_sums_kernel<<<(unsigned)(nb < 1 << 16 ? nb : 1 << 16), 256, 0, st>>>(codes, M, K, asum);
 }
 
 size_t act_bwd_floats(int M, int C) {

@@ -190,3 +190,31 @@ def test_float32_gelu_tail_to_a_millionth(M):
     cdf = tail / np.maximum(np.abs(z64), 1e-300)
     tol = 1e-6 * cdf + (4e-7 + 3 * u) * np.abs(z64) * phi + 2 * u * np.abs(sl) + 2.0 ** -149
     within(to_numpy(dz), np.tile(sl, (M, 1)), np.tile(tol, (M, 1)), "gelu slope")
+
+
+@pytest.mark.parametrize("C", [2 ** 29 + 16, 2 ** 30, 2 ** 31 - 16])
+def test_activation_backward_of_the_longest_rows(C):
+    """One row up to the longest that the calls take: more threads than a
+    launch has at 32 row lanes a block."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    dy = torch.empty((1, C), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    say("longest rows", C)
+    dz, db = Q.qlora_act_bwd("relu", dy, dy)
+    torch.cuda.synchronize()
+    want = dy.clamp_min(0)
+    assert torch.equal(dz, want)
+    assert torch.equal(db, want[0].float())
+    del dz, db, want
+    torch.cuda.empty_cache()
+
+
+def test_affine_forward_from_a_checkpoint_of_many_rows():
+    """More rows than the code sums have waves: the bytes of the forward that
+    wrote the checkpoint, whose row pass sums the codes on the way."""
+    c = Case(300001, 32, 16, 1, "w8o")
+    say("many affine rows")
+    y, t, _, xc = Q.qlora_fwd_epi(c.lin, c.x_t, save_x=True)
+    y2, _ = Q.qlora_fwd_ckpt(c.lin, xc, t, torch.bfloat16)
+    torch.cuda.synchronize()
+    assert torch.equal(bits(y), bits(y2))
