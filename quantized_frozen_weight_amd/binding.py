@@ -580,18 +580,35 @@ def _new_ckpt(M: int, C: int, fmt: str, like) -> Checkpoint:
     return Checkpoint(codes, scales, fmt)
 
 
-def _layer_on(layer: QLinear, device) -> qlora_linear:
+@functools.lru_cache(maxsize=4096)
+def _weight_form(K: int, N: int, fmt: str):
+    """Shape and dtype of a layer's codes, then of its scales."""
     import torch
-    A, B = layer.A, layer.B
-    if (A.dtype is torch.float32 and A.shape == (layer.K, layer.r) and A.device == device and A.is_contiguous()
-            and B.dtype is torch.float32 and B.shape == _b_shape(layer) and B.device == device
-            and B.is_contiguous() and layer.codes.device == device and layer.scales.device == device):
+    if fmt == "w8":
+        return (N, K), torch.int8, (N,), torch.float32
+    if fmt == "w4g128":
+        return (N, K // 2), torch.uint8, (N, K // 128), torch.float16
+    if fmt == "w8o":
+        return (N, K), torch.int8, (qlora_weight_bytes(K, N, fmt)[1],), torch.uint8
+    raise ValueError(f"unknown weight form {fmt!r}")
+
+
+def _layer_on(layer: QLinear, device) -> qlora_linear:
+    """The layer's C struct, its four tensors checked."""
+    import torch
+    c, s, A, B = layer.codes, layer.scales, layer.A, layer.B
+    cshape, ctype, sshape, stype = _weight_form(layer.K, layer.N, layer.fmt)
+    f32 = torch.float32
+    if (c.dtype is ctype and s.dtype is stype and A.dtype is f32 and B.dtype is f32
+            and c.device == device and s.device == device and A.device == device and B.device == device
+            and c.shape == cshape and s.shape == sshape and A.shape == (layer.K, layer.r)
+            and B.shape == _b_shape(layer) and c.is_contiguous() and s.is_contiguous()
+            and A.is_contiguous() and B.is_contiguous()):
         return layer.cstruct()
-    for t, what in ((layer.codes, "codes"), (layer.scales, "scales")):
-        if t.device != device:
-            raise ValueError(f"layer {what} on {t.device}, the activations on {device}")
-    _tensor(layer.A, "layer A", (layer.K, layer.r), torch.float32, device)
-    _tensor(layer.B, "layer B", _b_shape(layer), torch.float32, device)
+    _tensor(c, "layer codes", cshape, ctype, device)
+    _tensor(s, "layer scales", sshape, stype, device)
+    _tensor(A, "layer A", (layer.K, layer.r), f32, device)
+    _tensor(B, "layer B", _b_shape(layer), f32, device)
     raise AssertionError("unreachable: one of the checks above fails")
 
 
