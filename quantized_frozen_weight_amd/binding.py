@@ -559,6 +559,8 @@ def _ckpt(c, what: str, fmt: str, shape, device) -> Checkpoint:
     import torch
     if c.fmt != fmt:
         raise ValueError(f"{what}: form {c.fmt!r}, expected {fmt!r}")
+    if fmt not in _CFMT:
+        raise ValueError(f"{what}: unknown checkpoint form {fmt!r}")
     _tensor(c.codes, f"{what}.codes", shape, torch.int8, device)
     if fmt == "c8row":
         _tensor(c.scales, f"{what}.scales", (shape[0],), torch.float32, device)

@@ -49,3 +49,11 @@ def test_tensors_of_a_layer_are_checked(fmt):
         assert Q._layer_on(layer(fmt, heads=3), CPU).heads == 3
     with pytest.raises(ValueError):
         Q._layer_on(Q.QLinear(K, N, r, 8.0, "w2", good.codes, good.scales, good.A, good.B), CPU)
+
+
+def test_unknown_checkpoint_forms_are_refused():
+    codes, scales = torch.zeros(4, 32, dtype=torch.int8), torch.zeros(4, 1, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="unknown checkpoint form"):
+        Q.qlora_ckpt_read(Q.Checkpoint(codes, scales, "c8"), torch.float32)
+    with pytest.raises(ValueError, match="GPU"):
+        Q.qlora_ckpt_read(Q.Checkpoint(codes, scales, "c8g32"), torch.float32)      # not on a GPU
