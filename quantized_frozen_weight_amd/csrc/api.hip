@@ -968,8 +968,7 @@ int qlora_quantize_rows(const void* x, int M, int K, int dtype, int8_t* xq,
   if (!x || !xq || !sx || !aligned16(x) || !aligned16(xq) || !aligned16(sx))
     return QLORA_EINVAL;
   if (pending_error()) return QLORA_EHIP;
-  launch_rowquant(dtype, x, M, K, nullptr, 1, xq, sx, nullptr,
-                  static_cast<hipStream_t>(stream));
+  launch_ckpt_write_rows(dtype, x, M, K, xq, sx, static_cast<hipStream_t>(stream));
   return launch_status();
 }
 

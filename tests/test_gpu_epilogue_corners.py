@@ -218,3 +218,19 @@ def test_affine_forward_from_a_checkpoint_of_many_rows():
     y2, _ = Q.qlora_fwd_ckpt(c.lin, xc, t, torch.bfloat16)
     torch.cuda.synchronize()
     assert torch.equal(bits(y), bits(y2))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,C", [(1, 16), (130, 1040), (5, 16384), (600, 4112), (3, 40016)])
+def test_row_quantizer_and_row_checkpoint_are_one(M, C, dtype):
+    rng = np.random.default_rng(M + C)
+    x = rng.standard_normal((M, C)).astype(np.float32)
+    if M > 2:
+        x[0], x[1, 5], x[2, 7] = 0, np.inf, np.nan
+    x_t = WL.as_compute_dtype(x, dtype)[0].cuda()
+    say("rows", M, C, dtype)
+    xq, sx = Q.qlora_quantize_rows(x_t)
+    c = Q.qlora_ckpt_write(x_t)
+    torch.cuda.synchronize()
+    assert torch.equal(xq, c.codes)
+    assert torch.equal(bits(sx), bits(c.scales))
