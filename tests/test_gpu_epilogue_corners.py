@@ -234,3 +234,77 @@ def test_row_quantizer_and_row_checkpoint_are_one(M, C, dtype):
     torch.cuda.synchronize()
     assert torch.equal(xq, c.codes)
     assert torch.equal(bits(sx), bits(c.scales))
+
+
+@pytest.mark.parametrize("what", ["nan", "inf", "-inf", "zero"])
+@pytest.mark.parametrize("spec", [
+    (2, 64, 80, 3, "w8", "f32"), (4, 784, 272, 8, "w8", "bf16"),             # few rows, t in the same launch
+    (2, 8192, 144, 8, "w8", "f32"), (3, 16384, 80, 4, "w8", "bf16"),         # ... t by the launch before
+    (4, 256, 272, 8, "w4g128", "bf16"), (3, 16384, 144, 16, "w4g128", "bf16"),
+    (4, 256, 144, 32, "w8", "bf16"), (3, 256, 144, 8, "w8o", "bf16"),        # few rows, tiled product
+    (70, 256, 272, 8, "w4g128", "bf16"), (90, 8192, 144, 4, "w4g128", "bf16"),
+    (100, 256, 384, 8, "w8o", "bf16"), (130, 4096, 80, 4, "w8o", "bf16")],
+    ids=lambda s: "-".join(map(str, s)) if isinstance(s, tuple) else s)
+def test_odd_rows_of_every_format(spec, what):
+    """A row of x with a NaN or an infinity, or all zero: its checkpoints carry
+    it, its outputs show it, and every other row is the bytes it is without."""
+    c = Case(*spec)
+    row = c.M - 1
+    x = c.x_t.clone()
+    if what == "zero":
+        x[row] = 0
+    else:
+        x[row, 7] = float(what)
+    say("odd row", spec, what)
+    kw = dict(act="gelu", residual=c.res_t, save_z="c8g32", save_x=True)
+    y0, t0, z0, xc0 = Q.qlora_fwd_epi(c.lin, c.x_t, **kw)
+    y, t, z, xc = Q.qlora_fwd_epi(c.lin, x, **kw)
+    y2, z2 = Q.qlora_fwd_ckpt(c.lin, xc, t, c.td, act="gelu", residual=c.res_t, save_z="c8g32")
+    torch.cuda.synchronize()
+    keep = torch.arange(c.M, device="cuda") != row
+    for a, b in ((y, y0), (t, t0), (z.codes, z0.codes), (z.scales, z0.scales), (xc.codes, xc0.codes),
+                 (xc.scales, xc0.scales)):
+        assert torch.equal(bits(a[keep]), bits(b[keep])), "other rows"
+    assert not xc.codes[row].any()
+    if what == "zero":
+        assert float(xc.scales[row]) == 0 and not t[row].any()
+        for yy, zz in ((y, z), (y2, z2)):
+            assert torch.equal(yy[row], c.res_t[row])
+            assert not zz.codes[row].any() and bool((zz.scales[row] == 1).all())
+    else:
+        assert bool(torch.isnan(xc.scales[row])) and not torch.isfinite(t[row]).any()
+        for yy, zz in ((y, z), (y2, z2)):
+            assert not zz.codes[row].any() and bool((zz.scales[row] == 255).all())
+        assert torch.isnan(y2[row]).all()                    # from a NaN row scale
+        if c.fmt != "w4g128" or what == "nan":               # (4-bit: x itself, gelu(-inf) = 0)
+            assert torch.isnan(y[row]).all()
+    dx, dA, dB = Q.qlora_bwd_epi(c.lin, xc, c.dy_t, t, act="silu", z=c.z_t, add=c.add_t)
+    dx0 = Q.qlora_bwd_epi(c.lin, xc0, c.dy_t, t, act="silu", z=c.z_t, add=c.add_t)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(bits(dx), bits(dx0)), "dx does not depend on x"
+    assert bool(torch.isnan(dA).all()) == (what != "zero") and bool(torch.isfinite(dA).all()) == (what == "zero")
+    assert bool(torch.isfinite(dB).all()) == (what == "zero")
+
+
+@pytest.mark.parametrize("M", [3, 70])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_activations_at_the_ends_of_the_range_absolutely(M, dtype):
+    """Every value of the forward activations held to a bound of its own. A
+    sigma below 2^-126 may be 0 (the reciprocal instruction flushes denormal
+    results): z sigma(w) is then at most 87.4 2^-126 = 1.03e-36 in size, since
+    |z| e^-|z| falls past 1 and e^-87.34 = 2^-126 (silu; tanh gelu reaches that
+    sigma at a smaller |z|). Elsewhere float32 values within 2e-5 (w rounded
+    three times, times |w| < 89), and half a step of the output."""
+    vals = np.array([0.0, -0.0, 1e-45, -1e-45, 1e-39, -1e-39, 1e-20, -1e-20, 0.5, -0.5, 3, -3, 8, -8, 12, -12, 20, -20,
+                     88, -88, 90, -90, 200, -200, 1e9, -1e9, 1e20, -1e20, 3e38, -3e38, np.inf, -np.inf], np.float32)
+    lin = zero_layer(16, 32, "w8")
+    x = torch.ones((M, 16), device="cuda", dtype=TD[dtype])
+    u = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    for act in E.ACTS:
+        say("range", M, dtype, act)
+        y = Q.qlora_fwd_epi(lin, x, act=act, bias=dev(vals))[0]
+        torch.cuda.synchronize()
+        w = np.tile(E.act(act, vals), (M, 1))
+        with np.errstate(invalid="ignore"):
+            tol = (u + (2e-5 if act != "none" else 0)) * np.abs(w) + 1.04e-36
+            within(to_numpy(y), w, tol, act)
