@@ -421,7 +421,7 @@ typedef struct {
  * the compute dtype. Workspace: qlora_fwd_workspace. For int8 formats x_codes
  * costs nothing (the product reads the codes there). With an empty epilogue
  * the results are bitwise qlora_fwd's, except that up to four rows of int8 and
- * 4-bit layers (rank <= 16, K <= 16384) take a kernel of their own, whose int8
+ * 4-bit layers (rank <= 16, K <= 16384) may take a kernel of their own, whose int8
  * base product is the same and whose float32 sums (t; 4-bit: the base too) run
  * in another order. */
 int qlora_fwd_epi(const qlora_linear* L, int M, int dtype, const void* x,

@@ -796,7 +796,7 @@ int qlora_fwd_epi(const qlora_linear* L, int M, int dtype, const void* x,
   float* sx = e->x_scales ? e->x_scales : reinterpret_cast<float*>(at(ws, w.sx));
   float* rs = reinterpret_cast<float*>(at(ws, w.rs));
   if (pending_error()) return QLORA_EHIP;
-  if (fwd_few_takes(L->fmt, M, K, L->r)) {
+  if (fwd_few_takes(L->fmt, M, N, K, L->r)) {
     launch_fwd_few(dtype, L->fmt, M, N, K, x, L->codes, L->scales, L->A, L->B, head_width(L), L->r,
                    lora_s(L), epi, y, t_save, e->x_codes, e->x_scales,
                    reinterpret_cast<float*>(at(ws, w.xq)), s);

@@ -11,22 +11,25 @@
 //
 // With so few rows the weight is all the traffic there is, and the call ends
 // when its last byte has arrived: 16384 x 2048 int8 codes are 33.5 MB, 6.5 us
-// at the 5.1 TB/s of a large copy. So a block of 16 waves puts its whole
-// share of the weight in flight first (each lane 16 bytes of one output
-// channel per load, up to 16 loads held in registers), and does everything
-// that the small operands need while those loads travel: the rows' abs-max
-// and codes (every block quantizes the rows for itself, which costs less
-// than a launch that would do it once) and t = x A. Then the codes go from
-// registers straight into the matrix instructions: the 16 channels are the
-// columns of a 16 x 16 block, the rows sit in the first rows of the other
-// operand (read from LDS; the unused rows repeat the last one and their
-// sums are dropped), and the waves' partial sums over k are added in LDS in
-// wave order.
+// at the 5.1 TB/s of a large copy. So a block of 16 waves puts its share of
+// the weight in flight first (each lane 16 bytes of one output channel per
+// load, up to kHold of them held in registers; what a longer share has left
+// follows as the first are used), and does everything that the small operands
+// need while those loads travel: the rows' abs-max and codes (every block
+// quantizes the rows for itself, which costs less than a launch that would do
+// it once) and t = x A. Then the codes go from registers straight into the
+// matrix instructions: the 16 channels are the columns of a 16 x 16 block, the
+// rows sit in the first rows of the other operand (read from LDS; the unused
+// rows repeat the last one and their sums are dropped), and the waves' partial
+// sums over k are added in LDS in wave order.
 //
 // A block owns 16 NG columns; its 16 waves are NG groups of 16 columns times
-// 16 / NG spans of k. NG is the largest of 4, 2, 1 that still gives every
-// compute unit a block (and at least 2 where 32-column groups of z are
-// saved): wide blocks read the rows and A less often.
+// 16 / NG spans of k. A compute unit holds one block, so NG is the smallest of
+// 1, 2, 4 whose blocks all run at once (at least 2 where 32-column groups of z
+// are saved); narrow blocks split k further, but a second round costs a whole
+// one: 4 rows of 1024 -> 12288 take 8.6 us at 192 blocks of 64 columns, 13.8
+// at 384 of 32. Below 4096 outputs some compute units have no block
+// (16384 -> 2048: 128 blocks).
 //
 // Under a wide adapter over long rows (K R past kPreWords) A is the larger
 // part of what a block would read (512 KB at 16384 x 8, beside 262 KB of
@@ -473,8 +476,8 @@ void few_launch(const FewArgs& a, hipStream_t st) {
 
 template <typename T, bool W4, int R>
 void few_groups(const FewArgs& a, hipStream_t st) {
-  if (a.N / 64 >= kFewCUs) few_launch<T, W4, R, 4>(a, st);
-  else if (a.N / 32 >= kFewCUs || a.epi.zc != nullptr) few_launch<T, W4, R, 2>(a, st);
+  if (a.N > 32 * kFewCUs) few_launch<T, W4, R, 4>(a, st);
+  else if (a.N > 16 * kFewCUs || a.epi.zc != nullptr) few_launch<T, W4, R, 2>(a, st);
   else few_launch<T, W4, R, 1>(a, st);
 }
 
@@ -487,12 +490,17 @@ void few_ranks(const FewArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// Up to four rows (measured faster than the tiled product at every width
-// above; the four rows' sums of x A are vector work that grows with them),
-// int8 and 4-bit weights, ranks up to 16, and rows whose bf16 form fits in
-// LDS four times.
-bool fwd_few_takes(int fmt, int M, int K, int r) {
-  return (fmt == 0 || fmt == 1) && M <= 4 && r <= 16 && K <= kFewMaxK;
+// Up to four rows, int8 and 4-bit weights, ranks up to 16, and rows whose bf16
+// form fits in LDS four times. Against the tiled product with the same
+// epilogue (at five rows): one round of blocks is faster in every case
+// measured (int8 4 rows of 256 -> 4096 7.1 against 7.7 us, 4096 -> 4096 r 16
+// 13.4 against 30.5); past 16384 outputs one row and 4-bit rows still are, or
+// come within a tenth, but 2 to 4 int8 rows are not (2048 -> 32768 24 against
+// 19), save where the tiled product's row pass is slow, at ranks past 8 over
+// long rows (8192 -> 32768 r 16 59 against 78).
+bool fwd_few_takes(int fmt, int M, int N, int K, int r) {
+  if (!(fmt == 0 || fmt == 1) || M > 4 || r > 16 || K > kFewMaxK) return false;
+  return fmt == 1 || M == 1 || N <= 64 * kFewCUs || (r > 8 && K >= 4096);
 }
 
 void launch_fwd_few(int dtype, int fmt, int M, int N, int K, const void* x, const void* codes,

@@ -83,7 +83,7 @@ void launch_gemm_fwd_w4(int M, int N, int K, const uint16_t* x,
 // The layer with its epilogue for at most four rows in one launch (fmt 0 or
 // 1, rank up to 16, K <= 16384: fwd_few_takes); t, xq and sx (x's row
 // checkpoint) may be NULL; scratch: M K bytes.
-bool fwd_few_takes(int fmt, int M, int K, int r);
+bool fwd_few_takes(int fmt, int M, int N, int K, int r);
 void launch_fwd_few(int dtype, int fmt, int M, int N, int K, const void* x, const void* codes,
                     const void* scales, const float* A, const float* B, int hd, int r, float s,
                     const FwdEpi& epi, void* y, float* t, int8_t* xq, float* sx, float* scratch,

@@ -11,7 +11,7 @@ from oracle import qlora_oracle as O
 from quantized_frozen_weight_amd import binding as Q
 from quantized_frozen_weight_amd import workloads as WL
 from tests.helpers import to_numpy
-from tests.test_gpu_epilogue import Case, bits, dev, say, within
+from tests.test_gpu_epilogue import Case, bits, check_group_ckpt, dev, say, within
 
 pytestmark = pytest.mark.gpu
 
@@ -308,3 +308,29 @@ def test_activations_at_the_ends_of_the_range_absolutely(M, dtype):
         with np.errstate(invalid="ignore"):
             tol = (u + (2e-5 if act != "none" else 0)) * np.abs(w) + 1.04e-36
             within(to_numpy(y), w, tol, act)
+
+
+@pytest.mark.parametrize("spec", [
+    (1, 256, 4096, 3, "w8", "bf16"), (4, 272, 4112, 8, "w8", "f32"),          # 16 and 32 columns a block
+    (2, 784, 8192, 4, "w8", "bf16"), (3, 784, 8208, 16, "w8", "bf16"),        # 32 and 64
+    (4, 256, 12304, 8, "w4g128", "bf16"), (1, 4096, 16400, 8, "w8", "bf16"),  # 64, and a second round
+    (4, 4096, 16400, 11, "w8", "bf16"), (3, 128, 16400, 16, "w4g128", "bf16"),
+    (2, 256, 16400, 4, "w8", "f32"), (4, 64, 32768, 8, "w8", "bf16")],        # int8 past 16384 outputs: tiles
+    ids=lambda s: "-".join(map(str, s)))
+def test_few_rows_at_every_block_width(spec):
+    c = Case(*spec)
+    for act, save_z in (("gelu", "c8g32"), ("silu", "full")):
+        say("few rows", spec, act, save_z)
+        y, t, z, xc = Q.qlora_fwd_epi(c.lin, c.x_t, act=act, bias=dev(c.bias), residual=c.res_t, save_z=save_z,
+                                      save_x=True)
+        torch.cuda.synchronize()
+        (wy, wz, wt), (ty, tz, tt) = c.forward(act, True, True)
+        within(to_numpy(t), wt, tt, "t")
+        within(to_numpy(y), wy, ty, "y")
+        if save_z == "full":
+            within(to_numpy(z), wz, c.u * (np.abs(wz) + tz) + tz, "z")
+        else:
+            check_group_ckpt(z, wz, tz, "z")
+        oq, osx = O.quantize_rows(c.x)
+        assert np.array_equal(xc.codes.cpu().numpy(), oq)
+        assert np.array_equal(xc.scales.cpu().numpy().view(np.uint32), osx.view(np.uint32))
