@@ -145,6 +145,141 @@ struct X8Tile {
   }
 };
 
+// The u operand of the dA products, [UCB][BM / 32][64 lanes][16 B] at UF: u [BM
+// rows][R] at E split like B and t into bf16 hi, mid and lo columns, rows past
+// `rows` zero. Wave w of four builds fragments w, w + 4, ... With x in 8 bits
+// (x8) rows are first multiplied by their scales in float32: rsv[e] is that of
+// row 32 (w % (BM / 32)) + 8 (lane / 16) + e, the rows of all its fragments.
+template <int BM, int R>
+__device__ __forceinline__ void put_u_operand(int8_t* UF, const float* E, int rows, int r, bool x8,
+                                              const float (&rsv)[8]) {
+  constexpr int UCB = (3 * R + 15) / 16, MC = BM / 32;
+  static_assert(4 % MC == 0, "a wave's fragments are all of the same rows");
+  const int lane = threadIdx.x & 63, wid = wave_id();
+  for (int f = wid; f < UCB * MC; f += 4) {
+    const int cb = f / MC, c = f % MC;
+    const int j = cb * 16 + (lane & 15), part = j / R, jr = j - part * R;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int m = 32 * c + 8 * (lane >> 4) + e;
+      v[e] = (jr < r && part < 3 && m < rows) ? E[m * R + (jr < r ? jr : 0)] : 0.f;
+      if (x8) v[e] = m < rows ? v[e] * rsv[e] : 0.f;      // (a clamped row's scale may be NaN)
+    }
+    u32x4 hi, mid, lo;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t me, le;
+      hi[e] = pk_bf16_split3(v[2 * e], v[2 * e + 1], me, le);
+      mid[e] = me;
+      lo[e] = le;
+    }
+    *reinterpret_cast<u32x4*>(UF + (f * 64 + lane) * 16) = part == 0 ? hi : part == 1 ? mid : lo;
+  }
+}
+
+// The dA partial of a block on the matrix cores: dA^T[k][j] = sum_m x[m][k]
+// u[m][j] over its rows, u from the operand above and x^T read from the x tile
+// through transposing reads (in each 16-lane group lane 4 i + p fetches the 4
+// columns at c0 + 4 p of row i, and lane q receives column c0 + q of rows
+// 0..3). Wave w of four takes the columns [BN / 4 w, BN / 4 (w + 1)) and writes
+// out[j K + k] for the block's columns k0 + k < K. sx (x in 8 bits, else NULL):
+// the scales of the block's rows.
+template <int BM, int BN, int R>
+__device__ __forceinline__ void da_products(const int8_t* Xs, const int8_t* UF, const float* E, const float* sx,
+                                            int rows, int r, int k0, int K, float* out) {
+  constexpr int UCB = (3 * R + 15) / 16, RCB = (R + 15) / 16, MC = BM / 32;
+  constexpr int KB = BN / 64, RH = BN / 64;               // 16-column blocks per wave
+  const int lane = threadIdx.x & 63, wid = wave_id();
+  f32x4 dacc[KB][UCB];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int cb = 0; cb < UCB; ++cb) dacc[kb][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int q = lane & 15, i4 = q >> 2, p4 = q & 3;
+#pragma unroll
+  for (int c0 = 0; c0 < MC; c0 += 2) {
+    uint32_t tra[4 * KB];
+    uint64_t trv[4 * KB];
+#pragma unroll
+    for (int cc = 0; cc < 2; ++cc)
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int m = 32 * (c0 + cc) + 8 * (lane >> 4) + 4 * h + i4;
+          const int col = (BN / 4) * wid + 16 * kb + 4 * p4;
+          tra[(cc * KB + kb) * 2 + h] = lds_addr(Xs + swz128(m * RH + col / 64, (col % 64) >> 3) + (col & 7) * 2);
+        }
+    tr16_reads<4 * KB>(tra, trv);
+#pragma unroll
+    for (int cc = 0; cc < 2; ++cc) {
+      const int c = c0 + cc;
+      bf16x8 uf[UCB];
+#pragma unroll
+      for (int cb = 0; cb < UCB; ++cb)
+        uf[cb] = *reinterpret_cast<const bf16x8*>(UF + ((cb * MC + c) * 64 + lane) * 16);
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        const int t0 = (cc * KB + kb) * 2;
+        const bf16x8 xT = __builtin_bit_cast(bf16x8, u32x4{(uint32_t)trv[t0], (uint32_t)(trv[t0] >> 32),
+                                                           (uint32_t)trv[t0 + 1], (uint32_t)(trv[t0 + 1] >> 32)});
+#pragma unroll
+        for (int cb = 0; cb < UCB; ++cb)
+          dacc[kb][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xT, uf[cb], dacc[kb][cb], 0, 0, 0);
+      }
+    }
+  }
+  float dav[KB][RCB][4];
+  bool nan = false;
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int cb = 0; cb < RCB; ++cb)
+#pragma unroll
+      for (int ii = 0; ii < 4; ++ii) {
+        dav[kb][cb][ii] = split3_sum<R, UCB>(dacc[kb], cb, ii, lane);
+        nan |= dav[kb][cb][ii] != dav[kb][cb][ii];
+      }
+  if (__builtin_amdgcn_ballot_w64(nan) == 0) {
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int cb = 0; cb < RCB; ++cb) {
+        const int j = cb * 16 + (lane & 15);
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) {
+          const int kl = (BN / 4) * wid + 16 * kb + 4 * (lane >> 4) + ii;
+          if (j < r && k0 + kl < K) out[(long)j * K + k0 + kl] = dav[kb][cb][ii];
+        }
+      }
+  } else {
+    // A NaN in the wave's columns: an infinite x times the three parts of
+    // u can give inf - inf where the plain product is infinite, so the
+    // wave takes its columns again as float32 sums in row order (lane ->
+    // column (BN / 4) w + lane % (BN / 4), ranks jb + TPK jj).
+    constexpr int CPW = BN / 4, TPK = 64 / CPW, JPT = (R + TPK - 1) / TPK;
+    const int kl = CPW * wid + lane % CPW, jb = lane / CPW;
+    float da[JPT];
+#pragma unroll
+    for (int jj = 0; jj < JPT; ++jj) da[jj] = 0.f;
+    for (int m = 0; m < rows; ++m) {
+      const int e = kl % 64;
+      const uint16_t xb = *reinterpret_cast<const uint16_t*>(Xs + swz128(m * RH + kl / 64, e >> 3) + 2 * (e & 7));
+      float xv = __uint_as_float((uint32_t)xb << 16);
+      if (sx != nullptr) xv *= sx[m];
+#pragma unroll
+      for (int jj = 0; jj < JPT; ++jj)
+        if (jb + TPK * jj < R) da[jj] = __builtin_fmaf(xv, E[m * R + jb + TPK * jj], da[jj]);
+    }
+#pragma unroll
+    for (int jj = 0; jj < JPT; ++jj) {
+      const int j = jb + TPK * jj;
+      if (j < r && k0 + kl < K) out[(long)j * K + k0 + kl] = da[jj];
+    }
+  }
+}
+
 // The eight codes of a packed 4-bit word (nibble e = k offset e, two's
 // complement) times sc: w ^ 0x88888888 turns each code q into q + 8 in
 // [0, 15], two masks spread the nibbles over bytes (v_cvt_f32_ubyte takes a

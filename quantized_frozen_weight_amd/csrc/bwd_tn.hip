@@ -17,7 +17,8 @@
 // an issue slot; at 128 x 128 (4096 x 2048 x 16384) 36 % busy and the LDS 23 %:
 // a stage's 36 KB in and 72 KB out and its 576 cycles of matrix work a SIMD
 // follow one another in each block, and two blocks a compute unit overlap
-// them in part.
+// them in part (up to rank 8, at 82 KB of LDS a block of 128 x 128; ranks 16
+// and 32 take 90 and 115 KB for B's parts, and one block a compute unit).
 //
 // Around the product it does what gemm_bwd.hip does, with the same operands
 // and the same partial-sum layout (so the same combine and, where the
@@ -449,122 +450,12 @@ __global__ __launch_bounds__(256, 2) void bwd_tn_kernel(TnArgs a) {
   }
   if (x8on) x8.put(Xs, tid);
   __syncthreads();
-  // the u operand in three parts (x in 8 bits: times the row scales, in
-  // float32), rows past M zero
-  for (int f = wid; f < UCB * MC; f += 4) {
-    const int cb = f / MC, c = f % MC;
-    const int j = cb * 16 + (lane & 15), part = j / R, jr = j - part * R;
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int m = 32 * c + 8 * (lane >> 4) + e;
-      v[e] = (jr < r && part < 3 && m < rows_here) ? E[m * R + (jr < r ? jr : 0)] : 0.f;
-      if (x8on) v[e] *= rsv[e];
-      if (m >= rows_here) v[e] = 0.f;                     // (a clamped row's scale may be NaN)
-    }
-    u32x4 hi, mid, lo;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint32_t me, le;
-      hi[e] = pk_bf16_split3(v[2 * e], v[2 * e + 1], me, le);
-      mid[e] = me;
-      lo[e] = le;
-    }
-    *reinterpret_cast<u32x4*>(UF + (f * 64 + lane) * 16) = part == 0 ? hi : part == 1 ? mid : lo;
-  }
+  put_u_operand<BM, R>(UF, E, rows_here, r, x8on, rsv);
   EpiSide<uint16_t, GradEpi, FM, FN> es;
   __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));              // the x tile
   es.start(a.ge, M, K, m0 + wm * (BM / 2), k0 + wn * (BN / 2));   // (lands behind the dA products)
   __syncthreads();
-  {
-    // dA^T[k][j] = sum_m x[m][k] u[m][j]; wave w takes the columns
-    // [BN / 4 w, BN / 4 (w + 1)), x^T through transposing reads
-    constexpr int KB = BN / 64, RH = BN / 64;
-    f32x4 dacc[KB][UCB];
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-      for (int cb = 0; cb < UCB; ++cb) dacc[kb][cb] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const int q = lane & 15, i4 = q >> 2, p4 = q & 3;
-#pragma unroll
-    for (int c0 = 0; c0 < MC; c0 += 2) {
-      uint32_t tra[4 * KB];
-      uint64_t trv[4 * KB];
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int m = 32 * (c0 + cc) + 8 * (lane >> 4) + 4 * h + i4;
-            const int col = (BN / 4) * wid + 16 * kb + 4 * p4;
-            tra[(cc * KB + kb) * 2 + h] = lds_addr(Xs + swz128(m * RH + col / 64, (col % 64) >> 3) + (col & 7) * 2);
-          }
-      tr16_reads<4 * KB>(tra, trv);
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        bf16x8 uf[UCB];
-#pragma unroll
-        for (int cb = 0; cb < UCB; ++cb)
-          uf[cb] = *reinterpret_cast<const bf16x8*>(UF + ((cb * MC + c0 + cc) * 64 + lane) * 16);
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          const int t0 = (cc * KB + kb) * 2;
-          const bf16x8 xT = __builtin_bit_cast(bf16x8, u32x4{(uint32_t)trv[t0], (uint32_t)(trv[t0] >> 32),
-                                                             (uint32_t)trv[t0 + 1], (uint32_t)(trv[t0 + 1] >> 32)});
-#pragma unroll
-          for (int cb = 0; cb < UCB; ++cb)
-            dacc[kb][cb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xT, uf[cb], dacc[kb][cb], 0, 0, 0);
-        }
-      }
-    }
-    float dav[KB][RCB][4];
-    bool nan = false;
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-      for (int cb = 0; cb < RCB; ++cb)
-#pragma unroll
-        for (int ii = 0; ii < 4; ++ii) {
-          dav[kb][cb][ii] = split3_sum<R, UCB>(dacc[kb], cb, ii, lane);
-          nan |= dav[kb][cb][ii] != dav[kb][cb][ii];
-        }
-    if (__builtin_amdgcn_ballot_w64(nan) == 0) {
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int cb = 0; cb < RCB; ++cb) {
-          const int j = cb * 16 + (lane & 15);
-#pragma unroll
-          for (int ii = 0; ii < 4; ++ii) {
-            const int kl = (BN / 4) * wid + 16 * kb + 4 * (lane >> 4) + ii;
-            if (j < r && k0 + kl < K) a.partA[((long)mt * r + j) * K + k0 + kl] = dav[kb][cb][ii];
-          }
-        }
-    } else {
-      // An infinite x times the three parts of u can give inf - inf where the
-      // plain product is infinite: the wave's columns again as float32 sums
-      constexpr int CPW = BN / 4, TPK = 64 / CPW, JPT = (R + TPK - 1) / TPK;
-      const int kl = CPW * wid + lane % CPW, jb = lane / CPW;
-      float da[JPT];
-#pragma unroll
-      for (int jj = 0; jj < JPT; ++jj) da[jj] = 0.f;
-      for (int m = 0; m < rows_here; ++m) {
-        const int e = kl % 64;
-        const uint16_t xb = *reinterpret_cast<const uint16_t*>(Xs + swz128(m * RH + kl / 64, e >> 3) + 2 * (e & 7));
-        float xv = __uint_as_float((uint32_t)xb << 16);
-        if (x8on) xv *= a.sx[m0 + m];
-#pragma unroll
-        for (int jj = 0; jj < JPT; ++jj)
-          if (jb + TPK * jj < R) da[jj] = __builtin_fmaf(xv, E[m * R + jb + TPK * jj], da[jj]);
-      }
-#pragma unroll
-      for (int jj = 0; jj < JPT; ++jj) {
-        const int j = jb + TPK * jj;
-        if (j < r && k0 + kl < K) a.partA[((long)mt * r + j) * K + k0 + kl] = da[jj];
-      }
-    }
-  }
+  da_products<BM, BN, R>(Xs, UF, E, x8on ? a.sx + m0 : nullptr, rows_here, r, k0, K, a.partA + (long)mt * r * K);
   __syncthreads();                                        // every wave is done with the x tile and the u operand
   epilogue_fused<BM, BN, R, false>(acc, E, M, K, m0, k0, wm * (BM / 2), wn * (BN / 2), a.s, a.dx, a.ge, es,
                                    Xs + wid * fused_strip_bytes<FN>());
