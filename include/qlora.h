@@ -354,7 +354,10 @@ const char* qlora_bwd_main_kernel(const qlora_linear* L, int M, int dtype);
  *
  *   z = x deq(W) + s (x A) B + bias,     y = act(z) + residual
  *
- * with the base product of qlora_fwd for the layer's format. The backward
+ * with the base product of qlora_fwd for the layer's format. (In bf16 the
+ * 4-bit product of many rows and the input gradient of every format multiply
+ * with the dequantized weight rounded once to bfloat16, as in qlora_fwd and
+ * qlora_bwd.) The backward
  * needs x (for dA), t and z (for act'), and keeping them takes most of a
  * training step's memory (keras-llm-light README, "Block-wise gradient
  * checkpointing": block inputs are cached and blocks recomputed from them).
