@@ -203,7 +203,8 @@ int qlora_fwd_workspace(const qlora_linear* L, int M, int dtype,
  * to the compute dtype. For QLORA_W8, x is quantized per row and the base
  * product is an int8 x int8 -> int32 sum rescaled by sx[m] * sw[n] (exact up
  * to K = 132096; past it rows and channels of nearly all the largest codes
- * could pass int32, which is not checked). If t_save is not NULL, t = x A (float32 [M, r]) is written there for the backward. */
+ * could pass int32, which is not checked). If t_save is not NULL, t = x A
+ * (float32 [M, r]) is written there for the backward. */
 int qlora_fwd(const qlora_linear* L, int M, int dtype, const void* x, void* y,
               float* t_save, void* ws, size_t ws_bytes, void* stream);
 
@@ -385,7 +386,8 @@ const char* qlora_bwd_main_kernel(const qlora_linear* L, int M, int dtype);
  *
  * Constraints as above, with M >= 1 and every pointer 16-byte aligned; the two
  * forwards take int8 formats up to K = 132096, where the int32 and float32
- * sums of codes are exact for any codes (EUNSUPPORTED above); of a pair (codes, scales) both or neither is given. Every tensor is dense
+ * sums of codes are exact for any codes (EUNSUPPORTED above); of a pair
+ * (codes, scales) both or neither is given. Every tensor is dense
  * row-major. Outputs must not overlap inputs or each other (EINVAL), except
  * that y may be residual, dx may be add, and dz may be dy, exactly. */
 typedef enum {

@@ -38,11 +38,12 @@
 // rank 8.
 //
 // Measured (graph replay, bias and tanh gelu; the tiled product without them
-// in brackets): one row of 2048 -> 16384 int8 9.5 us [13.8], 3.5 TB/s; 16384
-// -> 2048 14.9 [30.5]; 1024 -> 1024 4.5 [9.5]; 4096 -> 4096 4-bit 6.7
-// [27.0]. Four rows: 13.2 [13.8], 20.8 [30.4], 7.7 [9.5], 9.0 [27.2]; float32
-// 256 -> 256 6.6 [6.4]. What is left over the weight's 6.5 us is the launch
-// and the chain abs-max -> codes -> products -> sums, three barriers.
+// in brackets): one row of 2048 -> 16384 int8 8.6 us [13.9], 3.9 TB/s; 16384
+// -> 2048 14.8 [30.7]; 1024 -> 1024 4.7 [9.7] (rank 8); 4096 -> 4096 4-bit 7.4
+// [27.0]; float32 256 -> 256 4.0 [6.5] (rank 4). Four rows: 12.6 [14.0], 20.9
+// [30.8], 7.9 [9.7], 9.9 [27.3], 6.7 [6.7]. What is left over the weight's 6.5
+// us is the launch and the chain abs-max -> codes -> products -> sums, three
+// barriers.
 #include "epilogue.hpp"
 #include "launch.hpp"
 
@@ -75,26 +76,30 @@ struct FewArgs {
 };
 
 // The eight 4-bit codes q of a word (two's complement nibbles) as bf16 values
-// 136 + q, one operation per code: 0x4300 is bf16 128, whose last place is 1,
-// so or-ing the nibble q + 8 into it gives 128 + (q + 8) exactly. Pair i holds
+// q / 16, exact: v_cvt_off_f32_i4 takes the low nibble of a byte in one
+// operation, and the upper halves of two results are a bf16 pair. Pair i holds
 // nibbles i and i + 4, so the other operand's eight values come in the order
-// 0 4 1 5 2 6 3 7 (nibble_order). The 136 is taken out again by a second
-// product with the constant -136 (kNib): every product is exact, and the sum
-// is rounded at 136 / |q| times its own size, 2^-24 relative each, far below
-// a bf16 output's 2^-9.
-__device__ __forceinline__ bf16x8 nibbles_136(uint32_t w) {
-  const uint32_t u = w ^ 0x88888888u;          // q + 8
+// 0 4 1 5 2 6 3 7 (nibble_order). (Or-ing q + 8 into the last places of 128
+// and taking 136 out again by a second product is 8 instead of 14 operations
+// and 3 % faster over 1 to 4 rows, but rounds sums at 136 |x|, which drowns the
+// other terms where an x far above them meets a zero code.)
+__device__ __forceinline__ bf16x8 nibbles_exact(uint32_t w) {
+  const uint32_t odd = w >> 4;
   u32x4 o;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = ((u >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = i & 1 ? odd : w;
+    const float lo = __builtin_amdgcn_cvt_off_f32_i4((int)((v >> (8 * (i / 2))) & 0xffu));
+    const float hi = __builtin_amdgcn_cvt_off_f32_i4((int)((v >> (8 * (i / 2) + 16)) & 0xffu));
+    o[i] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+  }
   return __builtin_bit_cast(bf16x8, o);
 }
-constexpr uint32_t kNib = 0xC308C308u;         // bf16 -136, twice
 
 // The same codes as the tiled product takes them, bf16(q sc), pair i again
 // nibbles i and i + 4. A wave whose sums come out non-finite takes its steps
-// again with these: 136 |x| and |x q| pass the float range (from |x| = 2^113
-// on) where x times the weight does not.
+// again with these: sums of x q / 16 pass the float range (from |x| = 2^122
+// on) where those of x times the weight do not.
 __device__ __forceinline__ bf16x8 nibbles_scaled(uint32_t w, float sc) {
   const uint32_t u = w ^ 0x88888888u;          // q + 8
   const float nsc = -8.f * sc;
@@ -352,15 +357,12 @@ __global__ __launch_bounds__(kThreads) void fwd_few_kernel(FewArgs a) {
     if constexpr (W4) {
       const int8_t* xp = xs + ((long)xm * kpad + 128 * s + 32 * (lane >> 4)) * 2;
       f32x4 p = f32x4{0.f, 0.f, 0.f, 0.f};
-      const bf16x8 off = __builtin_bit_cast(bf16x8, u32x4{kNib, kNib, kNib, kNib});
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const bf16x8 xv = *reinterpret_cast<const bf16x8*>(xp + 16 * q);
-        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, nibbles_136(w[q]), p, 0, 0, 0);
-        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, off, p, 0, 0, 0);
-      }
+      for (int q = 0; q < 4; ++q)
+        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(*reinterpret_cast<const bf16x8*>(xp + 16 * q),
+                                                    nibbles_exact(w[q]), p, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) accf[i] = __builtin_fmaf((float)sc, p[i], accf[i]);
+      for (int i = 0; i < 4; ++i) accf[i] = __builtin_fmaf(16.f * (float)sc, p[i], accf[i]);
     } else {
       const i32x4 xv = *reinterpret_cast<const i32x4*>(xs + (long)xm * kpad + 64 * s + 16 * (lane >> 4));
       acci = __builtin_amdgcn_mfma_i32_16x16x64_i8(xv, __builtin_bit_cast(i32x4, w), acci, 0, 0, 0);

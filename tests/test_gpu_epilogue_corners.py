@@ -334,3 +334,31 @@ def test_few_rows_at_every_block_width(spec):
         oq, osx = O.quantize_rows(c.x)
         assert np.array_equal(xc.codes.cpu().numpy(), oq)
         assert np.array_equal(xc.scales.cpu().numpy().view(np.uint32), osx.view(np.uint32))
+
+
+@pytest.mark.parametrize("M,K,N,r", [(1, 256, 272, 4), (3, 4096, 144, 8), (4, 1024, 528, 16), (2, 16384, 80, 4)])
+def test_few_4bit_rows_with_an_outlier_on_zero_weights(M, K, N, r):
+    """An input far above the others that meets only zero codes (and zeros of
+    A) leaves the sums of the others to float32 accuracy."""
+    rng = np.random.default_rng(K + N)
+    c = Case(M, K, N, r, "w4g128")
+    W = (0.05 * rng.standard_normal((K, N))).astype(np.float32)
+    at = [7, 130, K - 1]
+    W[at] = 0
+    c.A[at] = 0
+    c.A64 = c.A.astype(F64)
+    packed, sc = O.quantize_w4(W)
+    c.W = O.dequant_w4(packed, sc)
+    c.Wabs = np.abs(c.W)
+    codes, scales = Q.qlora_quantize(dev(W), "w4g128")
+    c.lin = Q.QLinear(K, N, r, 16.0, "w4g128", codes, scales, dev(c.A), dev(c.B))
+    for big in (1e4, -1e6, 1e9, 1e30):
+        say("outlier on zeros", M, K, N, r, big)
+        x = c.x.copy()
+        x[:, at] = big
+        x_t, c.x = WL.as_compute_dtype(x, "bf16")
+        y, t, _, _ = Q.qlora_fwd_epi(c.lin, x_t.cuda())
+        torch.cuda.synchronize()
+        (wy, _, wt), (ty, _, tt) = c.forward("none", False, False)
+        within(to_numpy(t), wt, tt, "t")
+        within(to_numpy(y), wy, ty, "y")
