@@ -4,6 +4,7 @@
 
 #include <mutex>
 
+#include "abi.hpp"
 #include "epilogue.hpp"
 #include "launch.hpp"
 #include "outlier.hpp"
@@ -12,21 +13,6 @@
 namespace {
 
 using namespace qlora;
-
-constexpr size_t kAlign = 256;
-inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-inline bool aligned16(const void* p) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-}
-
-inline bool fits_int(long long a, long long b) {
-  return a > 0 && b > 0 && a * b < (1LL << 31);
-}
-
-int check_dtype(int dtype) {
-  return (dtype == QLORA_F32 || dtype == QLORA_BF16) ? QLORA_OK : QLORA_EINVAL;
-}
 
 int check_shape(int M, int K, int N, int r) {
   if (M < 1 || K < 16 || N < 16 || r < 1 || r > 32) return QLORA_EINVAL;
@@ -136,8 +122,6 @@ size_t bwd_epi_bytes(const qlora_linear* L, int M, int dtype) {
   return bwd_layout(L, M, dtype).total + (lays_out(L, M, dtype) ? bwd_tn_bytes(L->K, L->N, L->r) : 0);
 }
 
-inline char* at(void* ws, size_t off) { return static_cast<char*>(ws) + off; }
-
 // Scratch of qlora_bwd_noalloc: a static device array, one copy per GPU the
 // library runs on, held until the process ends. In host code `scratch`
 // names a host-side stand-in, not device memory: its device address is taken
@@ -168,22 +152,6 @@ int scratch_address(void** out) {
 // Optional timing marks around a call's main product kernel.
 void mark(void* ev, hipStream_t s) {
   if (ev != nullptr) (void)hipEventRecord(static_cast<hipEvent_t>(ev), s);
-}
-
-// Before a call enqueues anything: a HIP error that earlier work of the
-// caller left pending is not ours to clear, and launching on top of it would
-// blame it on this call. The call returns QLORA_EHIP, enqueues nothing and
-// leaves the error in place for the caller.
-int pending_error() {
-  return hipPeekAtLastError() == hipSuccess ? QLORA_OK : QLORA_EHIP;
-}
-
-// After a call's launches: nothing was pending before them (pending_error),
-// so an error now is one of this call's launches; it is reported and
-// cleared.
-int launch_status() {
-  hipError_t e = hipGetLastError();
-  return e == hipSuccess ? QLORA_OK : QLORA_EHIP;
 }
 
 // Row-block count of the adapter-gradient partial sums: the fused bf16
@@ -260,36 +228,6 @@ void enqueue_bwd_partial(const qlora_linear* L, int M, int dtype, const void* x,
 }
 
 // ---- the epilogue and checkpoint calls -------------------------------------
-
-inline size_t dtype_bytes(int dtype) { return dtype == QLORA_F32 ? 4 : 2; }
-
-// A pointer that may be NULL and must be aligned where it is not.
-inline bool opt16(const void* p) { return p == nullptr || aligned16(p); }
-
-// Byte ranges of a call's arguments; NULL ranges are left out.
-struct Ranges {
-  struct { const char* p; size_t n; } r[24];
-  int count = 0;
-  void add(const void* p, size_t n) {
-    if (p != nullptr && n > 0) { r[count].p = static_cast<const char*>(p); r[count].n = n; ++count; }
-  }
-  bool hits(const void* p, size_t n) const {
-    const char* q = static_cast<const char*>(p);
-    for (int i = 0; i < count; ++i)
-      if (q < r[i].p + r[i].n && r[i].p < q + n) return true;
-    return false;
-  }
-};
-
-// Outputs against inputs and against each other.
-bool disjoint(const Ranges& outs, const Ranges& ins) {
-  Ranges seen = ins;
-  for (int i = 0; i < outs.count; ++i) {
-    if (seen.hits(outs.r[i].p, outs.r[i].n)) return false;
-    seen.add(outs.r[i].p, outs.r[i].n);
-  }
-  return true;
-}
 
 void add_layer(Ranges& in, const qlora_linear* L) {
   size_t cb = 0, sb = 0;
