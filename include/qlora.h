@@ -492,6 +492,106 @@ int qlora_act_bwd(int act, int M, int N, int dtype, const void* dy, const void* 
                   const int8_t* z_codes, const uint8_t* z_scales, void* dz, float* dbias,
                   void* ws, size_t ws_bytes, void* stream);
 
+/* ---- the vocabulary layer: lookup at the input, loss at the output ----------
+ *
+ * A vocabulary is a layer like the others ("Introduce QLoRA-like technique":
+ * int8 Embedding layers; "Parameter-efficient fine-tuning of GPT-2 with LoRA":
+ * the model's token embedding is also its output layer): its K features and N
+ * columns, column v being entry v,
+ *
+ *   w_v = deq(W)[:, v] + s A B[:, v],        s = alpha / r
+ *
+ * so that one qlora_linear (quantized from W [K, N]; the codes [N, K] then hold
+ * one entry a row) serves both ends of a model with tied weights. `vocab` is
+ * the number of entries, 1 <= vocab <= N: the columns from vocab to N (a
+ * multiple of 16) are padding, are no class of the loss and get no gradient;
+ * what they hold is not read into any result.
+ *
+ * These calls take QLORA_W8 (float32 and bf16) and QLORA_W4G128 (bf16; K <=
+ * 16384) layers of one head (EUNSUPPORTED otherwise), and, unlike the others,
+ * r = 0 for a layer without adapter (A and B NULL, alpha not read). Tokens and
+ * targets are device arrays [M] of int32 or int64. One outside [0, vocab)
+ * (padding, prompts) stands for none: its row of x is zero, its loss 0, its
+ * gradients 0, whatever else the row holds. Constraints otherwise as above. */
+typedef enum { QLORA_I32 = 0, QLORA_I64 = 1 } qlora_itype;
+
+/* Lookup: x [M, K] = scale w_token(m), formed in float32 and rounded once to
+ * the compute dtype. */
+int qlora_embed(const qlora_linear* L, int vocab, int M, int dtype, const void* tokens, int itype,
+                float scale, void* x, void* stream);
+
+/* Its gradient for dy [M, K], the gradient of x (r >= 1; the frozen weight has
+ * none):
+ *   u  = scale s dy A                                  (float32, internal)
+ *   dB[:, v] = sum of u[m] over the rows m with token v, in increasing m;
+ *              0 for entries that no row names     float32 [r, N]
+ *   dA = scale s sum_m dy[m]^T B[:, token(m)]^T    float32 [K, r]
+ * The tokens are sorted on the way (stable). accumulate != 0 adds to what dA
+ * and dB hold, for a tied layer whose qlora_xent_bwd wrote them. M <= 2^20
+ * (ERANGE above). */
+int qlora_embed_bwd_workspace(const qlora_linear* L, int vocab, int M, int dtype, size_t* bytes);
+int qlora_embed_bwd(const qlora_linear* L, int vocab, int M, int dtype, const void* tokens, int itype,
+                    float scale, const void* dy, int accumulate, float* dA, float* dB, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/* ---- moving the adapters: AdamW over many tensors ----------------------------
+ *
+ * One step ("Introduce QLoRA-like technique", qlora.py: AdamW, learning rate
+ * 5e-5, weight decay 0.01 with exclusions, epsilon 1e-6, global clipnorm 1.0)
+ * of every float32 tensor p with its gradient g and moments m, v:
+ *
+ *   norm = sqrt(sum of g^2 over all tensors)            (sums in float64)
+ *   g'   = g clip_norm / max(norm, clip_norm)           (clip_norm > 0)
+ *   m <- beta1 m + (1 - beta1) g',   v <- beta2 v + (1 - beta2) g'^2
+ *   p <- p (1 - lr decay) - lr / (1 - beta1^k) m / (sqrt(v) / sqrt(1 - beta2^k) + eps)
+ *
+ * in float32, with k = *step + 1, which *step then holds (device memory, so
+ * that a captured step counts on in its replays). With clip_norm > 0 and a
+ * norm that is not finite nothing is moved and *step stays.
+ *
+ * The moments are float32 (QLORA_S32) or one byte an element (QLORA_S8): 32
+ * consecutive elements share the scale 2^e, e the smallest (at least -126) that
+ * covers them, kept as the byte e + 127 (255, which reads as NaN, for a group
+ * with an infinity or a NaN). m is a sign, 3 bits of exponent and 4 of mantissa,
+ * largest 31/16; v is kept as its root, 3 bits of exponent and 5 of mantissa,
+ * largest 63/32 (exponent 0: subnormal). A value between two codes takes the
+ * upper one as often as it is nearer to it: 16 bits of hash(item, element, k,
+ * seed) are added below the code's last bit, so that changes far smaller than
+ * a step of the code, which is every step's change of v, are kept on average;
+ * a v that is not 0 keeps a code that is not 0. The sizes and order of items
+ * enter the hash and the norm's sum, so the same calls give the same bytes. */
+typedef enum { QLORA_S32 = 0, QLORA_S8 = 1 } qlora_sfmt;
+
+typedef struct {
+  float* p;               /* [n] */
+  const float* g;         /* [n] */
+  void* m;                /* [n] float32, or uint8 codes */
+  void* v;
+  uint8_t* m_scales;      /* QLORA_S8: [ceil(n / 32)], else NULL */
+  uint8_t* v_scales;
+  int64_t n;              /* 1 <= n <= 2^30 */
+  double decay;           /* weight decay (0: an excluded tensor) */
+} qlora_adamw_item;
+
+typedef struct {
+  double lr, beta1, beta2, eps;
+  double clip_norm;       /* 0: no clipping */
+  const float* lr_dev;    /* NULL, or device memory: read instead of lr */
+  int32_t* step;          /* device: steps done, advanced by the call */
+  float* norm;            /* NULL, or device: the norm is written there */
+  uint32_t seed;          /* of the roundings of QLORA_S8 */
+  int32_t sfmt;           /* qlora_sfmt */
+} qlora_adamw_config;
+
+/* One step of `count` tensors in one launch per 48 tensors (and as many for
+ * the norm where clip_norm > 0 or norm is given). items[] and cfg are read
+ * during the call only (host memory). Tensors must not overlap each other.
+ * 0 <= beta < 1, eps > 0, lr, decay and clip_norm >= 0 and all finite; 0 <=
+ * *step (EINVAL for what the host can see). */
+int qlora_adamw_workspace(const qlora_adamw_item* items, int count, size_t* bytes);
+int qlora_adamw(const qlora_adamw_config* cfg, const qlora_adamw_item* items, int count, void* ws,
+                size_t ws_bytes, void* stream);
+
 /* Merge the trained adapter into the frozen int8 weight ("Parameter-efficient
  * fine-tuning of GPT-2 with LoRA", "Merge weights and generate text!": the
  * merged kernel is the frozen kernel plus the adapter product; "Introduce

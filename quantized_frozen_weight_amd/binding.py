@@ -27,6 +27,9 @@ _ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}      # qlora
 _CFMT = {"c8row": 0, "c8g32": 1}                                         # qlora_cfmt
 CKPT_GROUP = 32          # columns per scale of a "c8g32" checkpoint
 
+_SFMT = {"f32": 0, "s8": 1}                                              # qlora_sfmt
+S8_GROUP = 32            # elements per scale of an 8-bit moment
+
 _FMT = {"w8": QLORA_W8, "w4g128": QLORA_W4G128, "w8o": QLORA_W8O}
 
 
@@ -62,7 +65,8 @@ EXPORTS = (
     "qlora_bwd_partials_bytes", "qlora_bwd_main_kernel", "qlora_bwd_noalloc",
     "qlora_ckpt_bytes", "qlora_ckpt_write", "qlora_ckpt_read", "qlora_fwd_epi",
     "qlora_fwd_ckpt", "qlora_bwd_epi", "qlora_bwd_epi_partial", "qlora_bwd_epi_workspace",
-    "qlora_act_bwd_workspace", "qlora_act_bwd",
+    "qlora_act_bwd_workspace", "qlora_act_bwd", "qlora_embed", "qlora_embed_bwd_workspace",
+    "qlora_embed_bwd", "qlora_adamw_workspace", "qlora_adamw",
 )
 QLORA_NOALLOC_SCRATCH_BYTES = 16 << 20
 # include/qlora_probe.h: measurement probes (not part of the layer)
@@ -102,6 +106,34 @@ class qlora_grad_epilogue(ctypes.Structure):
         ("z_codes", ctypes.c_void_p),
         ("z_scales", ctypes.c_void_p),
         ("add", ctypes.c_void_p),
+    ]
+
+
+class qlora_adamw_item(ctypes.Structure):
+    _fields_ = [
+        ("p", ctypes.c_void_p),
+        ("g", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("decay", ctypes.c_double),
+    ]
+
+
+class qlora_adamw_config(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("clip_norm", ctypes.c_double),
+        ("lr_dev", ctypes.c_void_p),
+        ("step", ctypes.c_void_p),
+        ("norm", ctypes.c_void_p),
+        ("seed", ctypes.c_uint32),
+        ("sfmt", ctypes.c_int32),
     ]
 
 
@@ -151,6 +183,12 @@ def lib() -> ctypes.CDLL:
     L.qlora_bwd_epi_workspace.argtypes = [plin, i, i, psz]
     L.qlora_act_bwd_workspace.argtypes = [i, i, psz]
     L.qlora_act_bwd.argtypes = [i, i, i, i, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.qlora_embed.argtypes = [plin, i, i, i, vp, i, ctypes.c_float, vp, vp]
+    L.qlora_embed_bwd_workspace.argtypes = [plin, i, i, i, psz]
+    L.qlora_embed_bwd.argtypes = [plin, i, i, i, vp, i, ctypes.c_float, vp, i, vp, vp, vp, sz, vp]
+    pitem = ctypes.POINTER(qlora_adamw_item)
+    L.qlora_adamw_workspace.argtypes = [pitem, i, psz]
+    L.qlora_adamw.argtypes = [ctypes.POINTER(qlora_adamw_config), pitem, i, vp, sz, vp]
     for name in EXPORTS[1:]:
         getattr(L, name).restype = ctypes.c_int
     L.qlora_bwd_main_kernel.restype = ctypes.c_char_p
@@ -856,3 +894,200 @@ def qlora_act_bwd(act: str, dy, z=None, need_dz: bool = True, need_dbias: bool =
                                    _ptr(ws), 0 if ws is None else ws.nbytes,
                                    _stream()), "qlora_act_bwd")
     return dz, dbias
+
+
+# ---------------------------------------------------------------------------
+# The vocabulary layer (a QLinear of K features and N entries, r = 0 and A = B =
+# None for one without adapter) and the AdamW step. Devices and errors as above.
+# ---------------------------------------------------------------------------
+def _vocab_on(layer: QLinear, vocab: Optional[int], device):
+    """(C struct, vocab) of a vocabulary layer, its tensors checked."""
+    import torch
+    if layer.r > 0:
+        cs = _layer_on(layer, device)
+    else:
+        if layer.A is not None or layer.B is not None:
+            raise ValueError("layer: A and B given at rank 0")
+        cshape, ctype, sshape, stype = _weight_form(layer.K, layer.N, layer.fmt)
+        _tensor(layer.codes, "layer codes", cshape, ctype, device)
+        _tensor(layer.scales, "layer scales", sshape, stype, device)
+        cs = layer.cstruct()
+    return cs, layer.N if vocab is None else int(vocab)
+
+
+def _ids(ids, what: str, device=None):
+    """(M, itype) of a dense 1-D tensor of tokens or targets on a GPU."""
+    import torch
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"{what}: {ids.dtype}, expected torch.int32 or torch.int64")
+    if ids.dim() != 1 or not ids.is_cuda or not ids.is_contiguous():
+        raise ValueError(f"{what}: a contiguous 1-D GPU tensor is needed")
+    if device is not None and ids.device != device:
+        raise ValueError(f"{what}: on {ids.device}, expected {device}")
+    return ids.shape[0], 1 if ids.dtype == torch.int64 else 0
+
+
+@functools.lru_cache(maxsize=4096)
+def _vocab_sizes(query: str, K: int, N: int, r: int, fmt: int, heads: int, vocab: int, M: int, dtype: int) -> int:
+    """As _sizes, of the vocabulary calls."""
+    n = ctypes.c_size_t()
+    ab = 256 if r > 0 else None
+    s = qlora_linear(K, N, r, 1.0, fmt, 256, 256, ab, ab, heads)
+    _check(getattr(lib(), query)(ctypes.byref(s), vocab, M, dtype, ctypes.byref(n)), query)
+    return n.value
+
+
+def _vocab_scratch(query: str, layer: QLinear, cs: qlora_linear, vocab: int, M: int, dtype: int, device, ws):
+    """The caller's workspace, or a new one of the queried size."""
+    if ws is not None:
+        if ws.device != device or not ws.is_contiguous():
+            raise ValueError(f"ws: a contiguous tensor on {device} is needed")
+        return ws
+    n = _vocab_sizes(query, cs.K, cs.N, cs.r, cs.fmt, cs.heads, vocab, M, dtype)
+    return layer.codes.new_empty((max(n, 256),))
+
+
+def qlora_embed(layer: QLinear, tokens, vocab: Optional[int] = None, scale: float = 1.0, dtype=None, x=None):
+    """x [M, K] = scale w_token for tokens [M] (int32 or int64; one outside [0,
+    vocab) gives a row of zeros), in dtype (torch.bfloat16 unless x is given)."""
+    import torch
+    M, it = _ids(tokens, "tokens")
+    dev = tokens.device
+    cs, vocab = _vocab_on(layer, vocab, dev)
+    if x is None:
+        x = torch.empty((M, layer.K), dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
+    else:
+        _tensor(x, "x", (M, layer.K), x.dtype if dtype is None else dtype, dev)
+    dt = _dtype_code(x)
+    with _on(dev):
+        _check(lib().qlora_embed(ctypes.byref(cs), vocab, M, dt, _ptr(tokens), it, scale, _ptr(x), _stream()),
+               "qlora_embed")
+    return x
+
+
+def qlora_embed_bwd(layer: QLinear, tokens, dy, vocab: Optional[int] = None, scale: float = 1.0, dA=None, dB=None,
+                    accumulate: bool = False, ws=None):
+    """The adapter's gradients of qlora_embed for dy [M, K]: (dA, dB), dB by the
+    sorted tokens. accumulate adds to the dA and dB given."""
+    import torch
+    M, it = _ids(tokens, "tokens")
+    dev = tokens.device
+    rows, _, dt = _rows(dy, "dy", layer.K)
+    if rows != M or dy.device != dev:
+        raise ValueError(f"dy: {rows} rows on {dy.device}, expected {M} on {dev}")
+    cs, vocab = _vocab_on(layer, vocab, dev)
+    if layer.r < 1:
+        raise ValueError("layer: no adapter, nothing to differentiate")
+    if accumulate and (dA is None or dB is None):
+        raise ValueError("accumulate: needs dA and dB")
+    dA = layer.A.new_empty((layer.K, layer.r)) if dA is None else \
+        _tensor(dA, "dA", (layer.K, layer.r), torch.float32, dev)
+    dB = layer.B.new_empty((layer.r, layer.N)) if dB is None else \
+        _tensor(dB, "dB", (layer.r, layer.N), torch.float32, dev)
+    ws = _vocab_scratch("qlora_embed_bwd_workspace", layer, cs, vocab, M, dt, dev, ws)
+    with _on(dev):
+        _check(lib().qlora_embed_bwd(ctypes.byref(cs), vocab, M, dt, _ptr(tokens), it, scale, _ptr(dy),
+                                     int(accumulate), _ptr(dA), _ptr(dB), _ptr(ws), ws.nbytes, _stream()),
+               "qlora_embed_bwd")
+    return dA, dB
+
+
+class AdamW:
+    """AdamW's state over float32 tensors that the caller holds: moments in
+    float32 (state "f32") or in 8 bits ("s8": codes uint8, a scale byte per 32
+    elements), the step count (int32 [1] on the device) and the step's
+    workspace. decay: the weight decay of every tensor, or one per tensor (0:
+    excluded). What is not given is made here, zero. The tensors must not move
+    while the object lives."""
+
+    def __init__(self, params, state: str = "f32", decay=0.0, step=None, m=None, v=None, m_scales=None, v_scales=None,
+                 seed: int = 0):
+        import torch
+        params = list(params)
+        if not params:
+            raise ValueError("params: at least one tensor is needed")
+        if state not in _SFMT:
+            raise ValueError(f"unknown state form {state!r}")
+        s8, dev = state == "s8", params[0].device
+        count = len(params)
+        self.device, self.state, self.seed = dev, state, int(seed) & 0xFFFFFFFF
+        if not params[0].is_cuda:
+            raise ValueError("params: GPU tensors are needed")
+        for i, p in enumerate(params):
+            _tensor(p, f"params[{i}]", p.shape, torch.float32, dev)
+            if p.numel() == 0:
+                raise ValueError(f"params[{i}]: empty")
+        spans = sorted((p.data_ptr(), p.nbytes) for p in params)
+        if any(a + n > b for (a, n), (b, _) in zip(spans, spans[1:])):
+            raise ValueError("params: two of them overlap")
+
+        def held(given, what, n, dtype):
+            """One tensor of n(numel) elements per parameter, made (zero) or checked."""
+            if given is None:
+                return [torch.zeros((n(p.numel()),), dtype=dtype, device=dev) for p in params]
+            given = list(given)
+            if len(given) != count:
+                raise ValueError(f"{what}: {len(given)} tensors for {count} parameters")
+            for i, (t, p) in enumerate(zip(given, params)):
+                if t.numel() != n(p.numel()):
+                    raise ValueError(f"{what}[{i}]: {t.numel()} elements, expected {n(p.numel())}")
+                _tensor(t, f"{what}[{i}]", t.shape, dtype, dev)
+            return given
+
+        kind = torch.uint8 if s8 else torch.float32
+        self.params = params
+        self.m, self.v = held(m, "m", lambda n: n, kind), held(v, "v", lambda n: n, kind)
+        if s8:
+            groups = lambda n: -(-n // S8_GROUP)  # noqa: E731
+            self.m_scales = held(m_scales, "m_scales", groups, torch.uint8)
+            self.v_scales = held(v_scales, "v_scales", groups, torch.uint8)
+        elif m_scales is not None or v_scales is not None:
+            raise ValueError("m_scales, v_scales: float32 moments have none")
+        self.step = torch.zeros((1,), dtype=torch.int32, device=dev) if step is None else \
+            _tensor(step, "step", (1,), torch.int32, dev)
+        decay = [float(decay)] * count if isinstance(decay, (int, float)) else [float(d) for d in decay]
+        if len(decay) != count:
+            raise ValueError(f"decay: {len(decay)} values for {count} parameters")
+        self.items = (qlora_adamw_item * count)()
+        for i, p in enumerate(params):
+            self.items[i] = qlora_adamw_item(
+                _ptr(p), None, _ptr(self.m[i]), _ptr(self.v[i]), _ptr(self.m_scales[i]) if s8 else None,
+                _ptr(self.v_scales[i]) if s8 else None, p.numel(), decay[i])
+        n = ctypes.c_size_t()
+        _check(lib().qlora_adamw_workspace(self.items, count, ctypes.byref(n)), "qlora_adamw_workspace")
+        self.ws = torch.empty((max(n.value, 256),), dtype=torch.uint8, device=dev)
+
+
+def qlora_adamw(opt: AdamW, grads, lr, betas=(0.9, 0.999), eps: float = 1e-6, clip_norm: float = 0.0,
+                need_norm: bool = False, norm=None, ws=None):
+    """One step of every tensor of opt for its gradient (float32, one each); lr
+    a number, or a float32 [1] tensor on the device, read when the step runs.
+    Returns the gradients' norm before clipping (float32 [1]) if need_norm.
+    opt's own workspace serves one stream at a time; ws replaces it."""
+    import torch
+    grads = list(grads)
+    dev, items = opt.device, opt.items
+    if len(grads) != len(items):
+        raise ValueError(f"grads: {len(grads)} tensors for {len(items)} parameters")
+    f32 = torch.float32
+    for i, (g, p) in enumerate(zip(grads, opt.params)):
+        if not (g.dtype is f32 and g.shape == p.shape and g.device == dev and g.is_contiguous()):
+            _tensor(g, f"grads[{i}]", p.shape, f32, dev)
+        items[i].g = g.data_ptr()
+    c = qlora_adamw_config(beta1=betas[0], beta2=betas[1], eps=eps, clip_norm=clip_norm, step=_ptr(opt.step),
+                           seed=opt.seed, sfmt=_SFMT[opt.state])
+    if isinstance(lr, torch.Tensor):
+        c.lr_dev = _ptr(_tensor(lr, "lr", (1,), f32, dev))
+    else:
+        c.lr = lr
+    if need_norm:
+        norm = torch.empty((1,), dtype=f32, device=dev) if norm is None else _tensor(norm, "norm", (1,), f32, dev)
+        c.norm = _ptr(norm)
+    else:
+        _unused(norm, "norm", "need_norm")
+    ws = opt.ws if ws is None else ws
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: a contiguous tensor on {dev} is needed")
+    with _on(dev):
+        _check(lib().qlora_adamw(ctypes.byref(c), items, len(items), _ptr(ws), ws.nbytes, _stream()), "qlora_adamw")
+    return norm

@@ -1,0 +1,399 @@
+// One AdamW step of many float32 tensors, moments in 32 or 8 bits (formulas and
+// the 8-bit form: include/qlora.h).
+//
+// Memory-bound: an element moves 28 bytes with float32 moments, 16.1 with 8-bit
+// ones, and 4 more where the norm is taken first. Two kernels, each launched
+// once per 48 tensors, their pointers in the kernel's arguments:
+//
+//   norm    a block sums the squares of one chunk of one tensor in float64 and
+//           leaves the sum in the workspace; chunks grow with the total, so
+//           that there are about 512 sums whatever the sizes. Block 0 of the
+//           first launch also forms what depends on the step alone (the bias
+//           corrections, in float64) and advances the step: nothing else reads
+//           it there. Without a norm to take, that block is the whole launch.
+//   update  a block takes 4096 elements of one tensor, 16 a thread in four
+//           pieces of 16 bytes, all of them in flight before the block adds the
+//           sums of the norm (in their order, every block the same).
+//
+// Eight lanes hold one group of 32 8-bit moments, so its maximum is three DPP
+// steps. The operations are written as the formulas have them, each rounded
+// (no contraction), so that the float32 results do not depend on how a thread
+// holds them.
+#include "adamw.hpp"
+#include "abi.hpp"
+#include "common.hpp"
+
+#pragma clang fp contract(off)
+
+namespace qlora {
+
+namespace {
+
+constexpr int kItems = 48;           // tensors per launch
+constexpr int kChunk = 4096;         // elements per block of the update
+constexpr int kNormSums = 512;       // about as many partial sums of the norm
+
+// What the norm launch leaves for the update.
+struct Hyper {
+  float lr, c1, root_c2;             // learning rate, 1 - beta1^k, sqrt(1 - beta2^k)
+  int32_t k;
+};
+
+struct NormArgs {
+  const float* g[kItems];
+  int n[kItems];
+  int bstart[kItems + 1];            // first block of each tensor
+  int count, chunk, first;           // first: this launch holds block 0 of the call
+  long base;                         // partial sums of earlier launches
+  double lr, beta1, beta2;
+  const float* lr_dev;
+  int32_t* step;
+  Hyper* hyper;
+  double* sums;
+};
+static_assert(sizeof(NormArgs) <= 4096, "kernel arguments");
+
+template <int N>
+__device__ __forceinline__ int item_of(const int (&bstart)[N], int count, int b) {
+  int i = 0;
+  while (i + 1 < count && b >= bstart[i + 1]) ++i;          // block-uniform
+  return i;
+}
+
+// Sum over the block's 256 threads, the same in every thread and in a fixed
+// order; red: 4 doubles of LDS.
+__device__ __forceinline__ double block_sum(double v, double* red) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+__global__ __launch_bounds__(256) void adamw_norm_kernel(NormArgs a) {
+  __shared__ double red[4];
+  const int tid = threadIdx.x, b = blockIdx.x;
+  if (a.first && b == 0 && tid == 0) {
+    const int32_t k = *a.step + 1;
+    Hyper h;
+    h.lr = a.lr_dev != nullptr ? *a.lr_dev : (float)a.lr;
+    h.c1 = (float)(1.0 - pow(a.beta1, (double)k));
+    h.root_c2 = sqrtf((float)(1.0 - pow(a.beta2, (double)k)));
+    h.k = k;
+    *a.hyper = h;
+    *a.step = k;
+  }
+  if (a.sums == nullptr) return;
+  const int i = item_of(a.bstart, a.count, b);
+  const long e0 = (long)(b - a.bstart[i]) * a.chunk;
+  const long e1 = e0 + a.chunk < a.n[i] ? e0 + a.chunk : a.n[i];
+  const float* g = a.g[i];
+  double sum = 0.0;
+  const long q1 = e0 + ((e1 - e0) & ~3L);
+  for (long e = e0 + 4 * tid; e < q1; e += 4096) {          // four pieces in flight
+    f32x4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      v[u] = *reinterpret_cast<const f32x4*>(g + (e + 1024 * u < q1 ? e + 1024 * u : e));
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (e + 1024 * u < q1)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sum += (double)v[u][c] * (double)v[u][c];
+  }
+  if (q1 + tid < e1) sum += (double)g[q1 + tid] * (double)g[q1 + tid];
+  sum = block_sum(sum, red);
+  if (tid == 0) a.sums[a.base + b] = sum;
+}
+
+struct UpdateItem {
+  float* p;
+  const float* g;
+  void* m;
+  void* v;
+  uint8_t* ms;
+  uint8_t* vs;
+  int n;
+  float decay;
+};
+struct UpdateArgs {
+  UpdateItem it[kItems];
+  int bstart[kItems + 1];
+  int count, item0, first;
+  int clip, sums_n;                  // clip: the gradient is clipped
+  float beta1, rest1, beta2, rest2, eps, clip_norm;
+  uint32_t seed;
+  int32_t* step;
+  const Hyper* hyper;
+  const double* sums;                // NULL: no norm
+  float* norm;
+};
+static_assert(sizeof(UpdateArgs) <= 4096, "kernel arguments");
+
+// 32 bits for one element: two rounds of multiply and shift (odd constants: the
+// golden ratio's and the square roots' of 2 and 3 first 32 bits).
+__device__ __forceinline__ uint32_t hash32(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x6A09E667u;
+  x ^= x >> 15;
+  x *= 0xBB67AE85u;
+  return x ^ (x >> 16);
+}
+
+// The largest of the 8 lanes that hold one group.
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+#pragma unroll
+  for (int lvl = 1; lvl < 4; ++lvl) {
+    const uint32_t w = __float_as_uint(dpp_pair(__uint_as_float(v), lvl));
+    v = w > v ? w : v;
+  }
+  return v;
+}
+
+// The exponent e of a group's scale for BITS bits of mantissa, from the bits of
+// its largest magnitude (finite): the smallest with top <= (2 - 2^-BITS) 2^e,
+// held to [-126, 127].
+template <int BITS>
+__device__ __forceinline__ int scale_exp(uint32_t top) {
+  const int e = (int)(top >> 23) - 127 + ((top & 0x7fffffu) > (0x7fffffu & (~0u << (23 - BITS))) ? 1 : 0);
+  return e < -126 ? -126 : e > 127 ? 127 : e;
+}
+
+// A magnitude under its group's scale as a code: v 2^-(e + 120) is a float32
+// whose exponent field is the code's, 0 to 7; the hash's 16 bits are added
+// right below the code's last bit.
+template <int BITS>
+__device__ __forceinline__ uint32_t to_code(float v, int e, uint32_t rnd) {
+  const uint32_t f = __float_as_uint(__builtin_ldexpf(__builtin_ldexpf(__builtin_fabsf(v), -e), -120));
+  const uint32_t c = (f + (rnd << (23 - BITS - 16))) >> (23 - BITS);
+  constexpr uint32_t most = (8u << BITS) - 1;
+  return c < most ? c : most;
+}
+template <int BITS>
+__device__ __forceinline__ float of_code(uint32_t c, int e) {
+  return __builtin_ldexpf(__builtin_ldexpf(__uint_as_float(c << (23 - BITS)), 120), e);
+}
+
+template <bool S8>
+__global__ __launch_bounds__(256) void adamw_update_kernel(UpdateArgs a) {
+  __shared__ double red[4];
+  const int tid = threadIdx.x, b = blockIdx.x;
+  const int i = item_of(a.bstart, a.count, b);
+  const UpdateItem& it = a.it[i];
+  const int n = it.n;
+  const int c0 = (b - a.bstart[i]) * kChunk;
+  constexpr int U = kChunk / 1024;
+
+  // the block's operands, from clamped places (a piece past the end reads the
+  // first one again, a ragged last piece is read by elements)
+  float p[U][4], g[U][4], m[U][4], v[U][4];
+  uint32_t mc[U], vc[U];
+  int ms[U], vs[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int e = c0 + 1024 * u + 4 * tid;
+    if (e + 4 <= n || e >= n) {
+      const long at = e < n ? e : 0;
+      const bool whole = n >= 4;                            // (n < 4: nothing is whole, and nothing is used)
+      const f32x4 z{0.f, 0.f, 0.f, 0.f};
+      const f32x4 pv = whole ? *reinterpret_cast<const f32x4*>(it.p + at) : z;
+      const f32x4 gv = whole ? *reinterpret_cast<const f32x4*>(it.g + at) : z;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) { p[u][c] = pv[c]; g[u][c] = gv[c]; }
+      if constexpr (S8) {
+        mc[u] = whole ? *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(it.m) + at) : 0u;
+        vc[u] = whole ? *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(it.v) + at) : 0u;
+      } else {
+        const f32x4 mv = whole ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(it.m) + at) : z;
+        const f32x4 vv = whole ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(it.v) + at) : z;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) { m[u][c] = mv[c]; v[u][c] = vv[c]; }
+      }
+    } else {
+      if constexpr (S8) mc[u] = vc[u] = 0u;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int at = e + c < n ? e + c : e;
+        p[u][c] = it.p[at];
+        g[u][c] = e + c < n ? it.g[at] : 0.f;
+        if constexpr (S8) {
+          if (e + c < n) {
+            mc[u] |= (uint32_t)static_cast<const uint8_t*>(it.m)[at] << (8 * c);
+            vc[u] |= (uint32_t)static_cast<const uint8_t*>(it.v)[at] << (8 * c);
+          }
+        } else {
+          m[u][c] = static_cast<const float*>(it.m)[at];
+          v[u][c] = static_cast<const float*>(it.v)[at];
+        }
+      }
+    }
+    if constexpr (S8) {
+      ms[u] = it.ms[e < n ? e / 32 : 0];
+      vs[u] = it.vs[e < n ? e / 32 : 0];
+    }
+  }
+
+  const Hyper h = *a.hyper;
+  float coef = 1.f;
+  if (a.sums != nullptr) {
+    double sum = 0.0;
+    for (int q = tid; q < a.sums_n; q += 256) sum += a.sums[q];
+    const float norm = (float)sqrt(block_sum(sum, red));
+    const bool skip = a.clip && !(norm <= 3.4028234e38f);   // infinite or NaN: nothing is moved
+    if (a.first && b == 0 && tid == 0) {
+      if (a.norm != nullptr) *a.norm = norm;
+      if (skip) *a.step = h.k - 1;
+    }
+    if (skip) return;
+    if (a.clip) coef = a.clip_norm / (norm > a.clip_norm ? norm : a.clip_norm);
+  }
+  const float keep = 1.f - h.lr * it.decay, rate = h.lr / h.c1;
+
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int e = c0 + 1024 * u + 4 * tid;
+    float root[4];
+    if constexpr (S8) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t mb = (mc[u] >> (8 * c)) & 0xffu, vb = (vc[u] >> (8 * c)) & 0xffu;
+        const float mv = of_code<4>(mb & 127u, ms[u] - 127), rv = of_code<5>(vb, vs[u] - 127);
+        m[u][c] = ms[u] == 255 ? __uint_as_float(0x7fc00000u) : (mb & 128u) ? -mv : mv;
+        v[u][c] = vs[u] == 255 ? __uint_as_float(0x7fc00000u) : rv * rv;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float gc = a.clip ? g[u][c] * coef : g[u][c];
+      m[u][c] = a.beta1 * m[u][c] + a.rest1 * gc;
+      v[u][c] = a.beta2 * v[u][c] + a.rest2 * (gc * gc);
+      root[c] = sqrtf(v[u][c]);
+      const float moved = p[u][c] * keep;
+      p[u][c] = moved - rate * (m[u][c] / (root[c] / h.root_c2 + a.eps));
+    }
+    uint32_t mo = 0u, vo = 0u;
+    int me = 0, ve = 0;
+    if constexpr (S8) {
+      // elements past the end are no part of their group
+      uint32_t mt = 0u, vt = 0u;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (e + c < n) {
+          const uint32_t x = abs_bits(m[u][c]), y = abs_bits(root[c]);
+          mt = x > mt ? x : mt;
+          vt = y > vt ? y : vt;
+        }
+      mt = group_max(mt);
+      vt = group_max(vt);
+      const bool mbad = mt >= 0x7f800000u, vbad = vt >= 0x7f800000u;
+      me = scale_exp<4>(mt);
+      ve = scale_exp<5>(vt);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t rnd = hash32((uint32_t)(e + c) * 0x9E3779B1u + (uint32_t)(a.item0 + i) * 0x3C6EF373u +
+                                    (uint32_t)h.k * 0xBB67AE85u + a.seed);
+        uint32_t x = to_code<4>(m[u][c], me, rnd & 0xffffu) | (m[u][c] < 0.f ? 128u : 0u);
+        uint32_t y = to_code<5>(root[c], ve, rnd >> 16);
+        y = y == 0u && root[c] > 0.f ? 1u : y;
+        mo |= (mbad ? 0u : x) << (8 * c);
+        vo |= (vbad ? 0u : y) << (8 * c);
+      }
+      me = mbad ? 255 : me + 127;
+      ve = vbad ? 255 : ve + 127;
+    }
+    if (e + 4 <= n) {
+      *reinterpret_cast<f32x4*>(it.p + e) = f32x4{p[u][0], p[u][1], p[u][2], p[u][3]};
+      if constexpr (S8) {
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(it.m) + e) = mo;
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(it.v) + e) = vo;
+      } else {
+        *reinterpret_cast<f32x4*>(static_cast<float*>(it.m) + e) = f32x4{m[u][0], m[u][1], m[u][2], m[u][3]};
+        *reinterpret_cast<f32x4*>(static_cast<float*>(it.v) + e) = f32x4{v[u][0], v[u][1], v[u][2], v[u][3]};
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (e + c < n) {
+          it.p[e + c] = p[u][c];
+          if constexpr (S8) {
+            static_cast<uint8_t*>(it.m)[e + c] = (uint8_t)(mo >> (8 * c));
+            static_cast<uint8_t*>(it.v)[e + c] = (uint8_t)(vo >> (8 * c));
+          } else {
+            static_cast<float*>(it.m)[e + c] = m[u][c];
+            static_cast<float*>(it.v)[e + c] = v[u][c];
+          }
+        }
+    }
+    if constexpr (S8) {
+      if (e < n && (e & 31) == 0) {
+        it.ms[e / 32] = (uint8_t)me;
+        it.vs[e / 32] = (uint8_t)ve;
+      }
+    }
+  }
+}
+
+}  // namespace
+
+long adamw_norm_blocks(const qlora_adamw_item* items, int count, long* chunk) {
+  long total = 0, blocks = 0;
+  for (int i = 0; i < count; ++i) total += items[i].n;
+  const long c = (total / kNormSums + kChunk - 1) / kChunk * kChunk;
+  *chunk = c < kChunk ? kChunk : c > (1L << 30) ? (1L << 30) : c;
+  for (int i = 0; i < count; ++i) blocks += (items[i].n + *chunk - 1) / *chunk;
+  return blocks;
+}
+
+size_t adamw_bytes(const qlora_adamw_item* items, int count) {
+  long chunk;
+  return align_up(sizeof(Hyper)) + align_up((size_t)adamw_norm_blocks(items, count, &chunk) * 8);
+}
+
+void launch_adamw(const qlora_adamw_config& cfg, const qlora_adamw_item* items, int count, void* ws,
+                  hipStream_t st) {
+  Hyper* hyper = static_cast<Hyper*>(ws);
+  const bool clip = cfg.clip_norm > 0.0, norm = clip || cfg.norm != nullptr;
+  double* sums = norm ? reinterpret_cast<double*>(static_cast<char*>(ws) + align_up(sizeof(Hyper))) : nullptr;
+  long chunk;
+  const long nsums = adamw_norm_blocks(items, count, &chunk);
+  long base = 0;
+  for (int i0 = 0; i0 < (norm ? count : 1); i0 += kItems) {
+    NormArgs a{};
+    a.count = count - i0 < kItems ? count - i0 : kItems;
+    a.chunk = (int)chunk;
+    a.first = i0 == 0;
+    a.base = base;
+    a.lr = cfg.lr; a.beta1 = cfg.beta1; a.beta2 = cfg.beta2; a.lr_dev = cfg.lr_dev;
+    a.step = cfg.step; a.hyper = hyper; a.sums = sums;
+    for (int i = 0; i < a.count; ++i) {
+      a.g[i] = items[i0 + i].g;
+      a.n[i] = (int)items[i0 + i].n;
+      a.bstart[i + 1] = a.bstart[i] + (int)((items[i0 + i].n + chunk - 1) / chunk);
+    }
+    base += a.bstart[a.count];
+    adamw_norm_kernel<<<dim3(norm ? (unsigned)a.bstart[a.count] : 1u), 256, 0, st>>>(a);
+  }
+  for (int i0 = 0; i0 < count; i0 += kItems) {
+    UpdateArgs a{};
+    a.count = count - i0 < kItems ? count - i0 : kItems;
+    a.item0 = i0;
+    a.first = i0 == 0;
+    a.clip = clip;
+    a.sums_n = (int)nsums;
+    a.beta1 = (float)cfg.beta1; a.rest1 = (float)(1.0 - cfg.beta1);
+    a.beta2 = (float)cfg.beta2; a.rest2 = (float)(1.0 - cfg.beta2);
+    a.eps = (float)cfg.eps; a.clip_norm = (float)cfg.clip_norm;
+    a.seed = cfg.seed; a.step = cfg.step; a.hyper = hyper; a.sums = sums; a.norm = cfg.norm;
+    for (int i = 0; i < a.count; ++i) {
+      const qlora_adamw_item& s = items[i0 + i];
+      a.it[i] = UpdateItem{s.p, s.g, s.m, s.v, s.m_scales, s.v_scales, (int)s.n, (float)s.decay};
+      a.bstart[i + 1] = a.bstart[i] + (int)((s.n + kChunk - 1) / kChunk);
+    }
+    const dim3 grid((unsigned)a.bstart[a.count]);
+    if (cfg.sfmt == QLORA_S8) adamw_update_kernel<true><<<grid, 256, 0, st>>>(a);
+    else adamw_update_kernel<false><<<grid, 256, 0, st>>>(a);
+  }
+}
+
+}  // namespace qlora
