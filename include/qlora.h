@@ -534,6 +534,41 @@ int qlora_embed_bwd(const qlora_linear* L, int vocab, int M, int dtype, const vo
                     float scale, const void* dy, int accumulate, float* dA, float* dB, void* ws,
                     size_t ws_bytes, void* stream);
 
+/* Softmax cross entropy over the vocabulary ("Simplified loss splitting", of
+ * the keras-llm-light README, forms it in pieces to save the logits' memory):
+ *   l[m, v] = x[m] . w_v       the layer's integer forward: x quantized to 8
+ *                              bits by rows, exact sums of products (a group's
+ *                              for QLORA_W4G128, as qlora_fwd_a8w4), the
+ *                              adapter's part s (x A) B in float32
+ *   lse[m]  = log sum_{v < vocab} exp(l[m, v])         float32 [M]
+ *   loss[m] = lse[m] - l[m, target(m)]                 float32 [M]
+ * No logit is written to memory: a tile's rows leave their maximum and sum
+ * (8 bytes for 256 logits of int8 weights, for 128 of 4-bit ones). t_save as
+ * for qlora_fwd (r >= 1). A row of x with an infinity or a NaN has lse NaN, and
+ * touches no other row. Int8 layers up to K = 132096 (EUNSUPPORTED above). */
+int qlora_xent_fwd_workspace(const qlora_linear* L, int vocab, int M, int dtype, size_t* bytes);
+int qlora_xent_fwd(const qlora_linear* L, int vocab, int M, int dtype, const void* x,
+                   const void* targets, int itype, float* loss, float* lse, float* t_save, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/* Its gradient, the activation quantizer passed straight through:
+ *   dl[m, v] = dloss[m] (exp(l[m, v] - lse[m]) - [v = target(m)])
+ *   u  = dl B^T                                        (float32, internal)
+ *   dx = dl deq(W)^T + s u A^T      [M, K] in the compute dtype (or NULL)
+ *   dA = s x^T u   float32 [K, r],  dB = s t^T dl   float32 [r, N]   (r >= 1)
+ * dloss float32 [M]: the gradient of each row's loss (1 / count for a mean).
+ * lse is qlora_xent_fwd's; t_saved its t (NULL: formed again). The logits are
+ * formed again piece by piece of the vocabulary; dl, which is formed in
+ * float32, lives for one piece, for the products with W in bf16 (times the
+ * entry's scale for int8 weights; in three bf16 parts, float32's precision, in
+ * the float32 compute dtype), for those with B and t in two parts of 16 bits
+ * together. dA and dB are NULL where r = 0; dx may be NULL where r >= 1. */
+int qlora_xent_bwd_workspace(const qlora_linear* L, int vocab, int M, int dtype, size_t* bytes);
+int qlora_xent_bwd(const qlora_linear* L, int vocab, int M, int dtype, const void* x,
+                   const void* targets, int itype, const float* lse, const float* dloss,
+                   const float* t_saved, void* dx, float* dA, float* dB, void* ws, size_t ws_bytes,
+                   void* stream);
+
 /* ---- moving the adapters: AdamW over many tensors ----------------------------
  *
  * One step ("Introduce QLoRA-like technique", qlora.py: AdamW, learning rate

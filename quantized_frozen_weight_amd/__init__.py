@@ -11,5 +11,5 @@ from .binding import (  # noqa: F401
     qlora_bwd_epi_partial, qlora_bwd_workspace, qlora_ckpt_read,
     qlora_ckpt_write, qlora_embed, qlora_embed_bwd, qlora_fwd, qlora_fwd_acc, qlora_fwd_ckpt, qlora_fwd_epi,
     qlora_fwd_workspace, qlora_quantize, qlora_quantize_rows,
-    qlora_status_str, qlora_weight_bytes,
+    qlora_status_str, qlora_weight_bytes, qlora_xent_bwd, qlora_xent_fwd,
 )

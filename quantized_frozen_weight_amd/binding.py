@@ -67,6 +67,7 @@ EXPORTS = (
     "qlora_fwd_ckpt", "qlora_bwd_epi", "qlora_bwd_epi_partial", "qlora_bwd_epi_workspace",
     "qlora_act_bwd_workspace", "qlora_act_bwd", "qlora_embed", "qlora_embed_bwd_workspace",
     "qlora_embed_bwd", "qlora_adamw_workspace", "qlora_adamw",
+    "qlora_xent_fwd_workspace", "qlora_xent_fwd", "qlora_xent_bwd_workspace", "qlora_xent_bwd",
 )
 QLORA_NOALLOC_SCRATCH_BYTES = 16 << 20
 # include/qlora_probe.h: measurement probes (not part of the layer)
@@ -186,6 +187,10 @@ def lib() -> ctypes.CDLL:
     L.qlora_embed.argtypes = [plin, i, i, i, vp, i, ctypes.c_float, vp, vp]
     L.qlora_embed_bwd_workspace.argtypes = [plin, i, i, i, psz]
     L.qlora_embed_bwd.argtypes = [plin, i, i, i, vp, i, ctypes.c_float, vp, i, vp, vp, vp, sz, vp]
+    L.qlora_xent_fwd_workspace.argtypes = [plin, i, i, i, psz]
+    L.qlora_xent_fwd.argtypes = [plin, i, i, i, vp, vp, i, vp, vp, vp, vp, sz, vp]
+    L.qlora_xent_bwd_workspace.argtypes = [plin, i, i, i, psz]
+    L.qlora_xent_bwd.argtypes = [plin, i, i, i, vp, vp, i, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     pitem = ctypes.POINTER(qlora_adamw_item)
     L.qlora_adamw_workspace.argtypes = [pitem, i, psz]
     L.qlora_adamw.argtypes = [ctypes.POINTER(qlora_adamw_config), pitem, i, vp, sz, vp]
@@ -990,6 +995,69 @@ def qlora_embed_bwd(layer: QLinear, tokens, dy, vocab: Optional[int] = None, sca
                                      int(accumulate), _ptr(dA), _ptr(dB), _ptr(ws), ws.nbytes, _stream()),
                "qlora_embed_bwd")
     return dA, dB
+
+
+def _xent_args(layer, x, targets, vocab):
+    """What the loss and its gradient check alike."""
+    M, _, dt = _rows(x, "x", layer.K)
+    dev = x.device
+    rows, it = _ids(targets, "targets", dev)
+    if rows != M:
+        raise ValueError(f"targets: {rows}, expected {M}")
+    cs, vocab = _vocab_on(layer, vocab, dev)
+    return M, dt, dev, it, cs, vocab
+
+
+def qlora_xent_fwd(layer: QLinear, x, targets, vocab: Optional[int] = None, save_t: bool = True, loss=None, lse=None,
+                   t=None, ws=None):
+    """Softmax cross entropy of x [M, K] over the layer's first vocab entries for
+    targets [M] (int32 or int64; one outside [0, vocab) gives loss 0). Returns
+    (loss, lse, t): float32 [M] each, and t = x A (None unless save_t, or where
+    the layer has no adapter)."""
+    import torch
+    M, dt, dev, it, cs, vocab = _xent_args(layer, x, targets, vocab)
+    f32 = torch.float32
+    loss = torch.empty((M,), dtype=f32, device=dev) if loss is None else _tensor(loss, "loss", (M,), f32, dev)
+    lse = torch.empty((M,), dtype=f32, device=dev) if lse is None else _tensor(lse, "lse", (M,), f32, dev)
+    if save_t and layer.r > 0:
+        t = torch.empty((M, layer.r), dtype=f32, device=dev) if t is None else _tensor(t, "t", (M, layer.r), f32, dev)
+    else:
+        _unused(t, "t", "save_t")
+    ws = _vocab_scratch("qlora_xent_fwd_workspace", layer, cs, vocab, M, dt, dev, ws)
+    with _on(dev):
+        _check(lib().qlora_xent_fwd(ctypes.byref(cs), vocab, M, dt, _ptr(x), _ptr(targets), it, _ptr(loss), _ptr(lse),
+                                    _ptr(t), _ptr(ws), ws.nbytes, _stream()), "qlora_xent_fwd")
+    return loss, lse, t
+
+
+def qlora_xent_bwd(layer: QLinear, x, targets, lse, dloss, t=None, vocab: Optional[int] = None, need_dx: bool = True,
+                   dx=None, dA=None, dB=None, ws=None):
+    """The gradient of qlora_xent_fwd for dloss [M] (float32; 1 / count for a
+    mean): (dx or None, dA, dB), the latter None where the layer has no adapter."""
+    import torch
+    M, dt, dev, it, cs, vocab = _xent_args(layer, x, targets, vocab)
+    f32 = torch.float32
+    _tensor(lse, "lse", (M,), f32, dev)
+    _tensor(dloss, "dloss", (M,), f32, dev)
+    if layer.r > 0:
+        if t is not None:
+            _tensor(t, "t", (M, layer.r), f32, dev)
+        dA = layer.A.new_empty((layer.K, layer.r)) if dA is None else _tensor(dA, "dA", (layer.K, layer.r), f32, dev)
+        dB = layer.B.new_empty((layer.r, layer.N)) if dB is None else _tensor(dB, "dB", (layer.r, layer.N), f32, dev)
+    elif t is not None or dA is not None or dB is not None:
+        raise ValueError("t, dA, dB: the layer has no adapter")
+    if need_dx:
+        dx = torch.empty_like(x) if dx is None else _tensor(dx, "dx", (M, layer.K), x.dtype, dev)
+    else:
+        _unused(dx, "dx", "need_dx")
+        if layer.r < 1:
+            raise ValueError("need_dx: the layer has no adapter, nothing is left")
+    ws = _vocab_scratch("qlora_xent_bwd_workspace", layer, cs, vocab, M, dt, dev, ws)
+    with _on(dev):
+        _check(lib().qlora_xent_bwd(ctypes.byref(cs), vocab, M, dt, _ptr(x), _ptr(targets), it, _ptr(lse), _ptr(dloss),
+                                    _ptr(t), _ptr(dx), _ptr(dA), _ptr(dB), _ptr(ws), ws.nbytes, _stream()),
+               "qlora_xent_bwd")
+    return dx, dA, dB
 
 
 class AdamW:

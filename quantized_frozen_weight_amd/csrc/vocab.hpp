@@ -48,7 +48,7 @@ struct XentPlan {
   int parts;                         // bf16 parts of dl: 1, or 3 in float32
   size_t g, dxp, u, up, dbp;         // elements: dl (bf16), dx partials, u, its partials, dB's
 };
-XentPlan xent_plan(const VocabLayer& L, int vocab, int M, int dtype, bool want_dx);
+XentPlan xent_plan(const VocabLayer& L, int vocab, int M, int dtype);
 struct XentBuffers {
   uint16_t* g;
   float *dxp, *u, *up, *dbp;

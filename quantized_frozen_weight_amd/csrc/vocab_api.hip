@@ -59,6 +59,53 @@ void add_vocab(Ranges& in, const qlora_linear* L, const void* ids, int M, int it
   in.add(ids, ids_bytes(M, itype));
 }
 
+// Workspace of the loss, and of its gradient.
+struct XentFwdLayout {
+  size_t xq, sx, t, rs, part, total;
+};
+XentFwdLayout xent_fwd_layout(const qlora_linear* L, int vocab, int M) {
+  XentFwdLayout w{};
+  size_t off = 0;
+  w.xq = off; off = align_up(off + (size_t)M * L->K);
+  w.sx = off; off = align_up(off + (size_t)M * 4);
+  w.t = off; off = align_up(off + (size_t)M * L->r * 4);
+  w.rs = off; off = align_up(off + row_split_floats(M, L->K, L->r > 0 ? L->r : 1) * 4);
+  w.part = off; off = align_up(off + xent_part_floats(L->fmt, vocab, M) * 4);
+  w.total = off;
+  return w;
+}
+struct XentBwdLayout {
+  XentPlan plan;
+  size_t xq, sx, t, rs, g, dxp, u, up, dbp, pA, total;
+};
+XentBwdLayout xent_bwd_layout(const qlora_linear* L, int vocab, int M, int dtype) {
+  XentBwdLayout w{};
+  w.plan = xent_plan(vocab_layer(L), vocab, M, dtype);
+  size_t off = 0;
+  w.xq = off; off = align_up(off + (size_t)M * L->K);
+  w.sx = off; off = align_up(off + (size_t)M * 4);
+  w.t = off; off = align_up(off + (size_t)M * L->r * 4);
+  w.rs = off; off = align_up(off + row_split_floats(M, L->K, L->r > 0 ? L->r : 1) * 4);
+  w.g = off; off = align_up(off + w.plan.g * 2);
+  w.dxp = off; off = align_up(off + w.plan.dxp * 4);
+  w.u = off; off = align_up(off + w.plan.u * 4);
+  w.up = off; off = align_up(off + w.plan.up * 4);
+  w.dbp = off; off = align_up(off + w.plan.dbp * 4);
+  w.pA = off; off = align_up(off + (L->r > 0 ? (size_t)skinny_nsplit_host(M) * L->r * L->K * 4 : 0));
+  w.total = off;
+  return w;
+}
+
+// The rows' codes and scales, and (t not NULL) t = x A.
+void enqueue_rows(const qlora_linear* L, int M, int dtype, const void* x, int8_t* xq, float* sx, float* t,
+                  float* rs, hipStream_t s) {
+  launch_rowquant(dtype, x, M, L->K, t != nullptr ? L->A : nullptr, t != nullptr ? L->r : 1, xq, sx, t, s, nullptr,
+                  rs);
+}
+
+// int32 sums of products of codes up to 127 and 128 stay exact
+inline bool exact_sums(const qlora_linear* L) { return L->fmt == QLORA_W4G128 || L->K <= 132096; }
+
 inline bool ws_ok(const void* ws, size_t have, size_t need) {
   return have >= need && (need == 0 || (ws != nullptr && aligned16(ws)));
 }
@@ -114,6 +161,106 @@ int qlora_embed_bwd(const qlora_linear* L, int vocab, int M, int dtype, const vo
   if (pending_error()) return QLORA_EHIP;
   launch_embed_bwd(vocab_layer(L), M, dtype, make_ids(tokens, itype, vocab), scale, dy, accumulate != 0, dA,
                    dB, ws, static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+int qlora_xent_fwd_workspace(const qlora_linear* L, int vocab, int M, int dtype, size_t* bytes) {
+  if (bytes == nullptr) return QLORA_EINVAL;
+  const int st = check_vocab(L, vocab, M, dtype);
+  if (st) return st;
+  if (!exact_sums(L)) return QLORA_EUNSUPPORTED;
+  *bytes = xent_fwd_layout(L, vocab, M).total;
+  return QLORA_OK;
+}
+
+int qlora_xent_fwd(const qlora_linear* L, int vocab, int M, int dtype, const void* x,
+                   const void* targets, int itype, float* loss, float* lse, float* t_save, void* ws,
+                   size_t ws_bytes, void* stream) {
+  size_t need = 0;
+  int st = qlora_xent_fwd_workspace(L, vocab, M, dtype, &need);
+  if (st) return st;
+  st = check_ids(targets, itype);
+  if (st) return st;
+  if (!x || !aligned16(x) || !loss || !aligned16(loss) || !lse || !aligned16(lse) || !opt16(t_save))
+    return QLORA_EINVAL;
+  if (t_save != nullptr && L->r < 1) return QLORA_EINVAL;
+  if (!ws_ok(ws, ws_bytes, need)) return QLORA_EWORKSPACE;
+  Ranges in, out;
+  add_vocab(in, L, targets, M, itype);
+  in.add(x, (size_t)M * L->K * dtype_bytes(dtype));
+  out.add(loss, (size_t)M * 4);
+  out.add(lse, (size_t)M * 4);
+  out.add(t_save, (size_t)M * L->r * 4);
+  out.add(ws, need);
+  if (!disjoint(out, in)) return QLORA_EINVAL;
+  if (pending_error()) return QLORA_EHIP;
+  const XentFwdLayout w = xent_fwd_layout(L, vocab, M);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  int8_t* xq = reinterpret_cast<int8_t*>(at(ws, w.xq));
+  float* sx = reinterpret_cast<float*>(at(ws, w.sx));
+  float* t = L->r < 1 ? nullptr : t_save != nullptr ? t_save : reinterpret_cast<float*>(at(ws, w.t));
+  enqueue_rows(L, M, dtype, x, xq, sx, t, reinterpret_cast<float*>(at(ws, w.rs)), s);
+  launch_xent_fwd(vocab_layer(L), M, make_ids(targets, itype, vocab), xq, sx, t,
+                  reinterpret_cast<float*>(at(ws, w.part)), loss, lse, s);
+  return launch_status();
+}
+
+int qlora_xent_bwd_workspace(const qlora_linear* L, int vocab, int M, int dtype, size_t* bytes) {
+  if (bytes == nullptr) return QLORA_EINVAL;
+  const int st = check_vocab(L, vocab, M, dtype);
+  if (st) return st;
+  if (!exact_sums(L)) return QLORA_EUNSUPPORTED;
+  *bytes = xent_bwd_layout(L, vocab, M, dtype).total;
+  return QLORA_OK;
+}
+
+int qlora_xent_bwd(const qlora_linear* L, int vocab, int M, int dtype, const void* x,
+                   const void* targets, int itype, const float* lse, const float* dloss,
+                   const float* t_saved, void* dx, float* dA, float* dB, void* ws, size_t ws_bytes,
+                   void* stream) {
+  size_t need = 0;
+  int st = qlora_xent_bwd_workspace(L, vocab, M, dtype, &need);
+  if (st) return st;
+  st = check_ids(targets, itype);
+  if (st) return st;
+  if (!x || !aligned16(x) || !lse || !aligned16(lse) || !dloss || !aligned16(dloss) || !opt16(t_saved) || !opt16(dx))
+    return QLORA_EINVAL;
+  if (L->r > 0 ? (!dA || !aligned16(dA) || !dB || !aligned16(dB)) : (dA || dB || t_saved || !dx)) return QLORA_EINVAL;
+  if (!ws_ok(ws, ws_bytes, need)) return QLORA_EWORKSPACE;
+  Ranges in, out;
+  add_vocab(in, L, targets, M, itype);
+  in.add(x, (size_t)M * L->K * dtype_bytes(dtype));
+  in.add(lse, (size_t)M * 4);
+  in.add(dloss, (size_t)M * 4);
+  in.add(t_saved, (size_t)M * L->r * 4);
+  out.add(dx, (size_t)M * L->K * dtype_bytes(dtype));
+  out.add(dA, (size_t)L->K * L->r * 4);
+  out.add(dB, (size_t)L->N * L->r * 4);
+  out.add(ws, need);
+  if (!disjoint(out, in)) return QLORA_EINVAL;
+  if (pending_error()) return QLORA_EHIP;
+  const XentBwdLayout w = xent_bwd_layout(L, vocab, M, dtype);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  int8_t* xq = reinterpret_cast<int8_t*>(at(ws, w.xq));
+  float* sx = reinterpret_cast<float*>(at(ws, w.sx));
+  float* tw = L->r < 1 || t_saved != nullptr ? nullptr : reinterpret_cast<float*>(at(ws, w.t));
+  enqueue_rows(L, M, dtype, x, xq, sx, tw, reinterpret_cast<float*>(at(ws, w.rs)), s);
+  const auto f = [&](size_t off) { return reinterpret_cast<float*>(at(ws, off)); };
+  const XentBuffers buf{reinterpret_cast<uint16_t*>(at(ws, w.g)), f(w.dxp), f(w.u), f(w.up), f(w.dbp)};
+  launch_xent_bwd(vocab_layer(L), M, dtype, make_ids(targets, itype, vocab), xq, sx, tw != nullptr ? tw : t_saved,
+                  lse, dloss, w.plan, buf, dx, dB, s);
+  if (L->r > 0) {
+    // dA = s x^T u, as the layers' own adapter gradients
+    SkinnyJobs sk{};
+    sk.njobs = 1;
+    sk.M = M; sk.r = L->r; sk.s = L->alpha / (float)L->r;
+    sk.nsplit = skinny_nsplit_host(M);
+    sk.rows_per_split = ((M + sk.nsplit - 1) / sk.nsplit + 3) / 4 * 4;
+    sk.P[0] = buf.u; sk.Q[0] = x; sk.C[0] = L->K; sk.out[0] = dA; sk.transpose[0] = 1;
+    sk.partial[0] = f(w.pA); sk.ncb[0] = (L->K + kSkCols - 1) / kSkCols; sk.hd0 = L->K;
+    launch_skinny_stage1(dtype, sk, s);
+    launch_skinny_stage2(sk, s);
+  }
   return launch_status();
 }
 
