@@ -627,6 +627,18 @@ int qlora_adamw_workspace(const qlora_adamw_item* items, int count, size_t* byte
 int qlora_adamw(const qlora_adamw_config* cfg, const qlora_adamw_item* items, int count, void* ws,
                 size_t ws_bytes, void* stream);
 
+/* Moments in 8 bits read as float32 or bf16 (both hold every value of the form
+ * exactly), and written from them, to the nearest code (halves up; a second
+ * moment that is not 0 to at least the smallest): to look at a state, to keep
+ * it, or to begin from one in float32. QLORA_MOMENT1: m; QLORA_MOMENT2: the root
+ * of v (not negative; a sign is not kept). 1 <= n <= 2^30, x and codes 16-byte
+ * aligned. */
+typedef enum { QLORA_MOMENT1 = 0, QLORA_MOMENT2 = 1 } qlora_moment;
+int qlora_moment_read(const uint8_t* codes, const uint8_t* scales, int64_t n, int which, int dtype, void* x,
+                      void* stream);
+int qlora_moment_write(const void* x, int64_t n, int which, int dtype, uint8_t* codes, uint8_t* scales,
+                       void* stream);
+
 /* Merge the trained adapter into the frozen int8 weight ("Parameter-efficient
  * fine-tuning of GPT-2 with LoRA", "Merge weights and generate text!": the
  * merged kernel is the frozen kernel plus the adapter product; "Introduce

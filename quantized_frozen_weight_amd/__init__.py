@@ -10,6 +10,6 @@ from .binding import (  # noqa: F401
     AdamW, Checkpoint, QLinear, QloraError, qlora_act_bwd, qlora_adamw, qlora_bwd, qlora_bwd_epi,
     qlora_bwd_epi_partial, qlora_bwd_workspace, qlora_ckpt_read,
     qlora_ckpt_write, qlora_embed, qlora_embed_bwd, qlora_fwd, qlora_fwd_acc, qlora_fwd_ckpt, qlora_fwd_epi,
-    qlora_fwd_workspace, qlora_quantize, qlora_quantize_rows,
+    qlora_fwd_workspace, qlora_moment_read, qlora_moment_write, qlora_quantize, qlora_quantize_rows,
     qlora_status_str, qlora_weight_bytes, qlora_xent_bwd, qlora_xent_fwd,
 )

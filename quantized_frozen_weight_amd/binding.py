@@ -28,6 +28,7 @@ _CFMT = {"c8row": 0, "c8g32": 1}                                         # qlora
 CKPT_GROUP = 32          # columns per scale of a "c8g32" checkpoint
 
 _SFMT = {"f32": 0, "s8": 1}                                              # qlora_sfmt
+_MOMENT = {"m": 0, "root_v": 1}                                          # qlora_moment
 S8_GROUP = 32            # elements per scale of an 8-bit moment
 
 _FMT = {"w8": QLORA_W8, "w4g128": QLORA_W4G128, "w8o": QLORA_W8O}
@@ -68,6 +69,7 @@ EXPORTS = (
     "qlora_act_bwd_workspace", "qlora_act_bwd", "qlora_embed", "qlora_embed_bwd_workspace",
     "qlora_embed_bwd", "qlora_adamw_workspace", "qlora_adamw",
     "qlora_xent_fwd_workspace", "qlora_xent_fwd", "qlora_xent_bwd_workspace", "qlora_xent_bwd",
+    "qlora_moment_read", "qlora_moment_write",
 )
 QLORA_NOALLOC_SCRATCH_BYTES = 16 << 20
 # include/qlora_probe.h: measurement probes (not part of the layer)
@@ -191,6 +193,8 @@ def lib() -> ctypes.CDLL:
     L.qlora_xent_fwd.argtypes = [plin, i, i, i, vp, vp, i, vp, vp, vp, vp, sz, vp]
     L.qlora_xent_bwd_workspace.argtypes = [plin, i, i, i, psz]
     L.qlora_xent_bwd.argtypes = [plin, i, i, i, vp, vp, i, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.qlora_moment_read.argtypes = [vp, vp, ctypes.c_int64, i, i, vp, vp]
+    L.qlora_moment_write.argtypes = [vp, ctypes.c_int64, i, i, vp, vp, vp]
     pitem = ctypes.POINTER(qlora_adamw_item)
     L.qlora_adamw_workspace.argtypes = [pitem, i, psz]
     L.qlora_adamw.argtypes = [ctypes.POINTER(qlora_adamw_config), pitem, i, vp, sz, vp]
@@ -1159,3 +1163,42 @@ def qlora_adamw(opt: AdamW, grads, lr, betas=(0.9, 0.999), eps: float = 1e-6, cl
     with _on(dev):
         _check(lib().qlora_adamw(ctypes.byref(c), items, len(items), _ptr(ws), ws.nbytes, _stream()), "qlora_adamw")
     return norm
+
+
+def qlora_moment_read(codes, scales, which: str, dtype=None, x=None):
+    """8-bit moments (codes uint8 [n], scales uint8 [ceil(n / 32)]) in dtype
+    (torch.float32 unless given, or torch.bfloat16; exact in both): which "m",
+    or "root_v", the root of the second."""
+    import torch
+    dev, n = codes.device, codes.numel()
+    if which not in _MOMENT:
+        raise ValueError(f"unknown moment {which!r}")
+    if codes.dim() != 1 or not codes.is_cuda:
+        raise ValueError("codes: a 1-D GPU tensor is needed")
+    _tensor(codes, "codes", (n,), torch.uint8, dev)
+    _tensor(scales, "scales", (-(-n // S8_GROUP),), torch.uint8, dev)
+    x = torch.empty((n,), dtype=torch.float32 if dtype is None else dtype, device=dev) if x is None else \
+        _tensor(x, "x", (n,), x.dtype if dtype is None else dtype, dev)
+    with _on(dev):
+        _check(lib().qlora_moment_read(_ptr(codes), _ptr(scales), n, _MOMENT[which], _dtype_code(x), _ptr(x),
+                                       _stream()), "qlora_moment_read")
+    return x
+
+
+def qlora_moment_write(x, which: str, codes=None, scales=None):
+    """x [n] (float32 or bf16) as 8-bit moments, to the nearest: (codes, scales)."""
+    import torch
+    if which not in _MOMENT:
+        raise ValueError(f"unknown moment {which!r}")
+    if x.dim() != 1 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x: a contiguous 1-D GPU tensor is needed")
+    dev, n = x.device, x.numel()
+    groups = -(-n // S8_GROUP)
+    u8 = torch.uint8
+    codes = torch.empty((n,), dtype=u8, device=dev) if codes is None else _tensor(codes, "codes", (n,), u8, dev)
+    scales = torch.empty((groups,), dtype=u8, device=dev) if scales is None else \
+        _tensor(scales, "scales", (groups,), u8, dev)
+    with _on(dev):
+        _check(lib().qlora_moment_write(_ptr(x), n, _MOMENT[which], _dtype_code(x), _ptr(codes), _ptr(scales),
+                                        _stream()), "qlora_moment_write")
+    return codes, scales

@@ -334,7 +334,108 @@ __global__ __launch_bounds__(256) void adamw_update_kernel(UpdateArgs a) {
   }
 }
 
+// 8-bit moments to float32 or bf16 (exact in both) and back (to the nearest
+// code, halves up): 8 elements a thread, 4 lanes a group. BITS: 4 the first
+// moment, 5 the root of the second.
+template <typename T, int BITS>
+__global__ __launch_bounds__(256) void moment_read_kernel(const uint8_t* codes, const uint8_t* scales, long n,
+                                                          typename Elem<T>::type* x) {
+  const long e = ((long)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (e >= n) return;
+  const int sb = scales[e / 32];
+  uint32_t w[2] = {0u, 0u};
+  if (e + 8 <= n) {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(codes + e);
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+    for (int c = 0; e + c < n; ++c) w[c / 4] |= (uint32_t)codes[e + c] << (8 * (c % 4));
+  }
+  float v[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const uint32_t b = (w[c / 4] >> (8 * (c % 4))) & 0xffu;
+    const float y = of_code<BITS>(BITS == 4 ? b & 127u : b, sb - 127);
+    v[c] = sb == 255 ? __uint_as_float(0x7fc00000u) : BITS == 4 && (b & 128u) ? -y : y;
+  }
+  if (e + 8 <= n) {
+    if constexpr (sizeof(x[0]) == 4) {
+      *reinterpret_cast<f32x4*>(x + e) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4*>(x + e + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+      *reinterpret_cast<u32x4*>(x + e) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    }
+  } else {
+    for (int c = 0; e + c < n; ++c) store_out(x + e + c, v[c]);
+  }
+}
+
+template <typename T, int BITS>
+__global__ __launch_bounds__(256) void moment_write_kernel(const typename Elem<T>::type* x, long n, uint8_t* codes,
+                                                           uint8_t* scales) {
+  const long e = ((long)blockIdx.x * 256 + threadIdx.x) * 8;
+  float v[8];
+  if (e + 8 <= n) {
+    load8(x + e, v);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      v[c] = 0.f;
+      if (e + c < n) {
+        if constexpr (sizeof(x[0]) == 4) v[c] = x[e + c];
+        else v[c] = bf16_to_f32(x[e + c]);
+      }
+    }
+  }
+  uint32_t top = 0u;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) top = abs_bits(v[c]) > top ? abs_bits(v[c]) : top;
+#pragma unroll
+  for (int lvl = 2; lvl < 4; ++lvl) {                       // the 4 lanes of the group
+    const uint32_t w = __float_as_uint(dpp_pair(__uint_as_float(top), lvl));
+    top = w > top ? w : top;
+  }
+  if (e >= n) return;
+  const bool bad = top >= 0x7f800000u;
+  const int ex = scale_exp<BITS>(top);
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    uint32_t k = to_code<BITS>(v[c], ex, 0x8000u);
+    if (BITS == 5) k = k == 0u && v[c] != 0.f ? 1u : k;
+    else k |= v[c] < 0.f ? 128u : 0u;
+    w[c / 4] |= (bad ? 0u : k) << (8 * (c % 4));
+  }
+  if (e + 8 <= n) *reinterpret_cast<u32x2*>(codes + e) = u32x2{w[0], w[1]};
+  else
+    for (int c = 0; e + c < n; ++c) codes[e + c] = (uint8_t)(w[c / 4] >> (8 * (c % 4)));
+  if ((e & 31) == 0) scales[e / 32] = (uint8_t)(bad ? 255 : ex + 127);
+}
+
 }  // namespace
+
+void launch_moment_read(const uint8_t* codes, const uint8_t* scales, long n, int which, int dtype, void* x,
+                        hipStream_t st) {
+  const dim3 grid((unsigned)((n + 2047) / 2048));
+  float* f = static_cast<float*>(x);
+  uint16_t* h = static_cast<uint16_t*>(x);
+  if (which == 0 && dtype == 0) moment_read_kernel<F32, 4><<<grid, 256, 0, st>>>(codes, scales, n, f);
+  else if (which == 0) moment_read_kernel<BF16, 4><<<grid, 256, 0, st>>>(codes, scales, n, h);
+  else if (dtype == 0) moment_read_kernel<F32, 5><<<grid, 256, 0, st>>>(codes, scales, n, f);
+  else moment_read_kernel<BF16, 5><<<grid, 256, 0, st>>>(codes, scales, n, h);
+}
+
+void launch_moment_write(const void* x, long n, int which, int dtype, uint8_t* codes, uint8_t* scales,
+                         hipStream_t st) {
+  const dim3 grid((unsigned)((n + 2047) / 2048));
+  const float* f = static_cast<const float*>(x);
+  const uint16_t* h = static_cast<const uint16_t*>(x);
+  if (which == 0 && dtype == 0) moment_write_kernel<F32, 4><<<grid, 256, 0, st>>>(f, n, codes, scales);
+  else if (which == 0) moment_write_kernel<BF16, 4><<<grid, 256, 0, st>>>(h, n, codes, scales);
+  else if (dtype == 0) moment_write_kernel<F32, 5><<<grid, 256, 0, st>>>(f, n, codes, scales);
+  else moment_write_kernel<BF16, 5><<<grid, 256, 0, st>>>(h, n, codes, scales);
+}
 
 long adamw_norm_blocks(const qlora_adamw_item* items, int count, long* chunk) {
   long total = 0, blocks = 0;

@@ -316,4 +316,42 @@ int qlora_adamw(const qlora_adamw_config* cfg, const qlora_adamw_item* items, in
   return launch_status();
 }
 
+namespace {
+int check_moment(const void* x, const void* codes, const void* scales, int64_t n, int which, int dtype) {
+  const int st = check_dtype(dtype);
+  if (st) return st;
+  if (n < 1 || (which != QLORA_MOMENT1 && which != QLORA_MOMENT2)) return QLORA_EINVAL;
+  if (n > (1LL << 30)) return QLORA_ERANGE;
+  return x && aligned16(x) && codes && aligned16(codes) && scales ? QLORA_OK : QLORA_EINVAL;
+}
+}  // namespace
+
+int qlora_moment_read(const uint8_t* codes, const uint8_t* scales, int64_t n, int which, int dtype, void* x,
+                      void* stream) {
+  const int st = check_moment(x, codes, scales, n, which, dtype);
+  if (st) return st;
+  Ranges in, out;
+  in.add(codes, (size_t)n);
+  in.add(scales, (size_t)(n + 31) / 32);
+  out.add(x, (size_t)n * dtype_bytes(dtype));
+  if (!disjoint(out, in)) return QLORA_EINVAL;
+  if (pending_error()) return QLORA_EHIP;
+  launch_moment_read(codes, scales, n, which, dtype, x, static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
+int qlora_moment_write(const void* x, int64_t n, int which, int dtype, uint8_t* codes, uint8_t* scales,
+                       void* stream) {
+  const int st = check_moment(x, codes, scales, n, which, dtype);
+  if (st) return st;
+  Ranges in, out;
+  in.add(x, (size_t)n * dtype_bytes(dtype));
+  out.add(codes, (size_t)n);
+  out.add(scales, (size_t)(n + 31) / 32);
+  if (!disjoint(out, in)) return QLORA_EINVAL;
+  if (pending_error()) return QLORA_EHIP;
+  launch_moment_write(x, n, which, dtype, codes, scales, static_cast<hipStream_t>(stream));
+  return launch_status();
+}
+
 }  // extern "C"
