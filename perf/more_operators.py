@@ -397,7 +397,11 @@ def _run_own(st):
             st["grads"] = parts(st["g"])
         norm = Q.qlora_adamw(st["optimizer"], st["grads"], lr=st["lr"], betas=st["betas"], eps=st["eps"],
                              clip_norm=st["clip"], need_norm=True)
-        moments = _moments(st) if eight else dict(m=st["m"], v=st["v"])
+        moments = dict(m=st["m"], v=st["v"])
+        if eight:
+            # what the codes stand for, as a program that looks at its state reads it
+            moments = dict(m=Q.qlora_moment_read(st["m"], st["m_scales"], "m", torch.bfloat16),
+                           root_v=Q.qlora_moment_read(st["v"], st["v_scales"], "root_v", torch.bfloat16))
         return dict(p=st["p"], norm=norm.reshape(()), step=st["step"], **moments)
     layer = Q.QLinear(case["K"], st["N"], case["r"], st["alpha"], case["fmt"], st["codes"], st["scales"], st["A"], st["B"])
     V = case["vocab"]
