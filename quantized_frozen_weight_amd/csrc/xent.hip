@@ -71,17 +71,50 @@ struct LogitArgs {
   float* dbp;            // [tiles_m][r][ldg]
 };
 
-// Maximum and sum over the 16 lanes that hold one row of a 16 x 16 block.
-__device__ __forceinline__ float row16_max(float v) {
-#pragma unroll
-  for (int lvl = 0; lvl < 4; ++lvl) v = fmaxf(v, dpp_pair(v, lvl));
-  return v;
+// Maximum and sum over the four lanes that hold one row of a transposed block
+// (lanes l, l + 16, l + 32, l + 48); every one of them ends with the result.
+__device__ __forceinline__ float quad_max(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const auto s32 = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  v = fmaxf(__uint_as_float(s32[0]), __uint_as_float(s32[1]));
+  const uint32_t c = __float_as_uint(v);
+  const auto s16 = __builtin_amdgcn_permlane16_swap(c, c, false, false);
+  return fmaxf(__uint_as_float(s16[0]), __uint_as_float(s16[1]));
 }
-__device__ __forceinline__ float row16_sum(float v) {
-#pragma unroll
-  for (int lvl = 0; lvl < 4; ++lvl) v += dpp_pair(v, lvl);
-  return v;
+__device__ __forceinline__ float quad_sum(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const auto s32 = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  v = __uint_as_float(s32[0]) + __uint_as_float(s32[1]);
+  const uint32_t c = __float_as_uint(v);
+  const auto s16 = __builtin_amdgcn_permlane16_swap(c, c, false, false);
+  return __uint_as_float(s16[0]) + __uint_as_float(s16[1]);
 }
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ uint32_t pk_f16(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, f16x2));
+}
+
+// Four values as bf16 (packed), and what that leaves of them (0 of an infinity
+// or a NaN, whose first part is all).
+__device__ __forceinline__ u32x2 bf16_part(float (&v)[4]) {
+  u32x2 h;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    h[e] = pk_bf16(v[2 * e], v[2 * e + 1]);
+    const bool fa = (h[e] & 0x7f80u) != 0x7f80u, fb = (h[e] & 0x7f800000u) != 0x7f800000u;
+    v[2 * e] = fa ? v[2 * e] - __uint_as_float(h[e] << 16) : 0.f;
+    v[2 * e + 1] = fb ? v[2 * e + 1] - __uint_as_float(h[e] & 0xffff0000u) : 0.f;
+  }
+  return h;
+}
+
+// 4-bit weights: dl travels as float16 of 2^14 (p - [target]), without dloss,
+// and W as float16 of W / 8 (7 times the largest scale then fits): 11 bits of
+// each, where bf16 has 8. What is left to the rows' factor:
+constexpr float kHalfUp = 16384.f, kHalfDown = 8.f / 16384.f;
 
 constexpr int max_int(int a, int b) { return a > b ? a : b; }
 
@@ -95,13 +128,16 @@ struct LogitLds {
   static constexpr int ASZ = BM * 128, STG = ASZ + BN * (W4 ? 64 : 128);
   static constexpr int SLAB = W4 ? BN * G * 2 : 0;
   static constexpr int QP = BN + 4;                       // pitch of B's rows
-  static constexpr int TS = 0, QS = TS + BM * R * 4, SX = QS + R * QP * 4, SW = SX + BM * 4;
-  static constexpr int TG = SW + BN * 4, LS = TG + BM * 4, GM = LS + BM * 4, END = GM + BM * 4;
+  static constexpr int TS = 0, QS = TS + BM * R * 4, RS = QS + R * QP * 4, SW = RS + BM * 4;
+  static constexpr int TG = SW + BN * 4, LS = TG + BM * 4, END = LS + BM * 4;
   static constexpr int RED = WN * BM * 8;                 // loss: the waves' maxima and sums
-  static constexpr int PITCH = FN * 32 + 16, FPITCH = FN * 16 + 4;
-  static constexpr int STRIP = R > 0 ? max_int(16 * PITCH, 16 * FPITCH * 4) : 16 * PITCH;
-  static constexpr int UB = END + NW * STRIP;             // u [BM][R], dB [R][BN]
-  static constexpr int EPI = GRAD ? UB + (BM + BN) * R * 4 : END + RED;
+  // gradient: t dloss in two bf16 parts [2][R][TP]; a wave's strip of 16 rows of
+  // dl, and its two parts of 32 rows for dB (afterwards u [BM][R] and dB [R][BN])
+  static constexpr int TP = BM + 8, TB = END, PITCH = FN * 32 + 16;
+  static constexpr int ST = TB + (GRAD ? 2 * R * TP * 2 : 0), STRIP = 16 * PITCH;
+  static constexpr int PV = ST + NW * STRIP, PVB = 32 * PITCH;
+  static constexpr int SUMS = (BM + BN) * R * 4;
+  static constexpr int EPI = GRAD ? PV + (R > 0 ? max_int(NW * 2 * PVB, SUMS) : 0) : END + RED;
   static constexpr int BYTES = max_int(S * STG + SLAB, EPI);
   static_assert(BYTES <= 160 * 1024, "LDS of a block");
 };
@@ -132,17 +168,15 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
   // the epilogue's operands into registers, consumed after the loop
   constexpr int RT = (BM + NT - 1) / NT, CT = (BN + NT - 1) / NT;
   constexpr int NTS = (BM * R + NT - 1) / NT, NQS = (BN * R + NT - 1) / NT;
-  float esx[RT], else_[RT], egm[RT], esw[CT], ets[NTS > 0 ? NTS : 1], eqs[NQS > 0 ? NQS : 1];
-  int etg[RT];
+  constexpr int NTA = NTS > 0 ? NTS : 1;
+  float esx[RT], else_[RT], esw[CT], ets[NTA], egm[NTA], eqs[NQS > 0 ? NQS : 1];
+  int etg[RT], etr[NTA];                                   // targets, by row and by element of t
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     const int row = tid + NT * i, gm = m0 + row < M ? m0 + row : M - 1;
     esx[i] = a.sx[gm];
     etg[i] = row < BM && m0 + row < M ? entry_of(a.ids, gm) : -1;
-    if constexpr (GRAD) {
-      else_[i] = a.lse[gm];
-      egm[i] = a.dloss[gm];
-    }
+    if constexpr (GRAD) else_[i] = a.lse[gm];
   }
   if constexpr (!W4) {
 #pragma unroll
@@ -154,8 +188,12 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
   if constexpr (R > 0) {
 #pragma unroll
     for (int i = 0; i < NTS; ++i) {
-      const int e = tid + NT * i, gm = m0 + e / R, j = e % R;
-      ets[i] = a.t[(long)(gm < M ? gm : M - 1) * a.r + (j < a.r ? j : 0)];
+      const int e = tid + NT * i, j = e % R, gm = m0 + e / R < M ? m0 + e / R : M - 1;
+      ets[i] = a.t[(long)gm * a.r + (j < a.r ? j : 0)];
+      if constexpr (GRAD) {
+        etr[i] = entry_of(a.ids, gm);
+        egm[i] = a.dloss[gm];
+      }
     }
 #pragma unroll
     for (int i = 0; i < NQS; ++i) {
@@ -260,54 +298,67 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
       for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-          if constexpr (W4) part[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[i], bf[j], part[i][j], 0, 0, 0);
-          else acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[i], bf[j], acc[i][j], 0, 0, 0);
+          // transposed: lane l holds row l of the block, entries 4 q .. 4 q + 3
+          if constexpr (W4) part[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[j], af[i], part[i][j], 0, 0, 0);
+          else acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[j], af[i], acc[i][j], 0, 0, 0);
         }
     }
     if constexpr (W4) {
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        const float sc = (float)SC[((wn * FN + j) * 16 + l) * ngrp + kt];
+        float sc[4];
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) sc[ii] = (float)SC[((wn * FN + j) * 16 + 4 * q + ii) * ngrp + kt];
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
           for (int ii = 0; ii < 4; ++ii)
-            acc[i][j][ii] = __builtin_fmaf((float)part[i][j][ii], sc, acc[i][j][ii]);
+            acc[i][j][ii] = __builtin_fmaf((float)part[i][j][ii], sc[ii], acc[i][j][ii]);
       }
     }
     slot = slot == S - 1 ? 0 : slot + 1;
   }
 
   __syncthreads();                                         // every wave is done with the ring
-  float* ts = reinterpret_cast<float*>(lds + Lds::TS);
-  float* qs = reinterpret_cast<float*>(lds + Lds::QS);
-  float* sxv = reinterpret_cast<float*>(lds + Lds::SX);
+  float* ts = reinterpret_cast<float*>(lds + Lds::TS);     // s log2e t
+  float* qs = reinterpret_cast<float*>(lds + Lds::QS);     // B
+  float* rsv = reinterpret_cast<float*>(lds + Lds::RS);    // log2e sx
   float* swv = reinterpret_cast<float*>(lds + Lds::SW);
-  int* tgv = reinterpret_cast<int*>(lds + Lds::TG);
-  float* lsv = reinterpret_cast<float*>(lds + Lds::LS);
-  float* gmv = reinterpret_cast<float*>(lds + Lds::GM);
+  int* tgv = reinterpret_cast<int*>(lds + Lds::TG);        // the target's column here; INT32_MIN: none
+  float* lsv = reinterpret_cast<float*>(lds + Lds::LS);    // log2e lse
+  uint16_t* tb = reinterpret_cast<uint16_t*>(lds + Lds::TB);
+  // Gradient: a row without a target has logits 0 and lse infinite, so that its
+  // p is 0 whatever its codes' scale is.
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     const int row = tid + NT * i;
     if (row < BM) {
-      sxv[row] = esx[i];
-      tgv[row] = etg[i] >= 0 ? etg[i] - n0 : INT32_MIN;    // the target's column here; INT32_MIN: none
-      if constexpr (GRAD) {
-        lsv[row] = else_[i] * kLog2e;
-        gmv[row] = egm[i];
-      }
+      const bool none = GRAD && etg[i] < 0;
+      rsv[row] = none ? 0.f : esx[i] * kLog2e;
+      tgv[row] = etg[i] >= 0 ? etg[i] - n0 : INT32_MIN;
+      if constexpr (GRAD) lsv[row] = none ? INFINITY : else_[i] * kLog2e;
     }
   }
   if constexpr (!W4) {
 #pragma unroll
     for (int i = 0; i < CT; ++i)
-      if (tid + NT * i < BN) swv[tid + NT * i] = esw[i];
+      if (tid + NT * i < BN) swv[tid + NT * i] = n0 + tid + NT * i < a.V ? esw[i] : 0.f;
   }
   if constexpr (R > 0) {
 #pragma unroll
     for (int i = 0; i < NTS; ++i) {
-      const int e = tid + NT * i;
-      if (e < BM * R) ts[e] = e % R < a.r && m0 + e / R < M ? ets[i] : 0.f;
+      const int e = tid + NT * i, row = e / R, j = e % R;
+      if (e < BM * R) {
+        const bool in = j < a.r && m0 + row < M && !(GRAD && etr[i] < 0);
+        ts[e] = in ? ets[i] * (a.s * kLog2e) : 0.f;
+        if constexpr (GRAD) {
+          float v = in ? ets[i] * egm[i] : 0.f;
+          const uint32_t h = f32_to_bf16(v);
+          v = (h & 0x7f80u) != 0x7f80u ? v - bf16_to_f32(h) : 0.f;
+          tb[j * Lds::TP + row] = (uint16_t)h;
+          tb[(R + j) * Lds::TP + row] = (uint16_t)f32_to_bf16(v);
+        }
+      }
     }
 #pragma unroll
     for (int i = 0; i < NQS; ++i) {
@@ -318,144 +369,212 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
   __syncthreads();
 
   const int wr0 = wm * FM * 16, wc0 = wn * FN * 16;
+  const bool ragged = n0 + wc0 + FN * 16 > a.V;            // wave-uniform: some columns are no entries
   constexpr int RB = (R + 15) / 16, RBA = RB > 0 ? RB : 1;
-  f32x4 uacc[GRAD && R > 0 ? FM : 1][RBA], dbacc[GRAD && R > 0 ? FN : 1][RBA];
-  if constexpr (GRAD && R > 0) {
+  constexpr bool ADAPT = GRAD && R > 0;
+  f32x4 sw[FN];
 #pragma unroll
-    for (int j = 0; j < RB; ++j) {
+  for (int j = 0; j < FN; ++j)
+    sw[j] = W4 ? f32x4{1.f, 1.f, 1.f, 1.f} : *reinterpret_cast<const f32x4*>(swv + wc0 + j * 16 + 4 * q);
+
+  // u's operand, B of two column blocks (32 entries in the order in which a lane
+  // holds them), in two bf16 parts
+  constexpr int NP = FN / 2;
+  static_assert(FN % 2 == 0 && FM % 2 == 0, "blocks are taken in pairs");
+  u32x4 bh[ADAPT ? NP : 1][RBA], bl[ADAPT ? NP : 1][RBA];
+  f32x4 uacc[ADAPT ? FM : 1][RBA], dbacc[ADAPT ? FN : 1][RBA];
+  if constexpr (ADAPT) {
 #pragma unroll
-      for (int i = 0; i < FM; ++i) uacc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int jb = 0; jb < RB; ++jb) {
+      const int rank = 16 * jb + l;
 #pragma unroll
-      for (int i = 0; i < FN; ++i) dbacc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int p = 0; p < NP; ++p)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const f32x4 b4 = *reinterpret_cast<const f32x4*>(qs + (rank < R ? rank : 0) * Lds::QP + wc0 + 32 * p + 16 * h + 4 * q);
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = rank < R ? b4[e] : 0.f;
+          const u32x2 hi = bf16_part(v);
+          bh[p][jb][2 * h] = hi.x;
+          bh[p][jb][2 * h + 1] = hi.y;
+          bl[p][jb][2 * h] = pk_bf16(v[0], v[1]);
+          bl[p][jb][2 * h + 1] = pk_bf16(v[2], v[3]);
+        }
+#pragma unroll
+      for (int i = 0; i < FM; ++i) uacc[i][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < FN; ++i) dbacc[i][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
   }
-  int8_t* strip = lds + Lds::END + wid * Lds::STRIP;
+  int8_t* strip = lds + Lds::ST + wid * Lds::STRIP;
+  int8_t* pv = lds + Lds::PV + wid * 2 * Lds::PVB;
 
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const int r0 = wr0 + i * 16 + 4 * q;                   // the lane's four rows
+    const int row = wr0 + i * 16 + l;                      // the lane's row of the tile
+    const float rs = rsv[row];
+    const int tg = tgv[row] - wc0;                         // its target among the wave's columns
+    const bool hit = __builtin_amdgcn_ballot_w64(tg >= 0 && tg < FN * 16) != 0;
+    const float base = GRAD ? -lsv[row] : 0.f;
+    // x: logits in powers of two (gradient: minus lse)
+    float x[FN][4];
     f32x4 lo[FN];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) lo[j] = f32x4{0.f, 0.f, 0.f, 0.f};
     if constexpr (R > 0) {
 #pragma unroll
+      for (int j = 0; j < FN; ++j) lo[j] = f32x4{base, base, base, base};
+#pragma unroll
       for (int kc = 0; kc < R / 4; ++kc) {
-        const float ta = ts[(wr0 + i * 16 + l) * R + kc * 4 + q];
+        const float tv = ts[row * R + kc * 4 + q];
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-          lo[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(ta, qs[(kc * 4 + q) * Lds::QP + wc0 + j * 16 + l], lo[j], 0, 0, 0);
+          lo[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(qs[(kc * 4 + q) * Lds::QP + wc0 + j * 16 + l], tv, lo[j], 0, 0, 0);
       }
     }
-    const f32x4 sx4 = *reinterpret_cast<const f32x4*>(sxv + r0);
-    const i32x4 tg4 = *reinterpret_cast<const i32x4*>(tgv + r0);
-    f32x4 v[FN];                                           // the logits
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const float sw = W4 ? 1.f : swv[wc0 + j * 16 + l];
+    for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int ii = 0; ii < 4; ++ii) {
-        const float base = (float)acc[i][j][ii] * (W4 ? sx4[ii] : sx4[ii] * sw);
-        v[j][ii] = R > 0 ? __builtin_fmaf(a.s, lo[j][ii], base) : base;
+        const float t = W4 ? (float)acc[i][j][ii] : (float)acc[i][j][ii] * sw[j][ii];
+        x[j][ii] = R > 0 ? __builtin_fmaf(rs, t, lo[j][ii]) : GRAD ? __builtin_fmaf(rs, t, base) : rs * t;
       }
-    }
     if constexpr (!GRAD) {
       float* red = reinterpret_cast<float*>(lds + Lds::END);      // [WN][BM] pairs
+      if (hit) {
 #pragma unroll
-      for (int ii = 0; ii < 4; ++ii) {
-        float mx = -INFINITY;
+        for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          const int c = wc0 + j * 16 + l;
-          const float x = v[j][ii];
-          if (c == tg4[ii]) a.tl[m0 + r0 + ii] = x;        // (a row past M has no target)
-          v[j][ii] = n0 + c < a.V ? x * kLog2e : -INFINITY;
-          mx = fmaxf(mx, v[j][ii]);
-        }
-        mx = row16_max(mx);
-        const float ref = mx == -INFINITY ? 0.f : mx;      // (no column here)
-        float sum = 0.f;
+          for (int ii = 0; ii < 4; ++ii)
+            if (j * 16 + 4 * q + ii == tg) a.tl[m0 + row] = x[j][ii];   // (a row past M has no target)
+      }
+      if (ragged) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) sum += __builtin_amdgcn_exp2f(v[j][ii] - ref);
-        sum = row16_sum(sum);
-        if (l == 0) {
-          red[2 * (wn * BM + r0 + ii)] = mx;
-          red[2 * (wn * BM + r0 + ii) + 1] = sum;
-        }
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int ii = 0; ii < 4; ++ii)
+            if (n0 + wc0 + j * 16 + 4 * q + ii >= a.V) x[j][ii] = -INFINITY;
+      }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        mx = fmaxf(mx, fmaxf(fmaxf(x[j][0], x[j][1]), fmaxf(x[j][2], x[j][3])));
+      mx = quad_max(mx);
+      const float ref = mx == -INFINITY ? 0.f : mx;        // (no entry here)
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        sum += (__builtin_amdgcn_exp2f(x[j][0] - ref) + __builtin_amdgcn_exp2f(x[j][1] - ref)) +
+               (__builtin_amdgcn_exp2f(x[j][2] - ref) + __builtin_amdgcn_exp2f(x[j][3] - ref));
+      sum = quad_sum(sum);
+      if (q == 0) {
+        red[2 * (wn * BM + row)] = mx;
+        red[2 * (wn * BM + row) + 1] = sum;
       }
     } else {
-      const f32x4 ls4 = *reinterpret_cast<const f32x4*>(lsv + r0);
-      const f32x4 gm4 = *reinterpret_cast<const f32x4*>(gmv + r0);
+      // p - [target], without dloss (the rows' factor, applied where rows end)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int c = wc0 + j * 16 + l;
-        const bool in = n0 + c < a.V;
+      for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int ii = 0; ii < 4; ++ii) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(v[j][ii], kLog2e, -ls4[ii]));
-          const float d = gm4[ii] * (c == tg4[ii] ? p - 1.f : p);
-          v[j][ii] = in && tg4[ii] != INT32_MIN ? d : 0.f;
-        }
-      }
-      if constexpr (R > 0) {
-        // dB: D[rank][column] += t^T dl, step ii over rows 4 q + ii
-#pragma unroll
-        for (int ii = 0; ii < 4; ++ii)
-#pragma unroll
-          for (int jb = 0; jb < RB; ++jb) {
-            const float ta = 16 * jb + l < R ? ts[(r0 + ii) * R + (16 * jb + l < R ? 16 * jb + l : 0)] : 0.f;
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-              dbacc[j][jb] = __builtin_amdgcn_mfma_f32_16x16x4f32(ta, v[j][ii], dbacc[j][jb], 0, 0, 0);
-          }
-        // u: dl from the strip as the A operand (row l, columns 4 c + q)
-        float* fs = reinterpret_cast<float*>(strip);
+        for (int ii = 0; ii < 4; ++ii) x[j][ii] = __builtin_amdgcn_exp2f(x[j][ii]);
+      if (hit) {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int ii = 0; ii < 4; ++ii) fs[(4 * q + ii) * Lds::FPITCH + j * 16 + l] = v[j][ii];
-#pragma unroll
-        for (int c = 0; c < FN * 4; ++c) {
-          const float da = fs[l * Lds::FPITCH + 4 * c + q];
-#pragma unroll
-          for (int jb = 0; jb < RB; ++jb) {
-            const int j = 16 * jb + l;
-            const float bv = j < R ? qs[(j < R ? j : 0) * Lds::QP + wc0 + 4 * c + q] : 0.f;
-            uacc[i][jb] = __builtin_amdgcn_mfma_f32_16x16x4f32(da, bv, uacc[i][jb], 0, 0, 0);
-          }
-        }
+          for (int ii = 0; ii < 4; ++ii)
+            if (j * 16 + 4 * q + ii == tg) x[j][ii] -= 1.f;
       }
-      if constexpr (!W4) {
+      if (ragged) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int ii = 0; ii < 4; ++ii)
+            if (n0 + wc0 + j * 16 + 4 * q + ii >= a.V) x[j][ii] = 0.f;
+      }
+      if constexpr (ADAPT) {
+        u32x2 ph[FN], pl[FN];
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-          const float sw = swv[wc0 + j * 16 + l];
-          const bool in = n0 + wc0 + j * 16 + l < a.V;
+          float v[4] = {x[j][0], x[j][1], x[j][2], x[j][3]};
+          ph[j] = bf16_part(v);
+          pl[j] = u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+          *reinterpret_cast<u32x2*>(pv + ((i & 1) * 16 + l) * Lds::PITCH + j * 32 + q * 8) = ph[j];
+          *reinterpret_cast<u32x2*>(pv + Lds::PVB + ((i & 1) * 16 + l) * Lds::PITCH + j * 32 + q * 8) = pl[j];
+        }
+        // u^T [rank][row] += B dl^T: the lane's own values are the operand
 #pragma unroll
-          for (int ii = 0; ii < 4; ++ii) v[j][ii] = in && tg4[ii] != INT32_MIN ? v[j][ii] * sw : 0.f;
+        for (int p = 0; p < NP; ++p) {
+          const bf16x8 vh = __builtin_bit_cast(bf16x8, u32x4{ph[2 * p].x, ph[2 * p].y, ph[2 * p + 1].x, ph[2 * p + 1].y});
+          const bf16x8 vl = __builtin_bit_cast(bf16x8, u32x4{pl[2 * p].x, pl[2 * p].y, pl[2 * p + 1].x, pl[2 * p + 1].y});
+#pragma unroll
+          for (int jb = 0; jb < RB; ++jb) {
+            const bf16x8 wh = __builtin_bit_cast(bf16x8, bh[p][jb]), wl = __builtin_bit_cast(bf16x8, bl[p][jb]);
+            uacc[i][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wl, vh, uacc[i][jb], 0, 0, 0);
+            uacc[i][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wh, vl, uacc[i][jb], 0, 0, 0);
+            uacc[i][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wh, vh, uacc[i][jb], 0, 0, 0);
+          }
+        }
+        if (i & 1) {
+          // dB^T [entry][rank] += dl^T (t dloss) over the last 32 rows, dl^T by
+          // transposing reads (in each 16-lane group lanes 4 i + p fetch the 4
+          // columns at 4 p of row i, lane k receives column k of rows 0..3)
+          asm volatile("" ::: "memory");
+          const int i4 = l >> 2, p4 = l & 3;
+          bf16x8 th[RBA], tl2[RBA];
+#pragma unroll
+          for (int jb = 0; jb < RB; ++jb) {
+            const int rank = 16 * jb + l, rc = rank < R ? rank : 0;
+            const uint16_t* tp = tb + rc * Lds::TP + wr0 + (i - 1) * 16 + 8 * q;
+            u32x4 x0 = *reinterpret_cast<const u32x4*>(tp), x1 = *reinterpret_cast<const u32x4*>(tp + R * Lds::TP);
+            if (rank >= R) x0 = x1 = u32x4{0u, 0u, 0u, 0u};
+            th[jb] = __builtin_bit_cast(bf16x8, x0);
+            tl2[jb] = __builtin_bit_cast(bf16x8, x1);
+          }
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            uint32_t ad[4];
+            uint64_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)                    // parts, halves of 8 rows
+              ad[e] = lds_addr(pv + (e >> 1) * Lds::PVB + (8 * q + 4 * (e & 1) + i4) * Lds::PITCH + j * 32 + p4 * 8);
+            tr16_reads<4>(ad, v);
+            const bf16x8 dh = __builtin_bit_cast(bf16x8, u32x4{(uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1],
+                                                               (uint32_t)(v[1] >> 32)});
+            const bf16x8 dl = __builtin_bit_cast(bf16x8, u32x4{(uint32_t)v[2], (uint32_t)(v[2] >> 32), (uint32_t)v[3],
+                                                               (uint32_t)(v[3] >> 32)});
+#pragma unroll
+            for (int jb = 0; jb < RB; ++jb) {
+              dbacc[j][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dl, th[jb], dbacc[j][jb], 0, 0, 0);
+              dbacc[j][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dh, tl2[jb], dbacc[j][jb], 0, 0, 0);
+              dbacc[j][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dh, th[jb], dbacc[j][jb], 0, 0, 0);
+            }
+          }
         }
       }
-      // (the strip is read as float above and written as bf16 below: in this order)
-      asm volatile("" ::: "memory");
-      for (int p = 0; p < a.parts; ++p) {
-        // one 16-row strip in bf16 through LDS (this wave's own: no wait), what
-        // is left of the values to the next part
+      // dl to memory: one 16-row strip at a time through LDS (this wave's own: no
+      // wait), float32 dl as bf16 parts, what one leaves to the next
+      if constexpr (!W4) {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int ii = 0; ii < 4; ++ii) {
-            const uint32_t h = f32_to_bf16(v[j][ii]);
-            reinterpret_cast<uint16_t*>(strip + (4 * q + ii) * Lds::PITCH)[j * 16 + l] = (uint16_t)h;
-            // (of an infinity or a NaN the first part is all)
-            v[j][ii] = (h & 0x7f80u) == 0x7f80u ? 0.f : v[j][ii] - bf16_to_f32(h);
-          }
+          for (int ii = 0; ii < 4; ++ii) x[j][ii] *= sw[j][ii];
+      }
+      for (int p = 0; p < a.parts; ++p) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          u32x2 w;
+          if constexpr (W4) w = u32x2{pk_f16(x[j][0] * kHalfUp, x[j][1] * kHalfUp), pk_f16(x[j][2] * kHalfUp, x[j][3] * kHalfUp)};
+          else if (a.parts == 1) w = u32x2{pk_bf16(x[j][0], x[j][1]), pk_bf16(x[j][2], x[j][3])};
+          else w = bf16_part(x[j]);
+          *reinterpret_cast<u32x2*>(strip + l * Lds::PITCH + j * 32 + q * 8) = w;
+        }
 #pragma unroll
         for (int e = 0; e < FN / 2; ++e) {
-          const int u = lane + 64 * e, row = u / (FN * 2), cq = u % (FN * 2);
-          const int m = m0 + wr0 + i * 16 + row;
-          const u32x4 w = *reinterpret_cast<const u32x4*>(strip + row * Lds::PITCH + cq * 16);
+          const int u = lane + 64 * e, sr = u / (FN * 2), cq = u % (FN * 2);
+          const int m = m0 + wr0 + i * 16 + sr;
+          const u32x4 w = *reinterpret_cast<const u32x4*>(strip + sr * Lds::PITCH + cq * 16);
           if (m < M)
             *reinterpret_cast<u32x4*>(a.g + p * a.gstride + m * a.ldg + c0 + wc0 + cq * 8) = w;
         }
-        asm volatile("" ::: "memory");
       }
     }
   }
@@ -480,9 +599,10 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
       }
     }
   }
-  if constexpr (GRAD && R > 0) {
+  if constexpr (ADAPT) {
     // the tile's u and dB: the waves' sums added in order
-    float* ub = reinterpret_cast<float*>(lds + Lds::UB);
+    __syncthreads();                                       // the strips are read
+    float* ub = reinterpret_cast<float*>(lds + Lds::PV);
     float* db = ub + BM * R;
     for (int w = 0; w < max_int(WM, WN); ++w) {
       if (wn == w) {
@@ -492,9 +612,9 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
           for (int jb = 0; jb < RB; ++jb)
 #pragma unroll
             for (int ii = 0; ii < 4; ++ii) {
-              const int j = 16 * jb + l;
-              float* p = ub + (wr0 + i * 16 + 4 * q + ii) * R + j;
-              if (j < R) *p = w == 0 ? uacc[i][jb][ii] : *p + uacc[i][jb][ii];
+              const int rank = 16 * jb + 4 * q + ii;
+              float* p = ub + (wr0 + i * 16 + l) * R + rank;
+              if (rank < R) *p = w == 0 ? uacc[i][jb][ii] : *p + uacc[i][jb][ii];
             }
       }
       if (wm == w) {
@@ -504,8 +624,8 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
           for (int jb = 0; jb < RB; ++jb)
 #pragma unroll
             for (int ii = 0; ii < 4; ++ii) {
-              const int rank = 16 * jb + 4 * q + ii;
-              float* p = db + rank * BN + wc0 + j * 16 + l;
+              const int rank = 16 * jb + l;
+              float* p = db + rank * BN + wc0 + j * 16 + 4 * q + ii;
               if (rank < R) *p = w == 0 ? dbacc[j][jb][ii] : *p + dbacc[j][jb][ii];
             }
       }
@@ -522,12 +642,14 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
   }
 }
 
-// Joins the tiles of 64 rows, sixteen of them side by side, in a fixed order.
+// Joins the tiles: a block takes `rows` rows (a power of two up to 64), 1024 /
+// rows lanes each every so many tiles, then the lanes in a tree: few rows over
+// many tiles are as parallel as many rows.
 __global__ __launch_bounds__(1024) void xent_join_kernel(const float* part, const float* tl, Ids ids, int tiles, int M,
-                                                         float* loss, float* lse) {
-  __shared__ float red[16][64][2];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, m = blockIdx.x * 64 + lane;
-  const int mc = m < M ? m : M - 1;
+                                                         int rows, float* loss, float* lse) {
+  __shared__ float rm[1024], rsum[1024];
+  const int tid = threadIdx.x, row = tid & (rows - 1), lane = tid / rows, lanes = 1024 / rows;
+  const int m = blockIdx.x * rows + row, mc = m < M ? m : M - 1;
   float mx = -INFINITY, sum = 0.f;
   auto join = [&](float m2, float s2) {
     const float top = fmaxf(mx, m2);
@@ -535,28 +657,33 @@ __global__ __launch_bounds__(1024) void xent_join_kernel(const float* part, cons
     sum = sum * __builtin_amdgcn_exp2f(mx - ref) + s2 * __builtin_amdgcn_exp2f(m2 - ref);
     mx = top;
   };
-  for (int c = w; c < tiles; c += 64) {
+  for (int c = lane; c < tiles; c += 4 * lanes) {
     float pm[4], ps[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const float* p = part + 2 * ((long)(c + 16 * u < tiles ? c + 16 * u : c) * M + mc);
+      const float* p = part + 2 * ((long)(c + u * lanes < tiles ? c + u * lanes : c) * M + mc);
       pm[u] = p[0];
       ps[u] = p[1];
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      if (c + 16 * u < tiles) join(pm[u], ps[u]);
+      if (c + u * lanes < tiles) join(pm[u], ps[u]);
   }
-  red[w][lane][0] = mx;
-  red[w][lane][1] = sum;
-  __syncthreads();
-  if (w != 0 || m >= M) return;
-  for (int k = 1; k < 16; ++k) join(red[k][lane][0], red[k][lane][1]);
-  const int t = entry_of(ids, m);
-  const float top = mx * kLn2, rest = logf(sum);
-  lse[m] = top + rest;
+  rm[tid] = mx;
+  rsum[tid] = sum;
+  for (int d = 512; d >= rows; d >>= 1) {
+    __syncthreads();
+    if (tid < d) {
+      join(rm[tid + d], rsum[tid + d]);
+      rm[tid] = mx;
+      rsum[tid] = sum;
+    }
+  }
+  if (lane != 0 || m >= M) return;
+  const float rest = logf(sum);
+  lse[m] = mx * kLn2 + rest;
   // (the difference first: what the target's logit and the maximum share)
-  loss[m] = t >= 0 ? (top - tl[m]) + rest : 0.f;
+  loss[m] = entry_of(ids, m) >= 0 ? (mx - tl[m]) * kLn2 + rest : 0.f;
 }
 
 // ---- dx ---------------------------------------------------------------------------
@@ -683,7 +810,7 @@ __global__ __launch_bounds__(64 * WM * 4) void xent_dx_kernel(DxArgs a) {
           w[e] = *reinterpret_cast<const uint16_t*>(row + e * RB + ((wn ^ q) << 5) + 2 * l);
           const int half = ((v + e) * ngrp + grp) & 1;       // (past N the clamped entry's half: masked)
           const uint16_t hb = (uint16_t)(sp[e] >> (16 * half));
-          sc[e] = v + e < a.V ? (float)__builtin_bit_cast(_Float16, hb) : 0.f;
+          sc[e] = v + e < a.V ? 0.125f * (float)__builtin_bit_cast(_Float16, hb) : 0.f;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -691,14 +818,19 @@ __global__ __launch_bounds__(64 * WM * 4) void xent_dx_kernel(DxArgs a) {
           for (int e = 0; e < 4; ++e) {
             const float x = (float)((int)(w[2 * e] << (28 - 4 * j)) >> 28) * sc[2 * e];
             const float y = (float)((int)(w[2 * e + 1] << (28 - 4 * j)) >> 28) * sc[2 * e + 1];
-            bf[j][e] = pk_bf16(x, y);
+            bf[j][e] = pk_f16(x, y);
           }
       }
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[i], __builtin_bit_cast(bf16x8, bf[j]), acc[i][j], 0, 0, 0);
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (W4)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, af[i]),
+                                                              __builtin_bit_cast(f16x8, bf[j]), acc[i][j], 0, 0, 0);
+          else
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(af[i], __builtin_bit_cast(bf16x8, bf[j]), acc[i][j], 0, 0, 0);
+        }
     }
     slot = slot == S - 1 ? 0 : slot + 1;
   }
@@ -722,11 +854,18 @@ struct ReduceArgs {
   int M, N, r, tiles_x, tiles_m, v0, vc, first, last, V;
   long ldg;
   float s;
+  Ids ids;
+  const float* dloss;
   const float* up;
   const float* dbp;
   float* u;
   float* dB;
 };
+// The factor of a row's gradient: dloss, 0 where it has no target.
+__device__ __forceinline__ float row_factor(const Ids& ids, const float* dloss, long m) {
+  return entry_of(ids, m) >= 0 ? dloss[m] : 0.f;
+}
+
 __global__ __launch_bounds__(256) void xent_reduce_kernel(ReduceArgs a) {
   const long e = (long)blockIdx.x * 256 + threadIdx.x, nu = (long)a.M * a.r;
   const long ndb = (long)a.r * a.vc, npad = a.last ? (long)a.r * (a.N - a.V) : 0;
@@ -743,8 +882,8 @@ __global__ __launch_bounds__(256) void xent_reduce_kernel(ReduceArgs a) {
     return s;
   };
   if (e < nu) {
-    const float v = sum(a.up + e, nu, a.tiles_x);
-    a.u[e] = a.first ? v : a.u[e] + v;
+    const float v = sum(a.up + e, nu, a.tiles_x), u = a.first ? v : a.u[e] + v;
+    a.u[e] = a.last ? u * row_factor(a.ids, a.dloss, e / a.r) : u;
   } else if (e < nu + ndb) {
     const long j = (e - nu) / a.vc, c = (e - nu) % a.vc;
     a.dB[j * a.N + a.v0 + c] = a.s * sum(a.dbp + j * a.ldg + c, a.r * a.ldg, a.tiles_m);
@@ -754,27 +893,64 @@ __global__ __launch_bounds__(256) void xent_reduce_kernel(ReduceArgs a) {
   }
 }
 
-// dx = the splits' sums + s u A^T, four features a thread.
-template <typename OutT>
+// dx = factor times the splits' sums + s u A^T: a thread has four features (and
+// their rows of A) for kJoinRows rows.
+constexpr int kJoinRows = 16;
+template <typename OutT, int R>
 __global__ __launch_bounds__(256) void xent_dx_join_kernel(const float* dxp, int splits, int M, int K, int r, float s,
-                                                           const float* u, const float* A, OutT* dx) {
-  const long e = ((long)blockIdx.x * 256 + threadIdx.x) * 4, n = (long)M * K;
-  if (e >= n) return;
-  f32x4 v = *reinterpret_cast<const f32x4*>(dxp + e);
-  for (int i = 1; i < splits; ++i) v += *reinterpret_cast<const f32x4*>(dxp + i * n + e);
-  if (r > 0) {
-    const long m = e / K, k = e % K;
-    f32x4 low{0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < r; ++j) {
-      const float uj = u[m * r + j];
+                                                           const float* u, const float* A, Ids ids, const float* dloss,
+                                                           float down, OutT* dx) {
+  const int units = K / 4, k = (int)((blockIdx.x * 256 + threadIdx.x) % (unsigned)units) * 4;
+  const int m0 = (int)((blockIdx.x * 256 + threadIdx.x) / (unsigned)units) * kJoinRows;
+  if (m0 >= M) return;
+  const int m1 = m0 + kJoinRows < M ? m0 + kJoinRows : M;
+  const long n = (long)M * K;
+  float ar[4][R > 0 ? R : 1];
+  if constexpr (R > 0) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) low[c] = __builtin_fmaf(uj, A[(k + c) * r + j], low[c]);
-    }
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = __builtin_fmaf(s, low[c], v[c]);
+      for (int j = 0; j < R; ++j) ar[c][j] = j < r ? A[(long)(k + c) * r + j] : 0.f;
   }
-  if constexpr (sizeof(OutT) == 4) *reinterpret_cast<f32x4*>(dx + e) = v;
-  else *reinterpret_cast<u32x2*>(dx + e) = u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+  for (int m = m0; m < m1; ++m) {
+    const float f = row_factor(ids, dloss, m) * down;
+    const float* p = dxp + (long)m * K + k;
+    f32x4 v = *reinterpret_cast<const f32x4*>(p);
+    for (int i = 1; i < splits; ++i) v += *reinterpret_cast<const f32x4*>(p + i * n);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] *= f;
+    if constexpr (R > 0) {
+      f32x4 low{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const float uj = u[(long)m * r + (j < r ? j : 0)];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) low[c] = __builtin_fmaf(uj, ar[c][j], low[c]);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = __builtin_fmaf(s, low[c], v[c]);
+    }
+    OutT* out = dx + (long)m * K + k;
+    if constexpr (sizeof(OutT) == 4) *reinterpret_cast<f32x4*>(out) = v;
+    else *reinterpret_cast<u32x2*>(out) = u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+  }
+}
+
+template <typename OutT>
+void dx_join(const VocabLayer& L, int M, Ids ids, const float* dloss, const XentPlan& plan, const XentBuffers& buf,
+             void* dx, hipStream_t st) {
+  const long threads = (long)(L.K / 4) * ((M + kJoinRows - 1) / kJoinRows);
+  const dim3 grid((unsigned)((threads + 255) / 256));
+  const float down = L.fmt == 0 ? 1.f : kHalfDown;
+  OutT* out = static_cast<OutT*>(dx);
+#define JOIN(R) \
+  xent_dx_join_kernel<OutT, R><<<grid, 256, 0, st>>>(buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids, dloss, down, out)
+  if (L.r == 0) JOIN(0);
+  else if (L.r <= 4) JOIN(4);
+  else if (L.r <= 8) JOIN(8);
+  else if (L.r <= 16) JOIN(16);
+  else JOIN(32);
+#undef JOIN
 }
 
 // ---- launches ---------------------------------------------------------------------
@@ -841,7 +1017,10 @@ void launch_xent_fwd(const VocabLayer& L, int M, Ids ids, const int8_t* xq, cons
   a.tl = part;
   a.part = part + M;
   logits<false>(a, L.fmt, ids.vocab, st);
-  xent_join_kernel<<<dim3((unsigned)((M + 63) / 64)), 1024, 0, st>>>(a.part, a.tl, ids, a.tiles_x, M, loss, lse);
+  int rows = 1;
+  while (rows < 64 && rows < M) rows <<= 1;
+  xent_join_kernel<<<dim3((unsigned)((M + rows - 1) / rows)), 1024, 0, st>>>(a.part, a.tl, ids, a.tiles_x, M, rows,
+                                                                           loss, lse);
 }
 
 XentPlan xent_plan(const VocabLayer& L, int vocab, int M, int dtype) {
@@ -890,20 +1069,15 @@ void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const int8_
       else launch_dx<true>(d, rows, st);
     }
     if (L.r > 0) {
-      ReduceArgs r{M, L.N, L.r, a.tiles_x, a.tiles_m, v0, vc, v0 == 0, v0 + vc == V, V, ldg, L.s,
+      ReduceArgs r{M, L.N, L.r, a.tiles_x, a.tiles_m, v0, vc, v0 == 0, v0 + vc == V, V, ldg, L.s, ids, dloss,
                    buf.up, buf.dbp, buf.u, dB};
       const long n = (long)M * L.r + (long)L.r * vc + (r.last ? (long)L.r * (L.N - V) : 0);
       xent_reduce_kernel<<<dim3((unsigned)((n + 255) / 256)), 256, 0, st>>>(r);
     }
   }
   if (dx == nullptr) return;
-  const dim3 grid((unsigned)(((long)M * L.K / 4 + 255) / 256));
-  if (dtype == 0)
-    xent_dx_join_kernel<float><<<grid, 256, 0, st>>>(buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A,
-                                                    static_cast<float*>(dx));
-  else
-    xent_dx_join_kernel<uint16_t><<<grid, 256, 0, st>>>(buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A,
-                                                       static_cast<uint16_t*>(dx));
+  if (dtype == 0) dx_join<float>(L, M, ids, dloss, plan, buf, dx, st);
+  else dx_join<uint16_t>(L, M, ids, dloss, plan, buf, dx, st);
 }
 
 }  // namespace qlora
