@@ -46,17 +46,17 @@ struct XentPlan {
   int piece;                         // entries per piece, a multiple of 256
   int splits;                        // of a piece's contraction for dx
   int parts;                         // bf16 parts of dl: 1, or 3 in float32
-  size_t g, dxp, u, up, dbp;         // elements: dl (bf16), dx partials, u, its partials, dB's
+  size_t g, dxp, u, up, dbp, pA;     // elements: dl (16 bits), partial sums of dx, u, those of u, dB and dA
 };
 XentPlan xent_plan(const VocabLayer& L, int vocab, int M, int dtype);
 struct XentBuffers {
   uint16_t* g;
-  float *dxp, *u, *up, *dbp;
+  float *dxp, *u, *up, *dbp, *pA;
 };
-// dx (NULL: none), u [M, r] (in buf) and dB; dA = s x^T u is the caller's.
-void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const int8_t* xq, const float* sx,
+// dx (NULL: none), and with an adapter dA and dB.
+void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const void* x, const int8_t* xq, const float* sx,
                      const float* t, const float* lse, const float* dloss, const XentPlan& plan,
-                     const XentBuffers& buf, void* dx, float* dB, hipStream_t st);
+                     const XentBuffers& buf, void* dx, float* dA, float* dB, hipStream_t st);
 
 #ifdef __HIPCC__
 __device__ __forceinline__ int entry_of(const Ids& ids, long m) {

@@ -91,7 +91,7 @@ XentBwdLayout xent_bwd_layout(const qlora_linear* L, int vocab, int M, int dtype
   w.u = off; off = align_up(off + w.plan.u * 4);
   w.up = off; off = align_up(off + w.plan.up * 4);
   w.dbp = off; off = align_up(off + w.plan.dbp * 4);
-  w.pA = off; off = align_up(off + (L->r > 0 ? (size_t)skinny_nsplit_host(M) * L->r * L->K * 4 : 0));
+  w.pA = off; off = align_up(off + w.plan.pA * 4);
   w.total = off;
   return w;
 }
@@ -246,21 +246,9 @@ int qlora_xent_bwd(const qlora_linear* L, int vocab, int M, int dtype, const voi
   float* tw = L->r < 1 || t_saved != nullptr ? nullptr : reinterpret_cast<float*>(at(ws, w.t));
   enqueue_rows(L, M, dtype, x, xq, sx, tw, reinterpret_cast<float*>(at(ws, w.rs)), s);
   const auto f = [&](size_t off) { return reinterpret_cast<float*>(at(ws, off)); };
-  const XentBuffers buf{reinterpret_cast<uint16_t*>(at(ws, w.g)), f(w.dxp), f(w.u), f(w.up), f(w.dbp)};
-  launch_xent_bwd(vocab_layer(L), M, dtype, make_ids(targets, itype, vocab), xq, sx, tw != nullptr ? tw : t_saved,
-                  lse, dloss, w.plan, buf, dx, dB, s);
-  if (L->r > 0) {
-    // dA = s x^T u, as the layers' own adapter gradients
-    SkinnyJobs sk{};
-    sk.njobs = 1;
-    sk.M = M; sk.r = L->r; sk.s = L->alpha / (float)L->r;
-    sk.nsplit = skinny_nsplit_host(M);
-    sk.rows_per_split = ((M + sk.nsplit - 1) / sk.nsplit + 3) / 4 * 4;
-    sk.P[0] = buf.u; sk.Q[0] = x; sk.C[0] = L->K; sk.out[0] = dA; sk.transpose[0] = 1;
-    sk.partial[0] = f(w.pA); sk.ncb[0] = (L->K + kSkCols - 1) / kSkCols; sk.hd0 = L->K;
-    launch_skinny_stage1(dtype, sk, s);
-    launch_skinny_stage2(sk, s);
-  }
+  const XentBuffers buf{reinterpret_cast<uint16_t*>(at(ws, w.g)), f(w.dxp), f(w.u), f(w.up), f(w.dbp), f(w.pA)};
+  launch_xent_bwd(vocab_layer(L), M, dtype, make_ids(targets, itype, vocab), x, xq, sx,
+                  tw != nullptr ? tw : t_saved, lse, dloss, w.plan, buf, dx, dA, dB, s);
   return launch_status();
 }
 

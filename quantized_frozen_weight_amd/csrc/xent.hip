@@ -29,6 +29,7 @@
 #include "bwd_common.hpp"
 #include "launch.hpp"
 #include "nibbles.hpp"
+#include "rank_sums.hpp"
 #include "ring.hpp"
 #include "vocab.hpp"
 
@@ -953,6 +954,19 @@ void dx_join(const VocabLayer& L, int M, Ids ids, const float* dloss, const Xent
 #undef JOIN
 }
 
+// dA = s x^T u over the rows that have a target: partial sums, then their total.
+template <typename T, int RB>
+__global__ __launch_bounds__(256) void xent_da_kernel(const typename Elem<T>::type* x, const float* u, Ids ids, int M,
+                                                      int K, int r, int rows, float* part) {
+  rank_sum_block<T, RB>(blockIdx.x, M, K, r, rows, x, part, [&](int m) { return entry_of(ids, m) >= 0; },
+                        [&](int m, int j) { return u[(long)m * r + j]; });
+}
+__global__ __launch_bounds__(256) void xent_da_total_kernel(const float* part, int blocks, int K, int r, float s,
+                                                            float* dA) {
+  const long e = (long)blockIdx.x * 256 + threadIdx.x, n = (long)r * K;
+  if (e < n) dA[e % K * r + e / K] = s * rank_sum_total(part, blocks, n, e);
+}
+
 // ---- launches ---------------------------------------------------------------------
 template <bool W4, int BM, int BN, int WM, int WN, int S, int G, bool GRAD>
 void logits_ranks(LogitArgs& a, int cols, hipStream_t st) {
@@ -1041,13 +1055,14 @@ XentPlan xent_plan(const VocabLayer& L, int vocab, int M, int dtype) {
     p.u = (size_t)M * L.r;
     p.up = (size_t)(p.piece / 128) * M * L.r;
     p.dbp = (size_t)((M + 127) / 128) * L.r * p.piece;
+    p.pA = rank_sum_floats(M, L.K, L.r);
   }
   return p;
 }
 
-void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const int8_t* xq, const float* sx,
+void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const void* x, const int8_t* xq, const float* sx,
                      const float* t, const float* lse, const float* dloss, const XentPlan& plan,
-                     const XentBuffers& buf, void* dx, float* dB, hipStream_t st) {
+                     const XentBuffers& buf, void* dx, float* dA, float* dB, hipStream_t st) {
   const int V = ids.vocab;
   const int rows = dx_rows(M);
   for (int v0 = 0; v0 < V; v0 += plan.piece) {
@@ -1074,6 +1089,21 @@ void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const int8_
       const long n = (long)M * L.r + (long)L.r * vc + (r.last ? (long)L.r * (L.N - V) : 0);
       xent_reduce_kernel<<<dim3((unsigned)((n + 255) / 256)), 256, 0, st>>>(r);
     }
+  }
+  if (L.r > 0) {
+    const int rows_a = rank_sum_rows(M, L.K), blocks = rank_sum_blocks(M, L.K);
+    const float* xf = static_cast<const float*>(x);
+    const uint16_t* xh = static_cast<const uint16_t*>(x);
+    if (dtype == 0 && L.r <= 16)
+      xent_da_kernel<F32, 1><<<dim3((unsigned)blocks), 256, 0, st>>>(xf, buf.u, ids, M, L.K, L.r, rows_a, buf.pA);
+    else if (dtype == 0)
+      xent_da_kernel<F32, 2><<<dim3((unsigned)blocks), 256, 0, st>>>(xf, buf.u, ids, M, L.K, L.r, rows_a, buf.pA);
+    else if (L.r <= 16)
+      xent_da_kernel<BF16, 1><<<dim3((unsigned)blocks), 256, 0, st>>>(xh, buf.u, ids, M, L.K, L.r, rows_a, buf.pA);
+    else
+      xent_da_kernel<BF16, 2><<<dim3((unsigned)blocks), 256, 0, st>>>(xh, buf.u, ids, M, L.K, L.r, rows_a, buf.pA);
+    xent_da_total_kernel<<<dim3((unsigned)(((long)L.r * L.K + 255) / 256)), 256, 0, st>>>(
+        buf.pA, (M + rows_a - 1) / rows_a, L.K, L.r, L.s, dA);
   }
   if (dx == nullptr) return;
   if (dtype == 0) dx_join<float>(L, M, ids, dloss, plan, buf, dx, st);
