@@ -1,11 +1,13 @@
 // The vocabulary layer at the model's input: the lookup of tokens and its
 // gradient (formulas: include/qlora.h).
 //
-// Lookup. Memory-bound: a row reads K bytes of codes and writes K outputs. A
-// thread owns 8 features (4 from rank 9 on, whose rows of A would not fit in
-// its registers) of up to 8 rows, all of whose codes it has under way while the
-// block gathers the tokens' columns of B (r scattered floats each) into LDS; A is
-// read once per block.
+// Lookup. Memory-bound: a row reads K bytes of codes and writes K outputs. A wave
+// takes 64 features of up to 64 rows: its lanes' codes (16 a lane, the quarters of
+// a row side by side) are all under way while the block gathers the tokens'
+// columns of B (r scattered floats each) into LDS, and the adapter's part is
+// formed on v_mfma_f32_16x16x4_f32 in the layout of the codes, with A's rows in
+// registers (a lane that read its own features' rows of A for vector products
+// touched 64 lines an instruction, and took 37 us for 8192 x 2048 at rank 8).
 //
 // Gradient. One launch runs four kinds of blocks beside each other:
 //   place  the tokens sorted by (token, row): a row's place is the number of rows
@@ -45,126 +47,109 @@ struct EmbedArgs {
   void* x;
 };
 
-constexpr int kEmbedLanes = 32;      // rows side by side at most (narrow layers)
-
-// The value of code e of a unit's dword(s): int8, or 4-bit (nibble e).
-template <bool W4, int F>
-__device__ __forceinline__ void unit_codes(const uint32_t (&w)[2], float (&v)[F]) {
-#pragma unroll
-  for (int e = 0; e < F; ++e) {
-    if constexpr (W4) v[e] = (float)((int)(w[0] << (28 - 4 * e)) >> 28);
-    else v[e] = (float)(int8_t)(w[e / 4] >> (8 * (e % 4)));
-  }
-}
-
-// R: the rank rounded up (0: no adapter); F features and U rows per thread.
-template <typename T, bool W4, int R, int F, int U>
+// R: the rank rounded up (0: no adapter); NG groups of 16 rows a block. A wave
+// takes 64 features, lane (l, q) the 16 of quarter q for row l of every group.
+template <typename T, bool W4, int R, int NG>
 __global__ __launch_bounds__(256) void embed_kernel(EmbedArgs a) {
   typedef typename Elem<T>::type E;
-  constexpr int RA = R > 0 ? R : 1;
-  __shared__ int tok[U * kEmbedLanes];
-  __shared__ float bs[U * kEmbedLanes * RA];
-  const int tid = threadIdx.x, K = a.K;
-  const int units = K / F, wide = units < 256 ? units : 256;      // units a block covers of a row
-  const int fit = 256 / wide, lanes = fit < kEmbedLanes ? fit : kEmbedLanes;
-  const int all = U * lanes, m0 = blockIdx.x * all;
-  const int rows = a.M - m0 < all ? a.M - m0 : all;
-  const int unit = (int)blockIdx.y * wide + tid % wide, lane = tid / wide;
-  for (int i = tid; i < all; i += 256) tok[i] = i < rows ? entry_of(a.ids, m0 + i) : -1;
+  constexpr int RA = R > 0 ? R : 4, KC = RA / 4, RP = RA + 1;     // RP: pitch of a row of bs
+  __shared__ int tok[16 * NG];
+  __shared__ float bs[16 * NG * RP];
+  const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, q = lane >> 4, K = a.K;
+  const int m0 = blockIdx.x * (16 * NG), d0 = ((int)blockIdx.y * 4 + (tid >> 6)) * 64;
+  if (tid < 16 * NG) tok[tid] = m0 + tid < a.M ? entry_of(a.ids, m0 + tid) : -1;
   __syncthreads();
-  const bool on = lane < lanes && unit < units;
-  const int k = unit * F;
-  // the rows' codes and scales, and A, under way while B's columns are gathered
-  uint32_t w[U][2];
-  float sc[U], ar[F][RA];
-  if (on) {
+  const int k = d0 + 16 * q, kc0 = k < K ? k : 0;
+  u32x4 w[NG];
+  float sc[NG];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int t = tok[lane + u * lanes];
-      const long at = t >= 0 ? t : 0;
-      w[u][1] = 0u;
-      if constexpr (W4) {
-        const uint8_t* p = a.codes + at * (K / 2) + k / 2;
-        w[u][0] = F == 8 ? *reinterpret_cast<const uint32_t*>(p) : (uint32_t)*reinterpret_cast<const uint16_t*>(p);
-        sc[u] = (float)static_cast<const _Float16*>(a.scales)[at * (K / 128) + k / 128];
-      } else {
-        const uint8_t* p = a.codes + at * K + k;
-        if constexpr (F == 8) {
-          const u32x2 v = *reinterpret_cast<const u32x2*>(p);
-          w[u][0] = v.x;
-          w[u][1] = v.y;
-        } else {
-          w[u][0] = *reinterpret_cast<const uint32_t*>(p);
-        }
-        sc[u] = static_cast<const float*>(a.scales)[at];
-      }
-    }
-    if constexpr (R > 0) {
-#pragma unroll
-      for (int f = 0; f < F; ++f)
-#pragma unroll
-        for (int j = 0; j < R; ++j) ar[f][j] = a.A[(long)(k + f) * a.r + (j < a.r ? j : 0)];
+  for (int g = 0; g < NG; ++g) {
+    const int t = tok[16 * g + l];
+    const long at = t >= 0 ? t : 0;
+    if constexpr (W4) {
+      const u32x2 v = *reinterpret_cast<const u32x2*>(a.codes + at * (K / 2) + kc0 / 2);
+      w[g] = u32x4{v.x, v.y, 0u, 0u};
+      sc[g] = (float)static_cast<const _Float16*>(a.scales)[at * (K / 128) + kc0 / 128];
+    } else {
+      w[g] = *reinterpret_cast<const u32x4*>(a.codes + at * K + kc0);
+      sc[g] = static_cast<const float*>(a.scales)[at];
     }
   }
+  // A operand of column block b: row 4 q' + i of it is feature 16 q' + 4 b + i, so
+  // that the four blocks of a lane are its 16 features in order
+  float ar[4][KC];
   if constexpr (R > 0) {
-    for (int e = tid; e < all * R; e += 256) {
-      const int row = e / R, j = e % R, t = tok[row];
-      bs[e] = t >= 0 && j < a.r ? a.B[(long)j * a.N + t] : 0.f;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int d = d0 + 16 * (l >> 2) + 4 * b + (l & 3);
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        const int j = 4 * c + q;
+        const float v = a.A[(long)(d < K ? d : 0) * a.r + (j < a.r ? j : 0)];
+        ar[b][c] = d < K && j < a.r ? v : 0.f;
+      }
+    }
+    for (int e = tid; e < 16 * NG * R; e += 256) {
+      const int j = e / (16 * NG), row = e % (16 * NG), t = tok[row];
+      bs[row * RP + j] = t >= 0 && j < a.r ? a.B[(long)j * a.N + t] : 0.f;
     }
     __syncthreads();
   }
-  if (!on) return;
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int row = lane + u * lanes;
-    if (row >= rows) break;
-    const bool live = tok[row] >= 0;
-    float v[F];
-    unit_codes<W4, F>(w[u], v);
+  for (int g = 0; g < NG; ++g) {
+    f32x4 low[4];
+    if constexpr (R > 0) {
 #pragma unroll
-    for (int f = 0; f < F; ++f) {
-      float y = v[f] * sc[u];
-      if constexpr (R > 0) {
-        float low = 0.f;
+      for (int b = 0; b < 4; ++b) low[b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < R; ++j) low = __builtin_fmaf(j < a.r ? ar[f][j] : 0.f, bs[row * R + j], low);
-        y = __builtin_fmaf(a.s, low, y);
+      for (int c = 0; c < KC; ++c) {
+        const float bv = bs[(16 * g + l) * RP + 4 * c + q];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) low[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(ar[b][c], bv, low[b], 0, 0, 0);
       }
+    }
+    const int m = m0 + 16 * g + l;
+    if (m >= a.M || k >= K) continue;
+    const bool live = tok[16 * g + l] >= 0;
+    float v[16];
+#pragma unroll
+    for (int f = 0; f < 16; ++f) {
+      const float code = W4 ? (float)((int)(w[g][f / 8] << (28 - 4 * (f % 8))) >> 28) : (float)(int8_t)(w[g][f / 4] >> (8 * (f % 4)));
+      float y = code * sc[g];
+      if constexpr (R > 0) y = __builtin_fmaf(a.s, low[f / 4][f % 4], y);
       v[f] = live ? a.scale * y : 0.f;
     }
-    E* out = static_cast<E*>(a.x) + (long)(m0 + row) * K + k;
+    E* out = static_cast<E*>(a.x) + (long)m * K + k;
     if constexpr (sizeof(E) == 4) {
 #pragma unroll
-      for (int f = 0; f < F; f += 4) *reinterpret_cast<f32x4*>(out + f) = f32x4{v[f], v[f + 1], v[f + 2], v[f + 3]};
-    } else if constexpr (F == 8) {
-      *reinterpret_cast<u32x4*>(out) = u32x4{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3]), pk_bf16(v[4], v[5]),
-                                             pk_bf16(v[6], v[7])};
+      for (int f = 0; f < 16; f += 4) *reinterpret_cast<f32x4*>(out + f) = f32x4{v[f], v[f + 1], v[f + 2], v[f + 3]};
     } else {
-      *reinterpret_cast<u32x2*>(out) = u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+#pragma unroll
+      for (int f = 0; f < 16; f += 8)
+        *reinterpret_cast<u32x4*>(out + f) = u32x4{pk_bf16(v[f], v[f + 1]), pk_bf16(v[f + 2], v[f + 3]),
+                                                   pk_bf16(v[f + 4], v[f + 5]), pk_bf16(v[f + 6], v[f + 7])};
     }
   }
 }
 
-// Rows a thread takes: eight where that leaves about four blocks a compute unit,
-// so that A is read seldom; else two, for the latency.
-template <typename T, bool W4, int R, int F>
+// Rows a block takes: 64 where that leaves two blocks a compute unit, so that A
+// and B are gathered seldom; else 16, for the latency.
+template <typename T, bool W4, int R>
 void embed_rows(const EmbedArgs& a, hipStream_t st) {
-  const int units = a.K / F, wide = units < 256 ? units : 256, cols = (units + wide - 1) / wide;
-  const int fit = 256 / wide, lanes = fit < kEmbedLanes ? fit : kEmbedLanes;
-  const auto blocks = [&](int U) { return ((long)a.M + U * lanes - 1) / (U * lanes); };
-  if (blocks(8) * cols >= 1024)
-    embed_kernel<T, W4, R, F, 8><<<dim3((unsigned)blocks(8), (unsigned)cols), 256, 0, st>>>(a);
+  const unsigned cols = (unsigned)((a.K + 255) / 256);
+  if ((long)((a.M + 63) / 64) * cols >= 512)
+    embed_kernel<T, W4, R, 4><<<dim3((unsigned)((a.M + 63) / 64), cols), 256, 0, st>>>(a);
   else
-    embed_kernel<T, W4, R, F, 2><<<dim3((unsigned)blocks(2), (unsigned)cols), 256, 0, st>>>(a);
+    embed_kernel<T, W4, R, 1><<<dim3((unsigned)((a.M + 15) / 16), cols), 256, 0, st>>>(a);
 }
 
 template <typename T, bool W4>
 void embed_dispatch(const EmbedArgs& a, hipStream_t st) {
-  if (a.r == 0) embed_rows<T, W4, 0, 8>(a, st);
-  else if (a.r <= 4) embed_rows<T, W4, 4, 8>(a, st);
-  else if (a.r <= 8) embed_rows<T, W4, 8, 8>(a, st);
-  else if (a.r <= 16) embed_rows<T, W4, 16, 4>(a, st);
-  else embed_rows<T, W4, 32, 4>(a, st);
+  if (a.r == 0) embed_rows<T, W4, 0>(a, st);
+  else if (a.r <= 4) embed_rows<T, W4, 4>(a, st);
+  else if (a.r <= 8) embed_rows<T, W4, 8>(a, st);
+  else if (a.r <= 16) embed_rows<T, W4, 16>(a, st);
+  else embed_rows<T, W4, 32>(a, st);
 }
 
 // ---- gradient ---------------------------------------------------------------------
