@@ -11,9 +11,9 @@
 //
 // Gradient. One launch runs four kinds of blocks beside each other:
 //   place  the tokens sorted by (token, row): a row's place is the number of rows
-//          of its slice of 4096 that come before it, counted by comparing it with
-//          all of them (2 instructions a pair; 4096 rows: 16.8 million pairs, 1 us
-//          of the chip), the tokens in LDS, 16 rows a block and 16 threads a row.
+//          of its slice of 8192 that come before it, counted by comparing it with
+//          all of them (2 instructions a pair; 8192 rows: 67 million pairs, 3.4 us
+//          of the chip), the tokens in LDS, 32 rows a block.
 //          No pass over memory, no rounds that wait for each other;
 //   u      16 rows a block, the four waves a quarter of the features each:
 //          u = dy A on v_mfma_f32_16x16x4_f32, the waves added through LDS;
@@ -153,8 +153,8 @@ void embed_dispatch(const EmbedArgs& a, hipStream_t st) {
 }
 
 // ---- gradient ---------------------------------------------------------------------
-constexpr int kSlice = 4096;         // rows sorted together
-constexpr int kPlaceRows = 16;       // rows of a place block
+constexpr int kSlice = 8192;         // rows sorted together
+constexpr int kPlaceRows = 32;       // rows of a place block
 constexpr int kURows = 16;           // rows of a u block
 constexpr int kFill = 16384;         // floats a fill block clears
 constexpr int kSegRows = 256;        // sorted rows of a block of the last launch
@@ -198,20 +198,28 @@ __device__ __forceinline__ void u_block(const EmbedBwdArgs& a, int b, float* red
   for (int j = 0; j < RB; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
   // A operand: row l, features k0 + 8 q + e at step e; B operand: those
   // features of A, rank l (features past K are zero in the A operand)
-  for (int k0 = 32 * w; k0 < a.K; k0 += 128) {
-    const int k = k0 + 8 * q, kc = k < a.K ? k : 0;
-    float v[8];
-    dy8(dy + (long)mc * a.K + kc, k < a.K, v);
+  constexpr int KU = 4;                                  // steps of 32 features under way together
+  for (int k0 = 32 * w; k0 < a.K; k0 += 128 * KU) {
+    float v[KU][8], av[KU][RB][8];
 #pragma unroll
-    for (int j = 0; j < RB; ++j) {
-      const int rank = 16 * j + l;
-      const float* ap = a.A + (long)kc * a.r + (rank < a.r ? rank : 0);
-      float av[8];
+    for (int s = 0; s < KU; ++s) {
+      const int k = k0 + 128 * s + 8 * q, kc = k < a.K ? k : 0;
+      dy8(dy + (long)mc * a.K + kc, k < a.K, v[s]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) av[e] = k < a.K && rank < a.r ? ap[(long)e * a.r] : 0.f;
+      for (int j = 0; j < RB; ++j) {
+        const int rank = 16 * j + l;
+        const float* ap = a.A + (long)kc * a.r + (rank < a.r ? rank : 0);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[e], av[e], acc[j], 0, 0, 0);
+        for (int e = 0; e < 8; ++e) av[s][j][e] = k < a.K && rank < a.r ? ap[(long)e * a.r] : 0.f;
+      }
     }
+#pragma unroll
+    for (int s = 0; s < KU; ++s)
+#pragma unroll
+      for (int j = 0; j < RB; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[s][e], av[s][j][e], acc[j], 0, 0, 0);
   }
 #pragma unroll
   for (int j = 0; j < RB; ++j)
@@ -227,35 +235,58 @@ __device__ __forceinline__ void u_block(const EmbedBwdArgs& a, int b, float* red
   }
 }
 
-// The places of 16 rows of a slice. toks: the slice's tokens (N for none).
+// The places of 32 rows of a slice, four rows a thread and 32 threads a row (four
+// tokens read from LDS then serve sixteen comparisons; one row a thread left the
+// LDS the bound, 42 us for the launch at 8192 rows). toks: the slice's tokens (N
+// for none).
 __device__ __forceinline__ void place_block(const EmbedBwdArgs& a, int b, int* toks) {
-  const int tid = threadIdx.x, row = tid >> 4, part = tid & 15;
+  constexpr int RT = 4, PT = 256 * RT / kPlaceRows;              // rows a thread, threads a row
+  const int tid = threadIdx.x, part = tid % PT;
   const int m0 = b * kPlaceRows, s0 = m0 / kSlice * kSlice;
   const int n = a.M - s0 < kSlice ? a.M - s0 : kSlice;           // rows of the slice
-  const int n4 = (n + 63) / 64 * 64;
+  const int n4 = (n + 4 * PT - 1) / (4 * PT) * (4 * PT);
   for (int i = tid; i < n4; i += 256) {
     const int t = i < n ? entry_of(a.ids, s0 + i) : 0x7fffffff;   // (past the slice: behind every row)
     toks[i] = t >= 0 ? t : a.N;
   }
   __syncthreads();
-  const int mine = m0 + row - s0, t = toks[mine < n ? mine : 0];
-  // rows before `mine` come first where their token is not larger, rows behind
-  // it where it is smaller; thread `part` takes four of every 64
-  int before = 0;
-  for (int i = 4 * part; i < n4; i += 64) {
-    const i32x4 v = *reinterpret_cast<const i32x4*>(toks + i);
+  const int mine = m0 - s0 + tid / PT * RT;                      // the first of the thread's rows
+  int t[RT], before[RT];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) before += v[e] < t + (i + e < mine ? 1 : 0);
+  for (int r = 0; r < RT; ++r) {
+    t[r] = toks[mine + r < n ? mine + r : 0];
+    before[r] = 0;
   }
+  // rows before one's own come first where their token is not larger, rows behind it
+  // where it is smaller; only the block's own rows have to be told apart one by one
+  const int own = m0 - s0;
+  auto count = [&](int i0, int i1, int more) {                   // tokens below t + more
+    for (int i = i0 + 4 * part; i < i1; i += 4 * PT) {
+      const i32x4 v = *reinterpret_cast<const i32x4*>(toks + i);
 #pragma unroll
-  for (int d = 8; d >= 1; d >>= 1) before += __shfl_xor(before, d);
-  if (part != 0 || mine >= n) return;
-  const int at = s0 + before;
-  if (a.nslices == 1) {
-    a.tok[at] = t;
-    a.row[at] = m0 + row;
-  } else {
-    a.slices[at] = ((uint64_t)(uint32_t)t << 32) | (uint32_t)(m0 + row);
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) before[r] += v[e] < t[r] + more ? 1 : 0;
+    }
+  };
+  count(0, own, 1);
+  for (int i = own + part; i < own + kPlaceRows; i += PT) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) before[r] += toks[i] < t[r] + (i < mine + r ? 1 : 0) ? 1 : 0;
+  }
+  count(own + kPlaceRows, n4, 0);
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+#pragma unroll
+    for (int d = PT / 2; d >= 1; d >>= 1) before[r] += __shfl_xor(before[r], d);
+    if (part != r || mine + r >= n) continue;
+    const int at = s0 + before[r];
+    if (a.nslices == 1) {
+      a.tok[at] = t[r];
+      a.row[at] = s0 + mine + r;
+    } else {
+      a.slices[at] = ((uint64_t)(uint32_t)t[r] << 32) | (uint32_t)(s0 + mine + r);
+    }
   }
 }
 
@@ -263,14 +294,14 @@ __device__ __forceinline__ void place_block(const EmbedBwdArgs& a, int b, int* t
 template <typename T, int RB>
 __global__ __launch_bounds__(256) void embed_bwd_kernel(EmbedBwdArgs a) {
   __shared__ __attribute__((aligned(16))) char lds[kSlice * 4];
-  static_assert(4 * 256 * RB * 4 <= kSlice * 4, "the u blocks' sums fit");
+  static_assert(4 * 256 * RB * 4 <= kSlice * 4 && rank_sum_lds<RB>() <= kSlice * 4, "every kind of block fits");
   int b = blockIdx.x;
   if (b < a.nplace) { place_block(a, b, reinterpret_cast<int*>(lds)); return; }
   b -= a.nplace;
   if (b < a.nu) { u_block<T, RB>(a, b, reinterpret_cast<float*>(lds)); return; }
   b -= a.nu;
   if (b < a.nda) {
-    rank_sum_block<T, RB>(b, a.M, a.K, a.r, a.rows_a, static_cast<const typename Elem<T>::type*>(a.dy), a.pA,
+    rank_sum_block<T, RB>(b, a.M, a.K, a.r, a.rows_a, static_cast<const typename Elem<T>::type*>(a.dy), a.pA, lds,
                           [&](int m) { return entry_of(a.ids, m) >= 0; },
                           [&](int m, int j) { return a.B[(long)j * a.N + entry_of(a.ids, m)]; });
     return;
@@ -313,6 +344,7 @@ template <int R>
 __global__ __launch_bounds__(256) void embed_runs_kernel(EmbedBwdArgs a, int nseg) {
   __shared__ int first_tok[5];         // the token of each wave's first row, of the next block's
   __shared__ int whole[4];             // a wave that is one run
+  __shared__ int found[4];
   __shared__ float first_sum[4][R], rest[4][R];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, b = blockIdx.x;
   if (b >= nseg) {
@@ -369,11 +401,17 @@ __global__ __launch_bounds__(256) void embed_runs_kernel(EmbedBwdArgs a, int nse
     leaves = a.tok[i0 + kSegRows - 1] == t3;
   }
   if (leaves) {                                                // block-uniform
+    // where its token ends: 256 places looked at together, then between two of them
     int lo = i0 + kSegRows, hi = a.M;
     while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (a.tok[mid] <= t3) lo = mid + 1;
-      else hi = mid;
+      const int stride = (hi - lo + 255) / 256, p = lo + tid * stride;
+      const int here = __builtin_popcountll(__builtin_amdgcn_ballot_w64(p < hi && a.tok[p < hi ? p : lo] == t3));
+      if (lane == 0) found[w] = here;
+      __syncthreads();
+      const int c = found[0] + found[1] + found[2] + found[3];     // those before the end, in order
+      __syncthreads();
+      hi = lo + c * stride < hi ? lo + c * stride : hi;
+      lo = c > 0 ? lo + (c - 1) * stride + 1 : lo;
     }
     float x[R], y[4][R];
 #pragma unroll

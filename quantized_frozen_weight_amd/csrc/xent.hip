@@ -958,7 +958,8 @@ void dx_join(const VocabLayer& L, int M, Ids ids, const float* dloss, const Xent
 template <typename T, int RB>
 __global__ __launch_bounds__(256) void xent_da_kernel(const typename Elem<T>::type* x, const float* u, Ids ids, int M,
                                                       int K, int r, int rows, float* part) {
-  rank_sum_block<T, RB>(blockIdx.x, M, K, r, rows, x, part, [&](int m) { return entry_of(ids, m) >= 0; },
+  __shared__ __attribute__((aligned(16))) char lds[rank_sum_lds<RB>()];
+  rank_sum_block<T, RB>(blockIdx.x, M, K, r, rows, x, part, lds, [&](int m) { return entry_of(ids, m) >= 0; },
                         [&](int m, int j) { return u[(long)m * r + j]; });
 }
 __global__ __launch_bounds__(256) void xent_da_total_kernel(const float* part, int blocks, int K, int r, float s,
