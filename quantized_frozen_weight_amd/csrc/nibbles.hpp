@@ -20,4 +20,17 @@ __device__ __forceinline__ i32x4 widen_nibbles(u32x2 w) {
   return out;
 }
 
+// The same codes times 16: a code in the upper half of a byte is 16 q with its
+// sign in place.
+__device__ __forceinline__ i32x4 widen_nibbles16(u32x2 w) {
+  i32x4 out;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = (w[h] << 4) & 0xF0F0F0F0u, hi = w[h] & 0xF0F0F0F0u;   // even k, odd k
+    out[2 * h] = (int)__builtin_amdgcn_perm(hi, lo, 0x05010400u);
+    out[2 * h + 1] = (int)__builtin_amdgcn_perm(hi, lo, 0x07030602u);
+  }
+  return out;
+}
+
 }  // namespace qlora

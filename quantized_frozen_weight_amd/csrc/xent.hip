@@ -3,8 +3,9 @@
 //
 // logits kernel  The layer's integer product over tiles of the vocabulary, both
 //   operands K-contiguous rows that move from memory to LDS untouched
-//   (ring.hpp); 4-bit weights are widened in registers and their exact sums
-//   weighted group by group (as gemm_a8w4.hip). What a tile does with its
+//   (ring.hpp); 4-bit codes are widened in registers, as 16 q in the upper half
+//   of a byte (no sign to extend: the tile took 250 us at 1024 x 4096 x 32000 with
+//   it), and their exact sums weighted group by group. What a tile does with its
 //   logits:
 //   - loss: each row's maximum and sum of exp2 over the tile's columns, lanes by
 //     DPP, waves through LDS, 8 bytes a row and tile to the workspace; the
@@ -32,6 +33,8 @@
 #include "rank_sums.hpp"
 #include "ring.hpp"
 #include "vocab.hpp"
+
+#include <type_traits>
 
 namespace qlora {
 
@@ -112,9 +115,10 @@ __device__ __forceinline__ u32x2 bf16_part(float (&v)[4]) {
   return h;
 }
 
-// 4-bit weights: dl travels as float16 of 2^14 (p - [target]), without dloss,
-// and W as float16 of W / 8 (7 times the largest scale then fits): 11 bits of
-// each, where bf16 has 8. What is left to the rows' factor:
+// 4-bit weights: dl travels as float16 of 2^14 (p - [target]), without dloss, and
+// W as float16 of q times (scale / 8) (7 times the largest scale then fits; the
+// quotient loses bits of scales under 2^-11 only): 11 bits of each, where bf16 has
+// 8. What is left to the rows' factor:
 constexpr float kHalfUp = 16384.f, kHalfDown = 8.f / 16384.f;
 
 constexpr int max_int(int a, int b) { return a > b ? a : b; }
@@ -290,8 +294,8 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
       for (int j = 0; j < FN; ++j) {
         const int n = (wn * FN + j) * 16 + l;
         if constexpr (W4)
-          bf[j] = widen_nibbles(*reinterpret_cast<const u32x2*>(Bs + n * 64 + (((c >> 1) ^ ((n >> 2) & 3)) << 4) +
-                                                               (c & 1) * 8));
+          bf[j] = widen_nibbles16(*reinterpret_cast<const u32x2*>(Bs + n * 64 + (((c >> 1) ^ ((n >> 2) & 3)) << 4) +
+                                                                 (c & 1) * 8));
         else
           bf[j] = *reinterpret_cast<const i32x4*>(Bs + swz128(n, c));
       }
@@ -335,7 +339,7 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
     const int row = tid + NT * i;
     if (row < BM) {
       const bool none = GRAD && etg[i] < 0;
-      rsv[row] = none ? 0.f : esx[i] * kLog2e;
+      rsv[row] = none ? 0.f : esx[i] * (W4 ? kLog2e / 16.f : kLog2e);   // (the products are those of 16 q)
       tgv[row] = etg[i] >= 0 ? etg[i] - n0 : INT32_MIN;
       if constexpr (GRAD) lsv[row] = none ? INFINITY : else_[i] * kLog2e;
     }
@@ -710,8 +714,9 @@ __global__ __launch_bounds__(64 * WM * 4) void xent_dx_kernel(DxArgs a) {
   constexpr int FM = BM / WM / 16;
   constexpr int AI = BM / 8 / NW, BI = BSZ / 1024 / NW, LPS = AI + BI + (W4 ? 1 : 0);
   static_assert(AI * 8 * NW == BM && BI * 1024 * NW == BSZ, "whole instructions per wave");
-  static_assert(S * STG <= 160 * 1024, "LDS of a block");
-  __shared__ __attribute__((aligned(1024))) int8_t ring[S * STG];
+  constexpr int SCB = W4 ? NW * 128 : 0;                      // the waves' scales of a stage
+  static_assert(S * STG + SCB <= 160 * 1024, "LDS of a block");
+  __shared__ __attribute__((aligned(1024))) int8_t ring[S * STG + SCB];
 
   const int lane = threadIdx.x & 63, wid = wave_id(), l = lane & 15, q = lane >> 4;
   const int wm = wid / WN, wn = wid % WN;
@@ -781,6 +786,17 @@ __global__ __launch_bounds__(64 * WM * 4) void xent_dx_kernel(DxArgs a) {
     if (kt + S - 1 < kt1) issue(kt + S - 1, slot == 0 ? S - 1 : slot - 1);
     const int8_t* As = ring + slot * STG;
     const int8_t* Bs = As + ASZ;
+    int8_t* sch = ring + S * STG + wid * 128;               // this wave's scales / 8 of the stage's 64 entries
+    if constexpr (W4) {
+      // lane: one entry, the half of its dword by the place's parity; entries that
+      // are none get 0 (this wave's own bytes: no barrier)
+      const int v = a.v0 + kt * KC + lane, vc = v < a.N ? v : a.N - 1;
+      const uint32_t two = *reinterpret_cast<const uint32_t*>(Bs + BSZ + wid * 256 + lane * 4);
+      const uint16_t hb = (uint16_t)((vc * ngrp + (grp < ngrp ? grp : 0)) & 1 ? two >> 16 : two);
+      const float sc = v < a.V ? 0.125f * (float)__builtin_bit_cast(_Float16, hb) : 0.f;
+      *reinterpret_cast<_Float16*>(sch + lane * 2) = (_Float16)sc;
+      asm volatile("" ::: "memory");
+    }
 #pragma unroll
     for (int kk = 0; kk < KC / 32; ++kk) {
       bf16x8 af[FM];
@@ -802,25 +818,22 @@ __global__ __launch_bounds__(64 * WM * 4) void xent_dx_kernel(DxArgs a) {
             bf[j][e] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
           }
       } else {
-        uint32_t w[8];
-        float sc[8];
-        const uint32_t* sp = reinterpret_cast<const uint32_t*>(Bs + BSZ + wid * 256) + 32 * kk + 8 * q;
-        const int v = a.v0 + (a.parts == 1 ? kt : kt % nkv) * KC + 32 * kk + 8 * q;
+        // rows 2 e and 2 e + 1 share a register: nibble j of each, with its sign bit
+        // turned over, under the exponent of 1024 is 1032 + q in float16
+        const u32x4 s4 = *reinterpret_cast<const u32x4*>(sch + (32 * kk + 8 * q) * 2);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          w[e] = *reinterpret_cast<const uint16_t*>(row + e * RB + ((wn ^ q) << 5) + 2 * l);
-          const int half = ((v + e) * ngrp + grp) & 1;       // (past N the clamped entry's half: masked)
-          const uint16_t hb = (uint16_t)(sp[e] >> (16 * half));
-          sc[e] = v + e < a.V ? 0.125f * (float)__builtin_bit_cast(_Float16, hb) : 0.f;
-        }
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t lo = *reinterpret_cast<const uint16_t*>(row + (2 * e) * RB + ((wn ^ q) << 5) + 2 * l);
+          const uint32_t hi = *reinterpret_cast<const uint16_t*>(row + (2 * e + 1) * RB + ((wn ^ q) << 5) + 2 * l);
+          const uint32_t w = (lo | (hi << 16)) ^ 0x88888888u;
+          const uint32_t s2 = s4[e];                       // (a bit cast of a vector's element takes its first)
+          const f16x2 sc = __builtin_bit_cast(f16x2, s2);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = (float)((int)(w[2 * e] << (28 - 4 * j)) >> 28) * sc[2 * e];
-            const float y = (float)((int)(w[2 * e + 1] << (28 - 4 * j)) >> 28) * sc[2 * e + 1];
-            bf[j][e] = pk_f16(x, y);
+          for (int j = 0; j < 4; ++j) {
+            const f16x2 x = __builtin_bit_cast(f16x2, ((w >> (4 * j)) & 0x000f000fu) | 0x64006400u);
+            bf[j][e] = __builtin_bit_cast(uint32_t, (x - f16x2{(_Float16)1032.f, (_Float16)1032.f}) * sc);
           }
+        }
       }
 #pragma unroll
       for (int i = 0; i < FM; ++i)
@@ -895,16 +908,14 @@ __global__ __launch_bounds__(256) void xent_reduce_kernel(ReduceArgs a) {
 }
 
 // dx = factor times the splits' sums + s u A^T: a thread has four features (and
-// their rows of A) for kJoinRows rows.
-constexpr int kJoinRows = 16;
-template <typename OutT, int R>
+// their rows of A) for ROWS rows.
+template <typename OutT, int R, int ROWS>
 __global__ __launch_bounds__(256) void xent_dx_join_kernel(const float* dxp, int splits, int M, int K, int r, float s,
                                                            const float* u, const float* A, Ids ids, const float* dloss,
                                                            float down, OutT* dx) {
   const int units = K / 4, k = (int)((blockIdx.x * 256 + threadIdx.x) % (unsigned)units) * 4;
-  const int m0 = (int)((blockIdx.x * 256 + threadIdx.x) / (unsigned)units) * kJoinRows;
+  const int m0 = (int)((blockIdx.x * 256 + threadIdx.x) / (unsigned)units) * ROWS;
   if (m0 >= M) return;
-  const int m1 = m0 + kJoinRows < M ? m0 + kJoinRows : M;
   const long n = (long)M * K;
   float ar[4][R > 0 ? R : 1];
   if constexpr (R > 0) {
@@ -913,7 +924,10 @@ __global__ __launch_bounds__(256) void xent_dx_join_kernel(const float* dxp, int
 #pragma unroll
       for (int j = 0; j < R; ++j) ar[c][j] = j < r ? A[(long)(k + c) * r + j] : 0.f;
   }
-  for (int m = m0; m < m1; ++m) {
+#pragma unroll
+  for (int i0 = 0; i0 < ROWS; ++i0) {
+    const int m = m0 + i0;
+    if (m >= M) return;
     const float f = row_factor(ids, dloss, m) * down;
     const float* p = dxp + (long)m * K + k;
     f32x4 v = *reinterpret_cast<const f32x4*>(p);
@@ -940,18 +954,26 @@ __global__ __launch_bounds__(256) void xent_dx_join_kernel(const float* dxp, int
 template <typename OutT>
 void dx_join(const VocabLayer& L, int M, Ids ids, const float* dloss, const XentPlan& plan, const XentBuffers& buf,
              void* dx, hipStream_t st) {
-  const long threads = (long)(L.K / 4) * ((M + kJoinRows - 1) / kJoinRows);
+  // four rows a thread where that leaves eight waves a SIMD, else one
+  const int rows = (long)(L.K / 4) * M >= 4L * 64 * 8 * 4 * kCUs ? 4 : 1;
+  const long threads = (long)(L.K / 4) * ((M + rows - 1) / rows);
   const dim3 grid((unsigned)((threads + 255) / 256));
   const float down = L.fmt == 0 ? 1.f : kHalfDown;
   OutT* out = static_cast<OutT*>(dx);
-#define JOIN(R) \
-  xent_dx_join_kernel<OutT, R><<<grid, 256, 0, st>>>(buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids, dloss, down, out)
-  if (L.r == 0) JOIN(0);
-  else if (L.r <= 4) JOIN(4);
-  else if (L.r <= 8) JOIN(8);
-  else if (L.r <= 16) JOIN(16);
-  else JOIN(32);
-#undef JOIN
+  const auto launch = [&](auto rank) {
+    constexpr int R = decltype(rank)::value;
+    if (rows == 4)
+      xent_dx_join_kernel<OutT, R, 4><<<grid, 256, 0, st>>>(buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids,
+                                                           dloss, down, out);
+    else
+      xent_dx_join_kernel<OutT, R, 1><<<grid, 256, 0, st>>>(buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids,
+                                                           dloss, down, out);
+  };
+  if (L.r == 0) launch(std::integral_constant<int, 0>());
+  else if (L.r <= 4) launch(std::integral_constant<int, 4>());
+  else if (L.r <= 8) launch(std::integral_constant<int, 8>());
+  else if (L.r <= 16) launch(std::integral_constant<int, 16>());
+  else launch(std::integral_constant<int, 32>());
 }
 
 // dA = s x^T u over the rows that have a target: partial sums, then their total.
@@ -1048,8 +1070,9 @@ XentPlan xent_plan(const VocabLayer& L, int vocab, int M, int dtype) {
   const int rows = dx_rows(M);
   const long tiles = (long)((M + rows - 1) / rows) * ((L.K + 255) / 256);
   const int nk = p.parts * (p.piece / 64);
-  p.splits = 1;
-  while (tiles * p.splits * 2 <= kCUs && nk / (p.splits * 2) >= 8) p.splits *= 2;
+  // as many splits as leave one block a compute unit, each of at least four stages
+  p.splits = (int)(kCUs / tiles < 1 ? 1 : kCUs / tiles);
+  if (p.splits > nk / 4) p.splits = nk / 4 < 1 ? 1 : nk / 4;
   p.g = (size_t)p.parts * M * p.piece;
   p.dxp = (size_t)p.splits * M * L.K;
   if (L.r > 0) {

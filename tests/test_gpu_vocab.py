@@ -135,7 +135,9 @@ class Case:
         if self.fmt == "w4g128":                           # both operands in float16
             rel = 2 * H16 + H16 * H16
             tiny = 2.0 ** -38 * np.abs(g)[:, None] * np.ones_like(dl)
-            wtiny = 2.0 ** -22                             # a weight's step near 0, times 8
+            # a weight is fl16(q fl16(scale / 8)): near 0 each is off by half of 2^-24,
+            # the scale's error times |q| <= 7; times 8
+            wtiny = 8 * 2.0 ** -22
             tdx = (tdl + rel * np.abs(dl) + tiny) @ W + (np.abs(dl) + tdl) @ np.full_like(W, wtiny)
         elif self.dtype == "bf16":
             tdx = (tdl + (U16 + 2 * U32) * np.abs(dl)) @ W
