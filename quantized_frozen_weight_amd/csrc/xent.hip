@@ -156,6 +156,7 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
   // loads per wave and stage: 8 rows of 128 bytes (16 of 64) an instruction
   constexpr int AI = BM / 8 / NW, BI = BN / (W4 ? 16 : 8) / NW, LPS = AI + BI;
   static_assert(AI * 8 * NW == BM && BI * (W4 ? 16 : 8) * NW == BN, "whole instructions per wave");
+  static_assert(BK == 128, "two steps of 64 a stage");
   __shared__ __attribute__((aligned(1024))) int8_t lds[Lds::BYTES];
   int8_t* ring = lds;
   const _Float16* SC = reinterpret_cast<const _Float16*>(lds + S * STG);
@@ -283,30 +284,46 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
 #pragma unroll
         for (int j = 0; j < FN; ++j) part[i][j] = i32x4{0, 0, 0, 0};
     }
+    i32x4 af[2][FM], bf[2][FN];
 #pragma unroll
-    for (int kk = 0; kk < BK / 64; ++kk) {
+    for (int kk = 0; kk < 2; ++kk) {
       const int c = kk * 4 + q;
-      i32x4 af[FM], bf[FN];
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-        af[i] = *reinterpret_cast<const i32x4*>(As + swz128((wm * FM + i) * 16 + l, c));
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         const int n = (wn * FN + j) * 16 + l;
         if constexpr (W4)
-          bf[j] = widen_nibbles16(*reinterpret_cast<const u32x2*>(Bs + n * 64 + (((c >> 1) ^ ((n >> 2) & 3)) << 4) +
-                                                                 (c & 1) * 8));
+          bf[kk][j] = widen_nibbles16(*reinterpret_cast<const u32x2*>(Bs + n * 64 + (((c >> 1) ^ ((n >> 2) & 3)) << 4) +
+                                                                     (c & 1) * 8));
         else
-          bf[j] = *reinterpret_cast<const i32x4*>(Bs + swz128(n, c));
+          bf[kk][j] = *reinterpret_cast<const i32x4*>(Bs + swz128(n, c));
       }
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        af[kk][i] = *reinterpret_cast<const i32x4*>(As + swz128((wm * FM + i) * 16 + l, c));
+    }
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
           // transposed: lane l holds row l of the block, entries 4 q .. 4 q + 3
-          if constexpr (W4) part[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[j], af[i], part[i][j], 0, 0, 0);
-          else acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[j], af[i], acc[i][j], 0, 0, 0);
+          if constexpr (W4)
+            part[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[kk][j], af[kk][i], part[i][j], 0, 0, 0);
+          else
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[kk][j], af[kk][i], acc[i][j], 0, 0, 0);
         }
+    if constexpr (!W4) {
+      // The order of the stage's instructions: the operands of the first products,
+      // then two reads behind every FN products until all are under way (left to
+      // itself the compiler waits for every pair of reads before the next eight)
+      __builtin_amdgcn_sched_group_barrier(0x100, FN + 2, 0);
+#pragma unroll
+      for (int g = 0; g < (2 * (FM + FN) - FN - 2) / 2; ++g) {
+        __builtin_amdgcn_sched_group_barrier(0x008, FN, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, 2 * FM * FN - FN * ((2 * (FM + FN) - FN - 2) / 2), 0);
     }
     if constexpr (W4) {
 #pragma unroll
