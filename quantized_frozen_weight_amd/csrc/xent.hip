@@ -25,7 +25,7 @@
 //   comes as three bf16 parts, the contraction run over each. The contraction of
 //   a piece is split where there are few tiles; every split adds into a float32
 //   buffer of its own, piece after piece.
-// Pieces are as large as 128 MB of dl allow. Sums are in a fixed order.
+// Pieces are as large as 256 MB of dl allow. Sums are in a fixed order.
 #include "abi.hpp"
 #include "bwd_common.hpp"
 #include "launch.hpp"
@@ -70,7 +70,6 @@ struct LogitArgs {
   const float* dloss;
   uint16_t* g;           // [parts][M][ldg]
   long ldg, gstride;
-  int parts;
   float* up;             // [tiles_x][M][r]
   float* dbp;            // [tiles_m][r][ldg]
 };
@@ -147,8 +146,10 @@ struct LogitLds {
   static_assert(BYTES <= 160 * 1024, "LDS of a block");
 };
 
-template <bool W4, int BM, int BN, int WM, int WN, int S, int G, int R, bool GRAD>
+// PARTS: 0 the loss, 1 the gradient with dl in 16 bits, 3 in three bf16 parts.
+template <bool W4, int BM, int BN, int WM, int WN, int S, int G, int R, int PARTS>
 __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) {
+  constexpr bool GRAD = PARTS > 0;
   using Lds = LogitLds<W4, BM, BN, WM, WN, S, G, R, GRAD>;
   constexpr int NW = WM * WN, NT = 64 * NW, BK = 128;
   constexpr int ASZ = Lds::ASZ, STG = Lds::STG;
@@ -580,12 +581,13 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
 #pragma unroll
           for (int ii = 0; ii < 4; ++ii) x[j][ii] *= sw[j][ii];
       }
-      for (int p = 0; p < a.parts; ++p) {
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) {
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
           u32x2 w;
           if constexpr (W4) w = u32x2{pk_f16(x[j][0] * kHalfUp, x[j][1] * kHalfUp), pk_f16(x[j][2] * kHalfUp, x[j][3] * kHalfUp)};
-          else if (a.parts == 1) w = u32x2{pk_bf16(x[j][0], x[j][1]), pk_bf16(x[j][2], x[j][3])};
+          else if (p == PARTS - 1) w = u32x2{pk_bf16(x[j][0], x[j][1]), pk_bf16(x[j][2], x[j][3])};
           else w = bf16_part(x[j]);
           *reinterpret_cast<u32x2*>(strip + l * Lds::PITCH + j * 32 + q * 8) = w;
         }
@@ -631,25 +633,21 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
-          for (int jb = 0; jb < RB; ++jb)
-#pragma unroll
-            for (int ii = 0; ii < 4; ++ii) {
-              const int rank = 16 * jb + 4 * q + ii;
-              float* p = ub + (wr0 + i * 16 + l) * R + rank;
-              if (rank < R) *p = w == 0 ? uacc[i][jb][ii] : *p + uacc[i][jb][ii];
-            }
+          for (int jb = 0; jb < RB; ++jb) {
+            const int rank = 16 * jb + 4 * q;
+            f32x4* p = reinterpret_cast<f32x4*>(ub + (wr0 + i * 16 + l) * R + rank);
+            if (rank < R) *p = w == 0 ? uacc[i][jb] : *p + uacc[i][jb];
+          }
       }
       if (wm == w) {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int jb = 0; jb < RB; ++jb)
-#pragma unroll
-            for (int ii = 0; ii < 4; ++ii) {
-              const int rank = 16 * jb + l;
-              float* p = db + rank * BN + wc0 + j * 16 + 4 * q + ii;
-              if (rank < R) *p = w == 0 ? dbacc[j][jb][ii] : *p + dbacc[j][jb][ii];
-            }
+          for (int jb = 0; jb < RB; ++jb) {
+            const int rank = 16 * jb + l;
+            f32x4* p = reinterpret_cast<f32x4*>(db + rank * BN + wc0 + j * 16 + 4 * q);
+            if (rank < R) *p = w == 0 ? dbacc[j][jb] : *p + dbacc[j][jb];
+          }
       }
       __syncthreads();
     }
@@ -924,67 +922,68 @@ __global__ __launch_bounds__(256) void xent_reduce_kernel(ReduceArgs a) {
   }
 }
 
-// dx = factor times the splits' sums + s u A^T: a thread has four features (and
-// their rows of A) for ROWS rows.
-template <typename OutT, int R, int ROWS>
+// dx = factor times the splits' sums + s u A^T. A wave takes 16 rows of 64
+// features, lane (l, q) the 16 features of quarter q of row l; the adapter's part is
+// formed on v_mfma_f32_16x16x4_f32 in that layout (as the lookup's: a thread that
+// read its features' rows of A for itself took 49 us for 4096 x 768 at rank 8).
+template <typename OutT, int R>
 __global__ __launch_bounds__(256) void xent_dx_join_kernel(const float* dxp, int splits, int M, int K, int r, float s,
                                                            const float* u, const float* A, Ids ids, const float* dloss,
                                                            float down, OutT* dx) {
-  const int units = K / 4, k = (int)((blockIdx.x * 256 + threadIdx.x) % (unsigned)units) * 4;
-  const int m0 = (int)((blockIdx.x * 256 + threadIdx.x) / (unsigned)units) * ROWS;
-  if (m0 >= M) return;
+  const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
+  const int m = blockIdx.x * 16 + l, mc = m < M ? m : M - 1;
+  const int d0 = ((int)blockIdx.y * 4 + ((int)threadIdx.x >> 6)) * 64, k = d0 + 16 * q, kc = k < K ? k : 0;
   const long n = (long)M * K;
-  float ar[4][R > 0 ? R : 1];
+  const float* p = dxp + (long)mc * K + kc;
+  f32x4 v[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) v[b] = *reinterpret_cast<const f32x4*>(p + 4 * b);
+  const float f = row_factor(ids, dloss, mc) * down;
+  f32x4 low[4];
   if constexpr (R > 0) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int b = 0; b < 4; ++b) low[b] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < R; ++j) ar[c][j] = j < r ? A[(long)(k + c) * r + j] : 0.f;
-  }
+    for (int c = 0; c < R / 4; ++c) {
+      const int j = 4 * c + q, jc = j < r ? j : 0;
+      const float uv = j < r ? u[(long)mc * r + jc] : 0.f;
 #pragma unroll
-  for (int i0 = 0; i0 < ROWS; ++i0) {
-    const int m = m0 + i0;
-    if (m >= M) return;
-    const float f = row_factor(ids, dloss, m) * down;
-    const float* p = dxp + (long)m * K + k;
-    f32x4 v = *reinterpret_cast<const f32x4*>(p);
-    for (int i = 1; i < splits; ++i) v += *reinterpret_cast<const f32x4*>(p + i * n);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] *= f;
-    if constexpr (R > 0) {
-      f32x4 low{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        const float uj = u[(long)m * r + (j < r ? j : 0)];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) low[c] = __builtin_fmaf(uj, ar[c][j], low[c]);
+      for (int b = 0; b < 4; ++b) {
+        const int d = d0 + 16 * (l >> 2) + 4 * b + (l & 3);
+        const float av = d < K && j < r ? A[(long)(d < K ? d : 0) * r + jc] : 0.f;
+        low[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(av, uv, low[b], 0, 0, 0);
       }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = __builtin_fmaf(s, low[c], v[c]);
     }
-    OutT* out = dx + (long)m * K + k;
-    if constexpr (sizeof(OutT) == 4) *reinterpret_cast<f32x4*>(out) = v;
-    else *reinterpret_cast<u32x2*>(out) = u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+  }
+  for (int i = 1; i < splits; ++i)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) v[b] += *reinterpret_cast<const f32x4*>(p + i * n + 4 * b);
+  if (m >= M || k >= K) return;
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[b][c] = R > 0 ? __builtin_fmaf(s, low[b][c], v[b][c] * f) : v[b][c] * f;
+  OutT* out = dx + (long)m * K + k;
+  if constexpr (sizeof(OutT) == 4) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) *reinterpret_cast<f32x4*>(out + 4 * b) = v[b];
+  } else {
+#pragma unroll
+    for (int b = 0; b < 4; b += 2)
+      *reinterpret_cast<u32x4*>(out + 4 * b) = u32x4{pk_bf16(v[b][0], v[b][1]), pk_bf16(v[b][2], v[b][3]),
+                                                     pk_bf16(v[b + 1][0], v[b + 1][1]), pk_bf16(v[b + 1][2], v[b + 1][3])};
   }
 }
 
 template <typename OutT>
 void dx_join(const VocabLayer& L, int M, Ids ids, const float* dloss, const XentPlan& plan, const XentBuffers& buf,
              void* dx, hipStream_t st) {
-  // four rows a thread where that leaves eight waves a SIMD, else one
-  const int rows = (long)(L.K / 4) * M >= 4L * 64 * 8 * 4 * kCUs ? 4 : 1;
-  const long threads = (long)(L.K / 4) * ((M + rows - 1) / rows);
-  const dim3 grid((unsigned)((threads + 255) / 256));
+  const dim3 grid((unsigned)((M + 15) / 16), (unsigned)((L.K + 255) / 256));
   const float down = L.fmt == 0 ? 1.f : kHalfDown;
   OutT* out = static_cast<OutT*>(dx);
   const auto launch = [&](auto rank) {
-    constexpr int R = decltype(rank)::value;
-    if (rows == 4)
-      xent_dx_join_kernel<OutT, R, 4><<<grid, 256, 0, st>>>(buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids,
-                                                           dloss, down, out);
-    else
-      xent_dx_join_kernel<OutT, R, 1><<<grid, 256, 0, st>>>(buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids,
-                                                           dloss, down, out);
+    xent_dx_join_kernel<OutT, decltype(rank)::value><<<grid, 256, 0, st>>>(
+        buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids, dloss, down, out);
   };
   if (L.r == 0) launch(std::integral_constant<int, 0>());
   else if (L.r <= 4) launch(std::integral_constant<int, 4>());
@@ -1008,34 +1007,36 @@ __global__ __launch_bounds__(256) void xent_da_total_kernel(const float* part, i
 }
 
 // ---- launches ---------------------------------------------------------------------
-template <bool W4, int BM, int BN, int WM, int WN, int S, int G, bool GRAD>
+template <bool W4, int BM, int BN, int WM, int WN, int S, int G, int PARTS>
 void logits_ranks(LogitArgs& a, int cols, hipStream_t st) {
   a.tiles_m = (a.M + BM - 1) / BM;
   a.tiles_x = (cols + BN - 1) / BN;
   const dim3 grid((unsigned)(a.tiles_m * a.tiles_x));
   constexpr int NT = 64 * WM * WN;
-  if (a.r == 0) xent_logits_kernel<W4, BM, BN, WM, WN, S, G, 0, GRAD><<<grid, NT, 0, st>>>(a);
-  else if (a.r <= 4) xent_logits_kernel<W4, BM, BN, WM, WN, S, G, 4, GRAD><<<grid, NT, 0, st>>>(a);
-  else if (a.r <= 8) xent_logits_kernel<W4, BM, BN, WM, WN, S, G, 8, GRAD><<<grid, NT, 0, st>>>(a);
+  if (a.r == 0) xent_logits_kernel<W4, BM, BN, WM, WN, S, G, 0, PARTS><<<grid, NT, 0, st>>>(a);
+  else if (a.r <= 4) xent_logits_kernel<W4, BM, BN, WM, WN, S, G, 4, PARTS><<<grid, NT, 0, st>>>(a);
+  else if (a.r <= 8) xent_logits_kernel<W4, BM, BN, WM, WN, S, G, 8, PARTS><<<grid, NT, 0, st>>>(a);
   else if (BM * BN > 128 * 128 || a.r <= 16)
-    xent_logits_kernel<W4, BM, BN, WM, WN, S, G, 16, GRAD><<<grid, NT, 0, st>>>(a);
+    xent_logits_kernel<W4, BM, BN, WM, WN, S, G, 16, PARTS><<<grid, NT, 0, st>>>(a);
   else if constexpr (BM * BN <= 128 * 128)
-    xent_logits_kernel<W4, BM, BN, WM, WN, S, G, 32, GRAD><<<grid, NT, 0, st>>>(a);
+    xent_logits_kernel<W4, BM, BN, WM, WN, S, G, 32, PARTS><<<grid, NT, 0, st>>>(a);
 }
 
 // The tiles of a launch over `cols` entries; fills tiles_m and tiles_x.
-template <bool GRAD>
+template <int PARTS>
 void logits(LogitArgs& a, int fmt, int cols, hipStream_t st) {
   if (fmt == 0) {
-    if (a.M <= 32) logits_ranks<false, 32, 256, 1, 4, 4, 1, GRAD>(a, cols, st);
-    else if (a.M > 128 && a.r <= 16) logits_ranks<false, 256, 256, 2, 4, 2, 1, GRAD>(a, cols, st);
-    else logits_ranks<false, 128, 128, 2, 2, 2, 1, GRAD>(a, cols, st);
+    if (a.M <= 32) logits_ranks<false, 32, 256, 1, 4, 4, 1, PARTS>(a, cols, st);
+    else if (a.M > 128 && a.r <= 16) logits_ranks<false, 256, 256, 2, 4, 2, 1, PARTS>(a, cols, st);
+    else logits_ranks<false, 128, 128, 2, 2, 2, 1, PARTS>(a, cols, st);
+  } else if constexpr (PARTS == 3) {
+    return;                                                // (float32 has no 4-bit layers)
   } else if (a.M <= 32) {
-    if (a.K <= 4096) logits_ranks<true, 32, 128, 1, 4, 3, 32, GRAD>(a, cols, st);
-    else logits_ranks<true, 32, 128, 1, 4, 3, 128, GRAD>(a, cols, st);
+    if (a.K <= 4096) logits_ranks<true, 32, 128, 1, 4, 3, 32, PARTS>(a, cols, st);
+    else logits_ranks<true, 32, 128, 1, 4, 3, 128, PARTS>(a, cols, st);
   } else {
-    if (a.K <= 4096) logits_ranks<true, 128, 128, 2, 2, 2, 32, GRAD>(a, cols, st);
-    else logits_ranks<true, 128, 128, 2, 2, 2, 128, GRAD>(a, cols, st);
+    if (a.K <= 4096) logits_ranks<true, 128, 128, 2, 2, 2, 32, PARTS>(a, cols, st);
+    else logits_ranks<true, 128, 128, 2, 2, 2, 128, PARTS>(a, cols, st);
   }
 }
 
@@ -1070,7 +1071,7 @@ void launch_xent_fwd(const VocabLayer& L, int M, Ids ids, const int8_t* xq, cons
   LogitArgs a = logit_args(L, M, ids, xq, sx, t);
   a.tl = part;
   a.part = part + M;
-  logits<false>(a, L.fmt, ids.vocab, st);
+  logits<0>(a, L.fmt, ids.vocab, st);
   int rows = 1;
   while (rows < 64 && rows < M) rows <<= 1;
   xent_join_kernel<<<dim3((unsigned)((M + rows - 1) / rows)), 1024, 0, st>>>(a.part, a.tl, ids, a.tiles_x, M, rows,
@@ -1080,10 +1081,13 @@ void launch_xent_fwd(const VocabLayer& L, int M, Ids ids, const int8_t* xq, cons
 XentPlan xent_plan(const VocabLayer& L, int vocab, int M, int dtype) {
   XentPlan p{};
   p.parts = dtype == 0 ? 3 : 1;
-  const int all = (vocab + 255) / 256 * 256;
-  const long most = (64L << 20) / p.parts / M / 256 * 256;      // 128 MB of dl
-  p.piece = (int)(most < 512 ? 512 : most > all ? all : most);
-  if (p.piece > all) p.piece = all;
+  // pieces of up to 256 MB of dl (the sums of dx are read and written once a
+  // piece), of whole rounds of 256 x 256 tiles over the chip where they hold one
+  // (4096 x 768 x 50257 at rank 8: 1095 us, 1156 in two equal pieces, 1142 at 128 MB)
+  const long most = (128L << 20) / p.parts / M / 256 * 256, tiles_m = (M + 255) / 256;
+  const long round = 256 * (kCUs / tiles_m < 1 ? 1 : kCUs / tiles_m), all = ((long)vocab + 255) / 256 * 256;
+  const long fit = most >= round ? most / round * round : most < 512 ? 512 : most;
+  p.piece = (int)(fit > all ? all : fit);
   const int rows = dx_rows(M);
   const long tiles = (long)((M + rows - 1) / rows) * ((L.K + 255) / 256);
   const int nk = p.parts * (p.piece / 64);
@@ -1110,9 +1114,10 @@ void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const void*
     const int vc = V - v0 < plan.piece ? V - v0 : plan.piece;
     const long ldg = (vc + 255) / 256 * 256;
     LogitArgs a = logit_args(L, M, ids, xq, sx, t);
-    a.v0 = v0; a.lse = lse; a.dloss = dloss; a.g = buf.g; a.ldg = ldg; a.gstride = M * ldg; a.parts = plan.parts;
+    a.v0 = v0; a.lse = lse; a.dloss = dloss; a.g = buf.g; a.ldg = ldg; a.gstride = M * ldg;
     a.up = buf.up; a.dbp = buf.dbp;
-    logits<true>(a, L.fmt, (int)ldg, st);
+    if (plan.parts == 1) logits<1>(a, L.fmt, (int)ldg, st);
+    else logits<3>(a, L.fmt, (int)ldg, st);
     if (dx != nullptr) {
       DxArgs d{};
       d.M = M; d.N = L.N; d.K = L.K; d.V = V; d.g = buf.g; d.ldg = ldg; d.gstride = a.gstride; d.parts = plan.parts;

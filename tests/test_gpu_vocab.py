@@ -314,7 +314,7 @@ def test_loss_and_its_gradient(M, K, vocab, r, fmt, dtype, itype):
 
 
 @pytest.mark.parametrize("M,K,vocab,r,fmt,dtype", [
-    (131072, 16, 1100, 3, "w8", "bf16"), (43000, 16, 1100, 0, "w8", "f32"), (131072, 128, 560, 0, "w4g128", "bf16")])
+    (131072, 16, 1100, 3, "w8", "bf16"), (87000, 16, 1100, 0, "w8", "f32"), (262144, 128, 560, 0, "w4g128", "bf16")])
 def test_gradient_in_several_pieces(M, K, vocab, r, fmt, dtype):
     """So many rows that the vocabulary is taken in two or three pieces."""
     say("several pieces", M, K, vocab, r, fmt, dtype)
