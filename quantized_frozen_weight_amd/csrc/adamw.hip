@@ -32,12 +32,22 @@ namespace {
 constexpr int kItems = 48;           // tensors per launch
 constexpr int kChunk = 4096;         // elements per block of the update
 constexpr int kNormSums = 512;       // about as many partial sums of the norm
+constexpr int kSmall = 8192;         // elements in all that one block steps
 
 // What the norm launch leaves for the update.
 struct Hyper {
   float lr, c1, root_c2;             // learning rate, 1 - beta1^k, sqrt(1 - beta2^k)
   int32_t k;
 };
+
+__device__ __forceinline__ Hyper hyper_of(int32_t k, double lr, double beta1, double beta2, const float* lr_dev) {
+  Hyper h;
+  h.lr = lr_dev != nullptr ? *lr_dev : (float)lr;
+  h.c1 = (float)(1.0 - pow(beta1, (double)k));
+  h.root_c2 = sqrtf((float)(1.0 - pow(beta2, (double)k)));
+  h.k = k;
+  return h;
+}
 
 struct NormArgs {
   const float* g[kItems];
@@ -75,14 +85,9 @@ __global__ __launch_bounds__(256) void adamw_norm_kernel(NormArgs a) {
   __shared__ double red[4];
   const int tid = threadIdx.x, b = blockIdx.x;
   if (a.first && b == 0 && tid == 0) {
-    const int32_t k = *a.step + 1;
-    Hyper h;
-    h.lr = a.lr_dev != nullptr ? *a.lr_dev : (float)a.lr;
-    h.c1 = (float)(1.0 - pow(a.beta1, (double)k));
-    h.root_c2 = sqrtf((float)(1.0 - pow(a.beta2, (double)k)));
-    h.k = k;
+    const Hyper h = hyper_of(*a.step + 1, a.lr, a.beta1, a.beta2, a.lr_dev);
     *a.hyper = h;
-    *a.step = k;
+    *a.step = h.k;
   }
   if (a.sums == nullptr) return;
   const int i = item_of(a.bstart, a.count, b);
@@ -175,24 +180,24 @@ __device__ __forceinline__ float of_code(uint32_t c, int e) {
   return __builtin_ldexpf(__builtin_ldexpf(__uint_as_float(c << (23 - BITS)), 120), e);
 }
 
-template <bool S8>
-__global__ __launch_bounds__(256) void adamw_update_kernel(UpdateArgs a) {
-  __shared__ double red[4];
-  const int tid = threadIdx.x, b = blockIdx.x;
-  const int i = item_of(a.bstart, a.count, b);
-  const UpdateItem& it = a.it[i];
-  const int n = it.n;
-  const int c0 = (b - a.bstart[i]) * kChunk;
-  constexpr int U = kChunk / 1024;
+// What every element of a launch shares.
+struct Step {
+  float beta1, rest1, beta2, rest2, eps;
+  float rate, root_c2, coef;          // lr / (1 - beta1^k); coef: of the gradient
+  int clip;
+  uint32_t key;                       // of the hash: step and seed
+};
 
-  // the block's operands, from clamped places (a piece past the end reads the
-  // first one again, a ragged last piece is read by elements)
-  float p[U][4], g[U][4], m[U][4], v[U][4];
-  uint32_t mc[U], vc[U];
-  int ms[U], vs[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int e = c0 + 1024 * u + 4 * tid;
+// Four elements of one tensor from element e on, in registers.
+template <bool S8> struct Piece {
+  float p[4], g[4], m[4], v[4];
+  uint32_t mc, vc;
+  int ms, vs;
+
+  // From clamped places: a piece past the end reads the first one again, a ragged
+  // last piece is read by elements.
+  __device__ __forceinline__ void load(const UpdateItem& it, int e) {
+    const int n = it.n;
     if (e + 4 <= n || e >= n) {
       const long at = e < n ? e : 0;
       const bool whole = n >= 4;                            // (n < 4: nothing is whole, and nothing is used)
@@ -200,77 +205,62 @@ __global__ __launch_bounds__(256) void adamw_update_kernel(UpdateArgs a) {
       const f32x4 pv = whole ? *reinterpret_cast<const f32x4*>(it.p + at) : z;
       const f32x4 gv = whole ? *reinterpret_cast<const f32x4*>(it.g + at) : z;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) { p[u][c] = pv[c]; g[u][c] = gv[c]; }
+      for (int c = 0; c < 4; ++c) { p[c] = pv[c]; g[c] = gv[c]; }
       if constexpr (S8) {
-        mc[u] = whole ? *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(it.m) + at) : 0u;
-        vc[u] = whole ? *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(it.v) + at) : 0u;
+        mc = whole ? *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(it.m) + at) : 0u;
+        vc = whole ? *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(it.v) + at) : 0u;
       } else {
         const f32x4 mv = whole ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(it.m) + at) : z;
         const f32x4 vv = whole ? *reinterpret_cast<const f32x4*>(static_cast<const float*>(it.v) + at) : z;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) { m[u][c] = mv[c]; v[u][c] = vv[c]; }
+        for (int c = 0; c < 4; ++c) { m[c] = mv[c]; v[c] = vv[c]; }
       }
     } else {
-      if constexpr (S8) mc[u] = vc[u] = 0u;
+      if constexpr (S8) mc = vc = 0u;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const int at = e + c < n ? e + c : e;
-        p[u][c] = it.p[at];
-        g[u][c] = e + c < n ? it.g[at] : 0.f;
+        p[c] = it.p[at];
+        g[c] = e + c < n ? it.g[at] : 0.f;
         if constexpr (S8) {
           if (e + c < n) {
-            mc[u] |= (uint32_t)static_cast<const uint8_t*>(it.m)[at] << (8 * c);
-            vc[u] |= (uint32_t)static_cast<const uint8_t*>(it.v)[at] << (8 * c);
+            mc |= (uint32_t)static_cast<const uint8_t*>(it.m)[at] << (8 * c);
+            vc |= (uint32_t)static_cast<const uint8_t*>(it.v)[at] << (8 * c);
           }
         } else {
-          m[u][c] = static_cast<const float*>(it.m)[at];
-          v[u][c] = static_cast<const float*>(it.v)[at];
+          m[c] = static_cast<const float*>(it.m)[at];
+          v[c] = static_cast<const float*>(it.v)[at];
         }
       }
     }
     if constexpr (S8) {
-      ms[u] = it.ms[e < n ? e / 32 : 0];
-      vs[u] = it.vs[e < n ? e / 32 : 0];
+      ms = it.ms[e < n ? e / 32 : 0];
+      vs = it.vs[e < n ? e / 32 : 0];
     }
   }
 
-  const Hyper h = *a.hyper;
-  float coef = 1.f;
-  if (a.sums != nullptr) {
-    double sum = 0.0;
-    for (int q = tid; q < a.sums_n; q += 256) sum += a.sums[q];
-    const float norm = (float)sqrt(block_sum(sum, red));
-    const bool skip = a.clip && !(norm <= 3.4028234e38f);   // infinite or NaN: nothing is moved
-    if (a.first && b == 0 && tid == 0) {
-      if (a.norm != nullptr) *a.norm = norm;
-      if (skip) *a.step = h.k - 1;
-    }
-    if (skip) return;
-    if (a.clip) coef = a.clip_norm / (norm > a.clip_norm ? norm : a.clip_norm);
-  }
-  const float keep = 1.f - h.lr * it.decay, rate = h.lr / h.c1;
-
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int e = c0 + 1024 * u + 4 * tid;
+  // The step, and its results written. All lanes of a wave together (a group's
+  // maximum crosses lanes); keep: 1 - lr decay of the tensor, item: its number.
+  __device__ __forceinline__ void update(const UpdateItem& it, int e, int item, float keep, const Step& s) {
+    const int n = it.n;
     float root[4];
     if constexpr (S8) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint32_t mb = (mc[u] >> (8 * c)) & 0xffu, vb = (vc[u] >> (8 * c)) & 0xffu;
-        const float mv = of_code<4>(mb & 127u, ms[u] - 127), rv = of_code<5>(vb, vs[u] - 127);
-        m[u][c] = ms[u] == 255 ? __uint_as_float(0x7fc00000u) : (mb & 128u) ? -mv : mv;
-        v[u][c] = vs[u] == 255 ? __uint_as_float(0x7fc00000u) : rv * rv;
+        const uint32_t mb = (mc >> (8 * c)) & 0xffu, vb = (vc >> (8 * c)) & 0xffu;
+        const float mv = of_code<4>(mb & 127u, ms - 127), rv = of_code<5>(vb, vs - 127);
+        m[c] = ms == 255 ? __uint_as_float(0x7fc00000u) : (mb & 128u) ? -mv : mv;
+        v[c] = vs == 255 ? __uint_as_float(0x7fc00000u) : rv * rv;
       }
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const float gc = a.clip ? g[u][c] * coef : g[u][c];
-      m[u][c] = a.beta1 * m[u][c] + a.rest1 * gc;
-      v[u][c] = a.beta2 * v[u][c] + a.rest2 * (gc * gc);
-      root[c] = sqrtf(v[u][c]);
-      const float moved = p[u][c] * keep;
-      p[u][c] = moved - rate * (m[u][c] / (root[c] / h.root_c2 + a.eps));
+      const float gc = s.clip ? g[c] * s.coef : g[c];
+      m[c] = s.beta1 * m[c] + s.rest1 * gc;
+      v[c] = s.beta2 * v[c] + s.rest2 * (gc * gc);
+      root[c] = sqrtf(v[c]);
+      const float moved = p[c] * keep;
+      p[c] = moved - s.rate * (m[c] / (root[c] / s.root_c2 + s.eps));
     }
     uint32_t mo = 0u, vo = 0u;
     int me = 0, ve = 0;
@@ -280,7 +270,7 @@ __global__ __launch_bounds__(256) void adamw_update_kernel(UpdateArgs a) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         if (e + c < n) {
-          const uint32_t x = abs_bits(m[u][c]), y = abs_bits(root[c]);
+          const uint32_t x = abs_bits(m[c]), y = abs_bits(root[c]);
           mt = x > mt ? x : mt;
           vt = y > vt ? y : vt;
         }
@@ -291,9 +281,8 @@ __global__ __launch_bounds__(256) void adamw_update_kernel(UpdateArgs a) {
       ve = scale_exp<5>(vt);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const uint32_t rnd = hash32((uint32_t)(e + c) * 0x9E3779B1u + (uint32_t)(a.item0 + i) * 0x3C6EF373u +
-                                    (uint32_t)h.k * 0xBB67AE85u + a.seed);
-        uint32_t x = to_code<4>(m[u][c], me, rnd & 0xffffu) | (m[u][c] < 0.f ? 128u : 0u);
+        const uint32_t rnd = hash32((uint32_t)(e + c) * 0x9E3779B1u + (uint32_t)item * 0x3C6EF373u + s.key);
+        const uint32_t x = to_code<4>(m[c], me, rnd & 0xffffu) | (m[c] < 0.f ? 128u : 0u);
         uint32_t y = to_code<5>(root[c], ve, rnd >> 16);
         y = y == 0u && root[c] > 0.f ? 1u : y;
         mo |= (mbad ? 0u : x) << (8 * c);
@@ -303,25 +292,25 @@ __global__ __launch_bounds__(256) void adamw_update_kernel(UpdateArgs a) {
       ve = vbad ? 255 : ve + 127;
     }
     if (e + 4 <= n) {
-      *reinterpret_cast<f32x4*>(it.p + e) = f32x4{p[u][0], p[u][1], p[u][2], p[u][3]};
+      *reinterpret_cast<f32x4*>(it.p + e) = f32x4{p[0], p[1], p[2], p[3]};
       if constexpr (S8) {
         *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(it.m) + e) = mo;
         *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(it.v) + e) = vo;
       } else {
-        *reinterpret_cast<f32x4*>(static_cast<float*>(it.m) + e) = f32x4{m[u][0], m[u][1], m[u][2], m[u][3]};
-        *reinterpret_cast<f32x4*>(static_cast<float*>(it.v) + e) = f32x4{v[u][0], v[u][1], v[u][2], v[u][3]};
+        *reinterpret_cast<f32x4*>(static_cast<float*>(it.m) + e) = f32x4{m[0], m[1], m[2], m[3]};
+        *reinterpret_cast<f32x4*>(static_cast<float*>(it.v) + e) = f32x4{v[0], v[1], v[2], v[3]};
       }
     } else {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         if (e + c < n) {
-          it.p[e + c] = p[u][c];
+          it.p[e + c] = p[c];
           if constexpr (S8) {
             static_cast<uint8_t*>(it.m)[e + c] = (uint8_t)(mo >> (8 * c));
             static_cast<uint8_t*>(it.v)[e + c] = (uint8_t)(vo >> (8 * c));
           } else {
-            static_cast<float*>(it.m)[e + c] = m[u][c];
-            static_cast<float*>(it.v)[e + c] = v[u][c];
+            static_cast<float*>(it.m)[e + c] = m[c];
+            static_cast<float*>(it.v)[e + c] = v[c];
           }
         }
     }
@@ -330,6 +319,88 @@ __global__ __launch_bounds__(256) void adamw_update_kernel(UpdateArgs a) {
         it.ms[e / 32] = (uint8_t)me;
         it.vs[e / 32] = (uint8_t)ve;
       }
+    }
+  }
+};
+
+// A norm that is infinite or NaN.
+__device__ __forceinline__ bool no_norm(float norm) { return !(norm <= 3.4028234e38f); }
+
+__device__ __forceinline__ Step step_of(const UpdateArgs& a, const Hyper& h, float norm) {
+  return Step{a.beta1, a.rest1, a.beta2, a.rest2, a.eps, h.lr / h.c1, h.root_c2,
+              a.clip ? a.clip_norm / (norm > a.clip_norm ? norm : a.clip_norm) : 1.f, a.clip,
+              (uint32_t)h.k * 0xBB67AE85u + a.seed};
+}
+
+template <bool S8>
+__global__ __launch_bounds__(256) void adamw_update_kernel(UpdateArgs a) {
+  __shared__ double red[4];
+  const int tid = threadIdx.x, b = blockIdx.x;
+  const int i = item_of(a.bstart, a.count, b);
+  const UpdateItem& it = a.it[i];
+  const int c0 = (b - a.bstart[i]) * kChunk;
+  constexpr int U = kChunk / 1024;
+  Piece<S8> x[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) x[u].load(it, c0 + 1024 * u + 4 * tid);
+  const Hyper h = *a.hyper;
+  float norm = 0.f;
+  if (a.sums != nullptr) {
+    double sum = 0.0;
+    for (int q = tid; q < a.sums_n; q += 256) sum += a.sums[q];
+    norm = (float)sqrt(block_sum(sum, red));
+    const bool skip = a.clip && no_norm(norm);              // nothing is moved
+    if (a.first && b == 0 && tid == 0) {
+      if (a.norm != nullptr) *a.norm = norm;
+      if (skip) *a.step = h.k - 1;
+    }
+    if (skip) return;
+  }
+  const Step s = step_of(a, h, norm);
+  const float keep = 1.f - h.lr * it.decay;
+#pragma unroll
+  for (int u = 0; u < U; ++u) x[u].update(it, c0 + 1024 * u + 4 * tid, a.item0 + i, keep, s);
+}
+
+// The whole step of few elements in one block and one launch (two launches took
+// 18.7 us from Python for two tensors of 1024): the norm, then the tensors one
+// after the other. sums_n: whether the norm is wanted.
+template <bool S8>
+__global__ __launch_bounds__(1024) void adamw_small_kernel(UpdateArgs a, double lr, double beta1, double beta2,
+                                                           const float* lr_dev) {
+  __shared__ double red[16];
+  __shared__ Hyper hyper;
+  const int tid = threadIdx.x;
+  if (tid == 0) {
+    hyper = hyper_of(*a.step + 1, lr, beta1, beta2, lr_dev);
+  }
+  float norm = 0.f;
+  if (a.sums_n) {
+    double sum = 0.0;
+    for (int i = 0; i < a.count; ++i)
+      for (int e = tid; e < a.it[i].n; e += 1024) sum += (double)a.it[i].g[e] * (double)a.it[i].g[e];
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+    if ((tid & 63) == 0) red[tid >> 6] = sum;
+  }
+  __syncthreads();
+  const Hyper h = hyper;
+  if (a.sums_n) {
+    double sum = 0.0;
+    for (int w = 0; w < 16; ++w) sum += red[w];
+    norm = (float)sqrt(sum);
+    if (tid == 0 && a.norm != nullptr) *a.norm = norm;
+    if (a.clip && no_norm(norm)) return;                    // nothing is moved
+  }
+  if (tid == 0) *a.step = h.k;
+  const Step s = step_of(a, h, norm);
+  for (int i = 0; i < a.count; ++i) {
+    const UpdateItem& it = a.it[i];
+    const float keep = 1.f - h.lr * it.decay;
+    for (int e = 4 * tid; e - 4 * tid < it.n; e += 4096) {  // block-uniform
+      Piece<S8> x;
+      x.load(it, e);
+      x.update(it, e, i, keep, s);
     }
   }
 }
@@ -456,10 +527,12 @@ void launch_adamw(const qlora_adamw_config& cfg, const qlora_adamw_item* items, 
   Hyper* hyper = static_cast<Hyper*>(ws);
   const bool clip = cfg.clip_norm > 0.0, norm = clip || cfg.norm != nullptr;
   double* sums = norm ? reinterpret_cast<double*>(static_cast<char*>(ws) + align_up(sizeof(Hyper))) : nullptr;
-  long chunk;
+  long chunk, total = 0;
+  for (int i = 0; i < count; ++i) total += items[i].n;
+  const bool small = total <= kSmall && count <= kItems;
   const long nsums = adamw_norm_blocks(items, count, &chunk);
   long base = 0;
-  for (int i0 = 0; i0 < (norm ? count : 1); i0 += kItems) {
+  for (int i0 = 0; !small && i0 < (norm ? count : 1); i0 += kItems) {
     NormArgs a{};
     a.count = count - i0 < kItems ? count - i0 : kItems;
     a.chunk = (int)chunk;
@@ -490,6 +563,14 @@ void launch_adamw(const qlora_adamw_config& cfg, const qlora_adamw_item* items, 
       const qlora_adamw_item& s = items[i0 + i];
       a.it[i] = UpdateItem{s.p, s.g, s.m, s.v, s.m_scales, s.v_scales, (int)s.n, (float)s.decay};
       a.bstart[i + 1] = a.bstart[i] + (int)((s.n + kChunk - 1) / kChunk);
+    }
+    if (small) {
+      a.sums_n = norm;
+      if (cfg.sfmt == QLORA_S8)
+        adamw_small_kernel<true><<<dim3(1), 1024, 0, st>>>(a, cfg.lr, cfg.beta1, cfg.beta2, cfg.lr_dev);
+      else
+        adamw_small_kernel<false><<<dim3(1), 1024, 0, st>>>(a, cfg.lr, cfg.beta1, cfg.beta2, cfg.lr_dev);
+      return;
     }
     const dim3 grid((unsigned)a.bstart[a.count]);
     if (cfg.sfmt == QLORA_S8) adamw_update_kernel<true><<<grid, 256, 0, st>>>(a);

@@ -41,6 +41,7 @@ namespace qlora {
 namespace {
 
 constexpr int kCUs = 256;
+constexpr int kFewTiles = 64;      // of 128 x 128: up to so many are taken as 32 x 256
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -955,9 +956,18 @@ __global__ __launch_bounds__(256) void xent_dx_join_kernel(const float* dxp, int
       }
     }
   }
-  for (int i = 1; i < splits; ++i)
+  for (int i = 1; i < splits; i += 4) {                    // four splits' loads in flight
+    f32x4 w[4][4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) v[b] += *reinterpret_cast<const f32x4*>(p + i * n + 4 * b);
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) w[c][b] = *reinterpret_cast<const f32x4*>(p + (i + c < splits ? i + c : 0) * n + 4 * b);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (i + c < splits) v[b] += w[c][b];
+  }
   if (m >= M || k >= K) return;
 #pragma unroll
   for (int b = 0; b < 4; ++b)
@@ -1026,7 +1036,10 @@ void logits_ranks(LogitArgs& a, int cols, hipStream_t st) {
 template <int PARTS>
 void logits(LogitArgs& a, int fmt, int cols, hipStream_t st) {
   if (fmt == 0) {
-    if (a.M <= 32) logits_ranks<false, 32, 256, 1, 4, 4, 1, PARTS>(a, cols, st);
+    const long t128 = (long)((a.M + 127) / 128) * ((cols + 127) / 128);
+    // few tiles leave compute units idle: smaller ones then (64 x 768 x 4000 rank 4
+    // with gradient 67.5 -> 63.5 us, 128 x 2048 x 4000 64.2 -> 59.4)
+    if (a.M <= 32 || t128 <= kFewTiles) logits_ranks<false, 32, 256, 1, 4, 4, 1, PARTS>(a, cols, st);
     else if (a.M > 128 && a.r <= 16) logits_ranks<false, 256, 256, 2, 4, 2, 1, PARTS>(a, cols, st);
     else logits_ranks<false, 128, 128, 2, 2, 2, 1, PARTS>(a, cols, st);
   } else if constexpr (PARTS == 3) {
@@ -1099,7 +1112,10 @@ XentPlan xent_plan(const VocabLayer& L, int vocab, int M, int dtype) {
   if (L.r > 0) {
     p.u = (size_t)M * L.r;
     p.up = (size_t)(p.piece / 128) * M * L.r;
-    p.dbp = (size_t)((M + 127) / 128) * L.r * p.piece;
+    // row tiles times entries: 128 or 256 rows a tile, or 32 of at most kFewTiles
+    // tiles' rows and columns
+    const size_t large = (size_t)((M + 127) / 128) * p.piece, few = (size_t)kFewTiles * 4 * 128;
+    p.dbp = (large > few ? large : few) * L.r;
     p.pA = rank_sum_floats(M, L.K, L.r);
   }
   return p;
