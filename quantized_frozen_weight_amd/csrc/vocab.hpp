@@ -46,12 +46,13 @@ struct XentPlan {
   int piece;                         // entries per piece, a multiple of 256
   int splits;                        // of a piece's contraction for dx
   int parts;                         // bf16 parts of dl: 1, or 3 in float32
-  size_t g, dxp, u, up, dbp, pA;     // elements: dl (16 bits), partial sums of dx, u, those of u, dB and dA
+  size_t g, dxp, u, up, dbp, pA, smax;     // elements: dl (16 bits), partial sums of dx, u, those of u, dB and dA
 };
 XentPlan xent_plan(const VocabLayer& L, int vocab, int M, int dtype);
 struct XentBuffers {
   uint16_t* g;
   float *dxp, *u, *up, *dbp, *pA;
+  uint32_t* smax;
 };
 // dx (NULL: none), and with an adapter dA and dB.
 void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const void* x, const int8_t* xq, const float* sx,

@@ -76,7 +76,7 @@ XentFwdLayout xent_fwd_layout(const qlora_linear* L, int vocab, int M) {
 }
 struct XentBwdLayout {
   XentPlan plan;
-  size_t xq, sx, t, rs, g, dxp, u, up, dbp, pA, total;
+  size_t xq, sx, t, rs, g, dxp, u, up, dbp, pA, smax, total;
 };
 XentBwdLayout xent_bwd_layout(const qlora_linear* L, int vocab, int M, int dtype) {
   XentBwdLayout w{};
@@ -92,6 +92,7 @@ XentBwdLayout xent_bwd_layout(const qlora_linear* L, int vocab, int M, int dtype
   w.up = off; off = align_up(off + w.plan.up * 4);
   w.dbp = off; off = align_up(off + w.plan.dbp * 4);
   w.pA = off; off = align_up(off + w.plan.pA * 4);
+  w.smax = off; off = align_up(off + w.plan.smax * 4);
   w.total = off;
   return w;
 }
@@ -246,7 +247,8 @@ int qlora_xent_bwd(const qlora_linear* L, int vocab, int M, int dtype, const voi
   float* tw = L->r < 1 || t_saved != nullptr ? nullptr : reinterpret_cast<float*>(at(ws, w.t));
   enqueue_rows(L, M, dtype, x, xq, sx, tw, reinterpret_cast<float*>(at(ws, w.rs)), s);
   const auto f = [&](size_t off) { return reinterpret_cast<float*>(at(ws, off)); };
-  const XentBuffers buf{reinterpret_cast<uint16_t*>(at(ws, w.g)), f(w.dxp), f(w.u), f(w.up), f(w.dbp), f(w.pA)};
+  const XentBuffers buf{reinterpret_cast<uint16_t*>(at(ws, w.g)), f(w.dxp), f(w.u), f(w.up), f(w.dbp), f(w.pA),
+                        reinterpret_cast<uint32_t*>(at(ws, w.smax))};
   launch_xent_bwd(vocab_layer(L), M, dtype, make_ids(targets, itype, vocab), x, xq, sx,
                   tw != nullptr ? tw : t_saved, lse, dloss, w.plan, buf, dx, dA, dB, s);
   return launch_status();

@@ -12,10 +12,10 @@
 //     target's logit from the tile that holds it. A second, small launch joins
 //     the tiles in a fixed order;
 //   - gradient: dl = dloss (exp2(l log2e - lse log2e) - [target]) for one piece
-//     of the vocabulary, in bf16 (int8 weights: times the entry's scale, so that
-//     the next product multiplies with the codes, which bf16 holds exactly), and
+//     of the vocabulary, in float16 (int8 weights: times the entry's scale, so that
+//     the next product multiplies with the codes, which float16 holds exactly), and
 //     with an adapter the tile's parts of u = dl B^T and dB = t^T dl from the
-//     float32 dl.
+//     float32 dl in three bf16 parts.
 // dx kernel      dx += dl W over one piece: dl rows K-contiguous, W as stored,
 //   codes [v][d], contracted over v. The 16-bit operand that a matrix
 //   instruction wants of W is eight v of one d: a lane reads one dword (4 d) of
@@ -69,6 +69,7 @@ struct LogitArgs {
   // gradient
   const float* lse;
   const float* dloss;
+  const uint32_t* smax;  // [64] partial maxima of the scales (int8, dl in float16)
   uint16_t* g;           // [parts][M][ldg]
   long ldg, gstride;
   float* up;             // [tiles_x][M][r]
@@ -115,11 +116,55 @@ __device__ __forceinline__ u32x2 bf16_part(float (&v)[4]) {
   return h;
 }
 
-// 4-bit weights: dl travels as float16 of 2^14 (p - [target]), without dloss, and
-// W as float16 of q times (scale / 8) (7 times the largest scale then fits; the
-// quotient loses bits of scales under 2^-11 only): 11 bits of each, where bf16 has
-// 8. What is left to the rows' factor:
+// The same of values that are no infinities.
+__device__ __forceinline__ u32x2 bf16_cut(float (&v)[4]) {
+  u32x2 h;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    h[e] = pk_bf16(v[2 * e], v[2 * e + 1]);
+    v[2 * e] -= __uint_as_float(h[e] << 16);
+    v[2 * e + 1] -= __uint_as_float(h[e] & 0xffff0000u);
+  }
+  return h;
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// dl in 16 bits is float16, 11 bits where bf16 has 8 (dx of 2048 x 2048 x 256000 was
+// off by 0.26 % from the definition with bf16, where rounding dx alone is 0.17).
+// What travels is p - [target] without dloss (the rows' factor, applied where rows
+// end), scaled so that the largest is 2^14 and 2^-24 of that still has all bits:
+// int8 weights: 2^14 (p - [target]) scale / 2^E, E the smallest with every scale
+// below 2^E (a power of two: nothing more is rounded), against the codes;
+// 4-bit weights: 2^14 (p - [target]), against q times (scale / 8) in float16 (7
+// times the largest scale then fits; the quotient loses bits of scales under 2^-11
+// only).
 constexpr float kHalfUp = 16384.f, kHalfDown = 8.f / 16384.f;
+
+// The largest of the entries' scales, by 64 partial maxima (scales that are no
+// numbers left out: what they enter is none either way).
+constexpr int kMaxParts = 64;
+__global__ __launch_bounds__(1024) void xent_scale_max_kernel(const float* scales, int V, uint32_t* part) {
+  __shared__ uint32_t red[16];
+  uint32_t mx = 0u;
+#pragma unroll 4
+  for (long i = blockIdx.x * 1024 + threadIdx.x; i < V; i += 1024 * kMaxParts) {
+    const uint32_t b = abs_bits(scales[i]);
+    mx = b < 0x7f800000u && b > mx ? b : mx;
+  }
+  mx = wave_max_u32(mx);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = mx;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 16; ++w) mx = red[w] > mx ? red[w] : mx;
+    part[blockIdx.x] = mx;
+  }
+}
+// E of the above from a lane's partial maximum; every lane of the wave.
+__device__ __forceinline__ int scale_power(uint32_t part) {
+  const int e = (int)(wave_max_u32(part) >> 23) - 126;
+  return e < -100 ? -100 : e;
+}
 
 constexpr int max_int(int a, int b) { return a > b ? a : b; }
 
@@ -136,13 +181,12 @@ struct LogitLds {
   static constexpr int TS = 0, QS = TS + BM * R * 4, RS = QS + R * QP * 4, SW = RS + BM * 4;
   static constexpr int TG = SW + BN * 4, LS = TG + BM * 4, END = LS + BM * 4;
   static constexpr int RED = WN * BM * 8;                 // loss: the waves' maxima and sums
-  // gradient: t dloss in two bf16 parts [2][R][TP]; a wave's strip of 16 rows of
-  // dl, and its two parts of 32 rows for dB (afterwards u [BM][R] and dB [R][BN])
-  static constexpr int TP = BM + 8, TB = END, PITCH = FN * 32 + 16;
-  static constexpr int ST = TB + (GRAD ? 2 * R * TP * 2 : 0), STRIP = 16 * PITCH;
-  static constexpr int PV = ST + NW * STRIP, PVB = 32 * PITCH;
+  // gradient: t dloss in three bf16 parts [3][R][TP]; a wave's 16 rows of dl, in
+  // three parts for dB, then as they go to memory (afterwards u [BM][R] and dB [R][BN])
+  static constexpr int TP = BM + 8, TB = END, PITCH = FN * 32 + 16, PVB = 16 * PITCH;
+  static constexpr int ST = TB + (GRAD ? 3 * R * TP * 2 : 0), STRIP = (R > 0 ? 3 : 1) * PVB;
   static constexpr int SUMS = (BM + BN) * R * 4;
-  static constexpr int EPI = GRAD ? PV + (R > 0 ? max_int(NW * 2 * PVB, SUMS) : 0) : END + RED;
+  static constexpr int EPI = GRAD ? ST + max_int(NW * STRIP, SUMS) : END + RED;
   static constexpr int BYTES = max_int(S * STG + SLAB, EPI);
   static_assert(BYTES <= 160 * 1024, "LDS of a block");
 };
@@ -150,7 +194,7 @@ struct LogitLds {
 // PARTS: 0 the loss, 1 the gradient with dl in 16 bits, 3 in three bf16 parts.
 template <bool W4, int BM, int BN, int WM, int WN, int S, int G, int R, int PARTS>
 __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) {
-  constexpr bool GRAD = PARTS > 0;
+  constexpr bool GRAD = PARTS > 0, HALF = PARTS == 1;      // HALF: dl in float16
   using Lds = LogitLds<W4, BM, BN, WM, WN, S, G, R, GRAD>;
   constexpr int NW = WM * WN, NT = 64 * NW, BK = 128;
   constexpr int ASZ = Lds::ASZ, STG = Lds::STG;
@@ -179,6 +223,8 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
   constexpr int NTA = NTS > 0 ? NTS : 1;
   float esx[RT], else_[RT], esw[CT], ets[NTA], egm[NTA], eqs[NQS > 0 ? NQS : 1];
   int etg[RT], etr[NTA];                                   // targets, by row and by element of t
+  uint32_t emax = 0u;
+  if constexpr (HALF && !W4) emax = a.smax[lane];
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     const int row = tid + NT * i, gm = m0 + row < M ? m0 + row : M - 1;
@@ -351,6 +397,9 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
   int* tgv = reinterpret_cast<int*>(lds + Lds::TG);        // the target's column here; INT32_MIN: none
   float* lsv = reinterpret_cast<float*>(lds + Lds::LS);    // log2e lse
   uint16_t* tb = reinterpret_cast<uint16_t*>(lds + Lds::TB);
+  // int8, dl in float16: the scales times 2^(14 - E), the rows' the other way round
+  const int power = HALF && !W4 ? 14 - scale_power(emax) : 0;
+  const float up = __builtin_ldexpf(1.f, power), down = __builtin_ldexpf(1.f, -power);
   // Gradient: a row without a target has logits 0 and lse infinite, so that its
   // p is 0 whatever its codes' scale is.
 #pragma unroll
@@ -358,7 +407,7 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
     const int row = tid + NT * i;
     if (row < BM) {
       const bool none = GRAD && etg[i] < 0;
-      rsv[row] = none ? 0.f : esx[i] * (W4 ? kLog2e / 16.f : kLog2e);   // (the products are those of 16 q)
+      rsv[row] = none ? 0.f : esx[i] * (W4 ? kLog2e / 16.f : kLog2e) * down;   // (4-bit: the products are those of 16 q)
       tgv[row] = etg[i] >= 0 ? etg[i] - n0 : INT32_MIN;
       if constexpr (GRAD) lsv[row] = none ? INFINITY : else_[i] * kLog2e;
     }
@@ -366,7 +415,7 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
   if constexpr (!W4) {
 #pragma unroll
     for (int i = 0; i < CT; ++i)
-      if (tid + NT * i < BN) swv[tid + NT * i] = n0 + tid + NT * i < a.V ? esw[i] : 0.f;
+      if (tid + NT * i < BN) swv[tid + NT * i] = n0 + tid + NT * i < a.V ? esw[i] * up : 0.f;
   }
   if constexpr (R > 0) {
 #pragma unroll
@@ -376,11 +425,11 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
         const bool in = j < a.r && m0 + row < M && !(GRAD && etr[i] < 0);
         ts[e] = in ? ets[i] * (a.s * kLog2e) : 0.f;
         if constexpr (GRAD) {
-          float v = in ? ets[i] * egm[i] : 0.f;
-          const uint32_t h = f32_to_bf16(v);
-          v = (h & 0x7f80u) != 0x7f80u ? v - bf16_to_f32(h) : 0.f;
-          tb[j * Lds::TP + row] = (uint16_t)h;
-          tb[(R + j) * Lds::TP + row] = (uint16_t)f32_to_bf16(v);
+          uint32_t mid, low;
+          const uint32_t hi = pk_bf16_split3(in ? ets[i] * egm[i] : 0.f, 0.f, mid, low);
+          tb[j * Lds::TP + row] = (uint16_t)hi;
+          tb[(R + j) * Lds::TP + row] = (uint16_t)mid;
+          tb[(2 * R + j) * Lds::TP + row] = (uint16_t)low;
         }
       }
     }
@@ -402,10 +451,10 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
     sw[j] = W4 ? f32x4{1.f, 1.f, 1.f, 1.f} : *reinterpret_cast<const f32x4*>(swv + wc0 + j * 16 + 4 * q);
 
   // u's operand, B of two column blocks (32 entries in the order in which a lane
-  // holds them), in two bf16 parts
+  // holds them), in three bf16 parts
   constexpr int NP = FN / 2;
   static_assert(FN % 2 == 0 && FM % 2 == 0, "blocks are taken in pairs");
-  u32x4 bh[ADAPT ? NP : 1][RBA], bl[ADAPT ? NP : 1][RBA];
+  u32x4 bp[3][ADAPT ? NP : 1][RBA];
   f32x4 uacc[ADAPT ? FM : 1][RBA], dbacc[ADAPT ? FN : 1][RBA];
   if constexpr (ADAPT) {
 #pragma unroll
@@ -419,11 +468,12 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
           float v[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = rank < R ? b4[e] : 0.f;
-          const u32x2 hi = bf16_part(v);
-          bh[p][jb][2 * h] = hi.x;
-          bh[p][jb][2 * h + 1] = hi.y;
-          bl[p][jb][2 * h] = pk_bf16(v[0], v[1]);
-          bl[p][jb][2 * h + 1] = pk_bf16(v[2], v[3]);
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            const u32x2 w = bf16_part(v);
+            bp[c][p][jb][2 * h] = w.x;
+            bp[c][p][jb][2 * h + 1] = w.y;
+          }
         }
 #pragma unroll
       for (int i = 0; i < FM; ++i) uacc[i][jb] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -432,7 +482,6 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
     }
   }
   int8_t* strip = lds + Lds::ST + wid * Lds::STRIP;
-  int8_t* pv = lds + Lds::PV + wid * 2 * Lds::PVB;
 
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
@@ -515,63 +564,67 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
             if (n0 + wc0 + j * 16 + 4 * q + ii >= a.V) x[j][ii] = 0.f;
       }
       if constexpr (ADAPT) {
-        u32x2 ph[FN], pl[FN];
+        u32x2 pp[3][FN];
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
           float v[4] = {x[j][0], x[j][1], x[j][2], x[j][3]};
-          ph[j] = bf16_part(v);
-          pl[j] = u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
-          *reinterpret_cast<u32x2*>(pv + ((i & 1) * 16 + l) * Lds::PITCH + j * 32 + q * 8) = ph[j];
-          *reinterpret_cast<u32x2*>(pv + Lds::PVB + ((i & 1) * 16 + l) * Lds::PITCH + j * 32 + q * 8) = pl[j];
-        }
-        // u^T [rank][row] += B dl^T: the lane's own values are the operand
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          const bf16x8 vh = __builtin_bit_cast(bf16x8, u32x4{ph[2 * p].x, ph[2 * p].y, ph[2 * p + 1].x, ph[2 * p + 1].y});
-          const bf16x8 vl = __builtin_bit_cast(bf16x8, u32x4{pl[2 * p].x, pl[2 * p].y, pl[2 * p + 1].x, pl[2 * p + 1].y});
-#pragma unroll
-          for (int jb = 0; jb < RB; ++jb) {
-            const bf16x8 wh = __builtin_bit_cast(bf16x8, bh[p][jb]), wl = __builtin_bit_cast(bf16x8, bl[p][jb]);
-            uacc[i][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wl, vh, uacc[i][jb], 0, 0, 0);
-            uacc[i][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wh, vl, uacc[i][jb], 0, 0, 0);
-            uacc[i][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wh, vh, uacc[i][jb], 0, 0, 0);
+          for (int c = 0; c < 3; ++c) {
+            pp[c][j] = c < 2 ? bf16_cut(v) : u32x2{pk_bf16(v[0], v[1]), pk_bf16(v[2], v[3])};
+            *reinterpret_cast<u32x2*>(strip + c * Lds::PVB + l * Lds::PITCH + j * 32 + q * 8) = pp[c][j];
           }
         }
-        if (i & 1) {
-          // dB^T [entry][rank] += dl^T (t dloss) over the last 32 rows, dl^T by
-          // transposing reads (in each 16-lane group lanes 4 i + p fetch the 4
-          // columns at 4 p of row i, lane k receives column k of rows 0..3)
-          asm volatile("" ::: "memory");
-          const int i4 = l >> 2, p4 = l & 3;
-          bf16x8 th[RBA], tl2[RBA];
+        // u^T [rank][row] += B dl^T: the lane's own values are the operand; the six
+        // products of parts that float32 has, the small ones first
 #pragma unroll
-          for (int jb = 0; jb < RB; ++jb) {
-            const int rank = 16 * jb + l, rc = rank < R ? rank : 0;
-            const uint16_t* tp = tb + rc * Lds::TP + wr0 + (i - 1) * 16 + 8 * q;
-            u32x4 x0 = *reinterpret_cast<const u32x4*>(tp), x1 = *reinterpret_cast<const u32x4*>(tp + R * Lds::TP);
-            if (rank >= R) x0 = x1 = u32x4{0u, 0u, 0u, 0u};
-            th[jb] = __builtin_bit_cast(bf16x8, x0);
-            tl2[jb] = __builtin_bit_cast(bf16x8, x1);
-          }
+        for (int p = 0; p < NP; ++p)
 #pragma unroll
-          for (int j = 0; j < FN; ++j) {
-            uint32_t ad[4];
-            uint64_t v[4];
+          for (int o = 2; o >= 0; --o)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)                    // parts, halves of 8 rows
-              ad[e] = lds_addr(pv + (e >> 1) * Lds::PVB + (8 * q + 4 * (e & 1) + i4) * Lds::PITCH + j * 32 + p4 * 8);
-            tr16_reads<4>(ad, v);
-            const bf16x8 dh = __builtin_bit_cast(bf16x8, u32x4{(uint32_t)v[0], (uint32_t)(v[0] >> 32), (uint32_t)v[1],
-                                                               (uint32_t)(v[1] >> 32)});
-            const bf16x8 dl = __builtin_bit_cast(bf16x8, u32x4{(uint32_t)v[2], (uint32_t)(v[2] >> 32), (uint32_t)v[3],
-                                                               (uint32_t)(v[3] >> 32)});
+            for (int c = 0; c <= o; ++c) {
+              const u32x2 v0 = pp[o - c][2 * p], v1 = pp[o - c][2 * p + 1];
+              const bf16x8 vv = __builtin_bit_cast(bf16x8, u32x4{v0.x, v0.y, v1.x, v1.y});
 #pragma unroll
-            for (int jb = 0; jb < RB; ++jb) {
-              dbacc[j][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dl, th[jb], dbacc[j][jb], 0, 0, 0);
-              dbacc[j][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dh, tl2[jb], dbacc[j][jb], 0, 0, 0);
-              dbacc[j][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dh, th[jb], dbacc[j][jb], 0, 0, 0);
+              for (int jb = 0; jb < RB; ++jb)
+                uacc[i][jb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bp[c][p][jb]), vv,
+                                                                     uacc[i][jb], 0, 0, 0);
             }
+        // dB^T [entry][rank] += dl^T (t dloss) over these 16 rows, dl^T by transposing
+        // reads (in each 16-lane group lanes 4 i + p fetch the 4 columns at 4 p of row
+        // i, lane k receives column k of rows 0..3)
+        asm volatile("" ::: "memory");
+        const int i4 = l >> 2, p4 = l & 3;
+        s16x4 tp[3][RBA];
+#pragma unroll
+        for (int jb = 0; jb < RB; ++jb) {
+          const int rank = 16 * jb + l;
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            u32x2 w = *reinterpret_cast<const u32x2*>(tb + (c * R + (rank < R ? rank : 0)) * Lds::TP + wr0 + i * 16 + 4 * q);
+            if (rank >= R) w = u32x2{0u, 0u};
+            tp[c][jb] = __builtin_bit_cast(s16x4, w);
           }
+        }
+#pragma unroll
+        for (int j = 0; j < FN; j += 2) {
+          uint32_t ad[8];
+          uint64_t v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {                    // blocks j and j + 1, three parts each (two reads spare)
+            const int c = e % 4 < 3 ? e % 4 : 2;
+            ad[e] = lds_addr(strip + c * Lds::PVB + (4 * q + i4) * Lds::PITCH + (j + e / 4) * 32 + p4 * 8);
+          }
+          tr16_reads<8>(ad, v);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int o = 2; o >= 0; --o)
+#pragma unroll
+              for (int c = 0; c <= o; ++c)
+#pragma unroll
+                for (int jb = 0; jb < RB; ++jb)
+                  dbacc[j + h][jb] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, v[4 * h + o - c]),
+                                                                              tp[c][jb], dbacc[j + h][jb], 0, 0, 0);
         }
       }
       // dl to memory: one 16-row strip at a time through LDS (this wave's own: no
@@ -588,6 +641,7 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
         for (int j = 0; j < FN; ++j) {
           u32x2 w;
           if constexpr (W4) w = u32x2{pk_f16(x[j][0] * kHalfUp, x[j][1] * kHalfUp), pk_f16(x[j][2] * kHalfUp, x[j][3] * kHalfUp)};
+          else if constexpr (HALF) w = u32x2{pk_f16(x[j][0], x[j][1]), pk_f16(x[j][2], x[j][3])};
           else if (p == PARTS - 1) w = u32x2{pk_bf16(x[j][0], x[j][1]), pk_bf16(x[j][2], x[j][3])};
           else w = bf16_part(x[j]);
           *reinterpret_cast<u32x2*>(strip + l * Lds::PITCH + j * 32 + q * 8) = w;
@@ -627,7 +681,7 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
   if constexpr (ADAPT) {
     // the tile's u and dB: the waves' sums added in order
     __syncthreads();                                       // the strips are read
-    float* ub = reinterpret_cast<float*>(lds + Lds::PV);
+    float* ub = reinterpret_cast<float*>(lds + Lds::ST);
     float* db = ub + BM * R;
     for (int w = 0; w < max_int(WM, WN); ++w) {
       if (wn == w) {
@@ -722,8 +776,10 @@ struct DxArgs {
   float* dxp;            // [splits][M][K]
 };
 
-template <bool W4, int BM, int WM, int S>
+// F: 0 int8 codes and dl in bf16 parts, 1 int8 codes and dl in float16, 2 4-bit.
+template <int F, int BM, int WM, int S>
 __global__ __launch_bounds__(64 * WM * 4) void xent_dx_kernel(DxArgs a) {
+  constexpr bool W4 = F == 2;
   constexpr int WN = 4, NW = WM * WN, BN = 256, KC = 64;
   constexpr int ASZ = BM * 128, RB = W4 ? 128 : 256;         // bytes of a row of codes
   constexpr int BSZ = KC * RB, SSZ = W4 ? NW * 256 : 0, STG = ASZ + BSZ + SSZ;
@@ -830,8 +886,16 @@ __global__ __launch_bounds__(64 * WM * 4) void xent_dx_kernel(DxArgs a) {
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float x = (float)(int8_t)(w[2 * e] >> (8 * j)), y = (float)(int8_t)(w[2 * e + 1] >> (8 * j));
-            bf[j][e] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
+            if constexpr (F == 0) {
+              const float x = (float)(int8_t)(w[2 * e] >> (8 * j)), y = (float)(int8_t)(w[2 * e + 1] >> (8 * j));
+              bf[j][e] = __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u);
+            } else {
+              // a byte with its sign bit turned over, under the exponent of 1024, is
+              // 1152 + q in float16
+              const uint32_t b = __builtin_amdgcn_perm(w[2 * e + 1], w[2 * e], 0x0c040c00u + 0x00010001u * j) ^ 0x64806480u;
+              bf[j][e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, b) -
+                                                          f16x2{(_Float16)1152.f, (_Float16)1152.f});
+            }
           }
       } else {
         // rows 2 e and 2 e + 1 share a register: nibble j of each, with its sign bit
@@ -855,7 +919,7 @@ __global__ __launch_bounds__(64 * WM * 4) void xent_dx_kernel(DxArgs a) {
       for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if constexpr (W4)
+          if constexpr (F > 0)
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, af[i]),
                                                               __builtin_bit_cast(f16x8, bf[j]), acc[i][j], 0, 0, 0);
           else
@@ -930,7 +994,7 @@ __global__ __launch_bounds__(256) void xent_reduce_kernel(ReduceArgs a) {
 template <typename OutT, int R>
 __global__ __launch_bounds__(256) void xent_dx_join_kernel(const float* dxp, int splits, int M, int K, int r, float s,
                                                            const float* u, const float* A, Ids ids, const float* dloss,
-                                                           float down, OutT* dx) {
+                                                           float down, const uint32_t* smax, OutT* dx) {
   const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
   const int m = blockIdx.x * 16 + l, mc = m < M ? m : M - 1;
   const int d0 = ((int)blockIdx.y * 4 + ((int)threadIdx.x >> 6)) * 64, k = d0 + 16 * q, kc = k < K ? k : 0;
@@ -939,7 +1003,9 @@ __global__ __launch_bounds__(256) void xent_dx_join_kernel(const float* dxp, int
   f32x4 v[4];
 #pragma unroll
   for (int b = 0; b < 4; ++b) v[b] = *reinterpret_cast<const f32x4*>(p + 4 * b);
-  const float f = row_factor(ids, dloss, mc) * down;
+  // (int8, dl in float16: back from 2^(14 - E))
+  const float back = smax != nullptr ? __builtin_ldexpf(1.f, scale_power(smax[lane]) - 14) : down;
+  const float f = row_factor(ids, dloss, mc) * back;
   f32x4 low[4];
   if constexpr (R > 0) {
 #pragma unroll
@@ -993,7 +1059,8 @@ void dx_join(const VocabLayer& L, int M, Ids ids, const float* dloss, const Xent
   OutT* out = static_cast<OutT*>(dx);
   const auto launch = [&](auto rank) {
     xent_dx_join_kernel<OutT, decltype(rank)::value><<<grid, 256, 0, st>>>(
-        buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids, dloss, down, out);
+        buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids, dloss, down,
+        L.fmt == 0 && plan.parts == 1 ? buf.smax : nullptr, out);
   };
   if (L.r == 0) launch(std::integral_constant<int, 0>());
   else if (L.r <= 4) launch(std::integral_constant<int, 4>());
@@ -1064,12 +1131,12 @@ LogitArgs logit_args(const VocabLayer& L, int M, Ids ids, const int8_t* xq, cons
 // Rows of a dx tile.
 int dx_rows(int M) { return M <= 32 ? 32 : M <= 128 ? 128 : 256; }
 
-template <bool W4>
+template <int F>
 void launch_dx(const DxArgs& a, int rows, hipStream_t st) {
   const dim3 grid((unsigned)(a.tiles_m * a.tiles_k * a.splits));
-  if (rows == 32) xent_dx_kernel<W4, 32, 1, 3><<<grid, 256, 0, st>>>(a);
-  else if (rows == 128) xent_dx_kernel<W4, 128, 2, 3><<<grid, 512, 0, st>>>(a);
-  else xent_dx_kernel<W4, 256, 2, 3><<<grid, 512, 0, st>>>(a);
+  if (rows == 32) xent_dx_kernel<F, 32, 1, 3><<<grid, 256, 0, st>>>(a);
+  else if (rows == 128) xent_dx_kernel<F, 128, 2, 3><<<grid, 512, 0, st>>>(a);
+  else xent_dx_kernel<F, 256, 2, 3><<<grid, 512, 0, st>>>(a);
 }
 
 }  // namespace
@@ -1109,6 +1176,7 @@ XentPlan xent_plan(const VocabLayer& L, int vocab, int M, int dtype) {
   if (p.splits > nk / 4) p.splits = nk / 4 < 1 ? 1 : nk / 4;
   p.g = (size_t)p.parts * M * p.piece;
   p.dxp = (size_t)p.splits * M * L.K;
+  p.smax = kMaxParts;
   if (L.r > 0) {
     p.u = (size_t)M * L.r;
     p.up = (size_t)(p.piece / 128) * M * L.r;
@@ -1126,12 +1194,14 @@ void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const void*
                      const XentBuffers& buf, void* dx, float* dA, float* dB, hipStream_t st) {
   const int V = ids.vocab;
   const int rows = dx_rows(M);
+  if (L.fmt == 0 && plan.parts == 1)
+    xent_scale_max_kernel<<<dim3(kMaxParts), 1024, 0, st>>>(static_cast<const float*>(L.scales), V, buf.smax);
   for (int v0 = 0; v0 < V; v0 += plan.piece) {
     const int vc = V - v0 < plan.piece ? V - v0 : plan.piece;
     const long ldg = (vc + 255) / 256 * 256;
     LogitArgs a = logit_args(L, M, ids, xq, sx, t);
     a.v0 = v0; a.lse = lse; a.dloss = dloss; a.g = buf.g; a.ldg = ldg; a.gstride = M * ldg;
-    a.up = buf.up; a.dbp = buf.dbp;
+    a.up = buf.up; a.dbp = buf.dbp; a.smax = buf.smax;
     if (plan.parts == 1) logits<1>(a, L.fmt, (int)ldg, st);
     else logits<3>(a, L.fmt, (int)ldg, st);
     if (dx != nullptr) {
@@ -1142,8 +1212,9 @@ void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const void*
       d.splits = plan.splits;
       d.nks = (plan.parts * (int)(ldg / 64) + plan.splits - 1) / plan.splits;
       d.first = v0 == 0; d.dxp = buf.dxp;
-      if (L.fmt == 0) launch_dx<false>(d, rows, st);
-      else launch_dx<true>(d, rows, st);
+      if (L.fmt == 1) launch_dx<2>(d, rows, st);
+      else if (plan.parts == 1) launch_dx<1>(d, rows, st);
+      else launch_dx<0>(d, rows, st);
     }
     if (L.r > 0) {
       ReduceArgs r{M, L.N, L.r, a.tiles_x, a.tiles_m, v0, vc, v0 == 0, v0 + vc == V, V, ldg, L.s, ids, dloss,
