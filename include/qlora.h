@@ -510,9 +510,11 @@ int qlora_act_bwd(int act, int M, int N, int dtype, const void* dy, const void* 
  * These calls take QLORA_W8 (float32 and bf16) and QLORA_W4G128 (bf16; K <=
  * 16384) layers of one head (EUNSUPPORTED otherwise), and, unlike the others,
  * r = 0 for a layer without adapter (A and B NULL, alpha not read). Tokens and
- * targets are device arrays [M] of int32 or int64. One outside [0, vocab)
- * (padding, prompts) stands for none: its row of x is zero, its loss 0, its
- * gradients 0, whatever else the row holds. Constraints otherwise as above. */
+ * targets are device arrays [M] of int32 or int64, aligned as their type is (a
+ * slice of a longer array will do). One outside [0, vocab) (padding, prompts)
+ * stands for none: its row of x is zero, its loss 0, its gradients 0, whatever
+ * else the row or the layer holds. K <= 2^23 (ERANGE above). Constraints
+ * otherwise as above. */
 typedef enum { QLORA_I32 = 0, QLORA_I64 = 1 } qlora_itype;
 
 /* Lookup: x [M, K] = scale w_token(m), formed in float32 and rounded once to
@@ -543,9 +545,9 @@ int qlora_embed_bwd(const qlora_linear* L, int vocab, int M, int dtype, const vo
  *   lse[m]  = log sum_{v < vocab} exp(l[m, v])         float32 [M]
  *   loss[m] = lse[m] - l[m, target(m)]                 float32 [M]
  * No logit is written to memory: a tile's rows leave their maximum and sum
- * (8 bytes for 256 logits of int8 weights, for 128 of 4-bit ones). t_save as
- * for qlora_fwd (r >= 1). A row of x with an infinity or a NaN has lse NaN, and
- * touches no other row. Int8 layers up to K = 132096 (EUNSUPPORTED above). */
+ * (8 bytes for 128 or 256 logits). t_save as for qlora_fwd (r >= 1). A row of x
+ * with an infinity or a NaN has lse NaN, and touches no other row. Int8 layers
+ * up to K = 132096 (EUNSUPPORTED above); M <= 2^24, M vocab <= 2^37 (ERANGE). */
 int qlora_xent_fwd_workspace(const qlora_linear* L, int vocab, int M, int dtype, size_t* bytes);
 int qlora_xent_fwd(const qlora_linear* L, int vocab, int M, int dtype, const void* x,
                    const void* targets, int itype, float* loss, float* lse, float* t_save, void* ws,
@@ -558,11 +560,13 @@ int qlora_xent_fwd(const qlora_linear* L, int vocab, int M, int dtype, const voi
  *   dA = s x^T u   float32 [K, r],  dB = s t^T dl   float32 [r, N]   (r >= 1)
  * dloss float32 [M]: the gradient of each row's loss (1 / count for a mean).
  * lse is qlora_xent_fwd's; t_saved its t (NULL: formed again). The logits are
- * formed again piece by piece of the vocabulary; dl, which is formed in
- * float32, lives for one piece, for the products with W in bf16 (times the
- * entry's scale for int8 weights; in three bf16 parts, float32's precision, in
- * the float32 compute dtype), for those with B and t in two parts of 16 bits
- * together. dA and dB are NULL where r = 0; dx may be NULL where r >= 1. */
+ * formed again piece by piece of the vocabulary (about 256 MB of dl each, in
+ * the workspace). dl is formed in float32; for the product with W it is rounded
+ * to float16 (int8 weights: times the entry's scale over a power of two at
+ * least the largest scale; 4-bit weights: W is then rounded to float16, too),
+ * in the float32 compute dtype to three bf16 parts, which keep it; for those
+ * with B and t all three operands are in three bf16 parts. dA and dB are NULL
+ * where r = 0; dx may be NULL where r >= 1. Limits as for qlora_xent_fwd. */
 int qlora_xent_bwd_workspace(const qlora_linear* L, int vocab, int M, int dtype, size_t* bytes);
 int qlora_xent_bwd(const qlora_linear* L, int vocab, int M, int dtype, const void* x,
                    const void* targets, int itype, const float* lse, const float* dloss,
@@ -618,17 +622,19 @@ typedef struct {
   int32_t sfmt;           /* qlora_sfmt */
 } qlora_adamw_config;
 
-/* One step of `count` tensors in one launch per 48 tensors (and as many for
- * the norm where clip_norm > 0 or norm is given). items[] and cfg are read
- * during the call only (host memory). Tensors must not overlap each other.
+/* One step of `count` tensors: one launch where they hold at most 8192 elements
+ * in at most 48 tensors; else one launch that advances the step (with clip_norm
+ * > 0 or norm given, one per 48 tensors that sum the norm), and one per 48
+ * tensors that moves them. items[] and cfg are read during the call only (host
+ * memory). Tensors of different items must not overlap each other (not checked).
  * 0 <= beta < 1, eps > 0, lr, decay and clip_norm >= 0 and all finite; 0 <=
  * *step (EINVAL for what the host can see). */
 int qlora_adamw_workspace(const qlora_adamw_item* items, int count, size_t* bytes);
 int qlora_adamw(const qlora_adamw_config* cfg, const qlora_adamw_item* items, int count, void* ws,
                 size_t ws_bytes, void* stream);
 
-/* Moments in 8 bits read as float32 or bf16 (both hold every value of the form
- * exactly), and written from them, to the nearest code (halves up; a second
+/* Moments in 8 bits read as float32 or bf16 (exactly, but for what bf16 rounds of
+ * moments below 2^-126), and written from them, to the nearest code (halves up; a second
  * moment that is not 0 to at least the smallest): to look at a state, to keep
  * it, or to begin from one in float32. QLORA_MOMENT1: m; QLORA_MOMENT2: the root
  * of v (not negative; a sign is not kept). 1 <= n <= 2^30, x and codes 16-byte

@@ -1089,9 +1089,6 @@ class AdamW:
             _tensor(p, f"params[{i}]", p.shape, torch.float32, dev)
             if p.numel() == 0:
                 raise ValueError(f"params[{i}]: empty")
-        spans = sorted((p.data_ptr(), p.nbytes) for p in params)
-        if any(a + n > b for (a, n), (b, _) in zip(spans, spans[1:])):
-            raise ValueError("params: two of them overlap")
 
         def held(given, what, n, dtype):
             """One tensor of n(numel) elements per parameter, made (zero) or checked."""
@@ -1117,6 +1114,10 @@ class AdamW:
             raise ValueError("m_scales, v_scales: float32 moments have none")
         self.step = torch.zeros((1,), dtype=torch.int32, device=dev) if step is None else \
             _tensor(step, "step", (1,), torch.int32, dev)
+        written = params + self.m + self.v + (self.m_scales + self.v_scales if s8 else []) + [self.step]
+        spans = sorted((t.data_ptr(), t.nbytes) for t in written)
+        if any(a + n > b for (a, n), (b, _) in zip(spans, spans[1:])):
+            raise ValueError("params and state: two of the tensors overlap")
         decay = [float(decay)] * count if isinstance(decay, (int, float)) else [float(d) for d in decay]
         if len(decay) != count:
             raise ValueError(f"decay: {len(decay)} values for {count} parameters")
@@ -1167,7 +1168,7 @@ def qlora_adamw(opt: AdamW, grads, lr, betas=(0.9, 0.999), eps: float = 1e-6, cl
 
 def qlora_moment_read(codes, scales, which: str, dtype=None, x=None):
     """8-bit moments (codes uint8 [n], scales uint8 [ceil(n / 32)]) in dtype
-    (torch.float32 unless given, or torch.bfloat16; exact in both): which "m",
+    (torch.float32 unless given, or torch.bfloat16; exact from 2^-126 on): which "m",
     or "root_v", the root of the second."""
     import torch
     dev, n = codes.device, codes.numel()

@@ -2,8 +2,9 @@
 // the 8-bit form: include/qlora.h).
 //
 // Memory-bound: an element moves 28 bytes with float32 moments, 16.1 with 8-bit
-// ones, and 4 more where the norm is taken first. Two kernels, each launched
-// once per 48 tensors, their pointers in the kernel's arguments:
+// ones, and 4 more where the norm is taken first. Few elements (8192) are one
+// block's work in one launch; else two kernels, each launched once per 48
+// tensors, their pointers in the kernel's arguments:
 //
 //   norm    a block sums the squares of one chunk of one tensor in float64 and
 //           leaves the sum in the workspace; chunks grow with the total, so
@@ -405,7 +406,7 @@ __global__ __launch_bounds__(1024) void adamw_small_kernel(UpdateArgs a, double 
   }
 }
 
-// 8-bit moments to float32 or bf16 (exact in both) and back (to the nearest
+// 8-bit moments to float32 or bf16 (exact above 2^-126) and back (to the nearest
 // code, halves up): 8 elements a thread, 4 lanes a group. BITS: 4 the first
 // moment, 5 the root of the second.
 template <typename T, int BITS>

@@ -34,9 +34,12 @@ size_t embed_bwd_bytes(int M, int K, int r);
 void launch_embed_bwd(const VocabLayer& L, int M, int dtype, Ids ids, float scale, const void* dy,
                       bool accumulate, float* dA, float* dB, void* ws, hipStream_t st);
 
-// Softmax cross entropy. xq, sx: the rows' codes and scales; t [M, r] (NULL at
+// Softmax cross entropy, up to kMaxRows rows and kMaxLogits logits (launches of
+// fewer than 2^32 threads). xq, sx: the rows' codes and scales; t [M, r] (NULL at
 // r = 0). part: xent_part_floats(...) floats.
-size_t xent_part_floats(int fmt, int vocab, int M);
+constexpr int kMaxRows = 1 << 24;
+constexpr long kMaxLogits = 1L << 37;
+size_t xent_part_floats(int vocab, int M);
 void launch_xent_fwd(const VocabLayer& L, int M, Ids ids, const int8_t* xq, const float* sx,
                      const float* t, float* part, float* loss, float* lse, hipStream_t st);
 
@@ -45,8 +48,8 @@ void launch_xent_fwd(const VocabLayer& L, int M, Ids ids, const int8_t* xq, cons
 struct XentPlan {
   int piece;                         // entries per piece, a multiple of 256
   int splits;                        // of a piece's contraction for dx
-  int parts;                         // bf16 parts of dl: 1, or 3 in float32
-  size_t g, dxp, u, up, dbp, pA, smax;     // elements: dl (16 bits), partial sums of dx, u, those of u, dB and dA
+  int parts;                         // dl as 1 float16, or in float32 3 parts in bf16
+  size_t g, dxp, u, up, dbp, pA, smax;   // elements: dl (16 bits), partial sums of dx, u, those of u, dB and dA, maxima of scales
 };
 XentPlan xent_plan(const VocabLayer& L, int vocab, int M, int dtype);
 struct XentBuffers {

@@ -19,7 +19,7 @@ int check_vocab(const qlora_linear* L, int vocab, int M, int dtype) {
   if (st) return st;
   if (M < 1 || L->K < 16 || L->N < 16 || L->K % 16 || L->N % 16 || L->r < 0 || L->r > 32) return QLORA_EINVAL;
   if (vocab < 1 || vocab > L->N) return QLORA_EINVAL;
-  if (!fits_int(M, L->K) || !fits_int(L->K, L->N)) return QLORA_ERANGE;
+  if (!fits_int(M, L->K) || !fits_int(L->K, L->N) || L->K > (1 << 23)) return QLORA_ERANGE;
   if (L->fmt != QLORA_W8 && L->fmt != QLORA_W4G128 && L->fmt != QLORA_W8O) return QLORA_EINVAL;
   if (L->heads < 0) return QLORA_EINVAL;
   if (L->fmt == QLORA_W8O || L->heads > 1) return QLORA_EUNSUPPORTED;
@@ -38,7 +38,8 @@ int check_vocab(const qlora_linear* L, int vocab, int M, int dtype) {
 
 int check_ids(const void* ids, int itype) {
   if (itype != QLORA_I32 && itype != QLORA_I64) return QLORA_EINVAL;
-  return ids != nullptr && aligned16(ids) ? QLORA_OK : QLORA_EINVAL;
+  const uintptr_t off = itype == QLORA_I64 ? 7u : 3u;      // (a slice of a tensor starts anywhere)
+  return ids != nullptr && (reinterpret_cast<uintptr_t>(ids) & off) == 0 ? QLORA_OK : QLORA_EINVAL;
 }
 inline size_t ids_bytes(int M, int itype) { return (size_t)M * (itype == QLORA_I64 ? 8 : 4); }
 inline Ids make_ids(const void* p, int itype, int vocab) { return Ids{p, itype == QLORA_I64, vocab}; }
@@ -70,7 +71,7 @@ XentFwdLayout xent_fwd_layout(const qlora_linear* L, int vocab, int M) {
   w.sx = off; off = align_up(off + (size_t)M * 4);
   w.t = off; off = align_up(off + (size_t)M * L->r * 4);
   w.rs = off; off = align_up(off + row_split_floats(M, L->K, L->r > 0 ? L->r : 1) * 4);
-  w.part = off; off = align_up(off + xent_part_floats(L->fmt, vocab, M) * 4);
+  w.part = off; off = align_up(off + xent_part_floats(vocab, M) * 4);
   w.total = off;
   return w;
 }
@@ -104,8 +105,14 @@ void enqueue_rows(const qlora_linear* L, int M, int dtype, const void* x, int8_t
                   rs);
 }
 
-// int32 sums of products of codes up to 127 and 128 stay exact
-inline bool exact_sums(const qlora_linear* L) { return L->fmt == QLORA_W4G128 || L->K <= 132096; }
+// int32 sums of products of codes up to 127 and 128 stay exact; rows and logits
+// that one launch covers.
+int check_xent(const qlora_linear* L, int vocab, int M, int dtype) {
+  const int st = check_vocab(L, vocab, M, dtype);
+  if (st) return st;
+  if (L->fmt == QLORA_W8 && L->K > 132096) return QLORA_EUNSUPPORTED;
+  return M > kMaxRows || (long)M * vocab > kMaxLogits ? QLORA_ERANGE : QLORA_OK;
+}
 
 inline bool ws_ok(const void* ws, size_t have, size_t need) {
   return have >= need && (need == 0 || (ws != nullptr && aligned16(ws)));
@@ -167,9 +174,8 @@ int qlora_embed_bwd(const qlora_linear* L, int vocab, int M, int dtype, const vo
 
 int qlora_xent_fwd_workspace(const qlora_linear* L, int vocab, int M, int dtype, size_t* bytes) {
   if (bytes == nullptr) return QLORA_EINVAL;
-  const int st = check_vocab(L, vocab, M, dtype);
+  const int st = check_xent(L, vocab, M, dtype);
   if (st) return st;
-  if (!exact_sums(L)) return QLORA_EUNSUPPORTED;
   *bytes = xent_fwd_layout(L, vocab, M).total;
   return QLORA_OK;
 }
@@ -208,9 +214,8 @@ int qlora_xent_fwd(const qlora_linear* L, int vocab, int M, int dtype, const voi
 
 int qlora_xent_bwd_workspace(const qlora_linear* L, int vocab, int M, int dtype, size_t* bytes) {
   if (bytes == nullptr) return QLORA_EINVAL;
-  const int st = check_vocab(L, vocab, M, dtype);
+  const int st = check_xent(L, vocab, M, dtype);
   if (st) return st;
-  if (!exact_sums(L)) return QLORA_EUNSUPPORTED;
   *bytes = xent_bwd_layout(L, vocab, M, dtype).total;
   return QLORA_OK;
 }

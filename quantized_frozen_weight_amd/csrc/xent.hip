@@ -44,6 +44,7 @@ constexpr int kCUs = 256;
 constexpr int kFewTiles = 64;      // of 128 x 128: up to so many are taken as 32 x 256
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kNone = -(1 << 30);  // no target: far from every tile (a column is above -2^27)
 
 // Block b of nb as a position in an order that each XCD (every eighth block)
 // walks a contiguous part of.
@@ -134,8 +135,8 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // off by 0.26 % from the definition with bf16, where rounding dx alone is 0.17).
 // What travels is p - [target] without dloss (the rows' factor, applied where rows
 // end), scaled so that the largest is 2^14 and 2^-24 of that still has all bits:
-// int8 weights: 2^14 (p - [target]) scale / 2^E, E the smallest with every scale
-// below 2^E (a power of two: nothing more is rounded), against the codes;
+// int8 weights: 2^14 (p - [target]) scale / 2^E, E the smallest (at least -100) with
+// every scale below 2^E (a power of two: nothing more is rounded), against the codes;
 // 4-bit weights: 2^14 (p - [target]), against q times (scale / 8) in float16 (7
 // times the largest scale then fits; the quotient loses bits of scales under 2^-11
 // only).
@@ -394,21 +395,21 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
   float* qs = reinterpret_cast<float*>(lds + Lds::QS);     // B
   float* rsv = reinterpret_cast<float*>(lds + Lds::RS);    // log2e sx
   float* swv = reinterpret_cast<float*>(lds + Lds::SW);
-  int* tgv = reinterpret_cast<int*>(lds + Lds::TG);        // the target's column here; INT32_MIN: none
+  int* tgv = reinterpret_cast<int*>(lds + Lds::TG);        // the target's column here, or kNone
   float* lsv = reinterpret_cast<float*>(lds + Lds::LS);    // log2e lse
   uint16_t* tb = reinterpret_cast<uint16_t*>(lds + Lds::TB);
   // int8, dl in float16: the scales times 2^(14 - E), the rows' the other way round
   const int power = HALF && !W4 ? 14 - scale_power(emax) : 0;
   const float up = __builtin_ldexpf(1.f, power), down = __builtin_ldexpf(1.f, -power);
   // Gradient: a row without a target has logits 0 and lse infinite, so that its
-  // p is 0 whatever its codes' scale is.
+  // p is 0 whatever its x is (and is set to 0 below, for weights that are no numbers).
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     const int row = tid + NT * i;
     if (row < BM) {
       const bool none = GRAD && etg[i] < 0;
       rsv[row] = none ? 0.f : esx[i] * (W4 ? kLog2e / 16.f : kLog2e) * down;   // (4-bit: the products are those of 16 q)
-      tgv[row] = etg[i] >= 0 ? etg[i] - n0 : INT32_MIN;
+      tgv[row] = etg[i] >= 0 ? etg[i] - n0 : kNone;
       if constexpr (GRAD) lsv[row] = none ? INFINITY : else_[i] * kLog2e;
     }
   }
@@ -549,6 +550,12 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
       for (int j = 0; j < FN; ++j)
 #pragma unroll
         for (int ii = 0; ii < 4; ++ii) x[j][ii] = __builtin_amdgcn_exp2f(x[j][ii]);
+      if (__builtin_amdgcn_ballot_w64(tg < kNone / 2) != 0) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int ii = 0; ii < 4; ++ii) x[j][ii] = tg < kNone / 2 ? 0.f : x[j][ii];
+      }
       if (hit) {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
@@ -977,7 +984,7 @@ __global__ __launch_bounds__(256) void xent_reduce_kernel(ReduceArgs a) {
   };
   if (e < nu) {
     const float v = sum(a.up + e, nu, a.tiles_x), u = a.first ? v : a.u[e] + v;
-    a.u[e] = a.last ? u * row_factor(a.ids, a.dloss, e / a.r) : u;
+    a.u[e] = a.last ? u * row_factor(a.ids, a.dloss, e / a.r) : u;     // (u of a row without a target is 0)
   } else if (e < nu + ndb) {
     const long j = (e - nu) / a.vc, c = (e - nu) % a.vc;
     a.dB[j * a.N + a.v0 + c] = a.s * sum(a.dbp + j * a.ldg + c, a.r * a.ldg, a.tiles_m);
@@ -1005,7 +1012,8 @@ __global__ __launch_bounds__(256) void xent_dx_join_kernel(const float* dxp, int
   for (int b = 0; b < 4; ++b) v[b] = *reinterpret_cast<const f32x4*>(p + 4 * b);
   // (int8, dl in float16: back from 2^(14 - E))
   const float back = smax != nullptr ? __builtin_ldexpf(1.f, scale_power(smax[lane]) - 14) : down;
-  const float f = row_factor(ids, dloss, mc) * back;
+  const bool live = entry_of(ids, mc) >= 0;
+  const float f = dloss[mc] * back;
   f32x4 low[4];
   if constexpr (R > 0) {
 #pragma unroll
@@ -1038,7 +1046,10 @@ __global__ __launch_bounds__(256) void xent_dx_join_kernel(const float* dxp, int
 #pragma unroll
   for (int b = 0; b < 4; ++b)
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[b][c] = R > 0 ? __builtin_fmaf(s, low[b][c], v[b][c] * f) : v[b][c] * f;
+    for (int c = 0; c < 4; ++c) {
+      const float y = R > 0 ? __builtin_fmaf(s, low[b][c], v[b][c] * f) : v[b][c] * f;
+      v[b][c] = live ? y : 0.f;                            // (weights that are no numbers times 0)
+    }
   OutT* out = dx + (long)m * K + k;
   if constexpr (sizeof(OutT) == 4) {
 #pragma unroll
@@ -1141,8 +1152,7 @@ void launch_dx(const DxArgs& a, int rows, hipStream_t st) {
 
 }  // namespace
 
-size_t xent_part_floats(int fmt, int vocab, int M) {
-  (void)fmt;
+size_t xent_part_floats(int vocab, int M) {
   return ((size_t)((vocab + 127) / 128) * 2 + 1) * (size_t)M;
 }
 

@@ -223,3 +223,15 @@ def test_8_bit_moments_follow_a_steady_gradient():
     # a standard deviation under 0.15 in v once settled, a mean of 3968 of them 0.003
     assert abs(root[:, 1:].mean() / want - 1) < 0.03
     assert abs(m[:, 1:].mean() / 0.5 - 1) < 0.03
+
+
+def test_state_that_overlaps_is_refused():
+    z = lambda *s, **k: torch.zeros(*s, device="cuda", **k)  # noqa: E731
+    a, b, long = z(64), z(32), z(256)
+    for kw in (dict(params=[a, b, a]), dict(params=[long[:64], long[48:]]),
+               dict(params=[a, b], m=[long[:64], long[32:64]]), dict(params=[a, b], v=[long[:64], a[:32]]),
+               dict(params=[a, b], m=[long[:64], long[64:96]], v=[long[128:192], long[80:112]]),
+               dict(params=[a], step=a.view(torch.int32)[:1])):
+        with pytest.raises(ValueError, match="overlap"):
+            Q.AdamW(**kw)
+    Q.AdamW([a, b], m=[long[:64], long[64:96]], v=[long[128:192], long[192:224]])

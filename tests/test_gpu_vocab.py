@@ -24,7 +24,10 @@ F64 = np.float64
 U32 = 2.0 ** -24          # half a step of float32, relative
 U16 = 2.0 ** -8           # of bfloat16 (one part of a value: relative to it)
 H16 = 2.0 ** -11          # of float16
-TWO = 2.0 ** -16          # a value in two bf16 parts
+# A product of two values in three bf16 parts each (8 bits a part, each rounded: what
+# is left of a value is 2^-27 of it), without the products of parts 2^-27 and smaller
+# (second times third, both ways, third times third): 2 2^-27 + 2 2^-27 and a little
+THREE = 2.0 ** -24
 
 
 def say(*a):
@@ -140,7 +143,12 @@ class Case:
             wtiny = 8 * 2.0 ** -22
             tdx = (tdl + rel * np.abs(dl) + tiny) @ W + (np.abs(dl) + tdl) @ np.full_like(W, wtiny)
         elif self.dtype == "bf16":
-            tdx = (tdl + (U16 + 2 * U32) * np.abs(dl)) @ W
+            # dl times the scale in float16, 2^-24 the smallest step of it: off by half of
+            # that where it is small, in units of dloss 2^(E - 14), 2^E at most twice the
+            # largest scale; times a code of at most 127, over the vocabulary
+            top = float(to_numpy(self.lin.scales)[:self.vocab].max())
+            tiny = 2.0 ** -25 * 2.0 ** -14 * 2 * top * 127 * self.vocab
+            tdx = (tdl + (H16 + 2 * U32) * np.abs(dl)) @ W + tiny * np.abs(g)[:, None]
         else:
             tdx = (tdl + 4 * U32 * np.abs(dl)) @ W
         tdx = tdx + sums * ((np.abs(dl) + tdl) @ W)
@@ -150,7 +158,7 @@ class Case:
             return (dx, None, None), (self.u * (np.abs(dx) + tdx) + tdx, None, None)
         B = np.abs(self.B64[:, :self.vocab]).T
         u = dl @ self.B64[:, :self.vocab].T
-        tu = (tdl + (2 * TWO + 2 * sums) * np.abs(dl)) @ B
+        tu = (tdl + (THREE + 2 * sums) * np.abs(dl)) @ B
         A = np.abs(self.A64)
         low = np.abs(u) @ A.T
         tdx = tdx + self.s * (tu @ A.T + (self.r + 2) * U32 * low) + 2 * U32 * (np.abs(dx) + self.s * low)
@@ -158,7 +166,7 @@ class Case:
         tdA = self.s * (np.abs(x64).T @ (tu + rows * np.abs(u)) + 2 * U32 * (np.abs(x64).T @ np.abs(u)))
         at = np.abs(t).T
         tdB = np.zeros_like(dB)
-        tdB[:, :self.vocab] = self.s * (at @ tdl + tol_t.T @ np.abs(dl) + (2 * TWO + rows) * (at @ (np.abs(dl) + tdl)))
+        tdB[:, :self.vocab] = self.s * (at @ tdl + tol_t.T @ np.abs(dl) + (THREE + rows) * (at @ (np.abs(dl) + tdl)))
         return (dx, dA, dB), (self.u * (np.abs(dx) + tdx) + tdx, tdA, tdB)
 
 
@@ -425,6 +433,65 @@ def test_gradient_of_large_and_tiny_weights():
         within(to_numpy(lse), wlse, tol_lse, "lse")
         (dx, _, _), (tdx, _, _) = c.grads(l, tol, wlse, tol_lse, None, None)
         within(to_numpy(got), dx, tdx + 1e-37, "dx")
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-12, 1e12])
+def test_gradient_of_weights_far_from_one(scale):
+    """Every weight times `scale` (the rows of x divided by it where that is large):
+    dx is as far from 0."""
+    c = Case(150, 64, 300, 0, "w8", "bf16", wstd=0.05 * scale)
+    if scale > 1:
+        c.x_t, c.x = WL.as_compute_dtype((c.x / scale).astype(np.float32), "bf16")
+        c.x_t = c.x_t.cuda()
+    say("weights times", scale)
+    l, tol, _, _ = c.logits()
+    _, wlse = V.loss_of(l, c.ids)
+    _, lse, _ = Q.qlora_xent_fwd(c.lin, c.x_t, c.ids_t, vocab=300)
+    got = Q.qlora_xent_bwd(c.lin, c.x_t, c.ids_t, lse, dev(c.dloss), vocab=300)[0]
+    torch.cuda.synchronize()
+    tol_lse = c.lse_tol(l, tol)
+    within(to_numpy(lse), wlse, tol_lse, "lse")
+    (dx, _, _), (tdx, _, _) = c.grads(l, tol, wlse, tol_lse, None, None)
+    within(to_numpy(got), dx, tdx + 1e-37, "dx")
+
+
+@pytest.mark.parametrize("fmt,dtype", [("w8", "bf16"), ("w8", "f32"), ("w4g128", "bf16")])
+def test_rows_without_a_target_beside_weights_that_are_no_numbers(fmt, dtype):
+    """No row has a target: every gradient is 0, whatever the weights hold."""
+    c = Case(70, 128, 300, 4, fmt, dtype, tokens=np.full(70, -1))
+    B = c.B.copy()
+    B[1, 7], B[2, 9] = np.inf, np.nan
+    c.lin.B = dev(B)
+    c.lin.scales[5] = float("nan")
+    c.lin.scales[6] = float("inf")
+    say("no numbers, no targets", fmt, dtype)
+    loss, lse, t = Q.qlora_xent_fwd(c.lin, c.x_t, c.ids_t, vocab=300)
+    dx, dA, dB = Q.qlora_xent_bwd(c.lin, c.x_t, c.ids_t, lse, dev(c.dloss), t=t, vocab=300)
+    torch.cuda.synchronize()
+    assert not to_numpy(loss).any()
+    for g in (dx, dA, dB):
+        assert not to_numpy(g).any()
+
+
+@pytest.mark.parametrize("itype", ["i32", "i64"])
+def test_tokens_that_begin_anywhere(itype):
+    """Slices of a longer tensor of ids give what their copies give."""
+    c = Case(40, 64, 100, 4, "w8", "bf16", itype=itype)
+    say("slices", itype)
+    dloss = dev(c.dloss)
+    for off in (1, 2, 3):
+        long = torch.cat([c.ids_t.new_full((off,), 3), c.ids_t])
+        for ids in (long[off:],):
+            assert ids.data_ptr() % 16 == off * ids.element_size() % 16
+
+            def run(ids):
+                x = Q.qlora_embed(c.lin, ids, vocab=100, dtype=torch.bfloat16)
+                loss, lse, t = Q.qlora_xent_fwd(c.lin, c.x_t, ids, vocab=100)
+                return [x, loss, lse, *Q.qlora_xent_bwd(c.lin, c.x_t, ids, lse, dloss, t=t, vocab=100),
+                        *Q.qlora_embed_bwd(c.lin, ids, c.dy_t, vocab=100)]
+
+            for a, b in zip(run(ids), run(c.ids_t)):
+                assert torch.equal(bits(a), bits(b))
 
 
 def test_adapter_gradients_against_differences_of_the_loss():
