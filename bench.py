@@ -9,7 +9,8 @@ every layer in reverse (dy B^T, dB, dA, and the bf16 MFMA input gradient).
 For stacks of at least 4 layers (``--finish``) each layer's backward leaves
 its adapter-gradient partial sums in a workspace of its own and one batched
 call adds them into every layer's dA and dB after the last layer; otherwise
-each layer's ``qlora_bwd`` combines its own. Both steps are timed and
+each layer's ``qlora_bwd`` combines its own. ``--optimizer`` ends the step
+by one AdamW step of all adapters (``qlora_adamw``). Both steps are timed and
 reported (``batched_finish_ms_per_step``, ``layerwise_finish_ms_per_step``).
 The one-time weight quantization is timed separately (``quantize_ms``).
 Inputs are seeded synthetic tensors already resident in HBM. Steps are
@@ -71,6 +72,10 @@ def parse():
                    help="adapter-gradient combine of the timed step: one batched call after "
                         "the last layer, or one per layer (auto: batched for stacks of at "
                         "least 4 layers)")
+    p.add_argument("--optimizer", choices=("none", "f32", "s8"), default="none",
+                   help="end the step by one AdamW step of every layer's A and B, moments in "
+                        "float32 or in 8 bits (its time is in ms_per_step, its operations are not "
+                        "in value)")
     p.add_argument("--copy-calibration", action="store_true",
                    help="also run the library's copy (256 MiB) and read (1 GiB) probes, "
                         "known byte counts for scaling HBM counters")
@@ -223,6 +228,13 @@ def main():
     if w.cid == 4 and w.wfmt == "w8":
         heads_leg = multi_head_leg(torch, dev, lib, check, M)
 
+    # --optimizer: every adapter moved by its gradient at the step's end
+    move = lambda: None  # noqa: E731
+    if args.optimizer != "none":
+        opt = Q.AdamW([p for l in layers for p in (l.A, l.B)], state=args.optimizer, decay=0.01)
+        grads = [g for l in layers for g in (l.dA, l.dB)]
+        move = lambda: Q.qlora_adamw(opt, grads, 5e-5, clip_norm=1.0)  # noqa: E731
+
     def step(ev_b=None, repeats=1):
         st = torch.cuda.current_stream().cuda_stream
         for i, l in enumerate(layers):
@@ -236,6 +248,8 @@ def main():
                                       l.dy.data_ptr(), l.t.data_ptr(), l.dx.data_ptr(),
                                       l.dA.data_ptr(), l.dB.data_ptr(), wsp, ws_bytes, st,
                                       repeats if ev_b else 1, a, b), "bwd")
+        if ev_b is None:
+            move()
 
     # The timed step runs each layer's backward as qlora_bwd_partial (dx and
     # the adapter-gradient partial sums, into a workspace of its own) and
@@ -269,6 +283,7 @@ def main():
                                         l.dy.data_ptr(), l.t.data_ptr(), l.dx.data_ptr(),
                                         bws_ptr[i], bws_n[i], st), "bwd_partial")
         check(lib.qlora_bwd_finish_batch(items, len(layers), st), "finish_batch")
+        move()
 
     # eager warm-up (also loads every kernel)
     for _ in range(3):
@@ -416,6 +431,8 @@ def main():
         "roofline": roof,
         "cpu_baseline": cpu,
     }
+    if args.optimizer != "none":
+        out["optimizer"] = f"adamw {args.optimizer}"
     print(json.dumps(out), flush=True)
 
 
