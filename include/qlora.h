@@ -623,8 +623,8 @@ typedef struct {
 } qlora_adamw_config;
 
 /* One step of `count` tensors: one launch where they hold at most 8192 elements
- * in at most 48 tensors; else one launch that advances the step (with clip_norm
- * > 0 or norm given, one per 48 tensors that sum the norm), and one per 48
+ * in at most 64 tensors; else one launch that advances the step (with clip_norm
+ * > 0 or norm given, one per 64 tensors that sum the norm), and one per 64
  * tensors that moves them. items[] and cfg are read during the call only (host
  * memory). Tensors of different items must not overlap each other (not checked).
  * 0 <= beta < 1, eps > 0, lr, decay and clip_norm >= 0 and all finite; 0 <=

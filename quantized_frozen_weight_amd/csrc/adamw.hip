@@ -3,7 +3,7 @@
 //
 // Memory-bound: an element moves 28 bytes with float32 moments, 16.1 with 8-bit
 // ones, and 4 more where the norm is taken first. Few elements (8192) are one
-// block's work in one launch; else two kernels, each launched once per 48
+// block's work in one launch; else two kernels, each launched once per 64
 // tensors, their pointers in the kernel's arguments:
 //
 //   norm    a block sums the squares of one chunk of one tensor in float64 and
@@ -30,7 +30,7 @@ namespace qlora {
 
 namespace {
 
-constexpr int kItems = 48;           // tensors per launch
+constexpr int kItems = 64;           // tensors per launch (one a lane; 4 KB of arguments)
 constexpr int kChunk = 4096;         // elements per block of the update
 constexpr int kNormSums = 512;       // about as many partial sums of the norm
 constexpr int kSmall = 8192;         // elements in all that one block steps
@@ -64,11 +64,10 @@ struct NormArgs {
 };
 static_assert(sizeof(NormArgs) <= 4096, "kernel arguments");
 
-template <int N>
-__device__ __forceinline__ int item_of(const int (&bstart)[N], int count, int b) {
-  int i = 0;
-  while (i + 1 < count && b >= bstart[i + 1]) ++i;          // block-uniform
-  return i;
+// The tensor of block b: a lane looks at one tensor's first block each.
+__device__ __forceinline__ int item_of(const int* bstart, int count, int b) {
+  const int lane = threadIdx.x & 63;
+  return __builtin_popcountll(__builtin_amdgcn_ballot_w64(lane < count && b >= bstart[lane])) - 1;
 }
 
 // Sum over the block's 256 threads, the same in every thread and in a fixed
@@ -135,7 +134,7 @@ struct UpdateArgs {
   const double* sums;                // NULL: no norm
   float* norm;
 };
-static_assert(sizeof(UpdateArgs) <= 4096, "kernel arguments");
+static_assert(sizeof(UpdateArgs) + 32 <= 4096, "kernel arguments");
 
 // 32 bits for one element: two rounds of multiply and shift (odd constants: the
 // golden ratio's and the square roots' of 2 and 3 first 32 bits).
