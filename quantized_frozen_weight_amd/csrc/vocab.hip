@@ -245,10 +245,21 @@ __device__ __forceinline__ void place_block(const EmbedBwdArgs& a, int b, int* t
   const int m0 = b * kPlaceRows, s0 = m0 / kSlice * kSlice;
   const int n = a.M - s0 < kSlice ? a.M - s0 : kSlice;           // rows of the slice
   const int n4 = (n + 4 * PT - 1) / (4 * PT) * (4 * PT);
-  for (int i = tid; i < n4; i += 256) {
-    const int t = i < n ? entry_of(a.ids, s0 + i) : 0x7fffffff;   // (past the slice: behind every row)
-    toks[i] = t >= 0 ? t : a.N;
-  }
+  auto stage = [&](auto* ids) {
+    for (int i0 = tid; i0 < n4; i0 += 8 * 256) {                 // eight loads in flight
+      int t[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const auto v = ids[s0 + (i0 + 256 * u < n ? i0 + 256 * u : n - 1)];
+        t[u] = v >= 0 && v < a.ids.vocab ? (int)v : a.N;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)                                // (past the slice: behind every row)
+        if (i0 + 256 * u < n4) toks[i0 + 256 * u] = i0 + 256 * u < n ? t[u] : 0x7fffffff;
+    }
+  };
+  if (a.ids.wide) stage(static_cast<const int64_t*>(a.ids.p));
+  else stage(static_cast<const int32_t*>(a.ids.p));
   __syncthreads();
   const int mine = m0 - s0 + tid / PT * RT;                      // the first of the thread's rows
   int t[RT], before[RT];
@@ -261,6 +272,7 @@ __device__ __forceinline__ void place_block(const EmbedBwdArgs& a, int b, int* t
   // where it is smaller; only the block's own rows have to be told apart one by one
   const int own = m0 - s0;
   auto count = [&](int i0, int i1, int more) {                   // tokens below t + more
+#pragma unroll 4
     for (int i = i0 + 4 * part; i < i1; i += 4 * PT) {
       const i32x4 v = *reinterpret_cast<const i32x4*>(toks + i);
 #pragma unroll
