@@ -622,8 +622,8 @@ typedef struct {
   int32_t sfmt;           /* qlora_sfmt */
 } qlora_adamw_config;
 
-/* One step of `count` tensors: one launch where they hold at most 8192 elements
- * in at most 64 tensors; else one launch that advances the step (with clip_norm
+/* One step of `count` tensors: one launch where they are at most two of at most
+ * 8192 elements together; else one launch that advances the step (with clip_norm
  * > 0 or norm given, one per 64 tensors that sum the norm), and one per 64
  * tensors that moves them. items[] and cfg are read during the call only (host
  * memory). Tensors of different items must not overlap each other (not checked).

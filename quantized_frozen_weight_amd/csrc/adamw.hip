@@ -2,7 +2,7 @@
 // the 8-bit form: include/qlora.h).
 //
 // Memory-bound: an element moves 28 bytes with float32 moments, 16.1 with 8-bit
-// ones, and 4 more where the norm is taken first. Few elements (8192) are one
+// ones, and 4 more where the norm is taken first. Two small tensors are one
 // block's work in one launch; else two kernels, each launched once per 64
 // tensors, their pointers in the kernel's arguments:
 //
@@ -33,7 +33,8 @@ namespace {
 constexpr int kItems = 64;           // tensors per launch (one a lane; 4 KB of arguments)
 constexpr int kChunk = 4096;         // elements per block of the update
 constexpr int kNormSums = 512;       // about as many partial sums of the norm
-constexpr int kSmall = 8192;         // elements in all that one block steps
+constexpr int kSmall = 8192;         // elements in all that one block steps,
+constexpr int kSmallItems = 2;       // in up to so many tensors (a layer's A and B)
 
 // What the norm launch leaves for the update.
 struct Hyper {
@@ -362,9 +363,10 @@ __global__ __launch_bounds__(256) void adamw_update_kernel(UpdateArgs a) {
   for (int u = 0; u < U; ++u) x[u].update(it, c0 + 1024 * u + 4 * tid, a.item0 + i, keep, s);
 }
 
-// The whole step of few elements in one block and one launch (two launches took
-// 18.7 us from Python for two tensors of 1024): the norm, then the tensors one
-// after the other. sums_n: whether the norm is wanted.
+// The whole step of few elements in one block and one launch: the norm, then the
+// tensors one after the other, 1.8 us each with float32 moments and 3.2 with 8-bit
+// ones (replayed: 6.8 and 9.6 us for two tensors, 10.4 and 16 for four; two launches
+// take 8.8 and 10.7 for any number). sums_n: whether the norm is wanted.
 template <bool S8>
 __global__ __launch_bounds__(1024) void adamw_small_kernel(UpdateArgs a, double lr, double beta1, double beta2,
                                                            const float* lr_dev) {
@@ -529,7 +531,7 @@ void launch_adamw(const qlora_adamw_config& cfg, const qlora_adamw_item* items, 
   double* sums = norm ? reinterpret_cast<double*>(static_cast<char*>(ws) + align_up(sizeof(Hyper))) : nullptr;
   long chunk, total = 0;
   for (int i = 0; i < count; ++i) total += items[i].n;
-  const bool small = total <= kSmall && count <= kItems;
+  const bool small = total <= kSmall && count <= kSmallItems;
   const long nsums = adamw_norm_blocks(items, count, &chunk);
   long base = 0;
   for (int i0 = 0; !small && i0 < (norm ? count : 1); i0 += kItems) {

@@ -42,7 +42,9 @@ def same(a, b):
     return np.array_equal(np.asarray(a), np.asarray(b), equal_nan=True)
 
 
-SIZES = [[1], [3], [4, 5, 31, 32, 33], [64, 4095, 4096, 4097], [1000] * 60, [7, 100000, 12, 300007], [2] * 130]
+SIZES = [[1], [3], [4, 5, 31, 32, 33], [64, 4095, 4096, 4097], [1000] * 60, [7, 100000, 12, 300007], [2] * 130,
+         # two tensors of 8192 elements are the most that one block steps
+         [33] * 64, [96 + i for i in range(64)], [8192], [8193], [8160, 32], [1, 8191], [5, 7, 9], [20] * 64, [20] * 65]
 
 
 @pytest.mark.parametrize("state", ["f32", "s8"])
