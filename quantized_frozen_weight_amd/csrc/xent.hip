@@ -42,6 +42,7 @@ namespace {
 
 constexpr int kCUs = 256;
 constexpr int kFewTiles = 64;      // of 128 x 128: up to so many are taken as 32 x 256
+constexpr int kHalfTiles = 160;    // of 256 x 256: up to so many are taken as 128 x 128
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kNone = -(1 << 30);  // no target: far from every tile (a column is above -2^27)
@@ -950,9 +951,12 @@ __global__ __launch_bounds__(64 * WM * 4) void xent_dx_kernel(DxArgs a) {
 }
 
 // After a piece: u += its tiles' parts, dB of its entries = s times the row
-// tiles' parts; the last piece also clears dB's padding. Thread per element.
+// tiles' parts; the last piece also clears dB's padding. The first `ublocks` blocks
+// take `ue` elements of u each (a power of two), 256 / ue threads an element that
+// share its tiles, few elements where there are few (64 rows of rank 8 over 393
+// tiles: 4.8 us, a thread each 30); the others a thread an element.
 struct ReduceArgs {
-  int M, N, r, tiles_x, tiles_m, v0, vc, first, last, V;
+  int M, N, r, tiles_x, tiles_m, v0, vc, first, last, V, ue, ublocks;
   long ldg;
   float s;
   Ids ids;
@@ -968,7 +972,9 @@ __device__ __forceinline__ float row_factor(const Ids& ids, const float* dloss, 
 }
 
 __global__ __launch_bounds__(256) void xent_reduce_kernel(ReduceArgs a) {
-  const long e = (long)blockIdx.x * 256 + threadIdx.x, nu = (long)a.M * a.r;
+  __shared__ float red[256];
+  const int tid = threadIdx.x;
+  const long nu = (long)a.M * a.r;
   const long ndb = (long)a.r * a.vc, npad = a.last ? (long)a.r * (a.N - a.V) : 0;
   auto sum = [](const float* p, long stride, int n) {
     float s = 0.f;
@@ -982,34 +988,55 @@ __global__ __launch_bounds__(256) void xent_reduce_kernel(ReduceArgs a) {
     }
     return s;
   };
-  if (e < nu) {
-    const float v = sum(a.up + e, nu, a.tiles_x), u = a.first ? v : a.u[e] + v;
+  if ((int)blockIdx.x < a.ublocks) {
+    const int lane = tid / a.ue, lanes = 256 / a.ue;
+    const long e = (long)blockIdx.x * a.ue + tid % a.ue, ec = e < nu ? e : 0;
+    red[tid] = lane < a.tiles_x ? sum(a.up + lane * nu + ec, lanes * nu, (a.tiles_x - lane + lanes - 1) / lanes) : 0.f;
+    for (int d = 128; d >= a.ue; d >>= 1) {
+      __syncthreads();
+      if (tid < d) red[tid] += red[tid + d];
+    }
+    if (lane != 0 || e >= nu) return;
+    const float u = a.first ? red[tid] : a.u[e] + red[tid];
     a.u[e] = a.last ? u * row_factor(a.ids, a.dloss, e / a.r) : u;     // (u of a row without a target is 0)
-  } else if (e < nu + ndb) {
-    const long j = (e - nu) / a.vc, c = (e - nu) % a.vc;
+    return;
+  }
+  const long e = (long)((int)blockIdx.x - a.ublocks) * 256 + tid;
+  if (e < ndb) {
+    const long j = e / a.vc, c = e % a.vc;
     a.dB[j * a.N + a.v0 + c] = a.s * sum(a.dbp + j * a.ldg + c, a.r * a.ldg, a.tiles_m);
-  } else if (e < nu + ndb + npad) {
-    const long j = (e - nu - ndb) / (a.N - a.V), c = (e - nu - ndb) % (a.N - a.V);
+  } else if (e < ndb + npad) {
+    const long j = (e - ndb) / (a.N - a.V), c = (e - ndb) % (a.N - a.V);
     a.dB[j * a.N + a.V + c] = 0.f;
   }
 }
 
-// dx = factor times the splits' sums + s u A^T. A wave takes 16 rows of 64
-// features, lane (l, q) the 16 features of quarter q of row l; the adapter's part is
-// formed on v_mfma_f32_16x16x4_f32 in that layout (as the lookup's: a thread that
-// read its features' rows of A for itself took 49 us for 4096 x 768 at rank 8).
-template <typename OutT, int R>
-__global__ __launch_bounds__(256) void xent_dx_join_kernel(const float* dxp, int splits, int M, int K, int r, float s,
-                                                           const float* u, const float* A, Ids ids, const float* dloss,
-                                                           float down, const uint32_t* smax, OutT* dx) {
-  const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
+// dx = factor times the splits' sums + s u A^T, over tiles of 16 rows and 64
+// features: lane (l, q) holds the 16 features of quarter q of row l; the adapter's
+// part is formed on v_mfma_f32_16x16x4_f32 in that layout (as the lookup's: a thread
+// that read its features' rows of A for itself took 49 us for 4096 x 768 at rank 8).
+// SW = 1: a wave takes a tile, four a block. SW = 16: the waves of a block share the
+// splits of one tile and add through LDS, four of them a quarter of each lane's
+// features: where there are at most as many tiles as compute units (64 x 768 in 85
+// splits: 15.7 us, one wave a tile 41; 256 x 2048 in 32 splits, 512 tiles, the other
+// way round: 25.9 against 19.3).
+template <typename OutT, int R, int SW>
+__global__ __launch_bounds__(SW == 1 ? 256 : 64 * SW) void xent_dx_join_kernel(const float* dxp, int splits, int M, int K,
+                                                                               int r, float s, const float* u,
+                                                                               const float* A, Ids ids,
+                                                                               const float* dloss, float down,
+                                                                               const uint32_t* smax, OutT* dx) {
+  __shared__ f32x4 red[SW > 1 ? SW * 256 : 1];             // [wave][block of 4 features][lane]
+  const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4, w = threadIdx.x >> 6;
   const int m = blockIdx.x * 16 + l, mc = m < M ? m : M - 1;
-  const int d0 = ((int)blockIdx.y * 4 + ((int)threadIdx.x >> 6)) * 64, k = d0 + 16 * q, kc = k < K ? k : 0;
+  const int d0 = (SW > 1 ? (int)blockIdx.y : (int)blockIdx.y * 4 + w) * 64, k = d0 + 16 * q, kc = k < K ? k : 0;
+  const int first = SW > 1 ? w : 0;
   const long n = (long)M * K;
   const float* p = dxp + (long)mc * K + kc;
   f32x4 v[4];
 #pragma unroll
-  for (int b = 0; b < 4; ++b) v[b] = *reinterpret_cast<const f32x4*>(p + 4 * b);
+  for (int b = 0; b < 4; ++b)
+    v[b] = first < splits ? *reinterpret_cast<const f32x4*>(p + first * n + 4 * b) : f32x4{0.f, 0.f, 0.f, 0.f};
   // (int8, dl in float16: back from 2^(14 - E))
   const float back = smax != nullptr ? __builtin_ldexpf(1.f, scale_power(smax[lane]) - 14) : down;
   const bool live = entry_of(ids, mc) >= 0;
@@ -1024,23 +1051,45 @@ __global__ __launch_bounds__(256) void xent_dx_join_kernel(const float* dxp, int
       const float uv = j < r ? u[(long)mc * r + jc] : 0.f;
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
+        if (SW > 1 && b != w) continue;                    // (wave-uniform: what this wave writes)
         const int d = d0 + 16 * (l >> 2) + 4 * b + (l & 3);
         const float av = d < K && j < r ? A[(long)(d < K ? d : 0) * r + jc] : 0.f;
         low[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(av, uv, low[b], 0, 0, 0);
       }
     }
   }
-  for (int i = 1; i < splits; i += 4) {                    // four splits' loads in flight
-    f32x4 w[4][4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) w[c][b] = *reinterpret_cast<const f32x4*>(p + (i + c < splits ? i + c : 0) * n + 4 * b);
+  for (int i = first + SW; i < splits; i += 4 * SW) {      // four splits' loads in flight
+    f32x4 x[4][4];
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
       for (int b = 0; b < 4; ++b)
-        if (i + c < splits) v[b] += w[c][b];
+        x[c][b] = *reinterpret_cast<const f32x4*>(p + (i + c * SW < splits ? i + c * SW : 0) * n + 4 * b);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (i + c * SW < splits) v[b] += x[c][b];
+  }
+  OutT* out = dx + (long)m * K + k;
+  if constexpr (SW > 1) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) red[(w * 4 + b) * 64 + lane] = v[b];
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if (b != w || m >= M || k >= K) continue;
+      f32x4 y = red[b * 64 + lane];
+      for (int i = 1; i < SW && i < splits; ++i) y += red[(i * 4 + b) * 64 + lane];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float z = R > 0 ? __builtin_fmaf(s, low[b][c], y[c] * f) : y[c] * f;
+        y[c] = live ? z : 0.f;                             // (weights that are no numbers times 0)
+      }
+      if constexpr (sizeof(OutT) == 4) *reinterpret_cast<f32x4*>(out + 4 * b) = y;
+      else *reinterpret_cast<u32x2*>(out + 4 * b) = u32x2{pk_bf16(y[0], y[1]), pk_bf16(y[2], y[3])};
+    }
+    return;
   }
   if (m >= M || k >= K) return;
 #pragma unroll
@@ -1048,9 +1097,8 @@ __global__ __launch_bounds__(256) void xent_dx_join_kernel(const float* dxp, int
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const float y = R > 0 ? __builtin_fmaf(s, low[b][c], v[b][c] * f) : v[b][c] * f;
-      v[b][c] = live ? y : 0.f;                            // (weights that are no numbers times 0)
+      v[b][c] = live ? y : 0.f;
     }
-  OutT* out = dx + (long)m * K + k;
   if constexpr (sizeof(OutT) == 4) {
 #pragma unroll
     for (int b = 0; b < 4; ++b) *reinterpret_cast<f32x4*>(out + 4 * b) = v[b];
@@ -1065,13 +1113,19 @@ __global__ __launch_bounds__(256) void xent_dx_join_kernel(const float* dxp, int
 template <typename OutT>
 void dx_join(const VocabLayer& L, int M, Ids ids, const float* dloss, const XentPlan& plan, const XentBuffers& buf,
              void* dx, hipStream_t st) {
-  const dim3 grid((unsigned)((M + 15) / 16), (unsigned)((L.K + 255) / 256));
+  const unsigned rows = (unsigned)((M + 15) / 16), cols = (unsigned)((L.K + 63) / 64);
+  const bool shared = plan.splits >= 8 && (long)rows * cols <= kCUs;
   const float down = L.fmt == 0 ? 1.f : kHalfDown;
   OutT* out = static_cast<OutT*>(dx);
   const auto launch = [&](auto rank) {
-    xent_dx_join_kernel<OutT, decltype(rank)::value><<<grid, 256, 0, st>>>(
-        buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids, dloss, down,
-        L.fmt == 0 && plan.parts == 1 ? buf.smax : nullptr, out);
+    constexpr int R = decltype(rank)::value;
+    const uint32_t* smax = L.fmt == 0 && plan.parts == 1 ? buf.smax : nullptr;
+    if (shared)
+      xent_dx_join_kernel<OutT, R, 16><<<dim3(rows, cols), 1024, 0, st>>>(buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u,
+                                                                         L.A, ids, dloss, down, smax, out);
+    else
+      xent_dx_join_kernel<OutT, R, 1><<<dim3(rows, (cols + 3) / 4), 256, 0, st>>>(
+          buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids, dloss, down, smax, out);
   };
   if (L.r == 0) launch(std::integral_constant<int, 0>());
   else if (L.r <= 4) launch(std::integral_constant<int, 4>());
@@ -1115,10 +1169,15 @@ template <int PARTS>
 void logits(LogitArgs& a, int fmt, int cols, hipStream_t st) {
   if (fmt == 0) {
     const long t128 = (long)((a.M + 127) / 128) * ((cols + 127) / 128);
+    const long t256 = (long)((a.M + 255) / 256) * ((cols + 255) / 256);
     // few tiles leave compute units idle: smaller ones then (64 x 768 x 4000 rank 4
     // with gradient 67.5 -> 63.5 us, 128 x 2048 x 4000 64.2 -> 59.4)
+    // Large tiles read least from LDS for a product, but take a compute unit each: from
+    // 63 to 128 of them smaller ones are faster (256 x 2048 over 32000: loss 41.9 against
+    // 34.9 us, 4096 features 58 against 45, 8000 entries of 768 26.6 against 22.1), 189
+    // of them not (640 x 2048 over 16000: 42.9 against 44.8)
     if (a.M <= 32 || t128 <= kFewTiles) logits_ranks<false, 32, 256, 1, 4, 4, 1, PARTS>(a, cols, st);
-    else if (a.M > 128 && a.r <= 16) logits_ranks<false, 256, 256, 2, 4, 2, 1, PARTS>(a, cols, st);
+    else if (t256 > kHalfTiles && a.M > 128 && a.r <= 16) logits_ranks<false, 256, 256, 2, 4, 2, 1, PARTS>(a, cols, st);
     else logits_ranks<false, 128, 128, 2, 2, 2, 1, PARTS>(a, cols, st);
   } else if constexpr (PARTS == 3) {
     return;                                                // (float32 has no 4-bit layers)
@@ -1227,10 +1286,12 @@ void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const void*
       else launch_dx<0>(d, rows, st);
     }
     if (L.r > 0) {
-      ReduceArgs r{M, L.N, L.r, a.tiles_x, a.tiles_m, v0, vc, v0 == 0, v0 + vc == V, V, ldg, L.s, ids, dloss,
-                   buf.up, buf.dbp, buf.u, dB};
-      const long n = (long)M * L.r + (long)L.r * vc + (r.last ? (long)L.r * (L.N - V) : 0);
-      xent_reduce_kernel<<<dim3((unsigned)((n + 255) / 256)), 256, 0, st>>>(r);
+      const long nu = (long)M * L.r;
+      const int ue = nu > 8192 ? 32 : 8;                   // (32: whole lines of every tile's parts)
+      ReduceArgs r{M, L.N, L.r, a.tiles_x, a.tiles_m, v0, vc, v0 == 0, v0 + vc == V, V, ue, (int)((nu + ue - 1) / ue),
+                   ldg, L.s, ids, dloss, buf.up, buf.dbp, buf.u, dB};
+      const long n = (long)L.r * vc + (r.last ? (long)L.r * (L.N - V) : 0);
+      xent_reduce_kernel<<<dim3((unsigned)(r.ublocks + (n + 255) / 256)), 256, 0, st>>>(r);
     }
   }
   if (L.r > 0) {
