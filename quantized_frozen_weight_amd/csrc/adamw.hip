@@ -2,7 +2,9 @@
 // the 8-bit form: include/qlora.h).
 //
 // Memory-bound: an element moves 28 bytes with float32 moments, 16.1 with 8-bit
-// ones, and 4 more where the norm is taken first. Two small tensors are one
+// ones, and 4 more where the norm is taken first (100 million elements in one tensor:
+// 527 and 606 us with float32 moments, 5.3 TB/s, 308 and 412 with 8-bit ones, 5.2 and
+// 4.9, whose vector work is as long). Two small tensors are one
 // block's work in one launch; else two kernels, each launched once per 64
 // tensors, their pointers in the kernel's arguments:
 //
@@ -166,28 +168,46 @@ __device__ __forceinline__ int scale_exp(uint32_t top) {
   return e < -126 ? -126 : e > 127 ? 127 : e;
 }
 
-// A magnitude under its group's scale as a code: v 2^-(e + 120) is a float32
-// whose exponent field is the code's, 0 to 7; the hash's 16 bits are added
+// 2^e, e in [-127, 127]; the factor of a group by its scale byte (255: NaN).
+__device__ __forceinline__ float power_of_two(int e) {
+  return __uint_as_float(e > -127 ? (uint32_t)(e + 127) << 23 : 0x400000u);
+}
+__device__ __forceinline__ float group_factor(int byte) {
+  return byte == 255 ? __uint_as_float(0x7fc00000u) : power_of_two(byte - 127);
+}
+
+// A magnitude under its group's scale as a code: v 2^-(e + 120), `inv` = 2^-e, is a
+// float32 whose exponent field is the code's, 0 to 7; the hash's 16 bits are added
 // right below the code's last bit.
 template <int BITS>
-__device__ __forceinline__ uint32_t to_code(float v, int e, uint32_t rnd) {
-  const uint32_t f = __float_as_uint(__builtin_ldexpf(__builtin_ldexpf(__builtin_fabsf(v), -e), -120));
+__device__ __forceinline__ uint32_t to_code(float v, float inv, uint32_t rnd) {
+  const uint32_t f = __float_as_uint(__builtin_fabsf(v) * inv * 0x1p-120f);
   const uint32_t c = (f + (rnd << (23 - BITS - 16))) >> (23 - BITS);
   constexpr uint32_t most = (8u << BITS) - 1;
   return c < most ? c : most;
 }
+// A code times its group's factor; bit 31 of `sign` is the value's sign.
 template <int BITS>
-__device__ __forceinline__ float of_code(uint32_t c, int e) {
-  return __builtin_ldexpf(__builtin_ldexpf(__uint_as_float(c << (23 - BITS)), 120), e);
+__device__ __forceinline__ float of_code(uint32_t c, uint32_t sign, float factor) {
+  return __uint_as_float((c << (23 - BITS)) | (sign & 0x80000000u)) * 0x1p120f * factor;
 }
 
 // What every element of a launch shares.
 struct Step {
   float beta1, rest1, beta2, rest2, eps;
-  float rate, root_c2, coef;          // lr / (1 - beta1^k); coef: of the gradient
-  int clip;
+  float rate, root_c2, inv_c2;        // lr / (1 - beta1^k); 1 / root_c2
+  float coef;                         // of the gradient (1: not clipped)
   uint32_t key;                       // of the hash: step and seed
 };
+
+// root / root_c2, the rounded quotient, from the rounded reciprocal: the remainder of
+// the first product is exact (roots are 0, or 2^-75 and more), and its share rounds
+// once more (a divisor of 24 ones may leave it one step off). A division that knows
+// nothing of its divisor is ten instructions, and 8-bit steps are bound by theirs.
+__device__ __forceinline__ float over(float root, const Step& s) {
+  const float y = root * s.inv_c2, rest = __builtin_fmaf(-y, s.root_c2, root);
+  return root <= 3.4028234e38f ? __builtin_fmaf(rest, s.inv_c2, y) : root;
+}
 
 // Four elements of one tensor from element e on, in registers.
 template <bool S8> struct Piece {
@@ -246,49 +266,57 @@ template <bool S8> struct Piece {
     const int n = it.n;
     float root[4];
     if constexpr (S8) {
+      const float mf = group_factor(ms), vf = group_factor(vs);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const uint32_t mb = (mc >> (8 * c)) & 0xffu, vb = (vc >> (8 * c)) & 0xffu;
-        const float mv = of_code<4>(mb & 127u, ms - 127), rv = of_code<5>(vb, vs - 127);
-        m[c] = ms == 255 ? __uint_as_float(0x7fc00000u) : (mb & 128u) ? -mv : mv;
-        v[c] = vs == 255 ? __uint_as_float(0x7fc00000u) : rv * rv;
+        const float rv = of_code<5>(vb, 0u, vf);
+        m[c] = of_code<4>(mb & 127u, mb << 24, mf);
+        v[c] = rv * rv;
       }
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const float gc = s.clip ? g[c] * s.coef : g[c];
+      const float gc = g[c] * s.coef;
       m[c] = s.beta1 * m[c] + s.rest1 * gc;
       v[c] = s.beta2 * v[c] + s.rest2 * (gc * gc);
       root[c] = sqrtf(v[c]);
       const float moved = p[c] * keep;
-      p[c] = moved - s.rate * (m[c] / (root[c] / s.root_c2 + s.eps));
+      p[c] = moved - s.rate * (m[c] / (over(root[c], s) + s.eps));
     }
     uint32_t mo = 0u, vo = 0u;
     int me = 0, ve = 0;
     if constexpr (S8) {
       // elements past the end are no part of their group
+      if (e + 4 > n) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (e + c >= n) m[c] = root[c] = 0.f;
+      }
       uint32_t mt = 0u, vt = 0u;
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (e + c < n) {
-          const uint32_t x = abs_bits(m[c]), y = abs_bits(root[c]);
-          mt = x > mt ? x : mt;
-          vt = y > vt ? y : vt;
-        }
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t x = abs_bits(m[c]), y = abs_bits(root[c]);
+        mt = x > mt ? x : mt;
+        vt = y > vt ? y : vt;
+      }
       mt = group_max(mt);
       vt = group_max(vt);
       const bool mbad = mt >= 0x7f800000u, vbad = vt >= 0x7f800000u;
       me = scale_exp<4>(mt);
       ve = scale_exp<5>(vt);
+      const float mi = power_of_two(-me), vi = power_of_two(-ve);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const uint32_t rnd = hash32((uint32_t)(e + c) * 0x9E3779B1u + (uint32_t)item * 0x3C6EF373u + s.key);
-        const uint32_t x = to_code<4>(m[c], me, rnd & 0xffffu) | (m[c] < 0.f ? 128u : 0u);
-        uint32_t y = to_code<5>(root[c], ve, rnd >> 16);
-        y = y == 0u && root[c] > 0.f ? 1u : y;
-        mo |= (mbad ? 0u : x) << (8 * c);
-        vo |= (vbad ? 0u : y) << (8 * c);
+        const uint32_t x = to_code<4>(m[c], mi, rnd & 0xffffu) | (m[c] < 0.f ? 128u : 0u);
+        const uint32_t y = to_code<5>(root[c], vi, rnd >> 16), bits = __float_as_uint(root[c]);
+        const uint32_t least = bits < 1u ? bits : 1u;       // 1 where the root (not negative) is not 0
+        mo |= x << (8 * c);
+        vo |= (y > least ? y : least) << (8 * c);
       }
+      mo = mbad ? 0u : mo;
+      vo = vbad ? 0u : vo;
       me = mbad ? 255 : me + 127;
       ve = vbad ? 255 : ve + 127;
     }
@@ -328,8 +356,8 @@ template <bool S8> struct Piece {
 __device__ __forceinline__ bool no_norm(float norm) { return !(norm <= 3.4028234e38f); }
 
 __device__ __forceinline__ Step step_of(const UpdateArgs& a, const Hyper& h, float norm) {
-  return Step{a.beta1, a.rest1, a.beta2, a.rest2, a.eps, h.lr / h.c1, h.root_c2,
-              a.clip ? a.clip_norm / (norm > a.clip_norm ? norm : a.clip_norm) : 1.f, a.clip,
+  return Step{a.beta1, a.rest1, a.beta2, a.rest2, a.eps, h.lr / h.c1, h.root_c2, 1.f / h.root_c2,
+              a.clip ? a.clip_norm / (norm > a.clip_norm ? norm : a.clip_norm) : 1.f,
               (uint32_t)h.k * 0xBB67AE85u + a.seed};
 }
 
@@ -415,7 +443,7 @@ __global__ __launch_bounds__(256) void moment_read_kernel(const uint8_t* codes, 
                                                           typename Elem<T>::type* x) {
   const long e = ((long)blockIdx.x * 256 + threadIdx.x) * 8;
   if (e >= n) return;
-  const int sb = scales[e / 32];
+  const float factor = group_factor(scales[e / 32]);
   uint32_t w[2] = {0u, 0u};
   if (e + 8 <= n) {
     const u32x2 v = *reinterpret_cast<const u32x2*>(codes + e);
@@ -428,8 +456,7 @@ __global__ __launch_bounds__(256) void moment_read_kernel(const uint8_t* codes, 
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     const uint32_t b = (w[c / 4] >> (8 * (c % 4))) & 0xffu;
-    const float y = of_code<BITS>(BITS == 4 ? b & 127u : b, sb - 127);
-    v[c] = sb == 255 ? __uint_as_float(0x7fc00000u) : BITS == 4 && (b & 128u) ? -y : y;
+    v[c] = of_code<BITS>(BITS == 4 ? b & 127u : b, BITS == 4 ? b << 24 : 0u, factor);
   }
   if (e + 8 <= n) {
     if constexpr (sizeof(x[0]) == 4) {
@@ -472,10 +499,11 @@ __global__ __launch_bounds__(256) void moment_write_kernel(const typename Elem<T
   if (e >= n) return;
   const bool bad = top >= 0x7f800000u;
   const int ex = scale_exp<BITS>(top);
+  const float inv = power_of_two(-ex);
   uint32_t w[2] = {0u, 0u};
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    uint32_t k = to_code<BITS>(v[c], ex, 0x8000u);
+    uint32_t k = to_code<BITS>(v[c], inv, 0x8000u);
     if (BITS == 5) k = k == 0u && v[c] != 0.f ? 1u : k;
     else k |= v[c] < 0.f ? 128u : 0u;
     w[c / 4] |= (bad ? 0u : k) << (8 * (c % 4));
