@@ -288,6 +288,10 @@ LOSSES = [
     (1, 128, 5, 2, "w4g128", "bf16", "i64"), (31, 256, 400, 0, "w4g128", "bf16", "i64"),
     (200, 512, 700, 8, "w4g128", "bf16", "i32"), (130, 4096, 300, 20, "w4g128", "bf16", "i64"),
     (20, 8192, 150, 4, "w4g128", "bf16", "i64"), (140, 16384, 130, 0, "w4g128", "bf16", "i64"),
+    # few rows over many entries: many splits, and tiles between the smallest and the largest
+    (40, 256, 9000, 8, "w4g128", "bf16", "i64"), (5, 64, 20000, 4, "w8", "f32", "i32"),
+    (1, 32, 30000, 9, "w8", "bf16", "i64"), (256, 512, 16000, 8, "w8", "bf16", "i64"),
+    (200, 320, 33000, 16, "w8", "bf16", "i64"), (600, 64, 9001, 2, "w8", "f32", "i64"),
 ]
 
 
