@@ -1025,13 +1025,31 @@ __global__ __launch_bounds__(256) void xent_reduce_kernel(ReduceArgs a) {
 // features: where there are at most as many tiles as compute units (64 x 768 in 85
 // splits: 15.7 us, one wave a tile 41; 256 x 2048 in 32 splits, 512 tiles, the other
 // way round: 25.9 against 19.3).
+// dA = s times the row blocks' partial sums (xent_da_kernel) is taken beside it, by the
+// blocks with blockIdx.y past the tiles' (its own launch cost 3 to 10 us).
+struct DaTotal {
+  const float* part;
+  int blocks;            // of rows
+  float* dA;             // NULL: none
+  int y0;                // the first blockIdx.y
+};
+__device__ __forceinline__ void da_total(const DaTotal& t, long e, int K, int r, float s) {
+  const long n = (long)r * K;
+  if (e < n) t.dA[e % K * r + e / K] = s * rank_sum_total(t.part, t.blocks, n, e);
+}
+
 template <typename OutT, int R, int SW>
 __global__ __launch_bounds__(SW == 1 ? 256 : 64 * SW) void xent_dx_join_kernel(const float* dxp, int splits, int M, int K,
                                                                                int r, float s, const float* u,
                                                                                const float* A, Ids ids,
                                                                                const float* dloss, float down,
-                                                                               const uint32_t* smax, OutT* dx) {
+                                                                               const uint32_t* smax, OutT* dx,
+                                                                               DaTotal total) {
   __shared__ f32x4 red[SW > 1 ? SW * 256 : 1];             // [wave][block of 4 features][lane]
+  if constexpr (R > 0) {
+    if ((int)blockIdx.y >= total.y0)
+      return da_total(total, ((long)((int)blockIdx.y - total.y0) * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x, K, r, s);
+  }
   const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4, w = threadIdx.x >> 6;
   const int m = blockIdx.x * 16 + l, mc = m < M ? m : M - 1;
   const int d0 = (SW > 1 ? (int)blockIdx.y : (int)blockIdx.y * 4 + w) * 64, k = d0 + 16 * q, kc = k < K ? k : 0;
@@ -1117,7 +1135,7 @@ __global__ __launch_bounds__(SW == 1 ? 256 : 64 * SW) void xent_dx_join_kernel(c
 
 template <typename OutT>
 void dx_join(const VocabLayer& L, int M, Ids ids, const float* dloss, const XentPlan& plan, const XentBuffers& buf,
-             void* dx, hipStream_t st) {
+             void* dx, DaTotal total, hipStream_t st) {
   const unsigned rows = (unsigned)((M + 15) / 16), cols = (unsigned)((L.K + 63) / 64);
   const bool shared = plan.splits >= 8 && (long)rows * cols <= kCUs;
   const float down = L.fmt == 0 ? 1.f : kHalfDown;
@@ -1125,12 +1143,16 @@ void dx_join(const VocabLayer& L, int M, Ids ids, const float* dloss, const Xent
   const auto launch = [&](auto rank) {
     constexpr int R = decltype(rank)::value;
     const uint32_t* smax = L.fmt == 0 && plan.parts == 1 ? buf.smax : nullptr;
+    const int threads = shared ? 1024 : 256;
+    total.y0 = (int)(shared ? cols : (cols + 3) / 4);
+    const long per = (long)threads * rows, extra = R > 0 ? ((long)L.r * L.K + per - 1) / per : 0;
+    const dim3 grid(rows, (unsigned)(total.y0 + extra));
     if (shared)
-      xent_dx_join_kernel<OutT, R, 16><<<dim3(rows, cols), 1024, 0, st>>>(buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u,
-                                                                         L.A, ids, dloss, down, smax, out);
+      xent_dx_join_kernel<OutT, R, 16><<<grid, 1024, 0, st>>>(buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids,
+                                                             dloss, down, smax, out, total);
     else
-      xent_dx_join_kernel<OutT, R, 1><<<dim3(rows, (cols + 3) / 4), 256, 0, st>>>(
-          buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids, dloss, down, smax, out);
+      xent_dx_join_kernel<OutT, R, 1><<<grid, 256, 0, st>>>(buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids,
+                                                            dloss, down, smax, out, total);
   };
   if (L.r == 0) launch(std::integral_constant<int, 0>());
   else if (L.r <= 4) launch(std::integral_constant<int, 4>());
@@ -1147,10 +1169,8 @@ __global__ __launch_bounds__(256) void xent_da_kernel(const typename Elem<T>::ty
   rank_sum_block<T, RB>(blockIdx.x, M, K, r, rows, x, part, lds, [&](int m) { return entry_of(ids, m) >= 0; },
                         [&](int m, int j) { return u[(long)m * r + j]; });
 }
-__global__ __launch_bounds__(256) void xent_da_total_kernel(const float* part, int blocks, int K, int r, float s,
-                                                            float* dA) {
-  const long e = (long)blockIdx.x * 256 + threadIdx.x, n = (long)r * K;
-  if (e < n) dA[e % K * r + e / K] = s * rank_sum_total(part, blocks, n, e);
+__global__ __launch_bounds__(256) void xent_da_total_kernel(DaTotal t, int K, int r, float s) {
+  da_total(t, (long)blockIdx.x * 256 + threadIdx.x, K, r, s);
 }
 
 // ---- launches ---------------------------------------------------------------------
@@ -1299,6 +1319,7 @@ void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const void*
       xent_reduce_kernel<<<dim3((unsigned)(r.ublocks + (n + 255) / 256)), 256, 0, st>>>(r);
     }
   }
+  DaTotal total{};
   if (L.r > 0) {
     const int rows_a = rank_sum_rows(M, L.K), blocks = rank_sum_blocks(M, L.K);
     const float* xf = static_cast<const float*>(x);
@@ -1311,12 +1332,13 @@ void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const void*
       xent_da_kernel<BF16, 1><<<dim3((unsigned)blocks), 256, 0, st>>>(xh, buf.u, ids, M, L.K, L.r, rows_a, buf.pA);
     else
       xent_da_kernel<BF16, 2><<<dim3((unsigned)blocks), 256, 0, st>>>(xh, buf.u, ids, M, L.K, L.r, rows_a, buf.pA);
-    xent_da_total_kernel<<<dim3((unsigned)(((long)L.r * L.K + 255) / 256)), 256, 0, st>>>(
-        buf.pA, (M + rows_a - 1) / rows_a, L.K, L.r, L.s, dA);
+    total = DaTotal{buf.pA, (M + rows_a - 1) / rows_a, dA, 0};
+    if (dx == nullptr)
+      xent_da_total_kernel<<<dim3((unsigned)(((long)L.r * L.K + 255) / 256)), 256, 0, st>>>(total, L.K, L.r, L.s);
   }
   if (dx == nullptr) return;
-  if (dtype == 0) dx_join<float>(L, M, ids, dloss, plan, buf, dx, st);
-  else dx_join<uint16_t>(L, M, ids, dloss, plan, buf, dx, st);
+  if (dtype == 0) dx_join<float>(L, M, ids, dloss, plan, buf, dx, total, st);
+  else dx_join<uint16_t>(L, M, ids, dloss, plan, buf, dx, total, st);
 }
 
 }  // namespace qlora
