@@ -563,7 +563,8 @@ int qlora_xent_fwd(const qlora_linear* L, int vocab, int M, int dtype, const voi
  * formed again piece by piece of the vocabulary (about 256 MB of dl each, in
  * the workspace). dl is formed in float32; for the product with W it is rounded
  * to float16 (int8 weights: times the entry's scale over a power of two at
- * least the largest scale; 4-bit weights: W is then rounded to float16, too),
+ * least the largest scale; 4-bit weights: W is rounded to float16, too, over such
+ * a power of two, so that it does not matter how large the layer's weights are),
  * in the float32 compute dtype to three bf16 parts, which keep it; for those
  * with B and t all three operands are in three bf16 parts. dA and dB are NULL
  * where r = 0; dx may be NULL where r >= 1. Limits as for qlora_xent_fwd. */

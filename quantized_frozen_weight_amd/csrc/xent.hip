@@ -143,20 +143,23 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 // end), scaled so that the largest is 2^14 and 2^-24 of that still has all bits:
 // int8 weights: 2^14 (p - [target]) scale / 2^E, E the smallest (at least -100) with
 // every scale below 2^E (a power of two: nothing more is rounded), against the codes;
-// 4-bit weights: 2^14 (p - [target]), against q times (scale / 8) in float16 (7
-// times the largest scale then fits; the quotient loses bits of scales under 2^-11
-// only).
-constexpr float kHalfUp = 16384.f, kHalfDown = 8.f / 16384.f;
+// 4-bit weights: 2^14 (p - [target]), against q scale 2^(13 - E) in float16, E of
+// the same kind: 8 times the largest scale then fits, and a scale keeps its bits
+// down to 2^-26 of that (a fixed 1 / 8 lost those of scales under 2^-11, and from
+// 2^-22 on all of them: dx of weights of 2e-5 was off by 5 %).
+constexpr float kHalfUp = 16384.f;
+constexpr int kHalfBits = 14, kHalfBits4 = 14 + 13;      // dx is formed times 2^(this - E)
 
-// The largest of the entries' scales, by 64 partial maxima (scales that are no
-// numbers left out: what they enter is none either way).
+// The largest of n scales (float32, or 4-bit weights' float16), by 64 partial maxima
+// (scales that are no numbers left out: what they enter is none either way).
 constexpr int kMaxParts = 64;
-__global__ __launch_bounds__(1024) void xent_scale_max_kernel(const float* scales, int V, uint32_t* part) {
+template <typename S>
+__global__ __launch_bounds__(1024) void xent_scale_max_kernel(const S* scales, int n, uint32_t* part) {
   __shared__ uint32_t red[16];
   uint32_t mx = 0u;
 #pragma unroll 4
-  for (long i = blockIdx.x * 1024 + threadIdx.x; i < V; i += 1024 * kMaxParts) {
-    const uint32_t b = abs_bits(scales[i]);
+  for (long i = blockIdx.x * 1024 + threadIdx.x; i < n; i += 1024 * kMaxParts) {
+    const uint32_t b = abs_bits((float)scales[i]);
     mx = b < 0x7f800000u && b > mx ? b : mx;
   }
   mx = wave_max_u32(mx);
@@ -405,7 +408,7 @@ __global__ __launch_bounds__(64 * WM * WN) void xent_logits_kernel(LogitArgs a) 
   float* lsv = reinterpret_cast<float*>(lds + Lds::LS);    // log2e lse
   uint16_t* tb = reinterpret_cast<uint16_t*>(lds + Lds::TB);
   // int8, dl in float16: the scales times 2^(14 - E), the rows' the other way round
-  const int power = HALF && !W4 ? 14 - scale_power(emax) : 0;
+  const int power = HALF && !W4 ? kHalfBits - scale_power(emax) : 0;
   const float up = __builtin_ldexpf(1.f, power), down = __builtin_ldexpf(1.f, -power);
   // Gradient: a row without a target has logits 0 and lse infinite, so that its
   // p is 0 whatever its x is (and is set to 0 below, for weights that are no numbers).
@@ -782,6 +785,7 @@ struct DxArgs {
   int parts;
   const int8_t* codes;
   const _Float16* scales;        // 4-bit
+  const uint32_t* smax;          // [64] partial maxima of them
   int v0;                // first entry of the piece
   int tiles_m, tiles_k;
   int splits, nks;       // stages (of all parts) per split
@@ -861,6 +865,8 @@ __global__ __launch_bounds__(64 * WM * 4) void xent_dx_kernel(DxArgs a) {
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // 4-bit: the power of two that takes the scales into float16
+  const float sf = W4 ? __builtin_ldexpf(1.f, 13 - scale_power(a.smax[lane])) : 0.f;
 #pragma unroll
   for (int st = 0; st < S - 1; ++st)
     if (kt0 + st < kt1) issue(kt0 + st, st);
@@ -871,14 +877,14 @@ __global__ __launch_bounds__(64 * WM * 4) void xent_dx_kernel(DxArgs a) {
     if (kt + S - 1 < kt1) issue(kt + S - 1, slot == 0 ? S - 1 : slot - 1);
     const int8_t* As = ring + slot * STG;
     const int8_t* Bs = As + ASZ;
-    int8_t* sch = ring + S * STG + wid * 128;               // this wave's scales / 8 of the stage's 64 entries
+    int8_t* sch = ring + S * STG + wid * 128;               // this wave's scales times sf of the stage's 64 entries
     if constexpr (W4) {
       // lane: one entry, the half of its dword by the place's parity; entries that
       // are none get 0 (this wave's own bytes: no barrier)
       const int v = a.v0 + kt * KC + lane, vc = v < a.N ? v : a.N - 1;
       const uint32_t two = *reinterpret_cast<const uint32_t*>(Bs + BSZ + wid * 256 + lane * 4);
       const uint16_t hb = (uint16_t)((vc * ngrp + (grp < ngrp ? grp : 0)) & 1 ? two >> 16 : two);
-      const float sc = v < a.V ? 0.125f * (float)__builtin_bit_cast(_Float16, hb) : 0.f;
+      const float sc = v < a.V ? sf * (float)__builtin_bit_cast(_Float16, hb) : 0.f;
       *reinterpret_cast<_Float16*>(sch + lane * 2) = (_Float16)sc;
       asm volatile("" ::: "memory");
     }
@@ -1042,7 +1048,7 @@ template <typename OutT, int R, int SW>
 __global__ __launch_bounds__(SW == 1 ? 256 : 64 * SW) void xent_dx_join_kernel(const float* dxp, int splits, int M, int K,
                                                                                int r, float s, const float* u,
                                                                                const float* A, Ids ids,
-                                                                               const float* dloss, float down,
+                                                                               const float* dloss, int bits,
                                                                                const uint32_t* smax, OutT* dx,
                                                                                DaTotal total) {
   __shared__ f32x4 red[SW > 1 ? SW * 256 : 1];             // [wave][block of 4 features][lane]
@@ -1060,8 +1066,8 @@ __global__ __launch_bounds__(SW == 1 ? 256 : 64 * SW) void xent_dx_join_kernel(c
 #pragma unroll
   for (int b = 0; b < 4; ++b)
     v[b] = first < splits ? *reinterpret_cast<const f32x4*>(p + first * n + 4 * b) : f32x4{0.f, 0.f, 0.f, 0.f};
-  // (int8, dl in float16: back from 2^(14 - E))
-  const float back = smax != nullptr ? __builtin_ldexpf(1.f, scale_power(smax[lane]) - 14) : down;
+  // (dl in float16: back from 2^(bits - E))
+  const float back = smax != nullptr ? __builtin_ldexpf(1.f, scale_power(smax[lane]) - bits) : 1.f;
   const bool live = entry_of(ids, mc) >= 0;
   const float f = dloss[mc] * back;
   f32x4 low[4];
@@ -1138,21 +1144,21 @@ void dx_join(const VocabLayer& L, int M, Ids ids, const float* dloss, const Xent
              void* dx, DaTotal total, hipStream_t st) {
   const unsigned rows = (unsigned)((M + 15) / 16), cols = (unsigned)((L.K + 63) / 64);
   const bool shared = plan.splits >= 8 && (long)rows * cols <= kCUs;
-  const float down = L.fmt == 0 ? 1.f : kHalfDown;
+  const int bits = L.fmt == 0 ? kHalfBits : kHalfBits4;
   OutT* out = static_cast<OutT*>(dx);
   const auto launch = [&](auto rank) {
     constexpr int R = decltype(rank)::value;
-    const uint32_t* smax = L.fmt == 0 && plan.parts == 1 ? buf.smax : nullptr;
+    const uint32_t* smax = plan.parts == 1 ? buf.smax : nullptr;
     const int threads = shared ? 1024 : 256;
     total.y0 = (int)(shared ? cols : (cols + 3) / 4);
     const long per = (long)threads * rows, extra = R > 0 ? ((long)L.r * L.K + per - 1) / per : 0;
     const dim3 grid(rows, (unsigned)(total.y0 + extra));
     if (shared)
       xent_dx_join_kernel<OutT, R, 16><<<grid, 1024, 0, st>>>(buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids,
-                                                             dloss, down, smax, out, total);
+                                                             dloss, bits, smax, out, total);
     else
       xent_dx_join_kernel<OutT, R, 1><<<grid, 256, 0, st>>>(buf.dxp, plan.splits, M, L.K, L.r, L.s, buf.u, L.A, ids,
-                                                            dloss, down, smax, out, total);
+                                                            dloss, bits, smax, out, total);
   };
   if (L.r == 0) launch(std::integral_constant<int, 0>());
   else if (L.r <= 4) launch(std::integral_constant<int, 4>());
@@ -1290,6 +1296,9 @@ void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const void*
   const int rows = dx_rows(M);
   if (L.fmt == 0 && plan.parts == 1)
     xent_scale_max_kernel<<<dim3(kMaxParts), 1024, 0, st>>>(static_cast<const float*>(L.scales), V, buf.smax);
+  else if (L.fmt == 1 && dx != nullptr)
+    xent_scale_max_kernel<<<dim3(kMaxParts), 1024, 0, st>>>(static_cast<const _Float16*>(L.scales), V * (L.K / 128),
+                                                            buf.smax);
   for (int v0 = 0; v0 < V; v0 += plan.piece) {
     const int vc = V - v0 < plan.piece ? V - v0 : plan.piece;
     const long ldg = (vc + 255) / 256 * 256;
@@ -1301,7 +1310,8 @@ void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const void*
     if (dx != nullptr) {
       DxArgs d{};
       d.M = M; d.N = L.N; d.K = L.K; d.V = V; d.g = buf.g; d.ldg = ldg; d.gstride = a.gstride; d.parts = plan.parts;
-      d.codes = a.codes; d.scales = static_cast<const _Float16*>(L.scales); d.v0 = v0;
+      d.codes = a.codes; d.scales = static_cast<const _Float16*>(L.scales); d.smax = buf.smax;
+      d.v0 = v0;
       d.tiles_m = (M + rows - 1) / rows; d.tiles_k = (L.K + 255) / 256;
       d.splits = plan.splits;
       d.nks = (plan.parts * (int)(ldg / 64) + plan.splits - 1) / plan.splits;
