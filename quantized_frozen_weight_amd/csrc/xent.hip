@@ -965,7 +965,7 @@ __global__ __launch_bounds__(64 * WM * 4) void xent_dx_kernel(DxArgs a) {
 // tiles' parts; the last piece also clears dB's padding. The first `ublocks` blocks
 // take `ue` elements of u each (a power of two), 256 / ue threads an element that
 // share its tiles, few elements where there are few (64 rows of rank 8 over 393
-// tiles: 4.8 us, a thread each 30); the others a thread an element.
+// tiles: 4.8 us, a thread each 30); the others a thread an element, in up to 2^21 blocks.
 struct ReduceArgs {
   int M, N, r, tiles_x, tiles_m, v0, vc, first, last, V, ue, ublocks;
   long ldg;
@@ -1012,13 +1012,15 @@ __global__ __launch_bounds__(256) void xent_reduce_kernel(ReduceArgs a) {
     a.u[e] = a.last ? u * row_factor(a.ids, a.dloss, e / a.r) : u;     // (u of a row without a target is 0)
     return;
   }
-  const long e = (long)((int)blockIdx.x - a.ublocks) * 256 + tid;
-  if (e < ndb) {
-    const long j = e / a.vc, c = e % a.vc;
-    a.dB[j * a.N + a.v0 + c] = a.s * sum(a.dbp + j * a.ldg + c, a.r * a.ldg, a.tiles_m);
-  } else if (e < ndb + npad) {
-    const long j = (e - ndb) / (a.N - a.V), c = (e - ndb) % (a.N - a.V);
-    a.dB[j * a.N + a.V + c] = 0.f;
+  const long step = (long)((int)gridDim.x - a.ublocks) * 256;
+  for (long e = (long)((int)blockIdx.x - a.ublocks) * 256 + tid; e < ndb + npad; e += step) {
+    if (e < ndb) {
+      const long j = e / a.vc, c = e % a.vc;
+      a.dB[j * a.N + a.v0 + c] = a.s * sum(a.dbp + j * a.ldg + c, a.r * a.ldg, a.tiles_m);
+    } else {
+      const long j = (e - ndb) / (a.N - a.V), c = (e - ndb) % (a.N - a.V);
+      a.dB[j * a.N + a.V + c] = 0.f;
+    }
   }
 }
 
@@ -1322,11 +1324,14 @@ void launch_xent_bwd(const VocabLayer& L, int M, int dtype, Ids ids, const void*
     }
     if (L.r > 0) {
       const long nu = (long)M * L.r;
-      const int ue = nu > 8192 ? 32 : 8;                   // (32: whole lines of every tile's parts)
+      // 32: whole lines of every tile's parts; 256 where 8 threads an element and those
+      // of dB could be the 2^32 threads that a launch has to stay below (2^24 rows of
+      // rank 32 are)
+      const int ue = nu > 3L << 27 ? 256 : nu > 8192 ? 32 : 8;
       ReduceArgs r{M, L.N, L.r, a.tiles_x, a.tiles_m, v0, vc, v0 == 0, v0 + vc == V, V, ue, (int)((nu + ue - 1) / ue),
                    ldg, L.s, ids, dloss, buf.up, buf.dbp, buf.u, dB};
-      const long n = (long)L.r * vc + (r.last ? (long)L.r * (L.N - V) : 0);
-      xent_reduce_kernel<<<dim3((unsigned)(r.ublocks + (n + 255) / 256)), 256, 0, st>>>(r);
+      const long n = (long)L.r * vc + (r.last ? (long)L.r * (L.N - V) : 0), nb = (n + 255) / 256;
+      xent_reduce_kernel<<<dim3((unsigned)(r.ublocks + (nb < 1L << 21 ? nb : 1L << 21))), 256, 0, st>>>(r);
     }
   }
   DaTotal total{};
