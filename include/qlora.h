@@ -544,6 +544,9 @@ int qlora_embed_bwd(const qlora_linear* L, int vocab, int M, int dtype, const vo
  *                              adapter's part s (x A) B in float32
  *   lse[m]  = log sum_{v < vocab} exp(l[m, v])         float32 [M]
  *   loss[m] = lse[m] - l[m, target(m)]                 float32 [M]
+ * A 4-bit layer's loss is thus that of qlora_fwd_a8w4's logits; qlora_fwd takes x
+ * as it is there, and has others by the rounding of x to 8 bits (one part in 254
+ * of the row's largest, which rows with a few features far above the rest feel).
  * No logit is written to memory: a tile's rows leave their maximum and sum
  * (8 bytes for 128 or 256 logits). t_save as for qlora_fwd (r >= 1). A row of x
  * with an infinity or a NaN has lse NaN, and touches no other row. Int8 layers

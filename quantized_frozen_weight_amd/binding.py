@@ -1015,9 +1015,10 @@ def _xent_args(layer, x, targets, vocab):
 def qlora_xent_fwd(layer: QLinear, x, targets, vocab: Optional[int] = None, save_t: bool = True, loss=None, lse=None,
                    t=None, ws=None):
     """Softmax cross entropy of x [M, K] over the layer's first vocab entries for
-    targets [M] (int32 or int64; one outside [0, vocab) gives loss 0). Returns
-    (loss, lse, t): float32 [M] each, and t = x A (None unless save_t, or where
-    the layer has no adapter)."""
+    targets [M] (int32 or int64; one outside [0, vocab) gives loss 0). The logits
+    are the layer's integer forward's: qlora_fwd of an int8 layer, qlora_fwd_a8w4
+    of a 4-bit one. Returns (loss, lse, t): float32 [M] each, and t = x A (None
+    unless save_t, or where the layer has no adapter)."""
     import torch
     M, dt, dev, it, cs, vocab = _xent_args(layer, x, targets, vocab)
     f32 = torch.float32
