@@ -525,10 +525,12 @@ int qlora_embed(const qlora_linear* L, int vocab, int M, int dtype, const void* 
 /* Its gradient for dy [M, K], the gradient of x (r >= 1; the frozen weight has
  * none):
  *   u  = scale s dy A                                  (float32, internal)
- *   dB[:, v] = sum of u[m] over the rows m with token v, in increasing m;
+ *   dB[:, v] = sum of u[m] over the rows m with token v;
  *              0 for entries that no row names     float32 [r, N]
  *   dA = scale s sum_m dy[m]^T B[:, token(m)]^T    float32 [K, r]
- * The tokens are sorted on the way (stable). accumulate != 0 adds to what dA
+ * The tokens are sorted on the way (stable). Sums are in float32, in an order
+ * that the tokens and sizes alone decide: the same call gives the same bytes.
+ * accumulate != 0 adds to what dA
  * and dB hold, for a tied layer whose qlora_xent_bwd wrote them. M <= 2^20
  * (ERANGE above). */
 int qlora_embed_bwd_workspace(const qlora_linear* L, int vocab, int M, int dtype, size_t* bytes);
@@ -563,11 +565,15 @@ int qlora_xent_fwd(const qlora_linear* L, int vocab, int M, int dtype, const voi
  *   dA = s x^T u   float32 [K, r],  dB = s t^T dl   float32 [r, N]   (r >= 1)
  * dloss float32 [M]: the gradient of each row's loss (1 / count for a mean).
  * lse is qlora_xent_fwd's; t_saved its t (NULL: formed again). The logits are
- * formed again piece by piece of the vocabulary (about 256 MB of dl each, in
- * the workspace). dl is formed in float32; for the product with W it is rounded
+ * formed again piece by piece of the vocabulary (up to 256 MB of dl each, in the
+ * workspace, or 512 entries' where that is more: from 2^18 rows on, in float32
+ * from a third of them, dl grows with the rows). dl is formed in float32; for the product with W it is rounded
  * to float16 (int8 weights: times the entry's scale over a power of two at
  * least the largest scale; 4-bit weights: W is rounded to float16, too, over such
  * a power of two, so that it does not matter how large the layer's weights are),
+ * of which values down to 2^-28 keep 11 bits and those under 2^-39 vanish (an int8
+ * entry's share of dx is as accurate as ever with a scale 2^20 times its own in the
+ * layer; with one of 2^24 times it is lost),
  * in the float32 compute dtype to three bf16 parts, which keep it; for those
  * with B and t all three operands are in three bf16 parts. dA and dB are NULL
  * where r = 0; dx may be NULL where r >= 1. Limits as for qlora_xent_fwd. */
@@ -631,7 +637,8 @@ typedef struct {
  * > 0 or norm given, one per 64 tensors that sum the norm), and one per 64
  * tensors that moves them. items[] and cfg are read during the call only (host
  * memory). Tensors of different items must not overlap each other (not checked).
- * 0 <= beta < 1, eps > 0, lr, decay and clip_norm >= 0 and all finite; 0 <=
+ * Each block of the latter adds all sums of the norm: up to 512 and one for each
+ * tensor. 0 <= beta < 1, eps > 0, lr, decay and clip_norm >= 0 and all finite; 0 <=
  * *step (EINVAL for what the host can see). */
 int qlora_adamw_workspace(const qlora_adamw_item* items, int count, size_t* bytes);
 int qlora_adamw(const qlora_adamw_config* cfg, const qlora_adamw_item* items, int count, void* ws,

@@ -1071,7 +1071,8 @@ class AdamW:
     elements), the step count (int32 [1] on the device) and the step's
     workspace. decay: the weight decay of every tensor, or one per tensor (0:
     excluded). What is not given is made here, zero. The tensors must not move
-    while the object lives."""
+    while the object lives, and it takes one call at a time: a step writes the
+    gradients' addresses into it (no two threads, no two streams without ws)."""
 
     def __init__(self, params, state: str = "f32", decay=0.0, step=None, m=None, v=None, m_scales=None, v_scales=None,
                  seed: int = 0):

@@ -10,7 +10,9 @@
 //
 //   norm    a block sums the squares of one chunk of one tensor in float64 and
 //           leaves the sum in the workspace; chunks grow with the total, so
-//           that there are about 512 sums whatever the sizes. Block 0 of the
+//           that there are up to 512 sums and one more for each tensor, which
+//           every block of the update adds (2000 tensors of 1000 elements: 320 us
+//           replayed, 32 launches of each kernel, 174 without the norm). Block 0 of the
 //           first launch also forms what depends on the step alone (the bias
 //           corrections, in float64) and advances the step: nothing else reads
 //           it there. Without a norm to take, that block is the whole launch.

@@ -25,7 +25,7 @@
 //   comes as three bf16 parts, the contraction run over each. The contraction of
 //   a piece is split where there are few tiles; every split adds into a float32
 //   buffer of its own, piece after piece.
-// Pieces are as large as 256 MB of dl allow. Sums are in a fixed order.
+// Pieces are as large as 256 MB of dl allow, and of at least 512 entries. Sums are in a fixed order.
 // 2048 x 2048 over 256000 entries: loss 963 us (2.2 POP/s), the gradient's logits 1090,
 // dx 1894 (1.13 PFLOP/s; a large library product in bf16 reaches 1.24), all three at
 // 40 to 50 % of the matrix units' time with the vector units a third busy. At 768
@@ -1263,7 +1263,7 @@ void launch_xent_fwd(const VocabLayer& L, int M, Ids ids, const int8_t* xq, cons
 XentPlan xent_plan(const VocabLayer& L, int vocab, int M, int dtype) {
   XentPlan p{};
   p.parts = dtype == 0 ? 3 : 1;
-  // pieces of up to 256 MB of dl (the sums of dx are read and written once a
+  // pieces of up to 256 MB of dl, or of 512 entries (the sums of dx are read and written once a
   // piece), of whole rounds of 256 x 256 tiles over the chip where they hold one
   // (4096 x 768 x 50257 at rank 8: 1095 us, 1156 in two equal pieces, 1142 at 128 MB)
   const long most = (128L << 20) / p.parts / M / 256 * 256, tiles_m = (M + 255) / 256;
